@@ -446,10 +446,209 @@ moe_status_t moe_greedy_verify(const void* logits, int32_t logits_bf16, int32_t 
                                const int32_t* draft, const int32_t* n_draft, int32_t* argmax_out,
                                int32_t* accept_len, int32_t* out_tokens, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * The attention side of the step: a paged K/V cache, rotary positions written
+ * into it, attention of the step's new tokens over it (single tokens, verify
+ * blocks, prefill chunks), and eviction by accumulated attention weight.
+ *
+ * A page index outside the cache or a sequence whose numbers do not fit (an
+ * offset past n_tokens or below the one before it, a length past its block
+ * table) is never followed: the call records MOE_ERR_INVALID_ARG in the error
+ * word of its workspace (read with moe_get_device_error), takes such a
+ * sequence's new tokens as none or its length as what the table holds, and
+ * reads such a page as zeros.
+ * ------------------------------------------------------------------------ */
+
+#define MOE_KV_BF16 0          /* cache elements: bf16                            */
+#define MOE_KV_E4M3 1          /* e4m3 codes; value = code * scale of the kv head */
+#define MOE_MAX_HEADS 256      /* query heads                                     */
+#define MOE_MAX_SEQS 4096      /* sequences per call                              */
+#define MOE_MAX_TOKENS 65536   /* new tokens per call                             */
+
+/*
+ * One layer's paged cache: element (page, head, token, d) of K at
+ * k + page * page_stride + head * head_stride + token * token_stride + d
+ * elements, V alike, so both [pages, heads, tokens, d] and [pages, tokens,
+ * heads, d] orders fit, as do K and V interleaved in one allocation.
+ *   head_dim    64 or 128        page_size   16, 32, 64 or 128 tokens
+ *   strides     multiples of 16 bytes, positive, each below 2^40 bytes
+ *   k, v        16-byte aligned device memory
+ *   k_scale, v_scale  fp32 [n_kv_heads], e4m3 only (NULL for bf16)
+ */
+typedef struct {
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t token_stride;
+    int32_t dtype;
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+} moe_kv_cache_t;
+
+/*
+ * The step's sequences, all on the device so that a captured graph follows
+ * them.  Sequence b's new tokens are rows cu_q[b] .. cu_q[b+1]-1 of the
+ * step's [n_tokens, ...] tensors; kv_len[b] counts its cached tokens, the new
+ * ones included, so new token i lies at cache place kv_len[b] - n_b + i, in
+ * page block_table[b, place / page_size].  Rows of no sequence are pad rows.
+ *   cu_q         int32 [n_seqs + 1]
+ *   kv_len       int32 [n_seqs]
+ *   block_table  int32 [n_seqs, max_pages]; entries past a sequence's length are not read
+ *   max_q        largest number of new tokens of a sequence; it only picks the
+ *                kernel, the results hold for any value >= 1
+ */
+typedef struct {
+    const int32_t* cu_q;
+    const int32_t* kv_len;
+    const int32_t* block_table;
+    int32_t n_seqs;
+    int32_t max_pages;
+    int32_t max_q;
+} moe_seqs_t;
+
+/*
+ * Rotary positions: rot_dim leading elements of a head are rotated (a
+ * multiple of 16, 0 .. head_dim), the rest copied.  Pair i is elements
+ * (i, i + rot_dim/2), or (2i, 2i+1) when interleaved.
+ *   freqs      fp32 [rot_dim/2, 2] device: turns per position of pair i as a
+ *              sum of two fp32 (moe_rope_freqs fills it)
+ *   magnitude  multiplies cos and sin (1 without long-context scaling)
+ */
+typedef struct {
+    const float* freqs;
+    int32_t rot_dim;
+    int32_t interleaved;
+    float magnitude;
+} moe_rope_t;
+
+/*
+ * moe_rope_freqs -- host only: fills freqs[rot_dim/2][2] (host memory) and
+ * *magnitude.  f_i = base^(-2i/rot_dim) / 2 pi turns per position, then
+ *   MOE_ROPE_PLAIN   f_i
+ *   MOE_ROPE_LINEAR  f_i / factor
+ *   MOE_ROPE_RAMP    f_i for pairs that turn more than beta_fast times within
+ *                    original_len positions, f_i / factor for those that turn
+ *                    less than beta_slow times, a linear ramp over the pair
+ *                    index between; magnitude = 0.1 ln(factor) + 1
+ * The pair of fp32 keeps the angle exact to fp32 for |position| < 2^24.
+ */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_RAMP 2
+moe_status_t moe_rope_freqs(int32_t rot_dim, double base, int32_t kind, double factor,
+                            int32_t original_len, double beta_fast, double beta_slow,
+                            float* freqs_host, float* magnitude_host);
+
+/*
+ * moe_rope_append -- rotates q and k of the step's new tokens and stores k and
+ * v at their places in the cache.
+ *   q           bf16 [n_tokens, n_q_heads, head_dim], token stride q_stride
+ *   k, v        bf16 [n_tokens, n_kv_heads, head_dim], token strides k_stride, v_stride
+ *   positions   int32 [n_tokens]
+ *   q_out       bf16 [n_tokens, n_q_heads, head_dim], token stride q_out_stride
+ *               (may be q itself); pad rows are +0
+ * Strides in elements, multiples of 8; pointers 16-byte aligned; q_out and the
+ * cache overlap no other argument.  fp32 arithmetic, one rounding: bf16
+ * (nearest even), or the e4m3 code of x / scale (nearest even, saturating).
+ * A new token whose place is negative or past its block table, or whose page
+ * lies outside the cache, is not stored.  n_tokens == 0 launches nothing.
+ */
+moe_status_t moe_rope_append(const moe_rope_t* rope, const moe_kv_cache_t* cache,
+                             const moe_seqs_t* seqs, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, int32_t n_tokens, int32_t n_q_heads,
+                             void* q_out, int64_t q_out_stride, moe_stream_t stream);
+
+/*
+ * Attention of the step: n_q_heads a multiple of the cache's kv heads, query
+ * head h reads kv head h / (n_q_heads / n_kv_heads); scores are scale * q.k.
+ * With F = kv_len[b] - n_b, query i of a sequence sees cache place j when
+ *   j < kv_len[b], and
+ *   causal:        j <= F + i            (no draft_mask given)
+ *   draft_mask:    j < F, or bit j - F of its mask is set (j - F < 64), and
+ *   window > 0:    j > F + i - window.
+ * A row that sees nothing gives +0 and a log-sum-exp of -inf.
+ * wait_timeout_us bounds every device-side wait (0 = 2 000 000 us).
+ */
+typedef struct {
+    int32_t n_q_heads;
+    float scale;
+    int32_t causal;
+    int32_t window;
+    uint32_t wait_timeout_us;
+} moe_attn_t;
+
+/* Bytes of a workspace that serves the calls below for this shape, whatever
+ * the batch (0 for a shape that is refused).  The caller zeroes it once; calls
+ * on one stream may share it. */
+size_t moe_attn_workspace_bytes(const moe_attn_t* attn, const moe_kv_cache_t* cache);
+
+/*
+ * moe_paged_attention -- softmax attention of the new tokens over the cache.
+ *   q          bf16 [n_tokens, n_q_heads, head_dim], token stride q_stride (elements)
+ *   draft_mask uint64 [n_tokens] or NULL
+ *   out        bf16 [n_tokens, n_q_heads, head_dim] contiguous; pad rows +0
+ *   lse        fp32 [n_tokens, n_q_heads] or NULL: natural-log sum of exp of the
+ *              row's scores; pad rows -inf
+ * The work is split over the card by the lengths on the device; a long cache
+ * of few rows is cut into pieces that are joined in a fixed order, so equal
+ * calls give equal bits.  Scores, statistics and sums in fp32; the
+ * probabilities are rounded to the matrix instructions' 16-bit type.
+ */
+moe_status_t moe_paged_attention(const moe_attn_t* attn, const moe_kv_cache_t* cache,
+                                 const moe_seqs_t* seqs, const void* q, int64_t q_stride,
+                                 const uint64_t* draft_mask, int32_t n_tokens, void* out,
+                                 float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_key_weights -- the attention weight each cached key received:
+ *   scores_out[b, h, j] = decay * scores[b, h, j] (j < F; 0 for the step's own
+ *   keys) + sum of exp(scale * q.k_j - lse) over the queries and heads of kv
+ *   head h that see j,            for j < kv_len[b]; the rest is not written.
+ *   q, draft_mask  as moe_paged_attention was given them; lse its output.  A
+ *                  row whose lse is -inf or +inf adds nothing (set +inf to
+ *                  leave out rejected drafts).
+ *   scores, scores_out  fp32 [n_seqs, n_kv_heads, score_stride]; they may be
+ *                  the same array; score_stride >= every kv_len (a longer
+ *                  sequence's further keys are left out)
+ * fp32 sums in a fixed order; no atomics.
+ */
+moe_status_t moe_key_weights(const moe_attn_t* attn, const moe_kv_cache_t* cache,
+                             const moe_seqs_t* seqs, const void* q, int64_t q_stride,
+                             const uint64_t* draft_mask, int32_t n_tokens, const float* lse,
+                             float decay, const float* scores, float* scores_out,
+                             int64_t score_stride, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/*
+ * moe_cache_evict -- cuts every sequence to at most `budget` keys per kv head:
+ * the last n_recent keys and, of the others, those with the largest scores
+ * (equal scores: the lower place; NaN last) are kept, in their order, and
+ * their K and V rows and scores move together into other pages:
+ *   kept        int32 [n_seqs, n_kv_heads, budget]: the kept places, ascending, then -1
+ *   new_len     int32 [n_seqs]: min(kv_len, budget)
+ *   scores_out  fp32 [n_seqs, n_kv_heads, score_stride]: the kept scores first, the rest
+ *               not written; not the scores array itself
+ *   to_table    int32 [n_seqs, to_pages]: the pages written, which must not be
+ *               pages that any sequence of this call still reads (shared
+ *               prefix pages stay as they are); to_pages * page_size >= budget
+ * cu_q and max_q of seqs are not read.  budget >= 1, 0 <= n_recent <= budget.
+ */
+moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs,
+                             const float* scores, int64_t score_stride, int32_t budget,
+                             int32_t n_recent, const int32_t* to_table, int32_t to_pages,
+                             int32_t* kept, float* scores_out, int32_t* new_len, void* ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
 /*
  * moe_get_device_error -- synchronises `stream`, then reads (and clears when
  * `clear` != 0) the device error word at the start of a workspace given to
- * moe_expert_ffn_fp8 or moe_layer.  Returns MOE_OK, MOE_ERR_TIMEOUT (a bounded
+ * moe_expert_ffn_fp8, moe_layer or one of the attention calls.  Returns MOE_OK, MOE_ERR_TIMEOUT (a bounded
  * wait ran out: the kernel stopped, released its tensor memory and returned)
  * or MOE_ERR_CUDA.
  */

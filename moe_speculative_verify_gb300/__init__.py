@@ -27,10 +27,18 @@ __all__ = [
     "MOE_MAX_ROWS", "moe_expert_ffn_w8a16", "moe_layer_w8a16", "W8A16_MAX_ROWS",
     "moe_tile_weights", "tile_weights", "LAYOUT_ROW_MAJOR", "LAYOUT_TILED",
     "moe_workspace_size",
+    "KVCache", "Seqs", "Rope", "Attn", "KV_BF16", "KV_E4M3", "ROPE_PLAIN", "ROPE_LINEAR",
+    "ROPE_RAMP", "moe_rope_freqs", "moe_rope_append", "moe_attn_workspace_bytes",
+    "moe_paged_attention", "moe_key_weights", "moe_cache_evict",
 ]
 
 LAYOUT_ROW_MAJOR = 0
 LAYOUT_TILED = 1
+KV_BF16 = 0
+KV_E4M3 = 1
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_RAMP = 2
 CODE_KEYS = ("w_gate", "w_up", "w_down", "sh_gate", "sh_up", "sh_down")
 
 MOE_MAX_ROWS = 4096
@@ -79,6 +87,83 @@ class Weights(C.Structure):
         return w
 
 
+class KVCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("page_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("token_stride", C.c_int64), ("dtype", C.c_int32), ("n_pages", C.c_int32),
+                ("page_size", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32)]
+
+    @classmethod
+    def from_tensors(cls, k, v, k_scale=None, v_scale=None) -> "KVCache":
+        """From K and V [pages, kv heads, page size, head dim], bf16 or e4m3
+        (torch.float8_e4m3fn or uint8 codes, with fp32 scales [kv heads]), of
+        equal shape and strides; any strides with head dim contiguous, so a
+        permuted view of a [pages, page size, kv heads, head dim] cache fits.
+        The result holds references to the tensors."""
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        if (k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype
+                or k.stride(3) != 1 or k.dtype not in codes + (torch.bfloat16,)):
+            raise MoeError(1, "KVCache")
+        e4m3 = k.dtype in codes
+        for s in (k_scale, v_scale):
+            if e4m3 and (s is None or s.dtype != torch.float32 or s.numel() != k.shape[1]
+                         or not s.is_contiguous()):
+                raise MoeError(1, "KVCache")
+        n, h, p, d = k.shape
+        st = [k.stride(i) if k.shape[i] > 1 else d for i in range(3)]
+        c = cls(k.data_ptr(), v.data_ptr(), _ptr(k_scale) if e4m3 else None,
+                _ptr(v_scale) if e4m3 else None, st[0], st[1], st[2],
+                KV_E4M3 if e4m3 else KV_BF16, n, p, h, d)
+        c._tensors = (k, v, k_scale, v_scale)
+        return c
+
+
+class Seqs(C.Structure):
+    _fields_ = [("cu_q", C.c_void_p), ("kv_len", C.c_void_p), ("block_table", C.c_void_p),
+                ("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("max_q", C.c_int32)]
+
+    @classmethod
+    def from_tensors(cls, cu_q, kv_len, block_table, max_q: int = 1) -> "Seqs":
+        """From int32 device tensors cu_q [n + 1] (may be None for eviction
+        alone), kv_len [n] and block_table [n, max_pages], whose values may
+        change between calls; max_q: most new tokens of a sequence."""
+        n = kv_len.shape[0]
+        for t in (cu_q, kv_len, block_table):
+            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+                raise MoeError(1, "Seqs")
+        if block_table.dim() != 2 or block_table.shape[0] != n or (
+                cu_q is not None and cu_q.shape != (n + 1,)):
+            raise MoeError(1, "Seqs")
+        s = cls(_ptr(cu_q), kv_len.data_ptr(), block_table.data_ptr(), n, block_table.shape[1],
+                max_q)
+        s._tensors = (cu_q, kv_len, block_table)
+        return s
+
+
+class Rope(C.Structure):
+    _fields_ = [("freqs", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("magnitude", C.c_float)]
+
+    @classmethod
+    def from_freqs(cls, freqs, interleaved: bool = False, magnitude: float = 1.0) -> "Rope":
+        """From moe_rope_freqs' table [rot_dim/2, 2], fp32 on the device."""
+        if (freqs.dim() != 2 or freqs.shape[1] != 2 or freqs.dtype != torch.float32
+                or not freqs.is_contiguous()):
+            raise MoeError(1, "Rope")
+        r = cls(freqs.data_ptr(), 2 * freqs.shape[0], 1 if interleaved else 0, magnitude)
+        r._tensors = (freqs,)
+        return r
+
+
+class Attn(C.Structure):
+    _fields_ = [("n_q_heads", C.c_int32), ("scale", C.c_float), ("causal", C.c_int32),
+                ("window", C.c_int32), ("wait_timeout_us", C.c_uint32)]
+
+    def __init__(self, n_q_heads: int, scale: float, causal: bool = True, window: int = 0,
+                 wait_timeout_us: int = 0):
+        super().__init__(n_q_heads, scale, 1 if causal else 0, window, wait_timeout_us)
+
+
 _LIB: Optional[C.CDLL] = None
 
 
@@ -120,6 +205,19 @@ def load() -> C.CDLL:
     L.moe_expert_ffn_w8a16.argtypes = L.moe_expert_ffn_fp8.argtypes
     L.moe_layer_w8a16.argtypes = L.moe_layer.argtypes
     L.moe_diag_wait_timeout.argtypes = [P, C.c_uint32, P]
+    kv, sq, at, I64 = C.POINTER(KVCache), C.POINTER(Seqs), C.POINTER(Attn), C.c_int64
+    L.moe_rope_freqs.argtypes = [I32, C.c_double, I32, C.c_double, I32, C.c_double, C.c_double,
+                                 P, P]
+    L.moe_rope_append.argtypes = [C.POINTER(Rope), kv, sq, P, I64, P, I64, P, I64, P, I32, I32, P,
+                                  I64, P]
+    L.moe_attn_workspace_bytes.restype = SZ
+    L.moe_attn_workspace_bytes.argtypes = [at, kv]
+    L.moe_paged_attention.argtypes = [at, kv, sq, P, I64, P, I32, P, P, P, SZ, P]
+    L.moe_key_weights.argtypes = [at, kv, sq, P, I64, P, I32, P, C.c_float, P, P, I64, P, SZ, P]
+    L.moe_cache_evict.argtypes = [kv, sq, P, I64, I32, I32, P, I32, P, P, P, P, SZ, P]
+    for n in ("moe_rope_freqs", "moe_rope_append", "moe_paged_attention", "moe_key_weights",
+              "moe_cache_evict"):
+        getattr(L, n).restype = C.c_int
     for n in ("moe_route", "moe_build_union", "moe_expert_ffn_fp8", "moe_combine", "moe_layer",
               "moe_get_device_error", "moe_diag_wait_timeout", "moe_dispatch", "moe_layer_noalloc", "moe_greedy_verify", "moe_combine_add_rmsnorm",
               "moe_gate_up_fp8", "moe_down_fp8", "moe_expert_gemms_fp8", "moe_expert_ffn_w8a16",
@@ -307,6 +405,107 @@ def tile_weights(t: dict, stream=None) -> dict:
         moe_tile_weights(src, dst, stream)
         out[k] = dst.view(v.dtype)
     return out
+
+
+# --------------------------------------------------------- attention side --
+def _refuse(ok: bool, where: str) -> None:
+    if not ok:
+        raise MoeError(1, where)
+
+
+def _is(t, dtype, *shape) -> bool:
+    return t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == shape
+
+
+def _heads(t, heads: int, dim: int, tokens: int) -> bool:
+    """bf16 [tokens, heads, dim] with a token's heads contiguous."""
+    return (t.dtype == torch.bfloat16 and tuple(t.shape) == (tokens, heads, dim)
+            and (t.stride(2) == 1 or dim == 1) and (t.stride(1) == dim or heads == 1))
+
+
+def moe_rope_freqs(rot_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN,
+                   factor: float = 1.0, original_len: int = 4096, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0):
+    """(freqs, magnitude): an fp32 CPU tensor [rot_dim/2, 2] for Rope.from_freqs
+    (after a copy to the device) and the factor of cos and sin."""
+    freqs = torch.empty((max(rot_dim, 0) // 2, 2), dtype=torch.float32)
+    one = C.c_float(0)
+    buf = freqs if freqs.numel() else torch.empty(2)
+    _check(load().moe_rope_freqs(rot_dim, base, kind, factor, original_len, beta_fast, beta_slow,
+                                 buf.data_ptr(), C.addressof(one)), "moe_rope_freqs")
+    return freqs, one.value
+
+
+def moe_rope_append(rope: Rope, cache: KVCache, seqs: Seqs, q, k, v, positions, q_out,
+                    stream=None) -> None:
+    """q, q_out bf16 [T, n_q_heads, head_dim]; k, v bf16 [T, n_kv_heads,
+    head_dim]; token strides are free, so slices of one projection's output fit."""
+    T, Hq = q.shape[0], q.shape[1]
+    D, Hkv = cache.head_dim, cache.n_kv_heads
+    _refuse(_heads(q, Hq, D, T) and _heads(q_out, Hq, D, T) and _heads(k, Hkv, D, T)
+            and _heads(v, Hkv, D, T) and _is(positions, torch.int32, T), "moe_rope_append")
+    row = lambda t, h: t.stride(0) if T > 1 else h * D
+    _check(load().moe_rope_append(C.byref(rope), C.byref(cache), C.byref(seqs), _ptr(q),
+                                  row(q, Hq), _ptr(k), row(k, Hkv), _ptr(v), row(v, Hkv),
+                                  _ptr(positions), T, Hq, _ptr(q_out), row(q_out, Hq),
+                                  _stream(stream)), "moe_rope_append")
+
+
+def moe_attn_workspace_bytes(attn: Attn, cache: KVCache) -> int:
+    """Bytes of a workspace, zeroed once by the caller, for the attention calls."""
+    return load().moe_attn_workspace_bytes(C.byref(attn), C.byref(cache))
+
+
+def _attn_ok(attn, cache, q, draft_mask) -> bool:
+    return (q.dim() == 3 and _heads(q, attn.n_q_heads, cache.head_dim, q.shape[0])
+            and (draft_mask is None or _is(draft_mask, torch.int64, q.shape[0])))
+
+
+def moe_paged_attention(attn: Attn, cache: KVCache, seqs: Seqs, q, out, ws, lse=None,
+                        draft_mask=None, stream=None) -> None:
+    """q bf16 [T, n_q_heads, head_dim] (free token stride), out the same,
+    contiguous; lse fp32 [T, n_q_heads] or None; draft_mask int64 [T] (the bits
+    of a uint64) or None."""
+    T, Hq, D = q.shape[0], attn.n_q_heads, cache.head_dim
+    _refuse(_attn_ok(attn, cache, q, draft_mask) and _is(out, torch.bfloat16, T, Hq, D)
+            and (lse is None or _is(lse, torch.float32, T, Hq)), "moe_paged_attention")
+    _check(load().moe_paged_attention(C.byref(attn), C.byref(cache), C.byref(seqs), _ptr(q),
+                                      q.stride(0) if T > 1 else Hq * D, _ptr(draft_mask), T,
+                                      _ptr(out), _ptr(lse), _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_paged_attention")
+
+
+def moe_key_weights(attn: Attn, cache: KVCache, seqs: Seqs, q, lse, scores, scores_out, ws,
+                    decay: float = 1.0, draft_mask=None, stream=None) -> None:
+    """scores, scores_out fp32 [n_seqs, n_kv_heads, places], possibly the same."""
+    T, Hq, D = q.shape[0], attn.n_q_heads, cache.head_dim
+    shape = (seqs.n_seqs, cache.n_kv_heads, scores.shape[-1])
+    _refuse(_attn_ok(attn, cache, q, draft_mask) and _is(lse, torch.float32, T, Hq)
+            and _is(scores, torch.float32, *shape) and _is(scores_out, torch.float32, *shape),
+            "moe_key_weights")
+    _check(load().moe_key_weights(C.byref(attn), C.byref(cache), C.byref(seqs), _ptr(q),
+                                  q.stride(0) if T > 1 else Hq * D, _ptr(draft_mask), T,
+                                  _ptr(lse), decay, _ptr(scores), _ptr(scores_out),
+                                  scores.shape[-1], _ptr(ws), ws.numel() * ws.element_size(),
+                                  _stream(stream)), "moe_key_weights")
+
+
+def moe_cache_evict(cache: KVCache, seqs: Seqs, scores, budget: int, n_recent: int, to_table,
+                    kept, scores_out, new_len, ws, stream=None) -> None:
+    """scores, scores_out fp32 [n_seqs, n_kv_heads, places]; to_table int32
+    [n_seqs, to_pages]; kept int32 [n_seqs, n_kv_heads, budget]; new_len int32 [n_seqs]."""
+    n, h = seqs.n_seqs, cache.n_kv_heads
+    shape = (n, h, scores.shape[-1])
+    _refuse(_is(scores, torch.float32, *shape) and _is(scores_out, torch.float32, *shape)
+            and _is(to_table, torch.int32, n, to_table.shape[-1])
+            and _is(kept, torch.int32, n, h, budget) and _is(new_len, torch.int32, n),
+            "moe_cache_evict")
+    _check(load().moe_cache_evict(C.byref(cache), C.byref(seqs), _ptr(scores), scores.shape[-1],
+                                  budget, n_recent, _ptr(to_table), to_table.shape[-1],
+                                  _ptr(kept), _ptr(scores_out), _ptr(new_len), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_cache_evict")
 
 
 def moe_get_device_error(ws, clear: bool = True, stream=None) -> int:

@@ -5,23 +5,22 @@
 // moe_get_device_error.
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
-#include <cudaTypedefs.h>
-
-#include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "layout.h"
 
 namespace {
 
+using moe::aligned;
+using moe::cuda_status;
+using moe::device_info;
+using moe::DeviceInfo;
+using moe::encode_fn;
 using moe::FfnLayout;
 using moe::LayerLayout;
+using moe::MapCache;
 using moe::UnionLayout;
-
-moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Shape checks: malformed shapes are invalid; well-formed ones beyond the
 // compiled limits are unsupported.
@@ -48,40 +47,6 @@ moe_status_t check_rows(int32_t R) {
 
 uint64_t timeout_ns(const moe_config_t* c) {
     return static_cast<uint64_t>(c->wait_timeout_us ? c->wait_timeout_us : 2000000u) * 1000ull;
-}
-
-struct DeviceInfo {
-    int sms = 0;
-    int smem_optin = 0;
-};
-
-DeviceInfo device_info() {
-    static std::mutex mu;
-    static DeviceInfo cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DeviceInfo{};
-    std::lock_guard<std::mutex> lock(mu);
-    if (cache[dev].sms == 0) {
-        DeviceInfo d;
-        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-        cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-        cache[dev] = d;
-    }
-    return cache[dev];
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
 }
 
 // 2-D uint8 tensor [rows, cols] (cols contiguous), 128-byte-swizzled boxes of
@@ -121,30 +86,6 @@ moe_status_t check_weights(const moe_config_t* c, const moe_weights_t* w) {
 // The large-R router's maps: x bf16 [R, H] and w fp32 [E, H], boxes of
 // kRouterStageCols columns x 32 rows, unswizzled; rows and columns past the
 // end read as zero.
-// The last few tensor-map sets built on this thread, keyed by everything
-// that goes into them (pointers, sizes, boxes, layout): a call on the same
-// buffers reuses them instead of encoding them again (each encoding is a
-// host call on the path of every layer).  Keys are compared bytewise and
-// built from zeroed memory.
-template <typename Key, typename Val, int N = 4>
-struct MapCache {
-    Key key[N];
-    Val val[N];
-    bool used[N] = {};
-    int next = 0;
-    const Val* find(const Key& k) const {
-        for (int i = 0; i < N; ++i)
-            if (used[i] && std::memcmp(&key[i], &k, sizeof(Key)) == 0) return &val[i];
-        return nullptr;
-    }
-    void put(const Key& k, const Val& v) {
-        key[next] = k;
-        val[next] = v;
-        used[next] = true;
-        next = (next + 1) % N;
-    }
-};
-
 struct RouterMapKey {
     const void* x;
     const void* wr;

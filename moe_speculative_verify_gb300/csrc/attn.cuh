@@ -1,0 +1,349 @@
+// attn.cuh -- device helpers shared by the attention-side kernels: the
+// sequences' numbers made safe, which keys a row sees, and the 16-bit matrix
+// instruction on registers.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace moe {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -INFINITY;
+
+// One sequence: its first row of the step's tensors, new tokens, cached keys
+// and the cache place of its first new token.  Numbers that do not fit are
+// cut to what does, and recorded.
+struct Seq {
+    int q0, nq, len, first;
+};
+
+__device__ __forceinline__ Seq load_seq(const SeqArgs& s, int page, int b, int32_t* err) {
+    const int c0 = s.cu_q[b], c1 = s.cu_q[b + 1], len = s.kv_len[b];
+    Seq r;
+    r.q0 = c0;
+    r.nq = c1 - c0;
+    const bool bad_q = c0 < 0 || c1 < c0 || c1 > s.tokens;
+    if (bad_q) {
+        r.q0 = 0;
+        r.nq = 0;
+    }
+    const int64_t cap = int64_t(s.max_pages) * page;
+    r.len = len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
+    r.first = r.len - r.nq;
+    if (bad_q || r.len != len) record_error(err, MOE_ERR_INVALID_ARG);
+    return r;
+}
+
+// The keys that row i of a sequence can see: [lo, hi), and among the new keys
+// (from `first` on) those of its draft mask.
+struct RowView {
+    int lo, hi;
+    uint64_t draft;
+};
+
+__device__ __forceinline__ RowView row_view(const AttnArgs& a, const Seq& s, int i) {
+    RowView r;
+    r.hi = s.len;
+    r.draft = ~0ull;
+    if (a.draft)
+        r.draft = a.draft[s.q0 + i];
+    else if (a.causal)
+        r.hi = min(s.len, s.first + i + 1);
+    r.lo = a.window > 0 ? max(0, s.first + i - a.window + 1) : 0;
+    return r;
+}
+
+__device__ __forceinline__ bool row_sees(const RowView& r, bool draft, int first, int j) {
+    bool ok = j >= r.lo && j < r.hi;
+    if (draft) {
+        const int c = j - first;
+        ok = ok && (c < 0 || (c < 64 && ((r.draft >> (c & 63)) & 1ull)));
+    }
+    return ok;
+}
+
+// Keys that some row of the rows i0 .. i1 of a sequence can see, as a range.
+__device__ __forceinline__ int2 rows_range(const AttnArgs& a, const Seq& s, int i0, int i1) {
+    int hi = s.len;
+    if (a.draft)
+        hi = min(s.len, max(s.first, 0) + 64);
+    else if (a.causal)
+        hi = min(s.len, s.first + i1 + 1);
+    const int lo = a.window > 0 ? max(0, s.first + i0 - a.window + 1) : 0;
+    return make_int2(lo, max(hi, 0));
+}
+
+// Whether every key of [j0, j1) is seen by every one of those rows.
+__device__ __forceinline__ bool rows_see_all(const AttnArgs& a, const Seq& s, int i0, int i1,
+                                             int j0, int j1) {
+    int hi = s.len;
+    if (a.draft)
+        hi = min(hi, s.first);
+    else if (a.causal)
+        hi = min(hi, s.first + i0 + 1);
+    return j1 <= hi && !(a.window > 0 && j0 < s.first + i1 - a.window + 1);
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 as bf16x2 / f16x2, `lo` in the low half, nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two e4m3 codes (low 16 bits) as f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+        : "=r"(r)
+        : "r"(codes));
+    return r;
+}
+
+// D[16x8] += A[16x16] B[16x8]: bf16 or f16 operands, fp32 sums.  Lane l = 4g+t
+// holds A rows g, g+8 at columns 2t,2t+1 (a0, a1) and 2t+8,2t+9 (a2, a3), B
+// column g at rows 2t,2t+1 (b0) and 2t+8,2t+9 (b1), D rows g (d0, d1) and g+8
+// (d2, d3) at columns 2t, 2t+1.
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A bf16 query row times 2^-e, e the exponent of its largest element, so that
+// it keeps its bits in f16 beside e4m3 codes (exact in f16 too): the element
+// range below 2^-14 of the largest, which f16 would cut, lies under the
+// product's fp32 rounding of the row's own largest terms.  Zero and
+// non-finite rows stay as they are.
+__device__ __forceinline__ float pow2_norm(float amax) {
+    const uint32_t e = __float_as_uint(amax) >> 23;
+    // 2^(127 - e): biased 254 - e; e = 0 (zero, subnormal) and 255 stay
+    return (e == 0u || e >= 254u) ? 1.0f : __uint_as_float((254u - e) << 23);
+}
+
+// 4-D tiled bulk tensor load global -> shared; c0 (innermost, elements) starts
+// on a 16-byte boundary.  A coordinate out of range reads as zeros.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3)
+        : "memory");
+}
+
+// ------------------------------------------------------------ work split ----
+// The attention kernels cut a call into items -- (sequence, kv head, tile of
+// MT query rows), rows r = i * group + g -- of one unit per KT-key tile that
+// some row of the item sees (one unit when none does), and give every CTA an
+// equal run of units in item order.  A CTA so meets at most two items that
+// it shares with its neighbours; it leaves those as partial results, and the
+// CTA that arrives last joins an item's pieces in CTA order.
+struct Item {
+    int b, h, rt;          // sequence, kv head, row tile
+    int lo, hi;            // keys some row sees
+    int tile0, n;          // first key tile, units
+    int t0, t1;            // this CTA's units of it
+    int64_t u;             // global index of its first unit
+    Seq s;
+};
+
+template <int MT, int KT>
+struct Work {
+    __device__ __forceinline__ static int row_tiles(const AttnArgs& a, const Seq& s) {
+        return (s.nq * a.group + MT - 1) / MT;
+    }
+    // keys and units of row tile rt
+    __device__ __forceinline__ static void extent(const AttnArgs& a, const Seq& s, int rt, int& lo,
+                                                  int& hi, int& tile0, int& n) {
+        const int r1 = min(s.nq * a.group, (rt + 1) * MT) - 1;
+        const int2 k = rows_range(a, s, rt * MT / a.group, r1 / a.group);
+        lo = k.x;
+        hi = k.y;
+        tile0 = lo / KT;
+        n = max(1, (hi + KT - 1) / KT - tile0);
+        if (hi <= lo) n = 1;
+    }
+    __device__ __forceinline__ static int64_t head_units(const AttnArgs& a, const Seq& s) {
+        const int rts = row_tiles(a, s);
+        int64_t u = 0;
+        for (int rt = 0; rt < rts; ++rt) {
+            int lo, hi, t0, n;
+            extent(a, s, rt, lo, hi, t0, n);
+            u += n;
+        }
+        return u;
+    }
+    // CTA c of C takes units [c*W/C, (c+1)*W/C)
+    __device__ __forceinline__ static int64_t begin(int c, int C, int64_t W) { return c * W / C; }
+    __device__ __forceinline__ static int owner(int64_t u, int C, int64_t W) {
+        return static_cast<int>(((u + 1) * C - 1) / W);
+    }
+};
+
+// What a CTA knows of the call's split once plan_work() has run.
+struct Plan {
+    int64_t total, u0, u1;
+    int ctas;              // CTAs that take part
+    int b;                 // sequence of unit u0, and the unit's offset in it
+    int64_t off;
+};
+
+// All threads of the block.  s_warp: one int64 per warp, s_plan: shared.
+template <int MT, int KT>
+__device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int64_t* s_warp,
+                                          Plan* s_plan) {
+    using W = Work<MT, KT>;
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
+    const int per = (a.sq.n + nt - 1) / nt;
+    const int b0 = min(a.sq.n, tid * per), b1 = min(a.sq.n, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += a.kv.heads * W::head_units(a, load_seq(a.sq, a.kv.page, b, a.err));
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_warp[wid] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < (nt >> 5); ++w) {
+        const int64_t v = s_warp[w];
+        before += w < wid ? v : 0;
+        total += v;
+    }
+    const int64_t want = (total + min_units - 1) / min_units;
+    const int C = static_cast<int>(want < int64_t(gridDim.x) ? (want > 0 ? want : 1) : gridDim.x);
+    const int c = blockIdx.x;
+    const int64_t u0 = c < C ? W::begin(c, C, total) : total;
+    const int64_t u1 = c < C ? W::begin(c + 1, C, total) : total;
+    if (tid == 0) {
+        s_plan->total = total;
+        s_plan->u0 = u0;
+        s_plan->u1 = u1;
+        s_plan->ctas = C;
+    }
+    const int64_t pre = before + incl - mine;
+    if (u0 < u1 && pre <= u0 && u0 < pre + mine) {
+        int64_t at = pre;
+        for (int b = b0; b < b1; ++b) {
+            const int64_t n =
+                a.kv.heads * W::head_units(a, load_seq(a.sq, a.kv.page, b, nullptr));
+            if (u0 < at + n) {
+                s_plan->b = b;
+                s_plan->off = u0 - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+}
+
+// Walks a CTA's units item by item; every warp keeps its own copy.
+template <int MT, int KT>
+struct Walk {
+    using W = Work<MT, KT>;
+    Seq s;
+    int b, h, rt, rts;
+    int64_t off, u, left;      // units to skip in the first item, next unit, units left
+
+    __device__ __forceinline__ void start(const AttnArgs& a, const Plan& p) {
+        left = p.u1 - p.u0;
+        u = p.u0;
+        b = h = rt = rts = 0;
+        off = 0;
+        if (left <= 0) return;
+        b = p.b;
+        s = load_seq(a.sq, a.kv.page, b, nullptr);
+        rts = W::row_tiles(a, s);
+        const int64_t per = W::head_units(a, s);
+        h = static_cast<int>(p.off / per);
+        off = p.off - h * per;
+        for (;; ++rt) {
+            int lo, hi, t0, n;
+            W::extent(a, s, rt, lo, hi, t0, n);
+            if (off < n) break;
+            off -= n;
+        }
+    }
+    __device__ __forceinline__ bool next(const AttnArgs& a, Item& it) {
+        if (left <= 0) return false;
+        while (rt >= rts) {
+            rt = 0;
+            if (++h >= a.kv.heads || rts == 0) {
+                h = 0;
+                if (++b >= a.sq.n) return false;
+                s = load_seq(a.sq, a.kv.page, b, nullptr);
+                rts = W::row_tiles(a, s);
+            }
+        }
+        W::extent(a, s, rt, it.lo, it.hi, it.tile0, it.n);
+        it.s = s;
+        it.b = b;
+        it.h = h;
+        it.rt = rt;
+        it.t0 = static_cast<int>(off);
+        it.t1 = static_cast<int>(left < it.n - off ? off + left : it.n);
+        it.u = u - off;
+        u += it.t1 - it.t0;
+        left -= it.t1 - it.t0;
+        off = 0;
+        ++rt;
+        return true;
+    }
+};
+
+// Zeroes the output rows that belong to no sequence.
+__device__ __forceinline__ void zero_pad_rows(const AttnArgs& a) {
+    const int first = min(max(a.sq.cu_q[0], 0), a.sq.tokens);
+    const int last = min(max(a.sq.cu_q[a.sq.n], first), a.sq.tokens);
+    const int n = first + (a.sq.tokens - last);
+    for (int p = blockIdx.x; p < n; p += gridDim.x) {
+        const int64_t t = p < first ? p : last + (p - first);
+        uint4* o = reinterpret_cast<uint4*>(a.out + t * a.q_heads * a.kv.dim);
+        for (int i = threadIdx.x; i < a.q_heads * a.kv.dim / 8; i += blockDim.x)
+            o[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int i = threadIdx.x; i < a.q_heads; i += blockDim.x)
+                a.lse[t * a.q_heads + i] = kNegInf;
+    }
+}
+
+}  // namespace moe

@@ -1,0 +1,109 @@
+// attn.h -- arguments, workspace layout and launch entry points of the
+// attention-side kernels (rope.cu, attn.cu, keyw.cu, evict.cu), used by their
+// host ABI (attn_abi.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// The paged cache as the kernels see it (strides in elements).
+struct KvArgs {
+    uint8_t* k;
+    uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    int64_t page_stride, head_stride, token_stride;
+    int32_t e4m3;
+    int32_t n_pages, page, page_log2, heads, dim;
+};
+
+struct SeqArgs {
+    const int32_t* cu_q;
+    const int32_t* kv_len;
+    const int32_t* table;
+    int32_t n, max_pages, tokens;
+};
+
+// Workspace of the attention calls: the control block (error word), one
+// arrival counter per CTA (zero between calls), then the partial results of
+// split rows: two slots per CTA, each `rows` x (dim + 2) fp32.
+constexpr int kAttnMaxCtas = 160;       // >= SMs of the card; larger grids are cut to it
+constexpr int kAttnSlotRows = 256;
+constexpr int64_t kAttnCounters = 256;  // byte offset
+constexpr int64_t kAttnPartials = 256 + ((kAttnMaxCtas * 4 + 255) / 256) * 256;
+
+inline int64_t attn_workspace_bytes(int dim) {
+    return kAttnPartials + int64_t(2) * kAttnMaxCtas * kAttnSlotRows * (dim + 2) * 4;
+}
+
+struct RopeArgs {
+    KvArgs kv;
+    SeqArgs sq;
+    const float* freqs;
+    int32_t rot, interleaved;
+    float magnitude;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const int32_t* pos;
+    uint16_t* q_out;
+    int32_t q_heads;
+};
+
+struct AttnArgs {
+    KvArgs kv;
+    SeqArgs sq;
+    const uint16_t* q;
+    int64_t q_stride;
+    const uint64_t* draft;   // NULL: causal or full
+    uint16_t* out;
+    float* lse;              // may be NULL
+    int32_t q_heads, group;  // group = q_heads / kv heads
+    float scale;
+    int32_t causal, window;
+    int32_t* err;
+    int32_t* counters;
+    float* partials;
+    uint64_t timeout_ns;
+};
+
+struct KeywArgs {
+    AttnArgs a;              // out, counters and partials unused; lse is read
+    float decay;
+    const float* scores;
+    float* scores_out;
+    int64_t score_stride;
+};
+
+struct EvictArgs {
+    KvArgs kv;
+    SeqArgs sq;              // cu_q unused
+    const float* scores;
+    int64_t score_stride;
+    int32_t budget, recent;
+    const int32_t* to_table;
+    int32_t to_pages;
+    int32_t* kept;
+    float* scores_out;
+    int32_t* new_len;
+    int32_t* err;
+};
+
+// Tensor maps of K and V: 4-D (d, token, head, page), 128 bytes wide boxes
+// (64 for e4m3 heads of 64) of min(page, tile) tokens, swizzled at that width.
+struct KvMaps {
+    CUtensorMap k, v;
+};
+
+constexpr int kAttnTile = 64;   // keys of a tile of the few-rows kernel
+
+cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_attn(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
+cudaError_t launch_keyw(const KeywArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+
+}  // namespace moe
