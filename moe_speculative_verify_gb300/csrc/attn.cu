@@ -1,6 +1,6 @@
 // attn.cu -- attention of the step's new tokens over the paged cache (sm_103a):
-// the kernel for few query rows (single tokens, verify blocks), and the choice
-// between it and the tensor-memory kernel.
+// the kernel for few query rows a kv head (single tokens; attn_tile.cu is the
+// one for more).
 //
 // out_i = sum_j p_ij v_j / sum_j p_ij with p_ij = 2^(c (s_ij) - m_i), m_i the
 // running row maximum: one pass over K and V, with the sums rescaled when the
@@ -396,6 +396,7 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
             l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+            if (l[r] != l[r]) m[r] = fmaxf(m[r], 0.0f);   // a NaN is a result, not an empty row
             if (t == 0) sh.ml[wid][g + 8 * r] = make_float2(m[r], l[r]);
         }
         named_bar(kBarMerge, 32 * kConsumers);
@@ -548,7 +549,7 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
 
 }  // namespace
 
-cudaError_t launch_attn(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s) {
+cudaError_t launch_attn_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s) {
     if (a.kv.dim == 128)
         return a.kv.e4m3 ? launch_rows<128, true>(a, m, n_sms, s) : launch_rows<128, false>(a, m, n_sms, s);
     return a.kv.e4m3 ? launch_rows<64, true>(a, m, n_sms, s) : launch_rows<64, false>(a, m, n_sms, s);

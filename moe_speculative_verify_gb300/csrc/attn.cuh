@@ -122,6 +122,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     return r;
 }
 
+// Two fp32 as e4m3 / e5m2 codes in the low 16 bits (nearest even, saturating;
+// NaN stays NaN), `lo` in the low byte; and back.
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack_e4m3(uint32_t codes) {
+    const uint32_t h = e4m3x2_to_f16x2(codes);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // D[16x8] += A[16x16] B[16x8]: bf16 or f16 operands, fp32 sums.  Lane l = 4g+t
 // holds A rows g, g+8 at columns 2t,2t+1 (a0, a1) and 2t+8,2t+9 (a2, a3), B
 // column g at rows 2t,2t+1 (b0) and 2t+8,2t+9 (b1), D rows g (d0, d1) and g+8
@@ -150,8 +169,9 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
 // non-finite rows stay as they are.
 __device__ __forceinline__ float pow2_norm(float amax) {
     const uint32_t e = __float_as_uint(amax) >> 23;
-    // 2^(127 - e): biased 254 - e; e = 0 (zero, subnormal) and 255 stay
-    return (e == 0u || e >= 254u) ? 1.0f : __uint_as_float((254u - e) << 23);
+    // 2^(127 - e): biased 254 - e (2^-127 is subnormal); e = 0 (zero, subnormal) and 255 stay
+    if (e == 0u || e == 255u) return 1.0f;
+    return e == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - e) << 23);
 }
 
 // 4-D tiled bulk tensor load global -> shared; c0 (innermost, elements) starts

@@ -99,10 +99,15 @@ struct KvMaps {
     CUtensorMap k, v;
 };
 
-constexpr int kAttnTile = 64;   // keys of a tile of the few-rows kernel
+// Rows a kv head (new tokens of a sequence times query heads a kv head) up to
+// which the few-rows kernel is taken: one 16-row matrix tile.
+constexpr int kAttnFewRows = 16;
+constexpr int kAttnTile = 64;       // keys of a tile of the few-rows kernel
+constexpr int kAttnBigTile = 128;   // and of the tensor-memory kernel
 
 cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t s);
-cudaError_t launch_attn(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
+cudaError_t launch_attn_tile(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
 cudaError_t launch_keyw(const KeywArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 

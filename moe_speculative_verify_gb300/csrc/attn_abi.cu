@@ -272,11 +272,14 @@ moe_status_t moe_paged_attention(const moe_attn_t* attn, const moe_kv_cache_t* c
         return MOE_ERR_INVALID_ARG;
     if ((st = check_ws(ws, ws_bytes, moe_attn_workspace_bytes(attn, cache))) != MOE_OK) return st;
     moe::KvMaps maps;
-    if (!make_kv_maps(cache, moe::kAttnTile, &maps)) return MOE_ERR_CUDA;
+    const bool few = int64_t(seqs->max_q) * (attn->n_q_heads / cache->n_kv_heads) <= moe::kAttnFewRows;
+    if (!make_kv_maps(cache, few ? moe::kAttnTile : moe::kAttnBigTile, &maps)) return MOE_ERR_CUDA;
     moe::AttnArgs a = attn_args(attn, cache, seqs, q, q_stride, draft_mask, n_tokens, ws);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    return cuda_status(moe::launch_attn(a, maps, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(few ? moe::launch_attn_rows(a, maps, device_info().sms, s)
+                           : moe::launch_attn_tile(a, maps, device_info().sms, s));
 }
 
 moe_status_t moe_key_weights(const moe_attn_t* attn, const moe_kv_cache_t* cache,

@@ -1,0 +1,742 @@
+// attn_tile.cu -- paged attention on tensor memory (sm_103a): verify blocks of
+// many heads per kv head, and prefill chunks.
+//
+// An item is up to 256 query rows of one sequence and kv head, worked on as
+// two streams of 128-row tiles.  Above 128 rows the streams are the two row
+// tiles, which share every K and V tile; up to 128 rows both hold the same
+// rows and take alternate key tiles, and are joined when the item ends.  Each
+// stream's step is S = Q K^T (tcgen05.mma, shared x shared), the softmax of a
+// warpgroup with a thread per row, and O += P V (P from tensor memory), so one
+// stream's products run while the other's softmax does.
+//
+// A row's sums use a reference that follows the running maximum only when
+// that has grown by more than 2^kLag: the rescaling of O in tensor memory is
+// rare then, and every power stays within the 16-bit types.
+//
+// e4m3 caches are multiplied as they are.  A query element (8 significant
+// bits) is the sum of two e4m3 codes of the row scaled by a power of two; a
+// probability the sum of an e4m3 and an e5m2 code (whose range reaches down to
+// 2^-20 of the reference): two 8-bit products take the time of one 16-bit one,
+// and K and V need no conversion.
+#include "attn.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMT = 256;                 // rows of an item
+constexpr int kKT = 128;                 // keys of a tile
+constexpr int kThreads = 384;            // 2 softmax warpgroups; TMA warp, MMA warp and 2 idle
+// Registers a thread, moved between the warpgroups after the launch at 168:
+// 8 * 208 + 4 * 80 = 1984 a lane column of the 12 * 168 = 2016 launched.
+constexpr int kRegsSoft = 208, kRegsRest = 80;
+constexpr int kSoft = 256;
+constexpr int kBarAll = 1;               // named barriers: both warpgroups
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;          // S/P of stream s at column 128 s, O at 256 + 128 s
+
+template <int D, bool E4M3>
+struct Cfg {
+    static constexpr int kRowBytes = E4M3 ? D : 2 * D;             // a cached row
+    static constexpr int kTileBytes = kKT * kRowBytes;
+    static constexpr int kQBytes = 128 * 2 * D;                    // bf16, or e4m3 high and low
+    static constexpr int kStages = kTileBytes == 32768 ? 5 : 10;
+    static constexpr int kMerge = 128 * D * 4;                     // == 2 * kQBytes: stream 1's O
+    static constexpr size_t kSmem = 1024 + 2 * kQBytes + kStages * kTileBytes;
+    static constexpr float kLag = E4M3 ? 4.0f : 8.0f;
+    static constexpr float kBias = E4M3 ? 4.0f : 0.0f;             // probabilities times 2^kBias
+};
+
+struct Shared {
+    alignas(8) uint64_t kv_full[10];
+    uint64_t kv_empty[10];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2];
+    int64_t warp_sum[kThreads / 32];
+    Plan plan;
+    float2 ml[128];
+    uint32_t tmem;
+    int last;
+};
+
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(lbo >> 4) << 16;
+    d |= static_cast<uint64_t>(sbo >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(swizzle) << 61;
+    return d;
+}
+
+constexpr uint32_t kSw128 = 2, kSw64 = 4;
+
+// Instruction descriptor: D fp32, A and B types at bits 7-9 and 10-12, B
+// MN-major at bit 16, N >> 3 at 17-22, M >> 4 at 24-28 (M = 128).
+constexpr uint32_t idesc(uint32_t ta, uint32_t tb, bool b_mn, int N) {
+    return (1u << 4) | (ta << 7) | (tb << 10) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// One step of D[tmem] (+)= A B^T: A in shared (SS) or tensor memory (TS);
+// 16-bit (K = 16) or 8-bit (K = 32) operands.
+template <bool F8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    if constexpr (F8)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+
+template <bool F8>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    if constexpr (F8)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                     "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                     "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+
+__device__ __forceinline__ void fence_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// An item as its CTA works on it: mode, tiles, and each stream's share.
+struct Share {
+    bool pair;               // two row tiles; else alternate key tiles of one
+    int rows;                // rows of the item
+    int tiles;               // key tiles of this CTA (0: nothing seen)
+    int a[2], b[2];          // pair: stream s takes local tiles a .. b-1
+    int lo[2], hi[2];        // keys that some row of the stream sees
+    int i0[2], i1[2];        // first and last query of the stream
+
+    __device__ __forceinline__ void set(const AttnArgs& at, const Item& it) {
+        rows = min(kMT, it.s.nq * at.group - it.rt * kMT);
+        pair = rows > 128;
+        tiles = it.hi > it.lo ? it.t1 - it.t0 : 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r0 = it.rt * kMT + (pair ? 128 * s : 0);
+            const int r1 = pair ? min(r0 + 128, it.rt * kMT + rows) : r0 + rows;
+            i0[s] = r0 / at.group;
+            i1[s] = (r1 - 1) / at.group;
+            const int2 k = rows_range(at, it.s, i0[s], i1[s]);
+            lo[s] = k.x;
+            hi[s] = k.y;
+            a[s] = 0;
+            b[s] = tiles;
+            if (pair) {
+                const int base = it.tile0 + it.t0;
+                a[s] = min(max(lo[s] / kKT - base, 0), tiles);
+                b[s] = hi[s] > lo[s] ? max(min((hi[s] + kKT - 1) / kKT - base, tiles), a[s]) : a[s];
+            }
+        }
+    }
+    __device__ __forceinline__ bool on(int s, int j) const { return j >= a[s] && j < b[s]; }
+    // tiles of stream s
+    __device__ __forceinline__ int count(int s) const {
+        return pair ? b[s] - a[s] : (tiles + 1 - s) / 2;
+    }
+    __device__ __forceinline__ int tile(int s, int n) const { return pair ? a[s] + n : 2 * n + s; }
+};
+
+template <int D, bool E4M3>
+__device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, Shared& sh, uint8_t* ring) {
+    using C = Cfg<D, E4M3>;
+    constexpr int kBox = E4M3 ? D : 64;
+    constexpr int kBoxBytes = E4M3 ? D : 128;
+    const int lane = threadIdx.x & 31;
+    const int page = a.kv.page, pl = a.kv.page_log2;
+    Walk<kMT, kKT> wk;
+    wk.start(a, sh.plan);
+    Item it;
+    Share sr;
+    int run = 0;
+    bool dead = false;
+    while (wk.next(a, it)) {
+        sr.set(a, it);
+        const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
+        const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl;
+        const int ahead = sr.pair ? 1 : 2;
+        int base = -1, entry = 0;
+        // K of `ahead` tiles, then V of a tile and K of the tile `ahead` of it in turn
+        for (int op = 0; op < 2 * sr.tiles; ++op, ++run) {
+            const int first = min(ahead, sr.tiles);
+            const int x = op - first, mid = 2 * (sr.tiles - first);
+            const bool is_v = op >= first && (x >= mid || (x & 1) == 0);
+            const int j = op < first ? op : (x >= mid ? sr.tiles - first + (x - mid) : (is_v ? x >> 1 : (x >> 1) + first));
+            const int st = run % C::kStages, ph = (run / C::kStages) & 1;
+            const int p0 = ((it.tile0 + it.t0 + j) * kKT) >> pl, np = kKT >> pl;
+            if (base < 0 || p0 + np > base + 32 || p0 < base) {
+                base = is_v ? p0 : max(p0 - ahead * np, 0);      // the V tiles still to come too
+                const int p = base + lane;
+                entry = p >= p_lo && p < p_hi ? table[p] : -1;
+            }
+            if (!dead && !mbar_wait(&sh.kv_empty[st], ph ^ 1, a.err, a.timeout_ns)) dead = true;
+            int boxes = 0;
+            for (int p = p0; p < p0 + np; ++p) boxes += p >= p_lo && p < p_hi;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], dead ? 0 : boxes * page * C::kRowBytes);
+            __syncwarp();
+            const CUtensorMap* map = is_v ? &maps.v : &maps.k;
+            uint8_t* dst = ring + st * C::kTileBytes;
+            for (int p = p0; p < p0 + np; ++p) {
+                int pg = __shfl_sync(0xFFFFFFFFu, entry, p - base);
+                if (dead || p < p_lo || p >= p_hi) continue;
+                if (pg < 0 || pg >= a.kv.n_pages) {
+                    if (lane == 0) record_error(a.err, MOE_ERR_INVALID_ARG);
+                    pg = a.kv.n_pages;                           // out of range: reads as zeros
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int x2 = 0; x2 < D / kBox; ++x2)
+                        tma_load_4d(dst + (p - p0) * page * kBoxBytes + x2 * kKT * 128, map, &sh.kv_full[st],
+                                    x2 * kBox, 0, it.h, pg);
+                }
+            }
+        }
+    }
+}
+
+// The MMA warp: lane 0 issues, the whole warp waits.
+template <int D, bool E4M3>
+__device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t* qs, uint8_t* ring) {
+    using C = Cfg<D, E4M3>;
+    constexpr uint32_t kIdQK = E4M3 ? idesc(0, 0, false, kKT) : idesc(1, 1, false, kKT);
+    constexpr uint32_t kIdPV = E4M3 ? idesc(0, 0, true, D) : idesc(1, 1, true, D);
+    constexpr uint32_t kIdPVlow = idesc(1, 0, true, D);          // e5m2 x e4m3
+    constexpr bool kNarrow = E4M3 && D == 64;                    // 64-byte cached rows
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = sh.tmem;
+    Walk<kMT, kKT> wk;
+    wk.start(a, sh.plan);
+    Item it;
+    Share sr;
+    int run = 0, items = 0;
+    uint32_t pp[2] = {0, 0};                                     // p_ready phases
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
+        tc_fence_after();
+    };
+    auto wait_kv = [&](int r) { wait(&sh.kv_full[r % C::kStages], (r / C::kStages) & 1); };
+    auto qk = [&](int s, int r) {
+        if (lane == 0 && !dead) {
+            const uint32_t q0 = smem_u32(qs + s * C::kQBytes), k0 = smem_u32(ring + (r % C::kStages) * C::kTileBytes);
+            const uint32_t d = tmem + 128 * s;
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+                    mma_ss<false>(d, sdesc(q0 + off, 16, 1024, kSw128), sdesc(k0 + off, 16, 1024, kSw128), kIdQK, k > 0);
+                }
+            } else {
+                constexpr int kSteps = D / 32;
+#pragma unroll
+                for (int k = 0; k < 2 * kSteps; ++k) {           // high codes, then low
+                    const uint32_t qo = D == 128 ? (k / kSteps) * 16384 + (k % kSteps) * 32 : k * 32;
+                    mma_ss<true>(d, sdesc(q0 + qo, 16, 1024, kSw128),
+                                 sdesc(k0 + (k % kSteps) * 32, 16, kNarrow ? 512 : 1024, kNarrow ? kSw64 : kSw128),
+                                 kIdQK, k > 0);
+                }
+            }
+            mma_commit(&sh.s_full[s]);
+        }
+        __syncwarp();
+    };
+    auto pv = [&](int s, int r, bool first) {
+        if (lane == 0 && !dead) {
+            const uint32_t v0 = smem_u32(ring + (r % C::kStages) * C::kTileBytes);
+            const uint32_t d = tmem + kColO + 128 * s, p0 = tmem + 128 * s;
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int k = 0; k < kKT / 16; ++k)
+                    mma_ts<false>(d, p0 + 8 * k, sdesc(v0 + k * 2048, 16384, 1024, kSw128), kIdPV, !first || k > 0);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kKT / 16; ++k) {
+                    const uint32_t vo = (k & 3) * 32 * C::kRowBytes;
+                    mma_ts<true>(d, p0 + 8 * k, sdesc(v0 + vo, 16384, kNarrow ? 512 : 1024, kNarrow ? kSw64 : kSw128),
+                                 k < 4 ? kIdPV : kIdPVlow, !first || k > 0);
+                }
+            }
+        }
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+        if (lane == 0 && !dead) mma_commit(bar);
+        __syncwarp();
+    };
+    // V rows of keys that no row of the item sees may hold anything: zero them
+    auto clean = [&](int r, int j) {
+        const int j0 = (it.tile0 + it.t0 + j) * kKT;
+        if (j0 >= it.lo && j0 + kKT <= it.hi) return;
+        uint8_t* v = ring + (r % C::kStages) * C::kTileBytes;
+        constexpr int kChunks = (E4M3 ? D : 128) / 16, kSub = E4M3 ? 1 : D / 64;
+        for (int e = lane; e < kKT * kChunks; e += 32) {
+            const int row = e / kChunks, key = j0 + row;
+            if (key >= it.lo && key < it.hi) continue;
+#pragma unroll
+            for (int x = 0; x < kSub; ++x)
+                *reinterpret_cast<uint4*>(v + x * kKT * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+    };
+    while (wk.next(a, it)) {
+        sr.set(a, it);
+        const int T = sr.tiles;
+        if (T == 0) continue;
+        wait(&sh.q_ready[0], items & 1);
+        wait(&sh.q_ready[1], items & 1);
+        ++items;
+        auto empty = [&](int r) { commit(&sh.kv_empty[r % C::kStages]); };
+        if (sr.pair) {
+            wait_kv(run);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (sr.on(s, 0)) qk(s, run);
+            empty(run);
+            for (int j = 0; j < T; ++j) {
+                const int rv = run + 1 + 2 * j, rk = rv + 1;
+                const bool more = j + 1 < T;
+                wait_kv(rv);
+                clean(rv, j);
+                if (more) wait_kv(rk);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (sr.on(s, j)) {
+                        wait(&sh.p_ready[s], pp[s]);
+                        pp[s] ^= 1;
+                        pv(s, rv, j == sr.a[s]);
+                        if (j + 1 == sr.b[s]) commit(&sh.o_full[s]);
+                    }
+                    if (s == 1) empty(rv);
+                    if (more && sr.on(s, j + 1)) qk(s, rk);
+                }
+                if (more) empty(rk);
+            }
+        } else {
+            // ring order: K0 K1, then V(j), K(j+2) while there is one, then the V left
+            const int first = min(2, T);
+            for (int s = 0; s < first; ++s) {
+                wait_kv(run + s);
+                qk(s, run + s);
+                empty(run + s);
+            }
+            int r = run + first;
+            for (int j = 0; j < T; ++j) {
+                const int s = j & 1;
+                const int rv = r++;
+                wait_kv(rv);
+                clean(rv, j);
+                wait(&sh.p_ready[s], pp[s]);
+                pp[s] ^= 1;
+                pv(s, rv, j < 2);
+                empty(rv);
+                if (j + 2 < T) {
+                    const int rk = r++;
+                    wait_kv(rk);
+                    qk(s, rk);
+                    empty(rk);
+                } else {
+                    commit(&sh.o_full[s]);
+                }
+            }
+        }
+        run += 2 * T;
+    }
+}
+
+template <int D, bool E4M3>
+__device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* qs) {
+    using C = Cfg<D, E4M3>;
+    const int tid = threadIdx.x, s = tid >> 7, lr = tid & 127, lane = tid & 31, wq = (tid >> 5) & 3;
+    const uint32_t tm_lane = sh.tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t colS = tm_lane + 128 * s, colO = tm_lane + kColO + 128 * s;
+    const bool draft = a.draft != nullptr;
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f, scale = fabsf(a.scale) * kLog2e;
+    const int64_t slot_floats = kAttnSlotRows * (D + 2);
+    uint8_t* qt = qs + s * C::kQBytes;
+    Walk<kMT, kKT> wk;
+    wk.start(a, sh.plan);
+    Item it;
+    Share sr;
+    uint32_t sp = 0, op[2] = {0, 0};
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
+        tc_fence_after();
+    };
+    while (wk.next(a, it)) {
+        sr.set(a, it);
+        // this thread's row; half-empty alternate tiles go to the other half of the lanes
+        const int row = sr.pair ? 128 * s + lr : (s == 1 && sr.rows <= 64 ? (lr + 64) & 127 : lr);
+        const bool valid = row < sr.rows;
+        const bool warp_on = __any_sync(0xFFFFFFFFu, valid);
+        const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+        // (never 0: an unseen key's -inf times it stays -inf)
+        float c = fmaxf(scale * (E4M3 ? a.kv.k_scale[it.h] : 1.0f), 1.2e-38f);
+        // --- the query row into shared memory, K-major, 128-byte swizzle
+        {
+            const uint16_t* src = a.q + (it.s.q0 + qi) * a.q_stride + hd * D;
+            uint4 w[D / 8];
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+                w[k] = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+            uint8_t* base = qt + lr * 128;
+            if constexpr (!E4M3) {
+                const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k)
+                    *reinterpret_cast<uint4*>(base + (k >> 3) * 16384 + (((k & 7) ^ (lr & 7)) << 4)) =
+                        make_uint4(w[k].x ^ flip, w[k].y ^ flip, w[k].z ^ flip, w[k].w ^ flip);
+            } else {
+                float amax = 0.0f;
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(x[e] & 0xFFFFu)),
+                                                 fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+                }
+                // the largest element to [128, 256); the factor may pass fp32's range only for rows
+                // whose products are zero or infinite anyway
+                const float f1 = pow2_norm(amax);
+                const float f2 = f1 == 1.0f && !(amax >= 1.0f && amax < 2.0f) ? 1.0f : 128.0f;
+                c = amax < INFINITY ? fmaxf(c / f2 / f1, 1.2e-38f) : __int_as_float(0x7FC00000);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {               // 16 elements: a chunk of each
+                    uint32_t hi4[4], lo4[4];
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const uint4 ww = w[2 * k + (q4 >> 1)];
+                        const uint32_t x[2] = {q4 & 1 ? ww.z : ww.x, q4 & 1 ? ww.w : ww.y};
+                        uint32_t h = 0, l = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f1 * f2 * sign;
+                            const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f1 * f2 * sign;
+                            const uint32_t hc = pack_e4m3(v0, v1);
+                            const float2 b = unpack_e4m3(hc);
+                            h |= hc << (16 * e);
+                            l |= pack_e4m3(v0 - b.x, v1 - b.y) << (16 * e);
+                        }
+                        hi4[q4] = h;
+                        lo4[q4] = l;
+                    }
+                    const int ch = k, cl = D == 128 ? k : k + 4;
+                    uint8_t* low = D == 128 ? base + 16384 : base;
+                    *reinterpret_cast<uint4*>(base + ((ch ^ (lr & 7)) << 4)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+                    *reinterpret_cast<uint4*>(low + ((cl ^ (lr & 7)) << 4)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && sr.tiles > 0) mbar_arrive(&sh.q_ready[s]);
+        }
+        RowView view{0, 0, 0ull};
+        if (valid) view = row_view(a, it.s, qi);
+        const int n = sr.count(s);
+        float ref = kNegInf, sum = 0.0f;
+        for (int i = 0; i < n; ++i) {
+            const int j0 = (it.tile0 + it.t0 + sr.tile(s, i)) * kKT;
+            wait(&sh.s_full[s], sp);
+            sp ^= 1;
+            if (warp_on) {
+                float x[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32(colS + 32 * q, x[q]);
+                tmem_wait_ld();
+                if (!rows_see_all(a, it.s, sr.i0[s], sr.i1[s], j0, j0 + kKT)) {
+                    const int lo = view.lo - j0, hi = view.hi - j0;
+                    if (!draft) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int k = 32 * q + e;
+                                if (k < lo || k >= hi) x[q][e] = kNegInf;
+                            }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!row_sees(view, true, it.s.first, j0 + 32 * q + e)) x[q][e] = kNegInf;
+                    }
+                }
+                float top = kNegInf;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, x[q][e]);
+                top *= c;
+                if (!(top > kNegInf)) top = kNegInf;             // (NaN: the sums carry it)
+                const bool grow = top > ref + C::kLag || (ref == kNegInf && top > kNegInf);
+                if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+                    const float f = !grow ? 1.0f : (ref == kNegInf ? 0.0f : fast_exp2(ref - top));
+                    sum *= f;
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        float o[32];
+                        tmem_ld32(colO + 32 * q, o);
+                        tmem_wait_ld();
+                        uint32_t u[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+                        tmem_st32(colO + 32 * q, u);
+                    }
+                }
+                if (grow) ref = top;
+                const float off = (ref == kNegInf ? 0.0f : ref) - C::kBias;
+                if constexpr (!E4M3) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t u[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float p0 = fast_exp2(fmaf(x[2 * q + (e >> 4)][(2 * e) & 31], c, -off));
+                            const float p1 = fast_exp2(fmaf(x[2 * q + (e >> 4)][(2 * e + 1) & 31], c, -off));
+                            sum += p0 + p1;
+                            u[e] = pack_bf16(p0, p1);
+                        }
+                        tmem_st32(colS + 32 * q, u);
+                    }
+                } else {
+                    uint32_t h[32], l[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        h[e] = l[e] = 0;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int col = 4 * e + 2 * k;
+                            const float p0 = fast_exp2(fmaf(x[col >> 5][col & 31], c, -off));
+                            const float p1 = fast_exp2(fmaf(x[col >> 5][(col + 1) & 31], c, -off));
+                            sum += p0 + p1;
+                            const uint32_t hc = pack_e4m3(p0, p1);
+                            const float2 b = unpack_e4m3(hc);
+                            h[e] |= hc << (16 * k);
+                            l[e] |= pack_e5m2(p0 - b.x, p1 - b.y) << (16 * k);
+                        }
+                    }
+                    tmem_st32(colS, h);
+                    tmem_st32(colS + 32, l);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_ready[s]);
+        }
+        if (sum != sum) ref = fmaxf(ref, 0.0f);                  // a NaN is a result, not an empty row
+        // --- the item's rows: normalised, or this CTA's piece of them
+        const bool piece = it.t0 > 0 || it.t1 < it.n;
+        float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * slot_floats;
+        const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
+        const float vs = E4M3 ? a.kv.v_scale[it.h] : 1.0f;
+        float* merge = reinterpret_cast<float*>(qs);
+        const int n1 = sr.count(1);
+        if (n > 0) wait(&sh.o_full[s], op[s]);
+        if (!sr.pair && n1 > 0) {
+            // both streams' products are done: the query tiles make room for stream 1's sums
+            if (s == 1) wait(&sh.o_full[0], op[0]);
+            if (s == 1 && warp_on) {
+                sh.ml[row & 127] = make_float2(ref, sum);
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    float o[32];
+                    tmem_ld32(colO + 32 * q, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (valid)
+                            *reinterpret_cast<float4*>(merge + row * D + (((8 * q + e) ^ (row & 7)) << 2)) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    __syncwarp();
+                }
+            }
+            named_bar(kBarAll, kSoft);
+        }
+        if (sr.count(0) > 0) op[0] ^= 1;
+        if (n1 > 0) op[1] ^= 1;
+        if ((sr.pair || s == 0) && warp_on) {
+            float f0 = 1.0f, f1 = 0.0f;
+            const bool other = !sr.pair && n1 > 0;
+            if (other) {
+                const float2 ml = valid ? sh.ml[row] : make_float2(kNegInf, 0.0f);
+                const float top = fmaxf(ref, ml.x);
+                f0 = ref == kNegInf ? 0.0f : fast_exp2(ref - top);
+                f1 = ml.x == kNegInf ? 0.0f : fast_exp2(ml.x - top);
+                sum = (f0 == 0.0f ? 0.0f : sum * f0) + (f1 == 0.0f ? 0.0f : ml.y * f1);
+                ref = top;
+            }
+            const bool none = ref == kNegInf;
+            const float inv = none ? 0.0f : vs / sum;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                if (n > 0) {
+                    tmem_ld32(colO + 32 * q, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float4 y = other && valid ? *reinterpret_cast<const float4*>(merge + row * D + (((8 * q + e) ^ (row & 7)) << 2))
+                                     : make_float4(0, 0, 0, 0);
+                    float* oo = o + 4 * e;
+                    float* yy = &y.x;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float u = n > 0 && f0 != 0.0f && !none ? oo[k] * f0 : 0.0f;
+                        oo[k] = u + (f1 != 0.0f ? yy[k] * f1 : 0.0f);
+                    }
+                    if (piece && valid)
+                        *reinterpret_cast<float4*>(slot + ((8 * q + e) * kAttnSlotRows + row) * 4) =
+                            make_float4(oo[0], oo[1], oo[2], oo[3]);
+                }
+                if (!piece && valid) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(a.out + at * D + 32 * q + 8 * e) =
+                            make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                       pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                       pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                }
+                __syncwarp();
+            }
+            if (valid && piece)
+                *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(ref, sum);
+            if (valid && !piece && a.lse) a.lse[at] = none ? kNegInf : (ref - C::kBias + log2f(sum)) * kLn2;
+        }
+        tc_fence_before();
+        if (!piece) {
+            // Alternate tiles: stream 1's sums have been read.  A stream without
+            // tiles must not run an item ahead of the MMA warp's wait for its queries.
+            if (!sr.pair || n1 == 0 || sr.count(0) == 0) named_bar(kBarAll, kSoft);
+            continue;
+        }
+        // --- the last CTA of a split item joins its pieces, in CTA order
+        using W = Work<kMT, kKT>;
+        const int first = W::owner(it.u, sh.plan.ctas, sh.plan.total);
+        const int lastc = W::owner(it.u + it.n - 1, sh.plan.ctas, sh.plan.total);
+        __threadfence();
+        named_bar(kBarAll, kSoft);
+        if (tid == 0) {
+            const int old = atomicAdd(a.counters + first, 1);
+            sh.last = old == lastc - first;
+            if (sh.last) a.counters[first] = 0;
+        }
+        named_bar(kBarAll, kSoft);
+        if (!sh.last) continue;
+        __threadfence();
+        const int np = lastc - first + 1;
+        auto piece_at = [&](int k) { return a.partials + (2 * int64_t(first + k) + (k == 0 ? 1 : 0)) * slot_floats; };
+        for (int e = tid; e < sr.rows * (D / 8); e += kSoft) {
+            const int rw = e % sr.rows, d8 = e / sr.rows;
+            float top = kNegInf, tot = 0.0f;
+            for (int k = 0; k < np; ++k) top = fmaxf(top, __ldcg(piece_at(k) + kAttnSlotRows * D + 2 * rw));
+            float y[8] = {};
+#pragma unroll 4
+            for (int k = 0; k < np; ++k) {
+                const float* ps = piece_at(k);
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(ps + kAttnSlotRows * D + 2 * rw));
+                const float4 u = __ldcg(reinterpret_cast<const float4*>(ps + (2 * d8 * kAttnSlotRows + rw) * 4));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(ps + ((2 * d8 + 1) * kAttnSlotRows + rw) * 4));
+                const bool some = ml.x != kNegInf;
+                const float w = some ? fast_exp2(ml.x - top) : 0.0f;
+                tot += some ? ml.y * w : 0.0f;
+                const float x8[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[q] += some ? x8[q] * w : 0.0f;
+            }
+            const int rr = it.rt * kMT + rw, ii = rr / a.group, hh = it.h * a.group + rr - ii * a.group;
+            const int64_t dst = int64_t(it.s.q0 + ii) * a.q_heads + hh;
+            const bool none = top == kNegInf;
+            const float inv = none ? 0.0f : vs / tot;
+            *reinterpret_cast<uint4*>(a.out + dst * D + 8 * d8) =
+                make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
+                           pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
+            if (d8 == 0 && a.lse) a.lse[dst] = none ? kNegInf : (top - C::kBias + log2f(tot)) * kLn2;
+        }
+    }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a,
+                                                                const __grid_constant__ KvMaps maps) {
+    using C = Cfg<D, E4M3>;
+    static_assert(C::kMerge == 2 * C::kQBytes, "stream 1's sums fit the two query tiles");
+    extern __shared__ uint8_t dyn[];
+    __shared__ Shared sh;
+    uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = qs + 2 * C::kQBytes;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.s_full[s], 1);
+            mbar_init(&sh.p_ready[s], 4);
+            mbar_init(&sh.o_full[s], 1);
+            mbar_init(&sh.q_ready[s], 4);
+        }
+        fence_barrier_init();
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+    }
+    if (warp == 9) {
+        tmem_alloc(&sh.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    pdl_wait();
+    pdl_launch_dependents();
+    plan_work<kMT, kKT>(a, 2, sh.warp_sum, &sh.plan);            // (its barriers publish sh.tmem)
+    tc_fence_after();
+    zero_pad_rows(a);
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        soften<D, E4M3>(a, sh, qs);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == 8)
+            produce<D, E4M3>(a, maps, sh, ring);
+        else if (warp == 9)
+            multiply<D, E4M3>(a, sh, qs, ring);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(sh.tmem, kTmemCols);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s) {
+    using C = Cfg<D, E4M3>;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(attn_tile_kernel<D, E4M3>),
+                                    static_cast<int>(C::kSmem));
+    if (e != cudaSuccess) return e;
+    const int grid = n_sms < kAttnMaxCtas ? n_sms : kAttnMaxCtas;
+    e = launch_pdl(attn_tile_kernel<D, E4M3>, dim3(grid), dim3(kThreads), C::kSmem, s, a, m);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tile(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s) {
+    if (a.kv.dim == 128) return a.kv.e4m3 ? launch<128, true>(a, m, n_sms, s) : launch<128, false>(a, m, n_sms, s);
+    return a.kv.e4m3 ? launch<64, true>(a, m, n_sms, s) : launch<64, false>(a, m, n_sms, s);
+}
+
+}  // namespace moe

@@ -188,10 +188,6 @@ __device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float* v) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_wait_st() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
 // One recursive-halving level over the first N values at xor distance D.
 template <int M, int N, int D>
 __device__ __forceinline__ void halve(float (&v)[M], int lane) {

@@ -63,6 +63,10 @@ SHAPES = [
     ([257], [40], 16, 16, 128, 64, "bf16", "hnd", (0, 0)),                  # no sharing of heads
     ([333, 150], [150, 150], 16, 2, 128, 64, "bf16", "hnd", (3, 3)),        # chunks, one without a prefix
     ([300], [200], 20, 4, 64, 32, "bf16", "nhd", (0, 0)),
+    ([500, 100], [11, 10], 16, 2, 128, 16, "bf16", "hnd", (0, 0)),          # 88 rows a kv head
+    ([900], [130], 8, 1, 64, 32, "bf16", "nhd", (1, 1)),                    # 1040 rows over many key tiles
+    ([500, 100], [11, 10], 16, 2, 128, 16, "e4m3", "nhd", (0, 0)),
+    ([900], [130], 8, 1, 64, 32, "e4m3", "hnd", (1, 1)),
     ([1, 2, 63, 64, 65], [1] * 5, 16, 2, 128, 64, "e4m3", "hnd", (0, 0)),
     ([300, 9, 4], [8, 8, 8], 32, 4, 128, 32, "e4m3", "nhd", (0, 1)),
     ([77, 400], [5, 3], 24, 3, 64, 16, "e4m3", "hnd", (1, 0)),
@@ -114,6 +118,25 @@ def test_e4m3_query_range(factor):
     p.cuda()
     out, lse, _ = attend(p)
     check(p, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 8, 40])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nan_query_stays_in_its_row(dtype, news, value):
+    """A NaN or infinite query gives NaN in its own row and head, and there alone."""
+    p = ref.Problem([300], [news], 8, 1, 128, 64, dtype, seed=7)
+    clean = ref.attention(p)
+    p.qkv[news // 2, 3, 5] = value
+    p.cuda()
+    out, lse, _ = attend(p)
+    assert torch.isnan(out[news // 2, 3]).all() and torch.isnan(lse[news // 2, 3])
+    x, z = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    rest = np.ones((news, 8), bool)
+    rest[news // 2, 3] = False
+    tol = clean[2] * (2.0 ** -8 + 2 * clean[3][..., None] + 2.0 ** -20) + 2.0 ** -8 * np.abs(clean[0]) + 1e-30
+    assert np.all(np.abs(x - clean[0])[rest] <= tol[rest])
+    assert np.all(np.abs(z - clean[1])[rest] <= (clean[3] + 2.0 ** -20 * (1 + np.abs(clean[1])))[rest])
 
 
 def test_page_offsets_past_32_bits():
