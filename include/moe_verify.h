@@ -584,8 +584,8 @@ typedef struct {
 } moe_attn_t;
 
 /* Bytes of a workspace that serves the calls below for this shape, whatever
- * the batch (0 for a shape that is refused).  The caller zeroes it once; calls
- * on one stream may share it. */
+ * the batch (0 for a shape that is refused).  The caller zeroes its first 256
+ * bytes (the error word) once; calls on one stream may share it. */
 size_t moe_attn_workspace_bytes(const moe_attn_t* attn, const moe_kv_cache_t* cache);
 
 /*

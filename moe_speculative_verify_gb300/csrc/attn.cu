@@ -46,7 +46,6 @@ struct Shared {
     int64_t warp_sum[kConsumers + 1];
     Plan plan;
     float2 ml[kConsumers][kRows];            // maximum (log2) and sum of a warp's keys
-    int last;
 };
 
 template <int D, bool E4M3>
@@ -426,15 +425,14 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
         }
         // --- write: the item's output, or this CTA's piece of it
         const bool piece = it.t0 > 0 || it.t1 < it.n;
-        const int first = piece ? Work<kRows, kTile>::owner(it.u, sh.plan.ctas, sh.plan.total) : 0;
         float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * slot_floats;
         const float vs = E4M3 ? a.kv.v_scale[it.h] : 1.0f;
         for (int e = ctid; e < rows * (D / 4); e += 32 * kConsumers) {
-            const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+            const int row = e / (D / 4), d4 = e % (D / 4);
             float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * D + d);
+                const float4 x = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * D + 4 * d4);
                 v.x += x.x;
                 v.y += x.y;
                 v.z += x.z;
@@ -449,63 +447,20 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
                 sum += x.x == kNegInf ? 0.0f : x.y * fast_exp2(x.x - top);
             }
             if (piece) {
-                *reinterpret_cast<float4*>(slot + row * D + d) = v;
-                if (d == 0) *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(top, sum);
+                *reinterpret_cast<float4*>(slot + (d4 * kAttnSlotRows + row) * 4) =
+                    make_float4(v.x * vs, v.y * vs, v.z * vs, v.w * vs);
+                if (d4 == 0) *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(top, sum);
             } else {
                 const int r = it.rt * kRows + row, i = r / a.group, hd = it.h * a.group + r - i * a.group;
                 const int64_t at = int64_t(it.s.q0 + i) * a.q_heads + hd;
                 const float inv = top == kNegInf ? 0.0f : vs / sum;
-                *reinterpret_cast<uint2*>(a.out + at * D + d) =
+                *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
                     make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-                if (d == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
+                if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
             }
         }
-        if (!piece) {
-            named_bar(kBarMerge, 32 * kConsumers);
-            continue;
-        }
-        // --- the last CTA of a split item joins its pieces, in CTA order
-        const int lastc = Work<kRows, kTile>::owner(it.u + it.n - 1, sh.plan.ctas, sh.plan.total);
-        __threadfence();
+        if (ctid == 0) note_split(a, it, rows, kRows, sh.plan);
         named_bar(kBarMerge, 32 * kConsumers);
-        if (ctid == 0) {
-            const int old = atomicAdd(a.counters + first, 1);
-            sh.last = old == lastc - first;
-            if (sh.last) a.counters[first] = 0;
-        }
-        named_bar(kBarMerge, 32 * kConsumers);
-        if (sh.last) {
-            __threadfence();
-            const int np = lastc - first + 1;
-            for (int e = ctid; e < rows * (D / 4); e += 32 * kConsumers) {
-                const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-                auto piece_at = [&](int k) {
-                    return a.partials + (2 * int64_t(first + k) + (k == 0 ? 1 : 0)) * slot_floats;
-                };
-                float top = kNegInf, sum = 0.0f;
-                for (int k = 0; k < np; ++k)
-                    top = fmaxf(top, __ldcg(piece_at(k) + kAttnSlotRows * D + 2 * row));
-                float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-                for (int k = 0; k < np; ++k) {
-                    const float* ps = piece_at(k);
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(ps + kAttnSlotRows * D + 2 * row));
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(ps + row * D + d));
-                    const float w = ml.x == kNegInf ? 0.0f : fast_exp2(ml.x - top);
-                    sum += ml.x == kNegInf ? 0.0f : ml.y * w;
-                    v.x += ml.x == kNegInf ? 0.0f : x.x * w;
-                    v.y += ml.x == kNegInf ? 0.0f : x.y * w;
-                    v.z += ml.x == kNegInf ? 0.0f : x.z * w;
-                    v.w += ml.x == kNegInf ? 0.0f : x.w * w;
-                }
-                const int r = it.rt * kRows + row, i = r / a.group, hd = it.h * a.group + r - i * a.group;
-                const int64_t at = int64_t(it.s.q0 + i) * a.q_heads + hd;
-                const float inv = top == kNegInf ? 0.0f : vs / sum;
-                *reinterpret_cast<uint2*>(a.out + at * D + d) =
-                    make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-                if (d == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
-            }
-        }
     }
 }
 
@@ -544,10 +499,64 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
     if (e != cudaSuccess) return e;
     const int grid = n_sms < kAttnMaxCtas ? n_sms : kAttnMaxCtas;
     e = launch_pdl(attn_rows_kernel<D, E4M3>, dim3(grid), dim3(kThreads), C::kSmem, s, a, m);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_attn_join(a, kRows, grid, s);
+}
+
+// Joins the pieces of the item that begins in CTA blockIdx.x, 8 rows a block:
+// out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k over the pieces in CTA
+// order.  A kernel of its own, not the work of the piece that comes last: that
+// CTA alone would read a verify block's 19 pieces of 64 rows (630 KB) at one
+// SM's rate, here every SM reads some.
+constexpr int kJoinRows = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinRows* D / 4) attn_join_kernel(const AttnArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const SplitNote n = a.notes[blockIdx.x];
+    if (n.pieces == 0) return;
+    const int d4 = threadIdx.x / kJoinRows;
+    constexpr int64_t kSlot = kAttnSlotRows * (D + 2);
+    const float* p0 = a.partials + (2 * int64_t(blockIdx.x) + 1) * kSlot;     // the first piece,
+    const float* p1 = a.partials + 2 * (int64_t(blockIdx.x) + 1) * kSlot;     // then every second slot
+    for (int row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows; row < n.rows; row += gridDim.y * kJoinRows) {
+        const int ml = kAttnSlotRows * D + 2 * row, od = (d4 * kAttnSlotRows + row) * 4;
+        float top = kNegInf, sum = 0.0f;
+        float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int k = 0; k < n.pieces; ++k) {
+            const float* p = k == 0 ? p0 : p1 + 2 * (k - 1) * kSlot;
+            const float2 x = *reinterpret_cast<const float2*>(p + ml);
+            const float4 y = *reinterpret_cast<const float4*>(p + od);
+            if (x.x == kNegInf) continue;
+            const float nt = fmaxf(top, x.x), f = top == kNegInf ? 0.0f : fast_exp2(top - nt), w = fast_exp2(x.x - nt);
+            top = nt;
+            sum = sum * f + x.y * w;
+            v.x = v.x * f + y.x * w;
+            v.y = v.y * f + y.y * w;
+            v.z = v.z * f + y.z * w;
+            v.w = v.w * f + y.w * w;
+        }
+        const int r = n.row0 + row, i = r / a.group, hd = n.head * a.group + r - i * a.group;
+        const int64_t at = int64_t(n.q0 + i) * a.q_heads + hd;
+        const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
+        *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
+            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+        if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
+    }
 }
 
 }  // namespace
+
+cudaError_t launch_attn_join(const AttnArgs& a, int rows, int grid, cudaStream_t s) {
+    const int most = a.max_rows < rows ? a.max_rows : rows;     // rows of an item
+    const dim3 g(grid, (most + kJoinRows - 1) / kJoinRows);
+    const cudaError_t e = a.kv.dim == 128
+                              ? launch_pdl(attn_join_kernel<128>, g, dim3(kJoinRows * 32), 0, s, a)
+                              : launch_pdl(attn_join_kernel<64>, g, dim3(kJoinRows * 16), 0, s, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 cudaError_t launch_attn_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s) {
     if (a.kv.dim == 128)

@@ -77,15 +77,21 @@ __device__ __forceinline__ int2 rows_range(const AttnArgs& a, const Seq& s, int 
     return make_int2(lo, max(hi, 0));
 }
 
-// Whether every key of [j0, j1) is seen by every one of those rows.
-__device__ __forceinline__ bool rows_see_all(const AttnArgs& a, const Seq& s, int i0, int i1,
-                                             int j0, int j1) {
+// Keys that every one of those rows sees, as a range.
+__device__ __forceinline__ int2 rows_whole(const AttnArgs& a, const Seq& s, int i0, int i1) {
     int hi = s.len;
     if (a.draft)
         hi = min(hi, s.first);
     else if (a.causal)
         hi = min(hi, s.first + i0 + 1);
-    return j1 <= hi && !(a.window > 0 && j0 < s.first + i1 - a.window + 1);
+    return make_int2(a.window > 0 ? s.first + i1 - a.window + 1 : 0, hi);
+}
+
+// Whether every key of [j0, j1) is seen by every one of those rows.
+__device__ __forceinline__ bool rows_see_all(const AttnArgs& a, const Seq& s, int i0, int i1,
+                                             int j0, int j1) {
+    const int2 w = rows_whole(a, s, i0, i1);
+    return j0 >= w.x && j1 <= w.y;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -98,6 +104,29 @@ __device__ __forceinline__ float fast_log2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// (d0, d1) = (a0, a1) * b + c, and (d0, d1) += (a0, a1), as one packed
+// instruction each, rounded as the scalar ones.
+__device__ __forceinline__ void fma2_to(float& d0, float& d1, float a0, float a1, float b, float c) {
+    asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+        "mov.b64 pa, {%2, %3};\n\t"
+        "mov.b64 pb, {%4, %4};\n\t"
+        "mov.b64 pc, {%5, %5};\n\t"
+        "fma.rn.f32x2 pc, pa, pb, pc;\n\t"
+        "mov.b64 {%0, %1}, pc;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+    asm("{\n\t.reg .b64 pa, pd;\n\t"
+        "mov.b64 pa, {%2, %3};\n\t"
+        "mov.b64 pd, {%0, %1};\n\t"
+        "add.rn.f32x2 pd, pd, pa;\n\t"
+        "mov.b64 {%0, %1}, pd;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
 }
 
 // Two fp32 as bf16x2 / f16x2, `lo` in the low half, nearest even.
@@ -191,8 +220,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // MT query rows), rows r = i * group + g -- of one unit per KT-key tile that
 // some row of the item sees (one unit when none does), and give every CTA an
 // equal run of units in item order.  A CTA so meets at most two items that
-// it shares with its neighbours; it leaves those as partial results, and the
-// CTA that arrives last joins an item's pieces in CTA order.
+// it shares with its neighbours: it leaves its pieces of those in its two
+// slots (the second slot for an item that begins with it), the CTA where an
+// item begins notes the split, and the join kernel (attn.cu) adds an item's
+// pieces up in CTA order.
 struct Item {
     int b, h, rt;          // sequence, kv head, row tile
     int lo, hi;            // keys some row sees
@@ -278,6 +309,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int6
         s_plan->u0 = u0;
         s_plan->u1 = u1;
         s_plan->ctas = C;
+        a.notes[c].pieces = 0;
     }
     const int64_t pre = before + incl - mine;
     if (u0 < u1 && pre <= u0 && u0 < pre + mine) {
@@ -349,6 +381,19 @@ struct Walk {
         return true;
     }
 };
+
+// One thread, for each item of the CTA: notes the split item that begins here.
+__device__ __forceinline__ void note_split(const AttnArgs& a, const Item& it, int rows, int mt, const Plan& p) {
+    if (it.t0 != 0 || it.t1 >= it.n) return;
+    // the last item of the CTA's run, so its note is not written over
+    SplitNote n;
+    n.pieces = static_cast<int>(((it.u + it.n) * p.ctas - 1) / p.total) - static_cast<int>(blockIdx.x) + 1;
+    n.rows = rows;
+    n.row0 = it.rt * mt;
+    n.q0 = it.s.q0;
+    n.head = it.h;
+    a.notes[blockIdx.x] = n;
+}
 
 // Zeroes the output rows that belong to no sequence.
 __device__ __forceinline__ void zero_pad_rows(const AttnArgs& a) {

@@ -27,13 +27,22 @@ struct SeqArgs {
     int32_t n, max_pages, tokens;
 };
 
-// Workspace of the attention calls: the control block (error word), one
-// arrival counter per CTA (zero between calls), then the partial results of
-// split rows: two slots per CTA, each `rows` x (dim + 2) fp32.
+// A split item that begins in CTA i: written there by every call's CTA i.
+struct SplitNote {
+    int32_t pieces;          // 0: none
+    int32_t rows, row0;      // rows of the item, the first one's index in its sequence
+    int32_t q0, head;        // its sequence's first token, its kv head
+    int32_t pad[3];
+};
+
+// Workspace of the attention calls: the control block (error word), one note
+// per CTA, then the pieces of split items: two slots per CTA, each of
+// kAttnSlotRows rows, fp32: sums [dim/4][row][4], then (reference in log2
+// units, sum of powers) [row][2].
 constexpr int kAttnMaxCtas = 160;       // >= SMs of the card; larger grids are cut to it
 constexpr int kAttnSlotRows = 256;
-constexpr int64_t kAttnCounters = 256;  // byte offset
-constexpr int64_t kAttnPartials = 256 + ((kAttnMaxCtas * 4 + 255) / 256) * 256;
+constexpr int64_t kAttnNotes = 256;     // byte offset
+constexpr int64_t kAttnPartials = kAttnNotes + ((kAttnMaxCtas * sizeof(SplitNote) + 255) / 256) * 256;
 
 inline int64_t attn_workspace_bytes(int dim) {
     return kAttnPartials + int64_t(2) * kAttnMaxCtas * kAttnSlotRows * (dim + 2) * 4;
@@ -65,14 +74,15 @@ struct AttnArgs {
     int32_t q_heads, group;  // group = q_heads / kv heads
     float scale;
     int32_t causal, window;
+    int32_t max_rows;        // rows of an item by the caller's max_q: sizes the join's grid only
     int32_t* err;
-    int32_t* counters;
+    SplitNote* notes;
     float* partials;
     uint64_t timeout_ns;
 };
 
 struct KeywArgs {
-    AttnArgs a;              // out, counters and partials unused; lse is read
+    AttnArgs a;              // out, notes and partials unused; lse is read
     float decay;
     const float* scores;
     float* scores_out;
@@ -107,6 +117,7 @@ constexpr int kAttnBigTile = 128;   // and of the tensor-memory kernel
 
 cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnArgs& a, int rows, int grid, cudaStream_t s);
 cudaError_t launch_attn_tile(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
 cudaError_t launch_keyw(const KeywArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);

@@ -155,7 +155,7 @@ moe::AttnArgs attn_args(const moe_attn_t* at, const moe_kv_cache_t* c, const moe
     a.window = at->window;
     uint8_t* base = static_cast<uint8_t*>(ws);
     a.err = reinterpret_cast<int32_t*>(base);
-    a.counters = reinterpret_cast<int32_t*>(base + moe::kAttnCounters);
+    a.notes = reinterpret_cast<moe::SplitNote*>(base + moe::kAttnNotes);
     a.partials = reinterpret_cast<float*>(base + moe::kAttnPartials);
     a.timeout_ns = uint64_t(at->wait_timeout_us ? at->wait_timeout_us : 2000000u) * 1000ull;
     return a;
@@ -272,11 +272,13 @@ moe_status_t moe_paged_attention(const moe_attn_t* attn, const moe_kv_cache_t* c
         return MOE_ERR_INVALID_ARG;
     if ((st = check_ws(ws, ws_bytes, moe_attn_workspace_bytes(attn, cache))) != MOE_OK) return st;
     moe::KvMaps maps;
-    const bool few = int64_t(seqs->max_q) * (attn->n_q_heads / cache->n_kv_heads) <= moe::kAttnFewRows;
+    const int64_t rows = int64_t(seqs->max_q) * (attn->n_q_heads / cache->n_kv_heads);
+    const bool few = rows <= moe::kAttnFewRows;
     if (!make_kv_maps(cache, few ? moe::kAttnTile : moe::kAttnBigTile, &maps)) return MOE_ERR_CUDA;
     moe::AttnArgs a = attn_args(attn, cache, seqs, q, q_stride, draft_mask, n_tokens, ws);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
+    a.max_rows = static_cast<int32_t>(rows < moe::kAttnSlotRows ? rows : moe::kAttnSlotRows);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return cuda_status(few ? moe::launch_attn_rows(a, maps, device_info().sms, s)
                            : moe::launch_attn_tile(a, maps, device_info().sms, s));
@@ -325,7 +327,7 @@ moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs
         !aligned(scores, 4) || !aligned(scores_out, 4) || !aligned(to_table, 4) ||
         !aligned(kept, 4) || !aligned(new_len, 4) || new_len == seqs->kv_len)
         return MOE_ERR_INVALID_ARG;
-    if ((st = check_ws(ws, ws_bytes, moe::kAttnCounters)) != MOE_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, moe::kAttnNotes)) != MOE_OK) return st;
     moe::EvictArgs a{};
     a.kv = kv_args(cache);
     a.sq = seq_args(seqs, 0);

@@ -4,7 +4,10 @@
 // An item is up to 256 query rows of one sequence and kv head, worked on as
 // two streams of 128-row tiles.  Above 128 rows the streams are the two row
 // tiles, which share every K and V tile; up to 128 rows both hold the same
-// rows and take alternate key tiles, and are joined when the item ends.  Each
+// rows and take alternate key tiles, and are joined when the item ends; with
+// 64 (or 32) rows or fewer the rows are repeated in the tile's other lanes,
+// and each copy takes its half (quarter) of a tile's keys through the softmax,
+// so all eight warps work on few rows too.  Each
 // stream's step is S = Q K^T (tcgen05.mma, shared x shared), the softmax of a
 // warpgroup with a thread per row, and O += P V (P from tensor memory), so one
 // stream's products run while the other's softmax does.
@@ -43,20 +46,9 @@ struct Cfg {
     static constexpr int kQBytes = 128 * 2 * D;                    // bf16, or e4m3 high and low
     static constexpr int kStages = kTileBytes == 32768 ? 5 : 10;
     static constexpr int kMerge = 128 * D * 4;                     // == 2 * kQBytes: stream 1's O
-    static constexpr size_t kSmem = 1024 + 2 * kQBytes + kStages * kTileBytes;
+    static constexpr size_t kSmem = 2 * kQBytes + kStages * kTileBytes;   // then Shared
     static constexpr float kLag = E4M3 ? 4.0f : 8.0f;
     static constexpr float kBias = E4M3 ? 4.0f : 0.0f;             // probabilities times 2^kBias
-};
-
-struct Shared {
-    alignas(8) uint64_t kv_full[10];
-    uint64_t kv_empty[10];
-    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2];
-    int64_t warp_sum[kThreads / 32];
-    Plan plan;
-    float2 ml[128];
-    uint32_t tmem;
-    int last;
 };
 
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
@@ -110,12 +102,11 @@ __device__ __forceinline__ void fence_async_smem() {
 
 // An item as its CTA works on it: mode, tiles, and each stream's share.
 struct Share {
-    bool pair;               // two row tiles; else alternate key tiles of one
+    int pair;                // two row tiles; else alternate key tiles of one
     int rows;                // rows of the item
     int tiles;               // key tiles of this CTA (0: nothing seen)
     int a[2], b[2];          // pair: stream s takes local tiles a .. b-1
-    int lo[2], hi[2];        // keys that some row of the stream sees
-    int i0[2], i1[2];        // first and last query of the stream
+    int wlo[2], whi[2];      // keys that every row of the stream sees
 
     __device__ __forceinline__ void set(const AttnArgs& at, const Item& it) {
         rows = min(kMT, it.s.nq * at.group - it.rt * kMT);
@@ -125,26 +116,59 @@ struct Share {
         for (int s = 0; s < 2; ++s) {
             const int r0 = it.rt * kMT + (pair ? 128 * s : 0);
             const int r1 = pair ? min(r0 + 128, it.rt * kMT + rows) : r0 + rows;
-            i0[s] = r0 / at.group;
-            i1[s] = (r1 - 1) / at.group;
-            const int2 k = rows_range(at, it.s, i0[s], i1[s]);
-            lo[s] = k.x;
-            hi[s] = k.y;
+            const int i0 = r0 / at.group, i1 = (r1 - 1) / at.group;
+            const int2 k = rows_range(at, it.s, i0, i1), w = rows_whole(at, it.s, i0, i1);
+            wlo[s] = w.x;
+            whi[s] = w.y;
             a[s] = 0;
             b[s] = tiles;
             if (pair) {
                 const int base = it.tile0 + it.t0;
-                a[s] = min(max(lo[s] / kKT - base, 0), tiles);
-                b[s] = hi[s] > lo[s] ? max(min((hi[s] + kKT - 1) / kKT - base, tiles), a[s]) : a[s];
+                a[s] = min(max(k.x / kKT - base, 0), tiles);
+                b[s] = k.y > k.x ? max(min((k.y + kKT - 1) / kKT - base, tiles), a[s]) : a[s];
             }
         }
     }
     __device__ __forceinline__ bool on(int s, int j) const { return j >= a[s] && j < b[s]; }
-    // tiles of stream s
+    // tiles of stream s, and its n-th
     __device__ __forceinline__ int count(int s) const {
-        return pair ? b[s] - a[s] : (tiles + 1 - s) / 2;
+        return pair ? (s ? b[1] - a[1] : b[0] - a[0]) : (tiles + 1 - s) / 2;
     }
-    __device__ __forceinline__ int tile(int s, int n) const { return pair ? a[s] + n : 2 * n + s; }
+    __device__ __forceinline__ int tile(int s, int n) const { return pair ? (s ? a[1] : a[0]) + n : 2 * n + s; }
+};
+
+// A warp's place in the CTA's work, kept in shared memory so that it takes no
+// registers from the loops over the tiles.
+struct Ctx {
+    Walk<kMT, kKT> wk;
+    Item it;
+    Share sr;
+
+    __device__ __forceinline__ void start(const AttnArgs& a, const Plan& p) {
+        if ((threadIdx.x & 31) == 0) wk.start(a, p);
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool next(const AttnArgs& a) {
+        __syncwarp();
+        int more = 0;
+        if ((threadIdx.x & 31) == 0) {
+            more = wk.next(a, it);
+            if (more) sr.set(a, it);
+        }
+        more = __shfl_sync(0xFFFFFFFFu, more, 0);
+        __syncwarp();
+        return more != 0;
+    }
+};
+
+struct Shared {
+    alignas(16) float2 ml[128];             // a lane's reference and sum, between the streams
+    uint64_t kv_full[10];
+    uint64_t kv_empty[10];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2];
+    Plan plan;
+    Ctx ctx[10];                            // the softmax warps', the TMA warp's, the MMA warp's
+    uint32_t tmem;
 };
 
 template <int D, bool E4M3>
@@ -154,14 +178,13 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
     constexpr int kBoxBytes = E4M3 ? D : 128;
     const int lane = threadIdx.x & 31;
     const int page = a.kv.page, pl = a.kv.page_log2;
-    Walk<kMT, kKT> wk;
-    wk.start(a, sh.plan);
-    Item it;
-    Share sr;
+    Ctx& ctx = sh.ctx[8];
+    ctx.start(a, sh.plan);
     int run = 0;
     bool dead = false;
-    while (wk.next(a, it)) {
-        sr.set(a, it);
+    while (ctx.next(a)) {
+        const Item& it = ctx.it;
+        const Share& sr = ctx.sr;
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
         const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl;
         const int ahead = sr.pair ? 1 : 2;
@@ -214,10 +237,10 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
     constexpr bool kNarrow = E4M3 && D == 64;                    // 64-byte cached rows
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = sh.tmem;
-    Walk<kMT, kKT> wk;
-    wk.start(a, sh.plan);
-    Item it;
-    Share sr;
+    Ctx& ctx = sh.ctx[9];
+    ctx.start(a, sh.plan);
+    const Item& it = ctx.it;
+    const Share& sr = ctx.sr;
     int run = 0, items = 0;
     uint32_t pp[2] = {0, 0};                                     // p_ready phases
     bool dead = false;
@@ -289,8 +312,7 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
         fence_async_smem();
         __syncwarp();
     };
-    while (wk.next(a, it)) {
-        sr.set(a, it);
+    while (ctx.next(a)) {
         const int T = sr.tiles;
         if (T == 0) continue;
         wait(&sh.q_ready[0], items & 1);
@@ -354,6 +376,197 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
     }
 }
 
+// N 32-bit columns (8, 16 or 32) of this thread's TMEM lane.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+    if constexpr (N == 32) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+            "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+            "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+            "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+            "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+            : "memory");
+    } else if constexpr (N == 16) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+            "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
+    } else {
+        static_assert(N == 8, "8, 16 or 32 columns");
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    }
+}
+
+// What a softmax thread carries through an item: its row's reference (log2
+// units) and sum of powers.
+struct RowState {
+    float ref, sum0, sum1;
+};
+
+// One key tile of a softmax thread: keys kFirst .. of the tile's 128 are its
+// copy's (W = 128 / NC of them, from W * copy on).  Reads S, writes P over it.
+template <int D, bool E4M3, int NC>
+__device__ __forceinline__ void soft_tile(uint32_t colS, uint32_t colO, int copy, float c, int i, int j0, bool whole,
+                                          bool draft, const RowView& view, int first, RowState& st) {
+    using C = Cfg<D, E4M3>;
+    constexpr int W = 128 / NC, Q = W / 32;
+    float x[Q][32];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) tmem_ld32(colS + W * copy + 32 * q, x[q]);
+    tmem_wait_ld();
+    if (!whole) {
+        const int k0 = j0 + W * copy, lo = view.lo - k0, hi = view.hi - k0;
+        if (!draft) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (32 * q + e < lo || 32 * q + e >= hi) x[q][e] = kNegInf;
+        } else {
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (!row_sees(view, true, first, k0 + 32 * q + e)) x[q][e] = kNegInf;
+        }
+    }
+    float t4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], fmaxf(x[q][e + 2 * k], x[q][e + 2 * k + 1]));
+    float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
+    if (!(top > kNegInf)) top = kNegInf;                         // (NaN: the sums carry it)
+    const bool grow = top > st.ref + C::kLag || (st.ref == kNegInf && top > kNegInf);
+    if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+        const float f = !grow ? 1.0f : (st.ref == kNegInf ? 0.0f : fast_exp2(st.ref - top));
+        st.sum0 *= f;
+        st.sum1 *= f;
+        for (int q = 0; q < D / 8; ++q) {
+            float o[8];
+            tmem_ld8(colO + 8 * q, o);
+            tmem_wait_ld();
+            uint32_t u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+            tmem_st<8>(colO + 8 * q, u);
+        }
+    }
+    if (grow) st.ref = top;
+    const float off = C::kBias - (st.ref == kNegInf ? 0.0f : st.ref);
+    // powers: summed in fp32, then rounded
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        uint32_t u[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            float p[4];
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                fma2_to(p[k], p[k + 1], x[q][e + k], x[q][e + k + 1], c, off);
+                p[k] = fast_exp2(p[k]);
+                p[k + 1] = fast_exp2(p[k + 1]);
+                add2(st.sum0, st.sum1, p[k], p[k + 1]);
+            }
+            if constexpr (!E4M3) {
+                u[e / 2] = pack_bf16(p[0], p[1]);
+                u[e / 2 + 1] = pack_bf16(p[2], p[3]);
+            } else {
+                const uint32_t h0 = pack_e4m3(p[0], p[1]), h1 = pack_e4m3(p[2], p[3]);
+                const float2 b0 = unpack_e4m3(h0), b1 = unpack_e4m3(h1);
+                u[e / 4] = h0 | (h1 << 16);
+                u[8 + e / 4] = pack_e5m2(p[0] - b0.x, p[1] - b0.y) | (pack_e5m2(p[2] - b1.x, p[3] - b1.y) << 16);
+            }
+        }
+        if constexpr (!E4M3) {
+            tmem_st<16>(colS + (W / 2) * copy + 16 * q, u);
+        } else {
+            tmem_st<8>(colS + (W / 4) * copy + 8 * q, u);
+            tmem_st<8>(colS + 32 + (W / 4) * copy + 8 * q, u + 8);
+        }
+    }
+    if constexpr (NC > 1) {                                      // the other copies' keys: zero
+        const uint32_t z[32] = {};
+#pragma unroll
+        for (int o = 1; o < NC; ++o) {
+            const int oc = (copy + o) & (NC - 1);
+            if constexpr (!E4M3) {
+                tmem_st<W / 2>(colS + (W / 2) * oc, z);
+            } else {
+                tmem_st<W / 4>(colS + (W / 4) * oc, z);
+                tmem_st<W / 4>(colS + 32 + (W / 4) * oc, z);
+            }
+        }
+    }
+    tmem_wait_st();
+}
+
+template <int D, bool E4M3>
+__device__ __forceinline__ void load_query(const AttnArgs& a, const uint16_t* src, bool valid, float sign, uint8_t* qt,
+                                           int lr, float& c) {
+    uint4 w[D / 8];
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k)
+        w[k] = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+    uint8_t* base = qt + lr * 128;
+    if constexpr (!E4M3) {
+        const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+            *reinterpret_cast<uint4*>(base + (k >> 3) * 16384 + (((k & 7) ^ (lr & 7)) << 4)) =
+                make_uint4(w[k].x ^ flip, w[k].y ^ flip, w[k].z ^ flip, w[k].w ^ flip);
+    } else {
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(x[e] & 0xFFFFu)),
+                                         fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+        }
+        // the row's largest element to [128, 256): f1 takes it to [1, 2)
+        const float f1 = pow2_norm(amax);
+        const float f2 = f1 == 1.0f && !(amax >= 1.0f && amax < 2.0f) ? 1.0f : 128.0f;
+        c = amax < INFINITY ? fmaxf(c / f2 / f1, 1.2e-38f) : __int_as_float(0x7FC00000);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {                       // 16 elements: a chunk of each code
+            uint32_t hi4[4], lo4[4];
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+                const uint4 ww = w[2 * k + (q4 >> 1)];
+                const uint32_t x[2] = {q4 & 1 ? ww.z : ww.x, q4 & 1 ? ww.w : ww.y};
+                uint32_t h = 0, l = 0;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f1 * f2 * sign;
+                    const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f1 * f2 * sign;
+                    const uint32_t hc = pack_e4m3(v0, v1);
+                    const float2 b = unpack_e4m3(hc);
+                    h |= hc << (16 * e);
+                    l |= pack_e4m3(v0 - b.x, v1 - b.y) << (16 * e);
+                }
+                hi4[q4] = h;
+                lo4[q4] = l;
+            }
+            const int cl = D == 128 ? k : k + 4;
+            uint8_t* low = D == 128 ? base + 16384 : base;
+            *reinterpret_cast<uint4*>(base + ((k ^ (lr & 7)) << 4)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+            *reinterpret_cast<uint4*>(low + ((cl ^ (lr & 7)) << 4)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+        }
+    }
+    fence_async_smem();
+}
+
 template <int D, bool E4M3>
 __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* qs) {
     using C = Cfg<D, E4M3>;
@@ -361,195 +574,75 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
     const uint32_t tm_lane = sh.tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t colS = tm_lane + 128 * s, colO = tm_lane + kColO + 128 * s;
     const bool draft = a.draft != nullptr;
-    const float sign = a.scale < 0.0f ? -1.0f : 1.0f, scale = fabsf(a.scale) * kLog2e;
-    const int64_t slot_floats = kAttnSlotRows * (D + 2);
-    uint8_t* qt = qs + s * C::kQBytes;
-    Walk<kMT, kKT> wk;
-    wk.start(a, sh.plan);
-    Item it;
-    Share sr;
-    uint32_t sp = 0, op[2] = {0, 0};
+    Ctx& ctx = sh.ctx[tid >> 5];
+    ctx.start(a, sh.plan);
+    const Item& it = ctx.it;
+    const Share& sr = ctx.sr;
+    uint32_t sp = 0, op0 = 0, op1 = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
         tc_fence_after();
     };
-    while (wk.next(a, it)) {
-        sr.set(a, it);
-        // this thread's row; half-empty alternate tiles go to the other half of the lanes
-        const int row = sr.pair ? 128 * s + lr : (s == 1 && sr.rows <= 64 ? (lr + 64) & 127 : lr);
+    while (ctx.next(a)) {
+        // this thread's row, and its copy where the rows repeat
+        const int copies = sr.pair || sr.rows > 64 ? 1 : (sr.rows > 32 ? 2 : 4);
+        const int span = 128 / copies, copy = lr / span;
+        const int row = sr.pair ? 128 * s + lr : lr - copy * span;
         const bool valid = row < sr.rows;
         const bool warp_on = __any_sync(0xFFFFFFFFu, valid);
-        const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+        const int n = sr.count(s);
+        RowView view{0, 0, 0ull};
         // (never 0: an unseen key's -inf times it stays -inf)
-        float c = fmaxf(scale * (E4M3 ? a.kv.k_scale[it.h] : 1.0f), 1.2e-38f);
-        // --- the query row into shared memory, K-major, 128-byte swizzle
+        float c = fmaxf(fabsf(a.scale) * kLog2e * (E4M3 ? a.kv.k_scale[it.h] : 1.0f), 1.2e-38f);
         {
-            const uint16_t* src = a.q + (it.s.q0 + qi) * a.q_stride + hd * D;
-            uint4 w[D / 8];
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k)
-                w[k] = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-            uint8_t* base = qt + lr * 128;
-            if constexpr (!E4M3) {
-                const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k)
-                    *reinterpret_cast<uint4*>(base + (k >> 3) * 16384 + (((k & 7) ^ (lr & 7)) << 4)) =
-                        make_uint4(w[k].x ^ flip, w[k].y ^ flip, w[k].z ^ flip, w[k].w ^ flip);
-            } else {
-                float amax = 0.0f;
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k) {
-                    const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(x[e] & 0xFFFFu)),
-                                                 fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-                }
-                // the largest element to [128, 256); the factor may pass fp32's range only for rows
-                // whose products are zero or infinite anyway
-                const float f1 = pow2_norm(amax);
-                const float f2 = f1 == 1.0f && !(amax >= 1.0f && amax < 2.0f) ? 1.0f : 128.0f;
-                c = amax < INFINITY ? fmaxf(c / f2 / f1, 1.2e-38f) : __int_as_float(0x7FC00000);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {               // 16 elements: a chunk of each
-                    uint32_t hi4[4], lo4[4];
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        const uint4 ww = w[2 * k + (q4 >> 1)];
-                        const uint32_t x[2] = {q4 & 1 ? ww.z : ww.x, q4 & 1 ? ww.w : ww.y};
-                        uint32_t h = 0, l = 0;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f1 * f2 * sign;
-                            const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f1 * f2 * sign;
-                            const uint32_t hc = pack_e4m3(v0, v1);
-                            const float2 b = unpack_e4m3(hc);
-                            h |= hc << (16 * e);
-                            l |= pack_e4m3(v0 - b.x, v1 - b.y) << (16 * e);
-                        }
-                        hi4[q4] = h;
-                        lo4[q4] = l;
-                    }
-                    const int ch = k, cl = D == 128 ? k : k + 4;
-                    uint8_t* low = D == 128 ? base + 16384 : base;
-                    *reinterpret_cast<uint4*>(base + ((ch ^ (lr & 7)) << 4)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-                    *reinterpret_cast<uint4*>(low + ((cl ^ (lr & 7)) << 4)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
-                }
-            }
-            fence_async_smem();
+            const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+            if (valid) view = row_view(a, it.s, qi);
+            load_query<D, E4M3>(a, a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid && a.scale != 0.0f,
+                                a.scale < 0.0f ? -1.0f : 1.0f, qs + s * C::kQBytes, lr, c);
             __syncwarp();
             if (lane == 0 && sr.tiles > 0) mbar_arrive(&sh.q_ready[s]);
         }
-        RowView view{0, 0, 0ull};
-        if (valid) view = row_view(a, it.s, qi);
-        const int n = sr.count(s);
-        float ref = kNegInf, sum = 0.0f;
-        for (int i = 0; i < n; ++i) {
-            const int j0 = (it.tile0 + it.t0 + sr.tile(s, i)) * kKT;
-            wait(&sh.s_full[s], sp);
-            sp ^= 1;
-            if (warp_on) {
-                float x[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(colS + 32 * q, x[q]);
-                tmem_wait_ld();
-                if (!rows_see_all(a, it.s, sr.i0[s], sr.i1[s], j0, j0 + kKT)) {
-                    const int lo = view.lo - j0, hi = view.hi - j0;
-                    if (!draft) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int k = 32 * q + e;
-                                if (k < lo || k >= hi) x[q][e] = kNegInf;
-                            }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!row_sees(view, true, it.s.first, j0 + 32 * q + e)) x[q][e] = kNegInf;
-                    }
+        RowState st{kNegInf, 0.0f, 0.0f};
+        {
+            const int base = (it.tile0 + it.t0 + sr.tile(s, 0)) * kKT, step = sr.pair ? kKT : 2 * kKT;
+            const int wlo = s ? sr.wlo[1] : sr.wlo[0], whi = s ? sr.whi[1] : sr.whi[0], first = it.s.first;
+            for (int i = 0; i < n; ++i) {
+                const int j0 = base + i * step;
+                wait(&sh.s_full[s], sp);
+                sp ^= 1;
+                if (warp_on) {
+                    const bool whole = j0 >= wlo && j0 + kKT <= whi;
+                    if (copies == 1)
+                        soft_tile<D, E4M3, 1>(colS, colO, 0, c, i, j0, whole, draft, view, first, st);
+                    else if (copies == 2)
+                        soft_tile<D, E4M3, 2>(colS, colO, copy, c, i, j0, whole, draft, view, first, st);
+                    else
+                        soft_tile<D, E4M3, 4>(colS, colO, copy, c, i, j0, whole, draft, view, first, st);
                 }
-                float top = kNegInf;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fmaxf(top, x[q][e]);
-                top *= c;
-                if (!(top > kNegInf)) top = kNegInf;             // (NaN: the sums carry it)
-                const bool grow = top > ref + C::kLag || (ref == kNegInf && top > kNegInf);
-                if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
-                    const float f = !grow ? 1.0f : (ref == kNegInf ? 0.0f : fast_exp2(ref - top));
-                    sum *= f;
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        float o[32];
-                        tmem_ld32(colO + 32 * q, o);
-                        tmem_wait_ld();
-                        uint32_t u[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
-                        tmem_st32(colO + 32 * q, u);
-                    }
-                }
-                if (grow) ref = top;
-                const float off = (ref == kNegInf ? 0.0f : ref) - C::kBias;
-                if constexpr (!E4M3) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t u[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float p0 = fast_exp2(fmaf(x[2 * q + (e >> 4)][(2 * e) & 31], c, -off));
-                            const float p1 = fast_exp2(fmaf(x[2 * q + (e >> 4)][(2 * e + 1) & 31], c, -off));
-                            sum += p0 + p1;
-                            u[e] = pack_bf16(p0, p1);
-                        }
-                        tmem_st32(colS + 32 * q, u);
-                    }
-                } else {
-                    uint32_t h[32], l[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        h[e] = l[e] = 0;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int col = 4 * e + 2 * k;
-                            const float p0 = fast_exp2(fmaf(x[col >> 5][col & 31], c, -off));
-                            const float p1 = fast_exp2(fmaf(x[col >> 5][(col + 1) & 31], c, -off));
-                            sum += p0 + p1;
-                            const uint32_t hc = pack_e4m3(p0, p1);
-                            const float2 b = unpack_e4m3(hc);
-                            h[e] |= hc << (16 * k);
-                            l[e] |= pack_e5m2(p0 - b.x, p1 - b.y) << (16 * k);
-                        }
-                    }
-                    tmem_st32(colS, h);
-                    tmem_st32(colS + 32, l);
-                }
-                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_ready[s]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_ready[s]);
         }
-        if (sum != sum) ref = fmaxf(ref, 0.0f);                  // a NaN is a result, not an empty row
         // --- the item's rows: normalised, or this CTA's piece of them
+        float ref = st.ref, sum = st.sum0 + st.sum1;
+        if (sum != sum) ref = fmaxf(ref, 0.0f);                  // a NaN is a result, not an empty row
         const bool piece = it.t0 > 0 || it.t1 < it.n;
-        float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * slot_floats;
-        const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
+        float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * kAttnSlotRows * (D + 2);
         const float vs = E4M3 ? a.kv.v_scale[it.h] : 1.0f;
         float* merge = reinterpret_cast<float*>(qs);
-        const int n1 = sr.count(1);
-        if (n > 0) wait(&sh.o_full[s], op[s]);
-        if (!sr.pair && n1 > 0) {
+        auto cell = [&](int r, int d4) {
+            return reinterpret_cast<float4*>(merge + r * D + ((d4 ^ (r & 7)) << 2));
+        };
+        const int n0 = sr.count(0), n1 = sr.count(1);
+        const bool other = !sr.pair && n1 > 0;
+        if (n > 0) wait(&sh.o_full[s], s ? op1 : op0);
+        if (other) {
             // both streams' products are done: the query tiles make room for stream 1's sums
-            if (s == 1) wait(&sh.o_full[0], op[0]);
+            if (s == 1) wait(&sh.o_full[0], op0);
             if (s == 1 && warp_on) {
-                sh.ml[row & 127] = make_float2(ref, sum);
+                sh.ml[lr] = make_float2(ref, sum);
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                     float o[32];
@@ -557,116 +650,102 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (valid)
-                            *reinterpret_cast<float4*>(merge + row * D + (((8 * q + e) ^ (row & 7)) << 2)) =
-                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    __syncwarp();
+                        *cell(lr, 8 * q + e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
             named_bar(kBarAll, kSoft);
         }
-        if (sr.count(0) > 0) op[0] ^= 1;
-        if (n1 > 0) op[1] ^= 1;
+        if (n0 > 0) op0 ^= 1;
+        if (n1 > 0) op1 ^= 1;
+        const bool spread = copies > 1;
         if ((sr.pair || s == 0) && warp_on) {
             float f0 = 1.0f, f1 = 0.0f;
-            const bool other = !sr.pair && n1 > 0;
             if (other) {
-                const float2 ml = valid ? sh.ml[row] : make_float2(kNegInf, 0.0f);
+                const float2 ml = sh.ml[lr];
                 const float top = fmaxf(ref, ml.x);
                 f0 = ref == kNegInf ? 0.0f : fast_exp2(ref - top);
                 f1 = ml.x == kNegInf ? 0.0f : fast_exp2(ml.x - top);
                 sum = (f0 == 0.0f ? 0.0f : sum * f0) + (f1 == 0.0f ? 0.0f : ml.y * f1);
                 ref = top;
             }
-            const bool none = ref == kNegInf;
-            const float inv = none ? 0.0f : vs / sum;
+            if (n == 0 || ref == kNegInf) f0 = 0.0f;
+            const float k0 = piece || spread ? vs : (ref == kNegInf ? 0.0f : vs / sum);
+            const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+            const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 float o[32];
-                if (n > 0) {
-                    tmem_ld32(colO + 32 * q, o);
-                    tmem_wait_ld();
-                }
+                tmem_ld32(colO + 32 * q, o);
+                tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float4 y = other && valid ? *reinterpret_cast<const float4*>(merge + row * D + (((8 * q + e) ^ (row & 7)) << 2))
-                                     : make_float4(0, 0, 0, 0);
+                    float4 y = make_float4(0, 0, 0, 0);
+                    if (other) y = *cell(lr, 8 * q + e);
                     float* oo = o + 4 * e;
-                    float* yy = &y.x;
+                    const float yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float u = n > 0 && f0 != 0.0f && !none ? oo[k] * f0 : 0.0f;
-                        oo[k] = u + (f1 != 0.0f ? yy[k] * f1 : 0.0f);
-                    }
-                    if (piece && valid)
+                    for (int k = 0; k < 4; ++k)
+                        oo[k] = ((f0 != 0.0f ? oo[k] * f0 : 0.0f) + (f1 != 0.0f ? yy[k] * f1 : 0.0f)) * k0;
+                    if (spread)
+                        *cell(lr, 8 * q + e) = make_float4(oo[0], oo[1], oo[2], oo[3]);
+                    else if (piece && valid)
                         *reinterpret_cast<float4*>(slot + ((8 * q + e) * kAttnSlotRows + row) * 4) =
                             make_float4(oo[0], oo[1], oo[2], oo[3]);
                 }
-                if (!piece && valid) {
+                if (!spread && !piece && valid) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         *reinterpret_cast<uint4*>(a.out + at * D + 32 * q + 8 * e) =
-                            make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                       pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                       pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                       pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                            make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                       pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                 }
                 __syncwarp();
             }
-            if (valid && piece)
-                *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(ref, sum);
-            if (valid && !piece && a.lse) a.lse[at] = none ? kNegInf : (ref - C::kBias + log2f(sum)) * kLn2;
+            if (spread)
+                sh.ml[lr] = make_float2(ref, sum);
+            else if (valid && piece)
+                *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(ref - C::kBias, sum);
+            else if (valid && a.lse)
+                a.lse[at] = ref == kNegInf ? kNegInf : (ref - C::kBias + log2f(sum)) * kLn2;
         }
         tc_fence_before();
-        if (!piece) {
-            // Alternate tiles: stream 1's sums have been read.  A stream without
-            // tiles must not run an item ahead of the MMA warp's wait for its queries.
-            if (!sr.pair || n1 == 0 || sr.count(0) == 0) named_bar(kBarAll, kSoft);
-            continue;
-        }
-        // --- the last CTA of a split item joins its pieces, in CTA order
-        using W = Work<kMT, kKT>;
-        const int first = W::owner(it.u, sh.plan.ctas, sh.plan.total);
-        const int lastc = W::owner(it.u + it.n - 1, sh.plan.ctas, sh.plan.total);
-        __threadfence();
-        named_bar(kBarAll, kSoft);
-        if (tid == 0) {
-            const int old = atomicAdd(a.counters + first, 1);
-            sh.last = old == lastc - first;
-            if (sh.last) a.counters[first] = 0;
-        }
-        named_bar(kBarAll, kSoft);
-        if (!sh.last) continue;
-        __threadfence();
-        const int np = lastc - first + 1;
-        auto piece_at = [&](int k) { return a.partials + (2 * int64_t(first + k) + (k == 0 ? 1 : 0)) * slot_floats; };
-        for (int e = tid; e < sr.rows * (D / 8); e += kSoft) {
-            const int rw = e % sr.rows, d8 = e / sr.rows;
-            float top = kNegInf, tot = 0.0f;
-            for (int k = 0; k < np; ++k) top = fmaxf(top, __ldcg(piece_at(k) + kAttnSlotRows * D + 2 * rw));
-            float y[8] = {};
-#pragma unroll 4
-            for (int k = 0; k < np; ++k) {
-                const float* ps = piece_at(k);
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(ps + kAttnSlotRows * D + 2 * rw));
-                const float4 u = __ldcg(reinterpret_cast<const float4*>(ps + (2 * d8 * kAttnSlotRows + rw) * 4));
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(ps + ((2 * d8 + 1) * kAttnSlotRows + rw) * 4));
-                const bool some = ml.x != kNegInf;
-                const float w = some ? fast_exp2(ml.x - top) : 0.0f;
-                tot += some ? ml.y * w : 0.0f;
-                const float x8[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] += some ? x8[q] * w : 0.0f;
+        if (spread) {
+            // --- the copies of a row, by both warpgroups
+            named_bar(kBarAll, kSoft);
+            for (int e = tid; e < sr.rows * (D / 4); e += kSoft) {
+                const int d4 = e / sr.rows, rw = e - d4 * sr.rows;
+                float top = kNegInf, tot = 0.0f;
+                for (int k = 0; k < copies; ++k) top = fmaxf(top, sh.ml[rw + k * span].x);
+                float4 y = make_float4(0, 0, 0, 0);
+                for (int k = 0; k < copies; ++k) {
+                    const float2 ml = sh.ml[rw + k * span];
+                    if (ml.x == kNegInf) continue;
+                    const float w = fast_exp2(ml.x - top);
+                    const float4 u = *cell(rw + k * span, d4);
+                    tot += ml.y * w;
+                    y.x += u.x * w;
+                    y.y += u.y * w;
+                    y.z += u.z * w;
+                    y.w += u.w * w;
+                }
+                if (piece) {
+                    *reinterpret_cast<float4*>(slot + (d4 * kAttnSlotRows + rw) * 4) = y;
+                    if (d4 == 0)
+                        *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * rw) = make_float2(top - C::kBias, tot);
+                } else {
+                    const int r = it.rt * kMT + rw, qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+                    const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
+                    const float inv = top == kNegInf ? 0.0f : 1.0f / tot;
+                    *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
+                        make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+                    if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top - C::kBias + log2f(tot)) * kLn2;
+                }
             }
-            const int rr = it.rt * kMT + rw, ii = rr / a.group, hh = it.h * a.group + rr - ii * a.group;
-            const int64_t dst = int64_t(it.s.q0 + ii) * a.q_heads + hh;
-            const bool none = top == kNegInf;
-            const float inv = none ? 0.0f : vs / tot;
-            *reinterpret_cast<uint4*>(a.out + dst * D + 8 * d8) =
-                make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
-                           pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
-            if (d8 == 0 && a.lse) a.lse[dst] = none ? kNegInf : (top - C::kBias + log2f(tot)) * kLn2;
         }
+        // One row tile: the query tiles' room has been read.  A stream without
+        // tiles must not run an item ahead of the MMA warp's wait for its queries.
+        if (!sr.pair || n1 == 0 || n0 == 0) named_bar(kBarAll, kSoft);
+        if (tid == 0) note_split(a, it, sr.rows, kMT, sh.plan);
     }
 }
 
@@ -675,10 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
                                                                 const __grid_constant__ KvMaps maps) {
     using C = Cfg<D, E4M3>;
     static_assert(C::kMerge == 2 * C::kQBytes, "stream 1's sums fit the two query tiles");
-    extern __shared__ uint8_t dyn[];
-    __shared__ Shared sh;
-    uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    uint8_t* qs = dyn;
     uint8_t* ring = qs + 2 * C::kQBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(dyn + C::kSmem);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -702,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     tc_fence_before();
     pdl_wait();
     pdl_launch_dependents();
-    plan_work<kMT, kKT>(a, 2, sh.warp_sum, &sh.plan);            // (its barriers publish sh.tmem)
+    plan_work<kMT, kKT>(a, 2, reinterpret_cast<int64_t*>(sh.ml), &sh.plan);   // (its barriers publish sh.tmem)
     tc_fence_after();
     zero_pad_rows(a);
     if (warp < 8) {
@@ -723,13 +802,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
 
 template <int D, bool E4M3>
 cudaError_t launch(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s) {
-    using C = Cfg<D, E4M3>;
-    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(attn_tile_kernel<D, E4M3>),
-                                    static_cast<int>(C::kSmem));
+    constexpr size_t smem = Cfg<D, E4M3>::kSmem + sizeof(Shared);
+    static_assert(smem <= 232448, "227 KB a CTA");
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(attn_tile_kernel<D, E4M3>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int grid = n_sms < kAttnMaxCtas ? n_sms : kAttnMaxCtas;
-    e = launch_pdl(attn_tile_kernel<D, E4M3>, dim3(grid), dim3(kThreads), C::kSmem, s, a, m);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    e = launch_pdl(attn_tile_kernel<D, E4M3>, dim3(grid), dim3(kThreads), smem, s, a, m);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_attn_join(a, kMT, grid, s);
 }
 
 }  // namespace

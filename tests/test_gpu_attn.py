@@ -25,15 +25,15 @@ def _built():
 
 def attend(p, causal=True, window=0, draft=None, stream=None):
     attn = m.Attn(p.hq, p.scale, causal, window)
-    ws = torch.zeros(m.moe_attn_workspace_bytes(attn, p.cache), dtype=torch.uint8, device="cuda")
+    # beyond its error word a workspace may hold anything
+    ws = torch.full((m.moe_attn_workspace_bytes(attn, p.cache),), 255, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
     out = torch.full((p.t, p.hq, p.dim), float("nan"), dtype=torch.bfloat16, device="cuda")
     lse = torch.full((p.t, p.hq), float("nan"), device="cuda")
     d = None if draft is None else draft.cuda()
     m.moe_paged_attention(attn, p.cache, p.seqs, p.d_q(), out, ws, lse=lse, draft_mask=d, stream=stream)
     torch.cuda.synchronize()
     assert m.moe_get_device_error(ws) == 0
-    # the counters are back at zero: the workspace serves the next call as it is
-    assert int(ws[256:1024].sum()) == 0
     return out, lse, ws
 
 
