@@ -508,42 +508,67 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
 // order.  A kernel of its own, not the work of the piece that comes last: that
 // CTA alone would read a verify block's 19 pieces of 64 rows (630 KB) at one
 // SM's rate, here every SM reads some.
-constexpr int kJoinRows = 8;
+// Four threads share four columns of a row, each a quarter of the pieces, so
+// that all of them are in flight at once.
+constexpr int kJoinRows = 8, kJoinParts = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinRows* D / 4) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel(const AttnArgs a) {
+    constexpr int64_t kSlot = kAttnSlotRows * (D + 2);
+    constexpr int kCells = kJoinRows * D / 4;                                  // threads of a part
+    __shared__ float4 s_v[kJoinParts][kCells];
+    __shared__ float s_sum[kJoinParts][kJoinRows];
     pdl_wait();
     pdl_launch_dependents();
     const SplitNote n = a.notes[blockIdx.x];
     if (n.pieces == 0) return;
-    const int d4 = threadIdx.x / kJoinRows;
-    constexpr int64_t kSlot = kAttnSlotRows * (D + 2);
-    const float* p0 = a.partials + (2 * int64_t(blockIdx.x) + 1) * kSlot;     // the first piece,
-    const float* p1 = a.partials + 2 * (int64_t(blockIdx.x) + 1) * kSlot;     // then every second slot
-    for (int row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows; row < n.rows; row += gridDim.y * kJoinRows) {
+    const int cell = threadIdx.x % kCells, part = threadIdx.x / kCells;
+    const int rl = cell % kJoinRows, d4 = cell / kJoinRows;
+    const float* p0 = a.partials + (2 * int64_t(blockIdx.x) + 1) * kSlot;     // the first piece, then
+    for (int row0 = blockIdx.y * kJoinRows; row0 < n.rows; row0 += gridDim.y * kJoinRows) {
+        const int row = min(row0 + rl, n.rows - 1);
         const int ml = kAttnSlotRows * D + 2 * row, od = (d4 * kAttnSlotRows + row) * 4;
-        float top = kNegInf, sum = 0.0f;
+        auto piece = [&](int k) { return p0 + (k == 0 ? 0 : (2 * k - 1) * kSlot); };   // every second slot
+        float top = kNegInf;
+#pragma unroll 8
+        for (int k = 0; k < n.pieces; ++k) top = fmaxf(top, piece(k)[ml]);
+        const float ref = top == kNegInf ? 0.0f : top;
+        float sum = 0.0f;
         float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll 8
-        for (int k = 0; k < n.pieces; ++k) {
-            const float* p = k == 0 ? p0 : p1 + 2 * (k - 1) * kSlot;
-            const float2 x = *reinterpret_cast<const float2*>(p + ml);
-            const float4 y = *reinterpret_cast<const float4*>(p + od);
-            if (x.x == kNegInf) continue;
-            const float nt = fmaxf(top, x.x), f = top == kNegInf ? 0.0f : fast_exp2(top - nt), w = fast_exp2(x.x - nt);
-            top = nt;
-            sum = sum * f + x.y * w;
-            v.x = v.x * f + y.x * w;
-            v.y = v.y * f + y.y * w;
-            v.z = v.z * f + y.z * w;
-            v.w = v.w * f + y.w * w;
+        for (int k = part; k < n.pieces; k += kJoinParts) {
+            const float2 x = *reinterpret_cast<const float2*>(piece(k) + ml);
+            const float4 y = *reinterpret_cast<const float4*>(piece(k) + od);
+            const float w = fast_exp2(x.x - ref);
+            sum += x.y * w;
+            v.x += y.x * w;
+            v.y += y.y * w;
+            v.z += y.z * w;
+            v.w += y.w * w;
         }
-        const int r = n.row0 + row, i = r / a.group, hd = n.head * a.group + r - i * a.group;
-        const int64_t at = int64_t(n.q0 + i) * a.q_heads + hd;
-        const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
-        *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
-            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-        if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
+        s_v[part][cell] = v;
+        if (d4 == 0) s_sum[part][rl] = sum;
+        __syncthreads();
+        if (part == 0 && row0 + rl < n.rows) {
+            sum = 0.0f;
+            v = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int p = 0; p < kJoinParts; ++p) {
+                const float4 y = s_v[p][cell];
+                sum += s_sum[p][rl];
+                v.x += y.x;
+                v.y += y.y;
+                v.z += y.z;
+                v.w += y.w;
+            }
+            const int r = n.row0 + row, i = r / a.group, hd = n.head * a.group + r - i * a.group;
+            const int64_t at = int64_t(n.q0 + i) * a.q_heads + hd;
+            const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
+            *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
+                make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+            if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
+        }
+        __syncthreads();
     }
 }
 
@@ -553,8 +578,8 @@ cudaError_t launch_attn_join(const AttnArgs& a, int rows, int grid, cudaStream_t
     const int most = a.max_rows < rows ? a.max_rows : rows;     // rows of an item
     const dim3 g(grid, (most + kJoinRows - 1) / kJoinRows);
     const cudaError_t e = a.kv.dim == 128
-                              ? launch_pdl(attn_join_kernel<128>, g, dim3(kJoinRows * 32), 0, s, a)
-                              : launch_pdl(attn_join_kernel<64>, g, dim3(kJoinRows * 16), 0, s, a);
+                              ? launch_pdl(attn_join_kernel<128>, g, dim3(kJoinRows * kJoinParts * 32), 0, s, a)
+                              : launch_pdl(attn_join_kernel<64>, g, dim3(kJoinRows * kJoinParts * 16), 0, s, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -66,6 +66,20 @@ __device__ __forceinline__ bool row_sees(const RowView& r, bool draft, int first
     return ok;
 }
 
+// row_sees() of the 32 keys from k0 on, key k0 + e at bit e.
+__device__ __forceinline__ uint32_t row_bits(const RowView& r, bool draft, int first, int k0) {
+    const int lo = min(max(r.lo - k0, 0), 32), hi = min(max(r.hi - k0, 0), 32);
+    uint32_t bits = lo >= hi ? 0u : (0xFFFFFFFFu << lo) & (0xFFFFFFFFu >> (32 - hi));
+    if (draft) {
+        const int d = first - k0;                 // bit of the first new key
+        if (d <= 0)
+            bits &= -d >= 64 ? 0u : static_cast<uint32_t>(r.draft >> -d);
+        else if (d < 32)
+            bits &= static_cast<uint32_t>(r.draft << d) | ((1u << d) - 1u);
+    }
+    return bits;
+}
+
 // Keys that some row of the rows i0 .. i1 of a sequence can see, as a range.
 __device__ __forceinline__ int2 rows_range(const AttnArgs& a, const Seq& s, int i0, int i1) {
     int hi = s.len;
@@ -259,19 +273,27 @@ struct Work {
         }
         return u;
     }
-    // CTA c of C takes units [c*W/C, (c+1)*W/C)
-    __device__ __forceinline__ static int64_t begin(int c, int C, int64_t W) { return c * W / C; }
-    __device__ __forceinline__ static int owner(int64_t u, int C, int64_t W) {
-        return static_cast<int>(((u + 1) * C - 1) / W);
-    }
 };
 
-// What a CTA knows of the call's split once plan_work() has run.
+// a / b for 0 <= a, 0 < b, by the 32-bit division where that does.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// What a CTA knows of the call's split once plan_work() has run: CTA c of
+// `ctas` takes `share` units, the first `extra` CTAs one more.
 struct Plan {
-    int64_t total, u0, u1;
+    int64_t u0, u1;        // this CTA's units
+    int64_t share, extra;
+    int64_t off;           // unit u0 lies `off` units into row tile rt of head h of sequence b
+    int b, h, rt;
     int ctas;              // CTAs that take part
-    int b;                 // sequence of unit u0, and the unit's offset in it
-    int64_t off;
+
+    __device__ __forceinline__ int owner(int64_t u) const {
+        const int64_t head = extra * (share + 1);
+        return static_cast<int>(u < head ? div64(u, share + 1) : extra + div64(u - head, share));
+    }
 };
 
 // All threads of the block.  s_warp: one int64 per warp, s_plan: shared.
@@ -282,9 +304,12 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int6
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
     const int per = (a.sq.n + nt - 1) / nt;
     const int b0 = min(a.sq.n, tid * per), b1 = min(a.sq.n, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += a.kv.heads * W::head_units(a, load_seq(a.sq, a.kv.page, b, a.err));
+    int64_t mine = 0, head = 0;                // units of the thread's sequences, of a head of the last one
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        head = W::head_units(a, load_seq(a.sq, a.kv.page, b, a.err));
+        mine += a.kv.heads * head;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -299,31 +324,48 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int6
         before += w < wid ? v : 0;
         total += v;
     }
-    const int64_t want = (total + min_units - 1) / min_units;
+    const int64_t want = div64(total + min_units - 1, min_units);
     const int C = static_cast<int>(want < int64_t(gridDim.x) ? (want > 0 ? want : 1) : gridDim.x);
     const int c = blockIdx.x;
-    const int64_t u0 = c < C ? W::begin(c, C, total) : total;
-    const int64_t u1 = c < C ? W::begin(c + 1, C, total) : total;
+    const int64_t share = div64(total, C), extra = total - share * C;
+    const int64_t u0 = c < C ? c * share + min(int64_t(c), extra) : total;
+    const int64_t u1 = c < C ? u0 + share + (c < extra ? 1 : 0) : total;
     if (tid == 0) {
-        s_plan->total = total;
         s_plan->u0 = u0;
         s_plan->u1 = u1;
+        s_plan->share = share;
+        s_plan->extra = extra;
         s_plan->ctas = C;
         a.notes[c].pieces = 0;
     }
     const int64_t pre = before + incl - mine;
     if (u0 < u1 && pre <= u0 && u0 < pre + mine) {
-        int64_t at = pre;
-        for (int b = b0; b < b1; ++b) {
-            const int64_t n =
-                a.kv.heads * W::head_units(a, load_seq(a.sq, a.kv.page, b, nullptr));
-            if (u0 < at + n) {
-                s_plan->b = b;
-                s_plan->off = u0 - at;
-                break;
+        int64_t off = u0 - pre;
+        int b = b0;
+        Seq s = load_seq(a.sq, a.kv.page, b, nullptr);
+        if (per > 1) {
+#pragma unroll 1
+            for (;;) {
+                head = W::head_units(a, s);
+                if (off < a.kv.heads * head) break;
+                off -= a.kv.heads * head;
+                s = load_seq(a.sq, a.kv.page, ++b, nullptr);
             }
-            at += n;
         }
+        const int h = static_cast<int>(div64(off, head));
+        off -= h * head;
+        int rt = 0;
+#pragma unroll 1
+        for (;; ++rt) {
+            int lo, hi, t0, n;
+            W::extent(a, s, rt, lo, hi, t0, n);
+            if (off < n) break;
+            off -= n;
+        }
+        s_plan->b = b;
+        s_plan->h = h;
+        s_plan->rt = rt;
+        s_plan->off = off;
     }
     __syncthreads();
 }
@@ -343,17 +385,11 @@ struct Walk {
         off = 0;
         if (left <= 0) return;
         b = p.b;
+        h = p.h;
+        rt = p.rt;
+        off = p.off;
         s = load_seq(a.sq, a.kv.page, b, nullptr);
         rts = W::row_tiles(a, s);
-        const int64_t per = W::head_units(a, s);
-        h = static_cast<int>(p.off / per);
-        off = p.off - h * per;
-        for (;; ++rt) {
-            int lo, hi, t0, n;
-            W::extent(a, s, rt, lo, hi, t0, n);
-            if (off < n) break;
-            off -= n;
-        }
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, Item& it) {
         if (left <= 0) return false;
@@ -387,7 +423,7 @@ __device__ __forceinline__ void note_split(const AttnArgs& a, const Item& it, in
     if (it.t0 != 0 || it.t1 >= it.n) return;
     // the last item of the CTA's run, so its note is not written over
     SplitNote n;
-    n.pieces = static_cast<int>(((it.u + it.n) * p.ctas - 1) / p.total) - static_cast<int>(blockIdx.x) + 1;
+    n.pieces = p.owner(it.u + it.n - 1) - static_cast<int>(blockIdx.x) + 1;
     n.rows = rows;
     n.row0 = it.rt * mt;
     n.q0 = it.s.q0;

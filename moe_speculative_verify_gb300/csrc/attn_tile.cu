@@ -35,7 +35,7 @@ constexpr int kThreads = 384;            // 2 softmax warpgroups; TMA warp, MMA 
 // 8 * 208 + 4 * 80 = 1984 a lane column of the 12 * 168 = 2016 launched.
 constexpr int kRegsSoft = 208, kRegsRest = 80;
 constexpr int kSoft = 256;
-constexpr int kBarAll = 1;               // named barriers: both warpgroups
+constexpr int kBarAll = 1, kBarGroup = 2;   // named barriers: both warpgroups, each of them
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;          // S/P of stream s at column 128 s, O at 256 + 128 s
 
@@ -129,7 +129,6 @@ struct Share {
             }
         }
     }
-    __device__ __forceinline__ bool on(int s, int j) const { return j >= a[s] && j < b[s]; }
     // tiles of stream s, and its n-th
     __device__ __forceinline__ int count(int s) const {
         return pair ? (s ? b[1] - a[1] : b[0] - a[0]) : (tiles + 1 - s) / 2;
@@ -137,37 +136,45 @@ struct Share {
     __device__ __forceinline__ int tile(int s, int n) const { return pair ? (s ? a[1] : a[0]) + n : 2 * n + s; }
 };
 
-// A warp's place in the CTA's work, kept in shared memory so that it takes no
-// registers from the loops over the tiles.
+// A role's place in the CTA's work (a softmax warpgroup's, the TMA warp's, the
+// MMA warp's), kept in shared memory so that it takes no registers from the
+// loops over the tiles.  THREADS threads share it, at named barrier `bar`.
 struct Ctx {
     Walk<kMT, kKT> wk;
     Item it;
     Share sr;
+    int more;
 
-    __device__ __forceinline__ void start(const AttnArgs& a, const Plan& p) {
-        if ((threadIdx.x & 31) == 0) wk.start(a, p);
-        __syncwarp();
+    template <int THREADS>
+    __device__ __forceinline__ void sync(int bar) {
+        if constexpr (THREADS == 32)
+            __syncwarp();
+        else
+            named_bar(bar, THREADS);
     }
-    __device__ __forceinline__ bool next(const AttnArgs& a) {
-        __syncwarp();
-        int more = 0;
-        if ((threadIdx.x & 31) == 0) {
+    template <int THREADS>
+    __device__ __forceinline__ void start(const AttnArgs& a, const Plan& p) {
+        if (threadIdx.x % THREADS == 0) wk.start(a, p);
+    }
+    template <int THREADS>
+    __device__ __forceinline__ bool next(const AttnArgs& a, int bar = 0) {
+        sync<THREADS>(bar);
+        if (threadIdx.x % THREADS == 0) {
             more = wk.next(a, it);
             if (more) sr.set(a, it);
         }
-        more = __shfl_sync(0xFFFFFFFFu, more, 0);
-        __syncwarp();
+        sync<THREADS>(bar);
         return more != 0;
     }
 };
 
 struct Shared {
-    alignas(16) float2 ml[128];             // a lane's reference and sum, between the streams
+    alignas(16) float2 ml[2][128];          // a lane's reference and sum, among a row's sharers
     uint64_t kv_full[10];
     uint64_t kv_empty[10];
     uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2];
     Plan plan;
-    Ctx ctx[10];                            // the softmax warps', the TMA warp's, the MMA warp's
+    Ctx ctx[4];                             // the softmax warpgroups', the TMA warp's, the MMA warp's
     uint32_t tmem;
 };
 
@@ -178,25 +185,27 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
     constexpr int kBoxBytes = E4M3 ? D : 128;
     const int lane = threadIdx.x & 31;
     const int page = a.kv.page, pl = a.kv.page_log2;
-    Ctx& ctx = sh.ctx[8];
-    ctx.start(a, sh.plan);
-    int run = 0;
+    Ctx& ctx = sh.ctx[2];
+    ctx.start<32>(a, sh.plan);
+    int st = -1;
+    uint32_t ph = 1;
     bool dead = false;
-    while (ctx.next(a)) {
+    while (ctx.next<32>(a)) {
         const Item& it = ctx.it;
         const Share& sr = ctx.sr;
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
-        const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl;
         const int ahead = sr.pair ? 1 : 2;
         int base = -1, entry = 0;
         // K of `ahead` tiles, then V of a tile and K of the tile `ahead` of it in turn
-        for (int op = 0; op < 2 * sr.tiles; ++op, ++run) {
+        const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl, head = it.h, tile0 = it.tile0 + it.t0;
+        for (int op = 0; op < 2 * sr.tiles; ++op) {
             const int first = min(ahead, sr.tiles);
             const int x = op - first, mid = 2 * (sr.tiles - first);
             const bool is_v = op >= first && (x >= mid || (x & 1) == 0);
             const int j = op < first ? op : (x >= mid ? sr.tiles - first + (x - mid) : (is_v ? x >> 1 : (x >> 1) + first));
-            const int st = run % C::kStages, ph = (run / C::kStages) & 1;
-            const int p0 = ((it.tile0 + it.t0 + j) * kKT) >> pl, np = kKT >> pl;
+            if (++st == C::kStages) st = 0;
+            if (st == 0) ph ^= 1;
+            const int p0 = ((tile0 + j) * kKT) >> pl, np = kKT >> pl;
             if (base < 0 || p0 + np > base + 32 || p0 < base) {
                 base = is_v ? p0 : max(p0 - ahead * np, 0);      // the V tiles still to come too
                 const int p = base + lane;
@@ -220,14 +229,24 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
 #pragma unroll
                     for (int x2 = 0; x2 < D / kBox; ++x2)
                         tma_load_4d(dst + (p - p0) * page * kBoxBytes + x2 * kKT * 128, map, &sh.kv_full[st],
-                                    x2 * kBox, 0, it.h, pg);
+                                    x2 * kBox, 0, head, pg);
                 }
             }
         }
     }
 }
 
-// The MMA warp: lane 0 issues, the whole warp waits.
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
+// The MMA warp: one thread issues, the whole warp waits.  Its issue rate
+// paces the kernel, so descriptors are a constant plus the stage's offset (the
+// 14-bit address field cannot carry: shared memory lies below 256 KB) and the
+// stage is counted, not divided out.
 template <int D, bool E4M3>
 __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t* qs, uint8_t* ring) {
     using C = Cfg<D, E4M3>;
@@ -235,300 +254,318 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
     constexpr uint32_t kIdPV = E4M3 ? idesc(0, 0, true, D) : idesc(1, 1, true, D);
     constexpr uint32_t kIdPVlow = idesc(1, 0, true, D);          // e5m2 x e4m3
     constexpr bool kNarrow = E4M3 && D == 64;                    // 64-byte cached rows
+    constexpr uint32_t kSbo = kNarrow ? 512 : 1024, kSw = kNarrow ? kSw64 : kSw128;
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = sh.tmem;
-    Ctx& ctx = sh.ctx[9];
-    ctx.start(a, sh.plan);
+    const uint64_t q_desc = sdesc(smem_u32(qs), 16, 1024, kSw128);
+    const uint64_t k_desc = sdesc(smem_u32(ring), 16, kSbo, kSw), v_desc = sdesc(smem_u32(ring), 16384, kSbo, kSw);
+    Ctx& ctx = sh.ctx[3];
+    ctx.start<32>(a, sh.plan);
     const Item& it = ctx.it;
     const Share& sr = ctx.sr;
-    int run = 0, items = 0;
-    uint32_t pp[2] = {0, 0};                                     // p_ready phases
+    uint32_t items = 0, pp[2] = {0, 0};                          // phases of q_ready, p_ready
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
         tc_fence_after();
     };
-    auto wait_kv = [&](int r) { wait(&sh.kv_full[r % C::kStages], (r / C::kStages) & 1); };
-    auto qk = [&](int s, int r) {
-        if (lane == 0 && !dead) {
-            const uint32_t q0 = smem_u32(qs + s * C::kQBytes), k0 = smem_u32(ring + (r % C::kStages) * C::kTileBytes);
-            const uint32_t d = tmem + 128 * s;
+    struct Slot {
+        uint32_t st, ph;
+        __device__ __forceinline__ Slot next() const {
+            return st + 1 == C::kStages ? Slot{0, ph ^ 1} : Slot{st + 1, ph};
+        }
+    };
+    Slot at{0, 0};                                               // next ring stage
+    auto wait_kv = [&](Slot r) { wait(&sh.kv_full[r.st], r.ph); };
+    auto qk = [&](int s, Slot r) {
+        const uint64_t qd = q_desc + s * (C::kQBytes >> 4), kd = k_desc + r.st * (C::kTileBytes >> 4);
+        const uint32_t d = tmem + 128 * s;
+        if (elect_one()) {
             if constexpr (!E4M3) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                    mma_ss<false>(d, sdesc(q0 + off, 16, 1024, kSw128), sdesc(k0 + off, 16, 1024, kSw128), kIdQK, k > 0);
+                    const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                    mma_ss<false>(d, qd + off, kd + off, kIdQK, k > 0);
                 }
             } else {
                 constexpr int kSteps = D / 32;
 #pragma unroll
-                for (int k = 0; k < 2 * kSteps; ++k) {           // high codes, then low
-                    const uint32_t qo = D == 128 ? (k / kSteps) * 16384 + (k % kSteps) * 32 : k * 32;
-                    mma_ss<true>(d, sdesc(q0 + qo, 16, 1024, kSw128),
-                                 sdesc(k0 + (k % kSteps) * 32, 16, kNarrow ? 512 : 1024, kNarrow ? kSw64 : kSw128),
-                                 kIdQK, k > 0);
-                }
+                for (int k = 0; k < 2 * kSteps; ++k)             // high codes, then low
+                    mma_ss<true>(d, qd + ((D == 128 ? (k / kSteps) * 16384 + (k % kSteps) * 32 : k * 32) >> 4),
+                                 kd + ((k % kSteps) * 32 >> 4), kIdQK, k > 0);
             }
             mma_commit(&sh.s_full[s]);
         }
         __syncwarp();
     };
-    auto pv = [&](int s, int r, bool first) {
-        if (lane == 0 && !dead) {
-            const uint32_t v0 = smem_u32(ring + (r % C::kStages) * C::kTileBytes);
-            const uint32_t d = tmem + kColO + 128 * s, p0 = tmem + 128 * s;
+    auto pv = [&](int s, Slot r, bool first) {
+        const uint64_t vd = v_desc + r.st * (C::kTileBytes >> 4);
+        const uint32_t d = tmem + kColO + 128 * s, p0 = tmem + 128 * s;
+        const uint32_t acc = first ? 0u : 1u;
+        if (elect_one()) {
             if constexpr (!E4M3) {
 #pragma unroll
                 for (int k = 0; k < kKT / 16; ++k)
-                    mma_ts<false>(d, p0 + 8 * k, sdesc(v0 + k * 2048, 16384, 1024, kSw128), kIdPV, !first || k > 0);
+                    mma_ts<false>(d, p0 + 8 * k, vd + (k * 2048 >> 4), kIdPV, k > 0 ? 1u : acc);
             } else {
 #pragma unroll
-                for (int k = 0; k < kKT / 16; ++k) {
-                    const uint32_t vo = (k & 3) * 32 * C::kRowBytes;
-                    mma_ts<true>(d, p0 + 8 * k, sdesc(v0 + vo, 16384, kNarrow ? 512 : 1024, kNarrow ? kSw64 : kSw128),
-                                 k < 4 ? kIdPV : kIdPVlow, !first || k > 0);
-                }
+                for (int k = 0; k < kKT / 16; ++k)
+                    mma_ts<true>(d, p0 + 16 * (k & 3) + 8 * (k >> 2), vd + ((k & 3) * 32 * C::kRowBytes >> 4),
+                                 k < 4 ? kIdPV : kIdPVlow, k > 0 ? 1u : acc);
             }
         }
         __syncwarp();
     };
     auto commit = [&](uint64_t* bar) {
-        if (lane == 0 && !dead) mma_commit(bar);
+        if (elect_one()) mma_commit(bar);
         __syncwarp();
     };
-    // V rows of keys that no row of the item sees may hold anything: zero them
-    auto clean = [&](int r, int j) {
-        const int j0 = (it.tile0 + it.t0 + j) * kKT;
-        if (j0 >= it.lo && j0 + kKT <= it.hi) return;
-        uint8_t* v = ring + (r % C::kStages) * C::kTileBytes;
-        constexpr int kChunks = (E4M3 ? D : 128) / 16, kSub = E4M3 ? 1 : D / 64;
-        for (int e = lane; e < kKT * kChunks; e += 32) {
-            const int row = e / kChunks, key = j0 + row;
-            if (key >= it.lo && key < it.hi) continue;
-#pragma unroll
-            for (int x = 0; x < kSub; ++x)
-                *reinterpret_cast<uint4*>(v + x * kKT * 128 + e * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_smem();
-        __syncwarp();
-    };
-    while (ctx.next(a)) {
+    auto empty = [&](Slot r) { commit(&sh.kv_empty[r.st]); };
+    while (ctx.next<32>(a)) {
         const int T = sr.tiles;
         if (T == 0) continue;
         wait(&sh.q_ready[0], items & 1);
         wait(&sh.q_ready[1], items & 1);
         ++items;
-        auto empty = [&](int r) { commit(&sh.kv_empty[r % C::kStages]); };
+        // V rows of keys that no row of the item sees may hold anything: zero them
+        const int lo = it.lo - (it.tile0 + it.t0) * kKT, hi = it.hi - (it.tile0 + it.t0) * kKT;
+        auto clean = [&](Slot r, int j) {
+            if (j * kKT >= lo && j * kKT + kKT <= hi) return;
+            uint8_t* v = ring + r.st * C::kTileBytes;
+            constexpr int kPitch = E4M3 ? D : 128, kSub = E4M3 ? 1 : D / 64;      // a row's bytes in each part
+            const int head = min(max(lo - j * kKT, 0), kKT) * kPitch, tail = min(max(hi - j * kKT, 0), kKT) * kPitch;
+#pragma unroll
+            for (int x = 0; x < kSub; ++x) {
+                uint8_t* part = v + x * kKT * 128;
+                for (int e = 16 * lane; e < head; e += 512) *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
+                for (int e = tail + 16 * lane; e < kKT * kPitch; e += 512)
+                    *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+        };
         if (sr.pair) {
-            wait_kv(run);
+            const int a0 = sr.a[0], b0 = sr.b[0], a1 = sr.a[1], b1 = sr.b[1];
+            auto on = [&](int s, int j) { return s ? j >= a1 && j < b1 : j >= a0 && j < b0; };
+            wait_kv(at);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                if (sr.on(s, 0)) qk(s, run);
-            empty(run);
+                if (on(s, 0)) qk(s, at);
+            empty(at);
+            at = at.next();
             for (int j = 0; j < T; ++j) {
-                const int rv = run + 1 + 2 * j, rk = rv + 1;
+                const Slot rv = at, rk = at.next();
                 const bool more = j + 1 < T;
                 wait_kv(rv);
                 clean(rv, j);
                 if (more) wait_kv(rk);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    if (sr.on(s, j)) {
+                    if (on(s, j)) {
                         wait(&sh.p_ready[s], pp[s]);
                         pp[s] ^= 1;
-                        pv(s, rv, j == sr.a[s]);
-                        if (j + 1 == sr.b[s]) commit(&sh.o_full[s]);
+                        pv(s, rv, j == (s ? a1 : a0));
+                        if (j + 1 == (s ? b1 : b0)) commit(&sh.o_full[s]);
                     }
                     if (s == 1) empty(rv);
-                    if (more && sr.on(s, j + 1)) qk(s, rk);
+                    if (more && on(s, j + 1)) qk(s, rk);
                 }
-                if (more) empty(rk);
+                at = rk;
+                if (more) {
+                    empty(rk);
+                    at = rk.next();
+                }
             }
         } else {
             // ring order: K0 K1, then V(j), K(j+2) while there is one, then the V left
-            const int first = min(2, T);
-            for (int s = 0; s < first; ++s) {
-                wait_kv(run + s);
-                qk(s, run + s);
-                empty(run + s);
+            for (int s = 0; s < min(2, T); ++s) {
+                wait_kv(at);
+                qk(s, at);
+                empty(at);
+                at = at.next();
             }
-            int r = run + first;
             for (int j = 0; j < T; ++j) {
                 const int s = j & 1;
-                const int rv = r++;
-                wait_kv(rv);
-                clean(rv, j);
-                wait(&sh.p_ready[s], pp[s]);
-                pp[s] ^= 1;
-                pv(s, rv, j < 2);
-                empty(rv);
+                wait_kv(at);
+                clean(at, j);
+                wait(&sh.p_ready[s], s ? pp[1] : pp[0]);
+                if (s)
+                    pp[1] ^= 1;
+                else
+                    pp[0] ^= 1;
+                pv(s, at, j < 2);
+                empty(at);
+                at = at.next();
                 if (j + 2 < T) {
-                    const int rk = r++;
-                    wait_kv(rk);
-                    qk(s, rk);
-                    empty(rk);
+                    wait_kv(at);
+                    qk(s, at);
+                    empty(at);
+                    at = at.next();
                 } else {
                     commit(&sh.o_full[s]);
                 }
             }
         }
-        run += 2 * T;
     }
 }
 
-// N 32-bit columns (8, 16 or 32) of this thread's TMEM lane.
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
-    if constexpr (N == 32) {
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-            "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-            "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-            "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-            "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-            : "memory");
-    } else if constexpr (N == 16) {
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-            "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-            : "memory");
-    } else {
-        static_assert(N == 8, "8, 16 or 32 columns");
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                     : "memory");
-    }
+// 16 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 
 // What a softmax thread carries through an item: its row's reference (log2
-// units) and sum of powers.
+// units) and sum of powers, in two parts.
 struct RowState {
     float ref, sum0, sum1;
 };
 
-// One key tile of a softmax thread: keys kFirst .. of the tile's 128 are its
-// copy's (W = 128 / NC of them, from W * copy on).  Reads S, writes P over it.
-template <int D, bool E4M3, int NC>
-__device__ __forceinline__ void soft_tile(uint32_t colS, uint32_t colO, int copy, float c, int i, int j0, bool whole,
-                                          bool draft, const RowView& view, int first, RowState& st) {
-    using C = Cfg<D, E4M3>;
-    constexpr int W = 128 / NC, Q = W / 32;
-    float x[Q][32];
+__device__ __forceinline__ float max32(const float (&x)[32]) {
+    float t[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-    for (int q = 0; q < Q; ++q) tmem_ld32(colS + W * copy + 32 * q, x[q]);
-    tmem_wait_ld();
-    if (!whole) {
-        const int k0 = j0 + W * copy, lo = view.lo - k0, hi = view.hi - k0;
-        if (!draft) {
+    for (int e = 0; e < 32; e += 8)
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (32 * q + e < lo || 32 * q + e >= hi) x[q][e] = kNegInf;
-        } else {
-#pragma unroll
-            for (int q = 0; q < Q; ++q)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!row_sees(view, true, first, k0 + 32 * q + e)) x[q][e] = kNegInf;
-        }
-    }
-    float t4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], fmaxf(x[q][e + 2 * k], x[q][e + 2 * k + 1]));
-    float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
+        for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], fmaxf(x[e + 2 * k], x[e + 2 * k + 1]));
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// Takes a tile's maximum into the reference: the reference follows when it
+// lags by more than kLag, and O in tensor memory with it (its products are
+// complete: S came after them in the MMA thread's order).
+template <int D, bool E4M3>
+__device__ __forceinline__ void follow(uint32_t colO, float top, bool started, RowState& st) {
     if (!(top > kNegInf)) top = kNegInf;                         // (NaN: the sums carry it)
-    const bool grow = top > st.ref + C::kLag || (st.ref == kNegInf && top > kNegInf);
-    if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+    const bool grow = top > st.ref + Cfg<D, E4M3>::kLag || (st.ref == kNegInf && top > kNegInf);
+    if (started && __any_sync(0xFFFFFFFFu, grow)) {
         const float f = !grow ? 1.0f : (st.ref == kNegInf ? 0.0f : fast_exp2(st.ref - top));
         st.sum0 *= f;
         st.sum1 *= f;
-        for (int q = 0; q < D / 8; ++q) {
-            float o[8];
-            tmem_ld8(colO + 8 * q, o);
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+            float o[16];
+            tmem_ld16(colO + 16 * q, o);
             tmem_wait_ld();
-            uint32_t u[8];
+            uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
-            tmem_st<8>(colO + 8 * q, u);
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+            tmem_st16(colO + 16 * q, u);
         }
     }
     if (grow) st.ref = top;
-    const float off = C::kBias - (st.ref == kNegInf ? 0.0f : st.ref);
-    // powers: summed in fp32, then rounded
+}
+
+// 32 scores to powers: summed in fp32, rounded, stored as P of their keys: 16
+// columns, bf16 pairs, or 8 of e4m3 codes and 8 of e5m2 codes of what they leave.
+template <int D, bool E4M3>
+__device__ __forceinline__ void powers(uint32_t colP, const float (&x)[32], float c, float off, RowState& st) {
+    uint32_t u[16];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        uint32_t u[16];
+    for (int e = 0; e < 32; e += 4) {
+        float p[4];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            float p[4];
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-                fma2_to(p[k], p[k + 1], x[q][e + k], x[q][e + k + 1], c, off);
-                p[k] = fast_exp2(p[k]);
-                p[k + 1] = fast_exp2(p[k + 1]);
-                add2(st.sum0, st.sum1, p[k], p[k + 1]);
-            }
-            if constexpr (!E4M3) {
-                u[e / 2] = pack_bf16(p[0], p[1]);
-                u[e / 2 + 1] = pack_bf16(p[2], p[3]);
-            } else {
-                const uint32_t h0 = pack_e4m3(p[0], p[1]), h1 = pack_e4m3(p[2], p[3]);
-                const float2 b0 = unpack_e4m3(h0), b1 = unpack_e4m3(h1);
-                u[e / 4] = h0 | (h1 << 16);
-                u[8 + e / 4] = pack_e5m2(p[0] - b0.x, p[1] - b0.y) | (pack_e5m2(p[2] - b1.x, p[3] - b1.y) << 16);
-            }
+        for (int k = 0; k < 4; k += 2) {
+            fma2_to(p[k], p[k + 1], x[e + k], x[e + k + 1], c, off);
+            p[k] = fast_exp2(p[k]);
+            p[k + 1] = fast_exp2(p[k + 1]);
+            add2(st.sum0, st.sum1, p[k], p[k + 1]);
         }
         if constexpr (!E4M3) {
-            tmem_st<16>(colS + (W / 2) * copy + 16 * q, u);
+            u[e / 2] = pack_bf16(p[0], p[1]);
+            u[e / 2 + 1] = pack_bf16(p[2], p[3]);
         } else {
-            tmem_st<8>(colS + (W / 4) * copy + 8 * q, u);
-            tmem_st<8>(colS + 32 + (W / 4) * copy + 8 * q, u + 8);
+            const uint32_t h0 = pack_e4m3(p[0], p[1]), h1 = pack_e4m3(p[2], p[3]);
+            const float2 b0 = unpack_e4m3(h0), b1 = unpack_e4m3(h1);
+            u[e / 4] = h0 | (h1 << 16);
+            u[8 + e / 4] = pack_e5m2(p[0] - b0.x, p[1] - b0.y) | (pack_e5m2(p[2] - b1.x, p[3] - b1.y) << 16);
         }
     }
-    if constexpr (NC > 1) {                                      // the other copies' keys: zero
-        const uint32_t z[32] = {};
-#pragma unroll
-        for (int o = 1; o < NC; ++o) {
-            const int oc = (copy + o) & (NC - 1);
-            if constexpr (!E4M3) {
-                tmem_st<W / 2>(colS + (W / 2) * oc, z);
-            } else {
-                tmem_st<W / 4>(colS + (W / 4) * oc, z);
-                tmem_st<W / 4>(colS + 32 + (W / 4) * oc, z);
-            }
-        }
-    }
-    tmem_wait_st();
+    tmem_st16(colP, u);
 }
 
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_query(const AttnArgs& a, const uint16_t* src, bool valid, float sign, uint8_t* qt,
-                                           int lr, float& c) {
-    uint4 w[D / 8];
+__device__ __forceinline__ float power_offset(const RowState& st) {
+    return Cfg<D, E4M3>::kBias - (st.ref == kNegInf ? 0.0f : st.ref);
+}
+
+// A key tile that every row sees, all of it this thread's: the long calls'
+// loop, S held in registers.
+template <int D, bool E4M3>
+__device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, float c, bool started, RowState& st) {
+    float x[4][32];
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k)
-        w[k] = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+    for (int q = 0; q < 4; ++q) tmem_ld32(colS + 32 * q, x[q]);
+    tmem_wait_ld();
+    follow<D, E4M3>(colO, fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * c, started, st);
+    const float off = power_offset<D, E4M3>(st);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) powers<D, E4M3>(colS + 16 * q, x[q], c, off, st);
+    tmem_wait_st();
+}
+
+// Any other: `count` pieces of 32 keys from piece `from` on are this copy's,
+// the others' P is zero.  A loop of small code over the pieces, S read twice:
+// a short call runs its code once, from cold instruction caches.
+template <int D, bool E4M3>
+__device__ __forceinline__ void soft_tile_part(uint32_t colS, uint32_t colO, int from, int count, float c, bool started,
+                                               bool whole, const RowView& view, bool draft, int first, int j0,
+                                               RowState& st) {
+    float x[32];
+    auto piece = [&](int q) {
+        tmem_ld32(colS + 32 * q, x);
+        tmem_wait_ld();
+        if (!whole) {
+            const uint32_t bits = row_bits(view, draft, first, j0 + 32 * q);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) x[e] = kNegInf;
+        }
+    };
+    float top = kNegInf;
+#pragma unroll 1
+    for (int q = from; q < from + count; ++q) {
+        piece(q);
+        top = fmaxf(top, max32(x));
+    }
+    follow<D, E4M3>(colO, top * c, started, st);
+    const float off = power_offset<D, E4M3>(st);
+    // P of piece q lies at columns 16 q, in S pieces that have been read
+#pragma unroll 1
+    for (int q = from; q < from + count; ++q) {
+        if (count > 1) piece(q);
+        powers<D, E4M3>(colS + 16 * q, x, c, off, st);
+    }
+    const uint32_t z[16] = {};
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q)
+        if (q < from || q >= from + count) tmem_st16(colS + 16 * q, z);
+    tmem_wait_st();
+}
+
+// A query row into shared memory, K-major with the 128-byte swizzle: bf16 as
+// it is, or (beside e4m3 codes) as high and low e4m3 codes of the row times a
+// power of two, which goes into c.
+template <int D, bool E4M3>
+__device__ __forceinline__ void load_query(const uint16_t* src, bool valid, bool negate, uint8_t* qt, int lr, float& c) {
     uint8_t* base = qt + lr * 128;
     if constexpr (!E4M3) {
-        const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
+#pragma unroll 8
+        for (int k = 0; k < D / 8; ++k) {
+            const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+            const uint32_t flip = negate ? 0x80008000u : 0u;
             *reinterpret_cast<uint4*>(base + (k >> 3) * 16384 + (((k & 7) ^ (lr & 7)) << 4)) =
-                make_uint4(w[k].x ^ flip, w[k].y ^ flip, w[k].z ^ flip, w[k].w ^ flip);
+                make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
+        }
     } else {
         float amax = 0.0f;
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < D / 8; ++k) {
-            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(x[e] & 0xFFFFu)),
@@ -538,25 +575,32 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, const uint16_t* sr
         const float f1 = pow2_norm(amax);
         const float f2 = f1 == 1.0f && !(amax >= 1.0f && amax < 2.0f) ? 1.0f : 128.0f;
         c = amax < INFINITY ? fmaxf(c / f2 / f1, 1.2e-38f) : __int_as_float(0x7FC00000);
-#pragma unroll
+        const float g = negate ? -f2 : f2;
+#pragma unroll 1
         for (int k = 0; k < D / 16; ++k) {                       // 16 elements: a chunk of each code
-            uint32_t hi4[4], lo4[4];
+            uint32_t hi4[4], lo4[4], x[8];
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                const uint4 ww = w[2 * k + (q4 >> 1)];
-                const uint32_t x[2] = {q4 & 1 ? ww.z : ww.x, q4 & 1 ? ww.w : ww.y};
+            for (int v = 0; v < 2; ++v) {
+                const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 16 * k + 8 * v) : make_uint4(0, 0, 0, 0);
+                x[4 * v] = w.x;
+                x[4 * v + 1] = w.y;
+                x[4 * v + 2] = w.z;
+                x[4 * v + 3] = w.w;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
                 uint32_t h = 0, l = 0;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f1 * f2 * sign;
-                    const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f1 * f2 * sign;
+                    const float v0 = bf16_bits_to_f32(x[2 * q + e] & 0xFFFFu) * f1 * g;
+                    const float v1 = __uint_as_float(x[2 * q + e] & 0xFFFF0000u) * f1 * g;
                     const uint32_t hc = pack_e4m3(v0, v1);
                     const float2 b = unpack_e4m3(hc);
                     h |= hc << (16 * e);
                     l |= pack_e4m3(v0 - b.x, v1 - b.y) << (16 * e);
                 }
-                hi4[q4] = h;
-                lo4[q4] = l;
+                hi4[q] = h;
+                lo4[q] = l;
             }
             const int cl = D == 128 ? k : k + 4;
             uint8_t* low = D == 128 ? base + 16384 : base;
@@ -574,8 +618,8 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
     const uint32_t tm_lane = sh.tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t colS = tm_lane + 128 * s, colO = tm_lane + kColO + 128 * s;
     const bool draft = a.draft != nullptr;
-    Ctx& ctx = sh.ctx[tid >> 5];
-    ctx.start(a, sh.plan);
+    Ctx& ctx = sh.ctx[s];
+    ctx.start<128>(a, sh.plan);
     const Item& it = ctx.it;
     const Share& sr = ctx.sr;
     uint32_t sp = 0, op0 = 0, op1 = 0;
@@ -584,7 +628,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
         tc_fence_after();
     };
-    while (ctx.next(a)) {
+    while (ctx.next<128>(a, kBarGroup + s)) {
         // this thread's row, and its copy where the rows repeat
         const int copies = sr.pair || sr.rows > 64 ? 1 : (sr.rows > 32 ? 2 : 4);
         const int span = 128 / copies, copy = lr / span;
@@ -598,8 +642,8 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         {
             const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
             if (valid) view = row_view(a, it.s, qi);
-            load_query<D, E4M3>(a, a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid && a.scale != 0.0f,
-                                a.scale < 0.0f ? -1.0f : 1.0f, qs + s * C::kQBytes, lr, c);
+            load_query<D, E4M3>(a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid, a.scale < 0.0f, qs + s * C::kQBytes,
+                                lr, c);
             __syncwarp();
             if (lane == 0 && sr.tiles > 0) mbar_arrive(&sh.q_ready[s]);
         }
@@ -613,12 +657,11 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
                 sp ^= 1;
                 if (warp_on) {
                     const bool whole = j0 >= wlo && j0 + kKT <= whi;
-                    if (copies == 1)
-                        soft_tile<D, E4M3, 1>(colS, colO, 0, c, i, j0, whole, draft, view, first, st);
-                    else if (copies == 2)
-                        soft_tile<D, E4M3, 2>(colS, colO, copy, c, i, j0, whole, draft, view, first, st);
+                    if (whole && copies == 1)
+                        soft_tile_whole<D, E4M3>(colS, colO, c, i > 0, st);
                     else
-                        soft_tile<D, E4M3, 4>(colS, colO, copy, c, i, j0, whole, draft, view, first, st);
+                        soft_tile_part<D, E4M3>(colS, colO, copy * (span >> 5), span >> 5, c, i > 0, whole, view, draft,
+                                                first, j0, st);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -626,122 +669,127 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
             }
         }
         // --- the item's rows: normalised, or this CTA's piece of them
-        float ref = st.ref, sum = st.sum0 + st.sum1;
+        float ref = st.ref, sum = st.sum0 + st.sum1;             // (lanes of no row: whatever)
         if (sum != sum) ref = fmaxf(ref, 0.0f);                  // a NaN is a result, not an empty row
         const bool piece = it.t0 > 0 || it.t1 < it.n;
-        float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * kAttnSlotRows * (D + 2);
-        const float vs = E4M3 ? a.kv.v_scale[it.h] : 1.0f;
-        float* merge = reinterpret_cast<float*>(qs);
-        auto cell = [&](int r, int d4) {
-            return reinterpret_cast<float4*>(merge + r * D + ((d4 ^ (r & 7)) << 2));
-        };
         const int n0 = sr.count(0), n1 = sr.count(1);
-        const bool other = !sr.pair && n1 > 0;
+        float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * kAttnSlotRows * (D + 2);
+        // What a row's sums are multiplied with here: its weight among the lanes that share the row (the
+        // streams of one row tile, the copies), v_scale and, unless the row goes on elsewhere, 1 / its sum.
+        float weight = ref == kNegInf ? 0.0f : 1.0f, top = ref;
+        const int sharers = sr.pair ? 0 : 2 * copies;
+        if (sharers) {
+            sh.ml[s][lr] = make_float2(ref, sum);
+            named_bar(kBarAll, kSoft);
+            for (int k = 0; k < sharers; ++k) top = fmaxf(top, sh.ml[k & 1][(lr & (span - 1)) + (k >> 1) * span].x);
+            sum = 0.0f;
+            for (int k = 0; k < sharers; ++k) {
+                const float2 x = sh.ml[k & 1][(lr & (span - 1)) + (k >> 1) * span];
+                sum += x.x == kNegInf ? 0.0f : x.y * fast_exp2(x.x - top);
+            }
+            weight = ref == kNegInf ? 0.0f : fast_exp2(ref - top);
+        }
+        weight *= (E4M3 ? a.kv.v_scale[it.h] : 1.0f) * (piece || top == kNegInf ? 1.0f : 1.0f / sum);
+        const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+        const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
+        if (valid && (sr.pair || (s == 0 && copy == 0))) {
+            if (piece)
+                *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(top - C::kBias, sum);
+            else if (a.lse)
+                a.lse[at] = top == kNegInf ? kNegInf : (top - C::kBias + log2f(sum)) * kLn2;
+        }
+        // four columns of a row, finished
+        auto put = [&](int64_t at_, int row_, int d4, const float4& y) {
+            if (piece)
+                *reinterpret_cast<float4*>(slot + (d4 * kAttnSlotRows + row_) * 4) = y;
+            else
+                *reinterpret_cast<uint2*>(a.out + at_ * D + 4 * d4) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+        };
         if (n > 0) wait(&sh.o_full[s], s ? op1 : op0);
-        if (other) {
-            // both streams' products are done: the query tiles make room for stream 1's sums
-            if (s == 1) wait(&sh.o_full[0], op0);
-            if (s == 1 && warp_on) {
-                sh.ml[lr] = make_float2(ref, sum);
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    float o[32];
-                    tmem_ld32(colO + 32 * q, o);
+        if (sr.pair) {
+            if (warp_on) {
+#pragma unroll 1
+                for (int q = 0; q < D / 16; ++q) {
+                    float o[16];
+                    tmem_ld16(colO + 16 * q, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        *cell(lr, 8 * q + e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int e = 0; e < 16; ++e) o[e] = weight != 0.0f && n > 0 ? o[e] * weight : 0.0f;
+                    if (valid) {
+                        if (piece) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                put(at, row, 4 * q + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<uint4*>(a.out + at * D + 16 * q + 8 * e) =
+                                    make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                               pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                        }
+                    }
+                    __syncwarp();
                 }
             }
-            named_bar(kBarAll, kSoft);
-        }
-        if (n0 > 0) op0 ^= 1;
-        if (n1 > 0) op1 ^= 1;
-        const bool spread = copies > 1;
-        if ((sr.pair || s == 0) && warp_on) {
-            float f0 = 1.0f, f1 = 0.0f;
-            if (other) {
-                const float2 ml = sh.ml[lr];
-                const float top = fmaxf(ref, ml.x);
-                f0 = ref == kNegInf ? 0.0f : fast_exp2(ref - top);
-                f1 = ml.x == kNegInf ? 0.0f : fast_exp2(ml.x - top);
-                sum = (f0 == 0.0f ? 0.0f : sum * f0) + (f1 == 0.0f ? 0.0f : ml.y * f1);
-                ref = top;
-            }
-            if (n == 0 || ref == kNegInf) f0 = 0.0f;
-            const float k0 = piece || spread ? vs : (ref == kNegInf ? 0.0f : vs / sum);
-            const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
-            const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
+        } else {
+            // The streams' sums meet in the query tiles' room, once both streams' products are done: each
+            // warpgroup leaves one half of its columns there, then adds the other's half to its own.
+            float* merge = reinterpret_cast<float*>(qs);
+            auto cell = [&](int l, int d4) { return reinterpret_cast<float4*>(merge + l * D + ((d4 ^ (l & 7)) << 2)); };
+            if (s == 0 ? n1 > 0 : n0 > 0) wait(&sh.o_full[s ^ 1], s ? op0 : op1);
+#pragma unroll 1
+            for (int step = 0; step < 2; ++step) {
+                const int c0 = (s ^ step ^ 1) * (D / 2);
+                if (warp_on) {
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        float o[16];
+                        tmem_ld16(colO + c0 + 16 * q, o);
+                        tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                float o[32];
-                tmem_ld32(colO + 32 * q, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float4 y = make_float4(0, 0, 0, 0);
-                    if (other) y = *cell(lr, 8 * q + e);
-                    float* oo = o + 4 * e;
-                    const float yy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        oo[k] = ((f0 != 0.0f ? oo[k] * f0 : 0.0f) + (f1 != 0.0f ? yy[k] * f1 : 0.0f)) * k0;
-                    if (spread)
-                        *cell(lr, 8 * q + e) = make_float4(oo[0], oo[1], oo[2], oo[3]);
-                    else if (piece && valid)
-                        *reinterpret_cast<float4*>(slot + ((8 * q + e) * kAttnSlotRows + row) * 4) =
-                            make_float4(oo[0], oo[1], oo[2], oo[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int d4 = c0 / 4 + 4 * q + e;
+                            float4 y = make_float4(0, 0, 0, 0);
+                            if (step) y = *cell(lr, d4);
+                            if (weight != 0.0f && n > 0) {
+                                y.x = fmaf(o[4 * e], weight, y.x);
+                                y.y = fmaf(o[4 * e + 1], weight, y.y);
+                                y.z = fmaf(o[4 * e + 2], weight, y.z);
+                                y.w = fmaf(o[4 * e + 3], weight, y.w);
+                            }
+                            if (step == 0 || copies > 1)
+                                *cell(lr, d4) = y;
+                            else if (valid)
+                                put(at, row, d4, y);
+                        }
+                        __syncwarp();
+                    }
                 }
-                if (!spread && !piece && valid) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint4*>(a.out + at * D + 32 * q + 8 * e) =
-                            make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                       pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-                }
-                __syncwarp();
+                named_bar(kBarAll, kSoft);
             }
-            if (spread)
-                sh.ml[lr] = make_float2(ref, sum);
-            else if (valid && piece)
-                *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(ref - C::kBias, sum);
-            else if (valid && a.lse)
-                a.lse[at] = ref == kNegInf ? kNegInf : (ref - C::kBias + log2f(sum)) * kLn2;
+            if (copies > 1) {
+                // thread: a row and every eighth (fourth) piece of four columns
+                const int tr = tid & (span - 1), rr = it.rt * kMT + tr, qj = rr / a.group;
+                const int64_t to = int64_t(it.s.q0 + qj) * a.q_heads + it.h * a.group + rr - qj * a.group;
+                if (tr < sr.rows) {
+#pragma unroll 2
+                    for (int d4 = tid / span; d4 < D / 4; d4 += kSoft / span) {
+                        float4 y = *cell(tr, d4);
+                        for (int k = 1; k < copies; ++k) {
+                            const float4 u = *cell(tr + k * span, d4);
+                            y.x += u.x;
+                            y.y += u.y;
+                            y.z += u.z;
+                            y.w += u.w;
+                        }
+                        put(to, tr, d4, y);
+                    }
+                }
+            }
         }
         tc_fence_before();
-        if (spread) {
-            // --- the copies of a row, by both warpgroups
-            named_bar(kBarAll, kSoft);
-            for (int e = tid; e < sr.rows * (D / 4); e += kSoft) {
-                const int d4 = e / sr.rows, rw = e - d4 * sr.rows;
-                float top = kNegInf, tot = 0.0f;
-                for (int k = 0; k < copies; ++k) top = fmaxf(top, sh.ml[rw + k * span].x);
-                float4 y = make_float4(0, 0, 0, 0);
-                for (int k = 0; k < copies; ++k) {
-                    const float2 ml = sh.ml[rw + k * span];
-                    if (ml.x == kNegInf) continue;
-                    const float w = fast_exp2(ml.x - top);
-                    const float4 u = *cell(rw + k * span, d4);
-                    tot += ml.y * w;
-                    y.x += u.x * w;
-                    y.y += u.y * w;
-                    y.z += u.z * w;
-                    y.w += u.w * w;
-                }
-                if (piece) {
-                    *reinterpret_cast<float4*>(slot + (d4 * kAttnSlotRows + rw) * 4) = y;
-                    if (d4 == 0)
-                        *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * rw) = make_float2(top - C::kBias, tot);
-                } else {
-                    const int r = it.rt * kMT + rw, qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
-                    const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
-                    const float inv = top == kNegInf ? 0.0f : 1.0f / tot;
-                    *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
-                        make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-                    if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top - C::kBias + log2f(tot)) * kLn2;
-                }
-            }
-        }
+        if (n0 > 0) op0 ^= 1;
+        if (n1 > 0) op1 ^= 1;
         // One row tile: the query tiles' room has been read.  A stream without
         // tiles must not run an item ahead of the MMA warp's wait for its queries.
         if (!sr.pair || n1 == 0 || n0 == 0) named_bar(kBarAll, kSoft);
