@@ -48,57 +48,62 @@ struct Shared {
     float2 ml[kConsumers][kRows];            // maximum (log2) and sum of a warp's keys
 };
 
+// The TMA warp.  A step is a key tile, K and V, a box or two a page, each page
+// issued by a lane of its own, one after the other; the next tile's page
+// indices are read a step ahead.
 template <int D, bool E4M3>
-__device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, Shared& sh,
-                                        uint8_t* ring) {
+__device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, Shared& sh, uint8_t* ring) {
     using C = Cfg<D, E4M3>;
-    constexpr int kBox = E4M3 ? D : 64;                 // elements of a box row
+    constexpr int kBox = E4M3 ? D : 64, kBoxBytes = E4M3 ? D : 128, kParts = D / kBox;
     const int lane = threadIdx.x & 31;
-    const int page = a.kv.page, pl = a.kv.page_log2;
-    const int box = page < kTile ? page : kTile;        // tokens of a box
+    const int page = a.kv.page, pl = a.kv.page_log2, n_pages = a.kv.n_pages;
+    const int rows = page < kTile ? page : kTile;       // tokens of a box
+    const int np = kTile / rows;                        // pages of a tile
+    uint8_t* box = ring + lane * rows * kBoxBytes;
     Walk<kRows, kTile> wk;
     wk.start(a, sh.plan);
     Item it;
-    int run = 0;
+    int st = 0;
+    uint32_t ph = 1;
     bool dead = false;
     while (wk.next(a, it)) {
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
-        const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl;   // pages with a seen key
-        int base = -1, entry = 0;
-        for (int t = it.t0; t < it.t1; ++t, ++run) {
-            const int st = run % C::kStages, ph = (run / C::kStages) & 1;
-            const int j0 = (it.tile0 + t) * kTile;
-            const int p0 = j0 >> pl, p1 = (j0 + kTile - 1) >> pl;
-            if (base < 0 || p1 >= base + 32) {
-                base = p0;
-                const int p = base + lane;
-                entry = p >= p_lo && p < p_hi && it.hi > it.lo ? table[p] : -1;
+        // pages with a seen key (none where no key is seen)
+        const int p_lo = it.lo >> pl, p_hi = it.hi > it.lo ? (it.hi + page - 1) >> pl : p_lo;
+        int j0 = (it.tile0 + it.t0) * kTile;
+        auto mine = [&]() {
+            const int p = (j0 >> pl) + lane;
+            return lane < np && p >= p_lo && p < p_hi;
+        };
+        int pg = mine() ? table[(j0 >> pl) + lane] : 0;
+        for (int t = it.t0; t < it.t1; ++t) {
+            const int first = j0 >> pl;
+            const bool issue = mine();
+            const int bytes = max(0, min(first + np, p_hi) - max(first, p_lo)) * rows * C::kRowBytes * 2;
+            if (issue && (pg < 0 || pg >= n_pages)) {
+                record_error(a.err, MOE_ERR_INVALID_ARG);
+                pg = n_pages;                           // out of range: reads as zeros
             }
-            if (!dead && !mbar_wait(&sh.empty[st], ph ^ 1, a.err, a.timeout_ns)) dead = true;
-            int boxes = 0;
-            for (int p = p0; p <= p1; ++p) boxes += p >= p_lo && p < p_hi && it.hi > it.lo;
-            uint8_t* kt = ring + st * 2 * C::kTileBytes;
-            if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], dead ? 0 : boxes * box * C::kRowBytes * 2);
+            if (!dead && !mbar_wait(&sh.empty[st], ph, a.err, a.timeout_ns)) dead = true;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], dead ? 0 : bytes);
             __syncwarp();
-            for (int p = p0; p <= p1; ++p) {
-                int pg = __shfl_sync(0xFFFFFFFFu, entry, p - base);
-                if (dead || p < p_lo || p >= p_hi || it.hi <= it.lo) continue;
-                if (pg < 0 || pg >= a.kv.n_pages) {
-                    if (lane == 0) record_error(a.err, MOE_ERR_INVALID_ARG);
-                    pg = a.kv.n_pages;                  // out of range: reads as zeros
-                }
-                if (lane == 0) {
-                    const int tok = page > kTile ? (j0 & (page - 1)) : 0;
-                    uint8_t* dst = kt + (p - p0) * box * (kBox * (E4M3 ? 1 : 2));
+            for (int b = 0; b < np; ++b) {
+                if (lane == b && issue && !dead) {
 #pragma unroll
-                    for (int x = 0; x < D / kBox; ++x) {
-                        tma_load_4d(dst + x * kTile * 128, &maps.k, &sh.full[st], x * kBox, tok,
-                                    it.h, pg);
-                        tma_load_4d(dst + C::kTileBytes + x * kTile * 128, &maps.v, &sh.full[st],
-                                    x * kBox, tok, it.h, pg);
+                    for (int x = 0; x < kParts; ++x) {
+                        uint8_t* dst = box + st * 2 * C::kTileBytes + x * kTile * 128;
+                        tma_load_4d(dst, &maps.k, &sh.full[st], x * kBox, j0 & (page - 1), it.h, pg);
+                        tma_load_4d(dst + C::kTileBytes, &maps.v, &sh.full[st], x * kBox, j0 & (page - 1), it.h, pg);
                     }
                 }
+                __syncwarp();
             }
+            if (++st == C::kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+            j0 += kTile;
+            if (t + 1 < it.t1 && mine()) pg = table[(j0 >> pl) + lane];
         }
     }
 }
@@ -148,7 +153,7 @@ struct QFrag {
         for (int r = 0; r < 2; ++r) {
             const int row = it.rt * kRows + g + 8 * r;
             const bool ok = row < rows;
-            const int i = ok ? row / at.group : 0;
+            const int i = ok ? at.query_of(row) : 0;
             const int hd = it.h * at.group + (ok ? row - i * at.group : 0);
             const uint16_t* src = at.q + (it.s.q0 + i) * at.q_stride + hd * D;
             mul[r] = 1.0f;
@@ -214,13 +219,13 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
         QFrag<D, E4M3> q;
         q.load(a, it);
         const int rows = min(kRows, it.s.nq * a.group - it.rt * kRows);
-        const int i0 = it.rt * kRows / a.group, i1 = (it.rt * kRows + rows - 1) / a.group;
+        const int i0 = a.query_of(it.rt * kRows), i1 = a.query_of(it.rt * kRows + rows - 1);
         RowView view[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = g + 8 * r;
             view[r] = RowView{0, 0, 0ull};
-            if (row < rows) view[r] = row_view(a, it.s, (it.rt * kRows + row) / a.group);
+            if (row < rows) view[r] = row_view(a, it.s, a.query_of(it.rt * kRows + row));
         }
         float c[2];
 #pragma unroll
@@ -451,7 +456,7 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
                     make_float4(v.x * vs, v.y * vs, v.z * vs, v.w * vs);
                 if (d4 == 0) *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(top, sum);
             } else {
-                const int r = it.rt * kRows + row, i = r / a.group, hd = it.h * a.group + r - i * a.group;
+                const int r = it.rt * kRows + row, i = a.query_of(r), hd = it.h * a.group + r - i * a.group;
                 const int64_t at = int64_t(it.s.q0 + i) * a.q_heads + hd;
                 const float inv = top == kNegInf ? 0.0f : vs / sum;
                 *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
@@ -500,7 +505,7 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
     const int grid = n_sms < kAttnMaxCtas ? n_sms : kAttnMaxCtas;
     e = launch_pdl(attn_rows_kernel<D, E4M3>, dim3(grid), dim3(kThreads), C::kSmem, s, a, m);
     if (e == cudaSuccess) e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_attn_join(a, kRows, grid, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, grid, s);
 }
 
 // Joins the pieces of the item that begins in CTA blockIdx.x, 8 rows a block:
@@ -508,24 +513,52 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
 // order.  A kernel of its own, not the work of the piece that comes last: that
 // CTA alone would read a verify block's 19 pieces of 64 rows (630 KB) at one
 // SM's rate, here every SM reads some.
-// Four threads share four columns of a row, each a quarter of the pieces, so
-// that all of them are in flight at once.
-constexpr int kJoinRows = 8, kJoinParts = 4;
+// A unit is kJoinRows rows of a split item; the blocks share the units of all
+// items out among them (each adds up the notes for itself).  Four threads have
+// four columns of a row, each a quarter of the pieces, so that all pieces are
+// in flight at once.
+constexpr int kJoinRows = 4, kJoinParts = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel(const AttnArgs a, int n_notes) {
     constexpr int64_t kSlot = kAttnSlotRows * (D + 2);
     constexpr int kCells = kJoinRows * D / 4;                                  // threads of a part
+    constexpr int kPer = kAttnMaxCtas / 32;
     __shared__ float4 s_v[kJoinParts][kCells];
     __shared__ float s_sum[kJoinParts][kJoinRows];
+    __shared__ int s_end[kAttnMaxCtas];                                        // units up to note i, inclusive
     pdl_wait();
     pdl_launch_dependents();
-    const SplitNote n = a.notes[blockIdx.x];
-    if (n.pieces == 0) return;
+    if (threadIdx.x < 32) {
+        int u[kPer], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = threadIdx.x * kPer + k;
+            u[k] = i < n_notes && a.notes[i].pieces > 0 ? (a.notes[i].rows + kJoinRows - 1) / kJoinRows : 0;
+            sum += u[k];
+        }
+        int before = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+            if (threadIdx.x >= d) before += o;
+        }
+        before -= sum;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) s_end[threadIdx.x * kPer + k] = before += u[k];
+    }
+    __syncthreads();
+    const int total = s_end[kAttnMaxCtas - 1];
     const int cell = threadIdx.x % kCells, part = threadIdx.x / kCells;
     const int rl = cell % kJoinRows, d4 = cell / kJoinRows;
-    const float* p0 = a.partials + (2 * int64_t(blockIdx.x) + 1) * kSlot;     // the first piece, then
-    for (int row0 = blockIdx.y * kJoinRows; row0 < n.rows; row0 += gridDim.y * kJoinRows) {
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        int i = 0;
+#pragma unroll
+        for (int step = 128; step > 0; step >>= 1)
+            if (i + step <= kAttnMaxCtas - 1 && s_end[i + step - 1] <= u) i += step;
+        const SplitNote n = a.notes[i];
+        const int row0 = (u - (i > 0 ? s_end[i - 1] : 0)) * kJoinRows;
+        const float* p0 = a.partials + (2 * int64_t(i) + 1) * kSlot;          // the first piece, then
         const int row = min(row0 + rl, n.rows - 1);
         const int ml = kAttnSlotRows * D + 2 * row, od = (d4 * kAttnSlotRows + row) * 4;
         auto piece = [&](int k) { return p0 + (k == 0 ? 0 : (2 * k - 1) * kSlot); };   // every second slot
@@ -561,8 +594,8 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel
                 v.z += y.z;
                 v.w += y.w;
             }
-            const int r = n.row0 + row, i = r / a.group, hd = n.head * a.group + r - i * a.group;
-            const int64_t at = int64_t(n.q0 + i) * a.q_heads + hd;
+            const int r = n.row0 + row, q = a.query_of(r), hd = n.head * a.group + r - q * a.group;
+            const int64_t at = int64_t(n.q0 + q) * a.q_heads + hd;
             const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
             *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
                 make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
@@ -574,12 +607,12 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel
 
 }  // namespace
 
-cudaError_t launch_attn_join(const AttnArgs& a, int rows, int grid, cudaStream_t s) {
-    const int most = a.max_rows < rows ? a.max_rows : rows;     // rows of an item
-    const dim3 g(grid, (most + kJoinRows - 1) / kJoinRows);
-    const cudaError_t e = a.kv.dim == 128
-                              ? launch_pdl(attn_join_kernel<128>, g, dim3(kJoinRows * kJoinParts * 32), 0, s, a)
-                              : launch_pdl(attn_join_kernel<64>, g, dim3(kJoinRows * kJoinParts * 16), 0, s, a);
+cudaError_t launch_attn_join(const AttnArgs& a, int n_notes, cudaStream_t s) {
+    // two blocks an SM
+    const cudaError_t e =
+        a.kv.dim == 128
+            ? launch_pdl(attn_join_kernel<128>, dim3(2 * n_notes), dim3(kJoinRows * kJoinParts * 32), 0, s, a, n_notes)
+            : launch_pdl(attn_join_kernel<64>, dim3(2 * n_notes), dim3(kJoinRows * kJoinParts * 16), 0, s, a, n_notes);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -256,7 +256,7 @@ struct Work {
     __device__ __forceinline__ static void extent(const AttnArgs& a, const Seq& s, int rt, int& lo,
                                                   int& hi, int& tile0, int& n) {
         const int r1 = min(s.nq * a.group, (rt + 1) * MT) - 1;
-        const int2 k = rows_range(a, s, rt * MT / a.group, r1 / a.group);
+        const int2 k = rows_range(a, s, a.query_of(rt * MT), a.query_of(r1));
         lo = k.x;
         hi = k.y;
         tile0 = lo / KT;

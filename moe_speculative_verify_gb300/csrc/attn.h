@@ -74,11 +74,18 @@ struct AttnArgs {
     int32_t q_heads, group;  // group = q_heads / kv heads
     float scale;
     int32_t causal, window;
-    int32_t max_rows;        // rows of an item by the caller's max_q: sizes the join's grid only
+    uint32_t group_magic;    // ceil(2^32 / group), 0 for a group of 1
     int32_t* err;
     SplitNote* notes;
     float* partials;
     uint64_t timeout_ns;
+
+#ifdef __CUDACC__
+    // row / group: exact for row * group < 2^32 (rows < 2^24, groups <= 256)
+    __device__ __forceinline__ int query_of(int row) const {
+        return group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), group_magic)) : row;
+    }
+#endif
 };
 
 struct KeywArgs {
@@ -117,7 +124,7 @@ constexpr int kAttnBigTile = 128;   // and of the tensor-memory kernel
 
 cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
-cudaError_t launch_attn_join(const AttnArgs& a, int rows, int grid, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnArgs& a, int n_notes, cudaStream_t s);
 cudaError_t launch_attn_tile(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
 cudaError_t launch_keyw(const KeywArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);

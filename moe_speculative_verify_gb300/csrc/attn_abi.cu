@@ -150,6 +150,7 @@ moe::AttnArgs attn_args(const moe_attn_t* at, const moe_kv_cache_t* c, const moe
     a.draft = draft;
     a.q_heads = at->n_q_heads;
     a.group = at->n_q_heads / c->n_kv_heads;
+    a.group_magic = a.group > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + a.group - 1) / a.group) : 0u;
     a.scale = at->scale;
     a.causal = at->causal != 0;
     a.window = at->window;
@@ -278,7 +279,6 @@ moe_status_t moe_paged_attention(const moe_attn_t* attn, const moe_kv_cache_t* c
     moe::AttnArgs a = attn_args(attn, cache, seqs, q, q_stride, draft_mask, n_tokens, ws);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    a.max_rows = static_cast<int32_t>(rows < moe::kAttnSlotRows ? rows : moe::kAttnSlotRows);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return cuda_status(few ? moe::launch_attn_rows(a, maps, device_info().sms, s)
                            : moe::launch_attn_tile(a, maps, device_info().sms, s));

@@ -30,12 +30,12 @@ namespace {
 
 constexpr int kMT = 256;                 // rows of an item
 constexpr int kKT = 128;                 // keys of a tile
-constexpr int kThreads = 384;            // 2 softmax warpgroups; TMA warp, MMA warp and 2 idle
+constexpr int kThreads = 384;            // 2 softmax warpgroups; TMA warp, 2 MMA warps and an idle one
 // Registers a thread, moved between the warpgroups after the launch at 168:
 // 8 * 208 + 4 * 80 = 1984 a lane column of the 12 * 168 = 2016 launched.
 constexpr int kRegsSoft = 208, kRegsRest = 80;
 constexpr int kSoft = 256;
-constexpr int kBarAll = 1, kBarGroup = 2;   // named barriers: both warpgroups, each of them
+constexpr int kBarAll = 1, kBarGroup = 2, kBarMma = 4;   // named barriers: both warpgroups, each, the MMA warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;          // S/P of stream s at column 128 s, O at 256 + 128 s
 
@@ -116,7 +116,7 @@ struct Share {
         for (int s = 0; s < 2; ++s) {
             const int r0 = it.rt * kMT + (pair ? 128 * s : 0);
             const int r1 = pair ? min(r0 + 128, it.rt * kMT + rows) : r0 + rows;
-            const int i0 = r0 / at.group, i1 = (r1 - 1) / at.group;
+            const int i0 = at.query_of(r0), i1 = at.query_of(r1 - 1);
             const int2 k = rows_range(at, it.s, i0, i1), w = rows_whole(at, it.s, i0, i1);
             wlo[s] = w.x;
             whi[s] = w.y;
@@ -137,7 +137,7 @@ struct Share {
 };
 
 // A role's place in the CTA's work (a softmax warpgroup's, the TMA warp's, the
-// MMA warp's), kept in shared memory so that it takes no registers from the
+// MMA warps'), kept in shared memory so that it takes no registers from the
 // loops over the tiles.  THREADS threads share it, at named barrier `bar`.
 struct Ctx {
     Walk<kMT, kKT> wk;
@@ -172,66 +172,80 @@ struct Shared {
     alignas(16) float2 ml[2][128];          // a lane's reference and sum, among a row's sharers
     uint64_t kv_full[10];
     uint64_t kv_empty[10];
-    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], turn[2];
     Plan plan;
-    Ctx ctx[4];                             // the softmax warpgroups', the TMA warp's, the MMA warp's
+    Ctx ctx[4];                             // the softmax warpgroups', the TMA warp's, the MMA warps'
     uint32_t tmem;
 };
 
+// The K/V ring's order: K V of a tile (two row tiles), or K K V V of two tiles
+// (alternate tiles).  The TMA warp fills stages in that order and both MMA
+// warps wait for every stage in that order, their own or not: a warp that
+// skipped a use of a stage would take the phase before it for its own
+// (parities repeat every two).
+template <int NS>
+struct Slot {
+    int st;
+    uint32_t ph;
+    __device__ __forceinline__ void step() {
+        if (++st == NS) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+// The TMA warp.  A tile is a box or two a page, each page issued by a lane of
+// its own, one after the other; page indices are read a group of tiles ahead.
 template <int D, bool E4M3>
 __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, Shared& sh, uint8_t* ring) {
     using C = Cfg<D, E4M3>;
-    constexpr int kBox = E4M3 ? D : 64;
-    constexpr int kBoxBytes = E4M3 ? D : 128;
+    constexpr int kBox = E4M3 ? D : 64, kBoxBytes = E4M3 ? D : 128, kParts = D / kBox;
     const int lane = threadIdx.x & 31;
-    const int page = a.kv.page, pl = a.kv.page_log2;
+    const int page = a.kv.page, pl = a.kv.page_log2, np = kKT >> pl, n_pages = a.kv.n_pages;
+    // lanes 0 .. np-1: the pages of a group's first tile, np .. 2 np - 1: of its second
+    const int i = lane >= np ? 1 : 0;
+    uint8_t* box = ring + (lane - i * np) * page * kBoxBytes;
     Ctx& ctx = sh.ctx[2];
     ctx.start<32>(a, sh.plan);
-    int st = -1;
-    uint32_t ph = 1;
+    Slot<C::kStages> at{0, 1u};
     bool dead = false;
     while (ctx.next<32>(a)) {
         const Item& it = ctx.it;
-        const Share& sr = ctx.sr;
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
-        const int ahead = sr.pair ? 1 : 2;
-        int base = -1, entry = 0;
-        // K of `ahead` tiles, then V of a tile and K of the tile `ahead` of it in turn
-        const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl, head = it.h, tile0 = it.tile0 + it.t0;
-        for (int op = 0; op < 2 * sr.tiles; ++op) {
-            const int first = min(ahead, sr.tiles);
-            const int x = op - first, mid = 2 * (sr.tiles - first);
-            const bool is_v = op >= first && (x >= mid || (x & 1) == 0);
-            const int j = op < first ? op : (x >= mid ? sr.tiles - first + (x - mid) : (is_v ? x >> 1 : (x >> 1) + first));
-            if (++st == C::kStages) st = 0;
-            if (st == 0) ph ^= 1;
-            const int p0 = ((tile0 + j) * kKT) >> pl, np = kKT >> pl;
-            if (base < 0 || p0 + np > base + 32 || p0 < base) {
-                base = is_v ? p0 : max(p0 - ahead * np, 0);      // the V tiles still to come too
-                const int p = base + lane;
-                entry = p >= p_lo && p < p_hi ? table[p] : -1;
+        const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl, head = it.h;
+        const int T = ctx.sr.tiles, group = ctx.sr.pair ? 1 : 2;
+        int p = (((it.tile0 + it.t0) * kKT) >> pl) + lane;       // this lane's page
+        auto mine = [&]() { return lane < group * np && p >= p_lo && p < p_hi; };
+        int pg = T > 0 && mine() ? table[p] : 0;
+        for (int j = 0; j < T; j += group) {
+            const bool issue = mine() && j + i < T;
+            if (issue && (pg < 0 || pg >= n_pages)) {
+                record_error(a.err, MOE_ERR_INVALID_ARG);
+                pg = n_pages;                                    // out of range: reads as zeros
             }
-            if (!dead && !mbar_wait(&sh.kv_empty[st], ph ^ 1, a.err, a.timeout_ns)) dead = true;
-            int boxes = 0;
-            for (int p = p0; p < p0 + np; ++p) boxes += p >= p_lo && p < p_hi;
-            if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], dead ? 0 : boxes * page * C::kRowBytes);
-            __syncwarp();
-            const CUtensorMap* map = is_v ? &maps.v : &maps.k;
-            uint8_t* dst = ring + st * C::kTileBytes;
-            for (int p = p0; p < p0 + np; ++p) {
-                int pg = __shfl_sync(0xFFFFFFFFu, entry, p - base);
-                if (dead || p < p_lo || p >= p_hi) continue;
-                if (pg < 0 || pg >= a.kv.n_pages) {
-                    if (lane == 0) record_error(a.err, MOE_ERR_INVALID_ARG);
-                    pg = a.kv.n_pages;                           // out of range: reads as zeros
-                }
-                if (lane == 0) {
+            const int p0 = p - lane, m = min(group, T - j);
 #pragma unroll
-                    for (int x2 = 0; x2 < D / kBox; ++x2)
-                        tma_load_4d(dst + (p - p0) * page * kBoxBytes + x2 * kKT * 128, map, &sh.kv_full[st],
-                                    x2 * kBox, 0, head, pg);
+            for (int v = 0; v < 2; ++v) {
+                for (int t = 0; t < m; ++t) {
+                    const int bytes = max(0, min(p0 + (t + 1) * np, p_hi) - max(p0 + t * np, p_lo)) * page * C::kRowBytes;
+                    if (!dead && !mbar_wait(&sh.kv_empty[at.st], at.ph, a.err, a.timeout_ns)) dead = true;
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at.st], dead ? 0 : bytes);
+                    __syncwarp();
+                    for (int b = t * np; b < (t + 1) * np; ++b) {
+                        if (lane == b && issue && !dead) {
+#pragma unroll
+                            for (int x = 0; x < kParts; ++x)
+                                tma_load_4d(box + at.st * C::kTileBytes + x * kKT * 128, v ? &maps.v : &maps.k,
+                                            &sh.kv_full[at.st], x * kBox, 0, head, pg);
+                        }
+                        __syncwarp();
+                    }
+                    at.step();
                 }
             }
+            p += group * np;
+            if (j + group < T && mine()) pg = table[p];
         }
     }
 }
@@ -243,12 +257,17 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
-// The MMA warp: one thread issues, the whole warp waits.  Its issue rate
-// paces the kernel, so descriptors are a constant plus the stage's offset (the
-// 14-bit address field cannot carry: shared memory lies below 256 KB) and the
-// stage is counted, not divided out.
+// The MMA warp of stream s: one thread issues, the whole warp waits.  The
+// streams' warps take turns, a burst each: PV of a tile, then QK of the next
+// (which writes S over that P).  Two warps, because the tensor pipe holds only
+// a few instructions: a warp's waits for its data run beside the other's
+// burst (one warp for both: 862 us for a chunk of 2048 over 16384 keys, its
+// four to six waits a burst leaving the pipe idle for 105 to 230 of 1025 cycles).
+// In turns, because bursts that mix finish together, and both softmaxes then
+// wait together (1049 us).  Descriptors are a constant plus the stage's offset
+// (the 14-bit address field cannot carry: shared memory lies below 256 KB).
 template <int D, bool E4M3>
-__device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t* qs, uint8_t* ring) {
+__device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t* qs, uint8_t* ring, int s) {
     using C = Cfg<D, E4M3>;
     constexpr uint32_t kIdQK = E4M3 ? idesc(0, 0, false, kKT) : idesc(1, 1, false, kKT);
     constexpr uint32_t kIdPV = E4M3 ? idesc(0, 0, true, D) : idesc(1, 1, true, D);
@@ -256,155 +275,123 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
     constexpr bool kNarrow = E4M3 && D == 64;                    // 64-byte cached rows
     constexpr uint32_t kSbo = kNarrow ? 512 : 1024, kSw = kNarrow ? kSw64 : kSw128;
     const int lane = threadIdx.x & 31;
-    const uint32_t tmem = sh.tmem;
-    const uint64_t q_desc = sdesc(smem_u32(qs), 16, 1024, kSw128);
+    const uint32_t colS = sh.tmem + 128 * s, colO = sh.tmem + kColO + 128 * s;
+    const uint64_t q_desc = sdesc(smem_u32(qs + s * C::kQBytes), 16, 1024, kSw128);
     const uint64_t k_desc = sdesc(smem_u32(ring), 16, kSbo, kSw), v_desc = sdesc(smem_u32(ring), 16384, kSbo, kSw);
     Ctx& ctx = sh.ctx[3];
-    ctx.start<32>(a, sh.plan);
+    ctx.start<64>(a, sh.plan);
     const Item& it = ctx.it;
     const Share& sr = ctx.sr;
-    uint32_t items = 0, pp[2] = {0, 0};                          // phases of q_ready, p_ready
+    Slot<C::kStages> at{0, 0u};
+    uint32_t qp = 0, pp = 0, tp = 0;                             // phases of q_ready, p_ready, turn
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
-        tc_fence_after();
     };
-    struct Slot {
-        uint32_t st, ph;
-        __device__ __forceinline__ Slot next() const {
-            return st + 1 == C::kStages ? Slot{0, ph ^ 1} : Slot{st + 1, ph};
-        }
-    };
-    Slot at{0, 0};                                               // next ring stage
-    auto wait_kv = [&](Slot r) { wait(&sh.kv_full[r.st], r.ph); };
-    auto qk = [&](int s, Slot r) {
-        const uint64_t qd = q_desc + s * (C::kQBytes >> 4), kd = k_desc + r.st * (C::kTileBytes >> 4);
-        const uint32_t d = tmem + 128 * s;
-        if (elect_one()) {
-            if constexpr (!E4M3) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                    mma_ss<false>(d, qd + off, kd + off, kIdQK, k > 0);
-                }
-            } else {
-                constexpr int kSteps = D / 32;
-#pragma unroll
-                for (int k = 0; k < 2 * kSteps; ++k)             // high codes, then low
-                    mma_ss<true>(d, qd + ((D == 128 ? (k / kSteps) * 16384 + (k % kSteps) * 32 : k * 32) >> 4),
-                                 kd + ((k % kSteps) * 32 >> 4), kIdQK, k > 0);
-            }
-            mma_commit(&sh.s_full[s]);
-        }
-        __syncwarp();
-    };
-    auto pv = [&](int s, Slot r, bool first) {
-        const uint64_t vd = v_desc + r.st * (C::kTileBytes >> 4);
-        const uint32_t d = tmem + kColO + 128 * s, p0 = tmem + 128 * s;
-        const uint32_t acc = first ? 0u : 1u;
-        if (elect_one()) {
-            if constexpr (!E4M3) {
-#pragma unroll
-                for (int k = 0; k < kKT / 16; ++k)
-                    mma_ts<false>(d, p0 + 8 * k, vd + (k * 2048 >> 4), kIdPV, k > 0 ? 1u : acc);
-            } else {
-#pragma unroll
-                for (int k = 0; k < kKT / 16; ++k)
-                    mma_ts<true>(d, p0 + 16 * (k & 3) + 8 * (k >> 2), vd + ((k & 3) * 32 * C::kRowBytes >> 4),
-                                 k < 4 ? kIdPV : kIdPVlow, k > 0 ? 1u : acc);
-            }
-        }
-        __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-        if (elect_one()) mma_commit(bar);
-        __syncwarp();
-    };
-    auto empty = [&](Slot r) { commit(&sh.kv_empty[r.st]); };
-    while (ctx.next<32>(a)) {
-        const int T = sr.tiles;
+    if (s == 1 && lane == 0) mbar_arrive(&sh.turn[0]);           // stream 0 begins
+    while (ctx.next<64>(a, kBarMma)) {
+        const int T = sr.tiles, pair = sr.pair;
         if (T == 0) continue;
-        wait(&sh.q_ready[0], items & 1);
-        wait(&sh.q_ready[1], items & 1);
-        ++items;
-        // V rows of keys that no row of the item sees may hold anything: zero them
+        // slots: this stream's tiles, or (two row tiles) all tiles, of which it uses a0 .. b0 - 1
+        const int slots = pair ? T : (T + 1) / 2;
+        const int a0 = pair ? (s ? sr.a[1] : sr.a[0]) : 0, b0 = pair ? (s ? sr.b[1] : sr.b[0]) : sr.count(s);
+        const int have = pair ? T : b0;                          // slots whose tile is this warp's to look at
         const int lo = it.lo - (it.tile0 + it.t0) * kKT, hi = it.hi - (it.tile0 + it.t0) * kKT;
-        auto clean = [&](Slot r, int j) {
-            if (j * kKT >= lo && j * kKT + kKT <= hi) return;
-            uint8_t* v = ring + r.st * C::kTileBytes;
-            constexpr int kPitch = E4M3 ? D : 128, kSub = E4M3 ? 1 : D / 64;      // a row's bytes in each part
-            const int head = min(max(lo - j * kKT, 0), kKT) * kPitch, tail = min(max(hi - j * kKT, 0), kKT) * kPitch;
-#pragma unroll
-            for (int x = 0; x < kSub; ++x) {
-                uint8_t* part = v + x * kKT * 128;
-                for (int e = 16 * lane; e < head; e += 512) *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
-                for (int e = tail + 16 * lane; e < kKT * kPitch; e += 512)
-                    *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
+        int op = 0;                                              // ring uses of this item waited for
+        // the stage of use `to`, once it and those before it are full; the others' are passed on
+        auto take = [&](int to) {
+            for (;; ++op, at.step()) {
+                wait(&sh.kv_full[at.st], at.ph);
+                if (op == to) break;
+                if (lane == 0) mbar_arrive(&sh.kv_empty[at.st]);
+                __syncwarp();
             }
-            fence_async_smem();
-            __syncwarp();
+            const int st = at.st;
+            ++op;
+            at.step();
+            return st;
         };
-        if (sr.pair) {
-            const int a0 = sr.a[0], b0 = sr.b[0], a1 = sr.a[1], b1 = sr.b[1];
-            auto on = [&](int s, int j) { return s ? j >= a1 && j < b1 : j >= a0 && j < b0; };
-            wait_kv(at);
+        if (b0 > a0) {
+            wait(&sh.q_ready[s], qp);
+            qp ^= 1;
+        }
+        for (int i = 0; i <= slots; ++i) {
+            const bool do_v = i > a0 && i <= b0, do_k = i >= a0 && i < b0;
+            int vs = 0, ks = 0;
+            const bool has_v = i > 0 && i <= have, has_k = i < have;
+            if (has_v) vs = take(pair ? 2 * i - 1 : 4 * (i - 1) + s + min(2, T - 2 * (i - 1)));
+            if (has_k) ks = take(pair ? 2 * i : 4 * i + s);
+            if (do_v) {
+                // V rows of keys that no row of the item sees may hold anything: zero them (in a pair both warps do)
+                const int j0 = (pair ? i - 1 : 2 * (i - 1) + s) * kKT;
+                if (j0 < lo || j0 + kKT > hi) {
+                    uint8_t* v = ring + vs * C::kTileBytes;
+                    constexpr int kPitch = E4M3 ? D : 128, kSub = E4M3 ? 1 : D / 64;      // a row's bytes in each part
+                    const int head = min(max(lo - j0, 0), kKT) * kPitch, tail = min(max(hi - j0, 0), kKT) * kPitch;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (on(s, 0)) qk(s, at);
-            empty(at);
-            at = at.next();
-            for (int j = 0; j < T; ++j) {
-                const Slot rv = at, rk = at.next();
-                const bool more = j + 1 < T;
-                wait_kv(rv);
-                clean(rv, j);
-                if (more) wait_kv(rk);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (on(s, j)) {
-                        wait(&sh.p_ready[s], pp[s]);
-                        pp[s] ^= 1;
-                        pv(s, rv, j == (s ? a1 : a0));
-                        if (j + 1 == (s ? b1 : b0)) commit(&sh.o_full[s]);
+                    for (int x = 0; x < kSub; ++x) {
+                        uint8_t* part = v + x * kKT * 128;
+                        for (int e = 16 * lane; e < head; e += 512)
+                            *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
+                        for (int e = tail + 16 * lane; e < kKT * kPitch; e += 512)
+                            *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
                     }
-                    if (s == 1) empty(rv);
-                    if (more && on(s, j + 1)) qk(s, rk);
+                    fence_async_smem();
+                    __syncwarp();
                 }
-                at = rk;
-                if (more) {
-                    empty(rk);
-                    at = rk.next();
+                wait(&sh.p_ready[s], pp);
+                pp ^= 1;
+            }
+            wait(&sh.turn[s], tp);
+            tp ^= 1;
+            tc_fence_after();
+            const uint64_t kd = k_desc + ks * (C::kTileBytes >> 4), vd = v_desc + vs * (C::kTileBytes >> 4);
+            const uint32_t acc = i - 1 > a0 ? 1u : 0u;
+            if (elect_one()) {
+                if (do_v) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t ac = k > 0 ? 1u : acc;
+                        if constexpr (!E4M3)
+                            mma_ts<false>(colO, colS + 8 * k, vd + (k * 2048 >> 4), kIdPV, ac);
+                        else                                     // 32 keys' high codes, then low
+                            mma_ts<true>(colO, colS + 8 * k, vd + ((k >> 1) * 32 * C::kRowBytes >> 4),
+                                         k & 1 ? kIdPVlow : kIdPV, ac);
+                    }
+                    if (i == b0) mma_commit(&sh.o_full[s]);
+                    mma_commit(&sh.kv_empty[vs]);
+                } else if (has_v) {
+                    mbar_arrive(&sh.kv_empty[vs]);
                 }
-            }
-        } else {
-            // ring order: K0 K1, then V(j), K(j+2) while there is one, then the V left
-            for (int s = 0; s < min(2, T); ++s) {
-                wait_kv(at);
-                qk(s, at);
-                empty(at);
-                at = at.next();
-            }
-            for (int j = 0; j < T; ++j) {
-                const int s = j & 1;
-                wait_kv(at);
-                clean(at, j);
-                wait(&sh.p_ready[s], s ? pp[1] : pp[0]);
-                if (s)
-                    pp[1] ^= 1;
-                else
-                    pp[0] ^= 1;
-                pv(s, at, j < 2);
-                empty(at);
-                at = at.next();
-                if (j + 2 < T) {
-                    wait_kv(at);
-                    qk(s, at);
-                    empty(at);
-                    at = at.next();
-                } else {
-                    commit(&sh.o_full[s]);
+                if (do_k) {
+                    if constexpr (!E4M3) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                            mma_ss<false>(colS, q_desc + off, kd + off, kIdQK, k > 0);
+                        }
+                    } else {
+                        constexpr int kSteps = D / 32;
+#pragma unroll
+                        for (int k = 0; k < 2 * kSteps; ++k)     // high codes, then low
+                            mma_ss<true>(colS,
+                                         q_desc + ((D == 128 ? (k / kSteps) * 16384 + (k % kSteps) * 32 : k * 32) >> 4),
+                                         kd + ((k % kSteps) * 32 >> 4), kIdQK, k > 0);
+                    }
+                    mma_commit(&sh.s_full[s]);
+                    mma_commit(&sh.kv_empty[ks]);
+                } else if (has_k) {
+                    mbar_arrive(&sh.kv_empty[ks]);
                 }
+                mbar_arrive(&sh.turn[s ^ 1]);
             }
+            __syncwarp();
+        }
+        // the other stream's last uses
+        for (; op < 2 * T; ++op, at.step()) {
+            wait(&sh.kv_full[at.st], at.ph);
+            if (lane == 0) mbar_arrive(&sh.kv_empty[at.st]);
+            __syncwarp();
         }
     }
 }
@@ -492,19 +479,39 @@ __device__ __forceinline__ float power_offset(const RowState& st) {
     return Cfg<D, E4M3>::kBias - (st.ref == kNegInf ? 0.0f : st.ref);
 }
 
-// A key tile that every row sees, all of it this thread's: the long calls'
-// loop, S held in registers.
-template <int D, bool E4M3>
-__device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, float c, bool started, RowState& st) {
-    float x[4][32];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) tmem_ld32(colS + 32 * q, x[q]);
-    tmem_wait_ld();
-    follow<D, E4M3>(colO, fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * c, started, st);
-    const float off = power_offset<D, E4M3>(st);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) powers<D, E4M3>(colS + 16 * q, x[q], c, off, st);
+// Hands P to the MMA warp.
+__device__ __forceinline__ void p_done(uint64_t* bar) {
     tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// A key tile that every row sees, N pieces of 32 keys from piece `from` on
+// this copy's (4: all of it) and the others' P zero: the long calls' loops, S
+// held in registers.
+template <int D, bool E4M3, int N>
+__device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, int from, float c, bool started,
+                                                uint64_t* ready, RowState& st) {
+    float x[N][32];
+#pragma unroll
+    for (int q = 0; q < N; ++q) tmem_ld32(colS + 32 * (from + q), x[q]);
+    tmem_wait_ld();
+    float top = max32(x[0]);
+#pragma unroll
+    for (int q = 1; q < N; ++q) top = fmaxf(top, max32(x[q]));
+    follow<D, E4M3>(colO, top * c, started, st);
+    const float off = power_offset<D, E4M3>(st);
+    if constexpr (N < 4) {
+        const uint32_t z[16] = {};
+#pragma unroll
+        for (int q = N; q < 4; ++q) tmem_st16(colS + 16 * ((from + q) & 3), z);
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        powers<D, E4M3>(colS + 16 * (from + q), x[q], c, off, st);
+    }
+    p_done(ready);
 }
 
 // Any other: `count` pieces of 32 keys from piece `from` on are this copy's,
@@ -513,7 +520,7 @@ __device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, fl
 template <int D, bool E4M3>
 __device__ __forceinline__ void soft_tile_part(uint32_t colS, uint32_t colO, int from, int count, float c, bool started,
                                                bool whole, const RowView& view, bool draft, int first, int j0,
-                                               RowState& st) {
+                                               uint64_t* ready, RowState& st) {
     float x[32];
     auto piece = [&](int q) {
         tmem_ld32(colS + 32 * q, x);
@@ -543,70 +550,76 @@ __device__ __forceinline__ void soft_tile_part(uint32_t colS, uint32_t colO, int
 #pragma unroll 1
     for (int q = 0; q < 4; ++q)
         if (q < from || q >= from + count) tmem_st16(colS + 16 * q, z);
-    tmem_wait_st();
+    p_done(ready);
 }
 
-// A query row into shared memory, K-major with the 128-byte swizzle: bf16 as
-// it is, or (beside e4m3 codes) as high and low e4m3 codes of the row times a
-// power of two, which goes into c.
+// A warp's 32 query rows into shared memory, K-major with the 128-byte
+// swizzle: bf16 as they are, or (beside e4m3 codes) as high and low e4m3 codes
+// of the row times a power of two, which goes into the row's c.  `src` is the
+// lane's own row; the warp reads whole rows, D / 8 lanes to one, so that a
+// load touches 4 lines and not 32, eight loads at a time before their use.
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_query(const uint16_t* src, bool valid, bool negate, uint8_t* qt, int lr, float& c) {
-    uint8_t* base = qt + lr * 128;
-    if constexpr (!E4M3) {
-#pragma unroll 8
-        for (int k = 0; k < D / 8; ++k) {
-            const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-            const uint32_t flip = negate ? 0x80008000u : 0u;
-            *reinterpret_cast<uint4*>(base + (k >> 3) * 16384 + (((k & 7) ^ (lr & 7)) << 4)) =
-                make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
-        }
-    } else {
-        float amax = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < D / 8; ++k) {
-            const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(x[e] & 0xFFFFu)),
-                                         fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-        }
-        // the row's largest element to [128, 256): f1 takes it to [1, 2)
-        const float f1 = pow2_norm(amax);
-        const float f2 = f1 == 1.0f && !(amax >= 1.0f && amax < 2.0f) ? 1.0f : 128.0f;
-        c = amax < INFINITY ? fmaxf(c / f2 / f1, 1.2e-38f) : __int_as_float(0x7FC00000);
-        const float g = negate ? -f2 : f2;
+__device__ __forceinline__ void load_queries(const uint16_t* src, bool valid, bool negate, uint8_t* qt, float& c) {
+    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 8;
+    const int lane = threadIdx.x & 31, ch = lane % kLanes, sub = lane / kLanes;
+    const int row0 = threadIdx.x & 96;                           // the warp's first row of the tile
+    const uint32_t flip = negate ? 0x80008000u : 0u, on = __ballot_sync(0xFFFFFFFFu, valid);
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(src);
+    float own = 0.0f;                                            // the largest element of the lane's own row
 #pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {                       // 16 elements: a chunk of each code
-            uint32_t hi4[4], lo4[4], x[8];
+    for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
+        uint4 w[kBatch];
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 16 * k + 8 * v) : make_uint4(0, 0, 0, 0);
-                x[4 * v] = w.x;
-                x[4 * v + 1] = w.y;
-                x[4 * v + 2] = w.z;
-                x[4 * v + 3] = w.w;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t h = 0, l = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float v0 = bf16_bits_to_f32(x[2 * q + e] & 0xFFFFu) * f1 * g;
-                    const float v1 = __uint_as_float(x[2 * q + e] & 0xFFFF0000u) * f1 * g;
-                    const uint32_t hc = pack_e4m3(v0, v1);
-                    const float2 b = unpack_e4m3(hc);
-                    h |= hc << (16 * e);
-                    l |= pack_e4m3(v0 - b.x, v1 - b.y) << (16 * e);
-                }
-                hi4[q] = h;
-                lo4[q] = l;
-            }
-            const int cl = D == 128 ? k : k + 4;
-            uint8_t* low = D == 128 ? base + 16384 : base;
-            *reinterpret_cast<uint4*>(base + ((k ^ (lr & 7)) << 4)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-            *reinterpret_cast<uint4*>(low + ((cl ^ (lr & 7)) << 4)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+        for (int k = 0; k < kBatch; ++k) {
+            const int rl = (i0 + k) * kRowsAt + sub;
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, mine, rl));
+            w[k] = __ldg(reinterpret_cast<const uint4*>(p + 8 * ch));
         }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int rl = (i0 + k) * kRowsAt + sub, r = row0 + rl;
+            const uint32_t keep = (on >> rl) & 1u ? 0xFFFFFFFFu : 0u;
+            const uint32_t x[4] = {(w[k].x ^ flip) & keep, (w[k].y ^ flip) & keep, (w[k].z ^ flip) & keep,
+                                   (w[k].w ^ flip) & keep};
+            uint8_t* base = qt + r * 128;
+            if constexpr (!E4M3) {
+                *reinterpret_cast<uint4*>(base + (ch >> 3) * 16384 + (((ch & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
+            } else {
+                float amax = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(x[e] & 0xFFFFu)),
+                                             fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+#pragma unroll
+                for (int d = 1; d < kLanes; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+                // the row's largest element to [128, 256): f1 takes it to [1, 2)
+                const float f1 = pow2_norm(amax);
+                const float f2 = f1 == 1.0f && !(amax >= 1.0f && amax < 2.0f) ? 1.0f : 128.0f;
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f1 * f2;
+                    const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f1 * f2;
+                    h[e] = pack_e4m3(v0, v1);
+                    const float2 b = unpack_e4m3(h[e]);
+                    l[e] = pack_e4m3(v0 - b.x, v1 - b.y);
+                }
+                const int chunk = ch >> 1, half = 8 * (ch & 1), cl = D == 128 ? chunk : chunk + 4;
+                uint8_t* low = D == 128 ? base + 16384 : base;
+                *reinterpret_cast<uint2*>(base + ((chunk ^ (r & 7)) << 4) + half) =
+                    make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+                *reinterpret_cast<uint2*>(low + ((cl ^ (r & 7)) << 4) + half) =
+                    make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+                // to the row's own lane, from the lanes that read it
+                const float a1 = __shfl_sync(0xFFFFFFFFu, amax, (lane % kRowsAt) * kLanes);
+                own = lane / kRowsAt == i0 + k ? a1 : own;
+            }
+        }
+    }
+    if constexpr (E4M3) {
+        const float f1 = pow2_norm(own), f2 = f1 == 1.0f && !(own >= 1.0f && own < 2.0f) ? 1.0f : 128.0f;
+        c = own < INFINITY ? fmaxf(c / f2 / f1, 1.2e-38f) : __int_as_float(0x7FC00000);
     }
     fence_async_smem();
 }
@@ -640,12 +653,12 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         // (never 0: an unseen key's -inf times it stays -inf)
         float c = fmaxf(fabsf(a.scale) * kLog2e * (E4M3 ? a.kv.k_scale[it.h] : 1.0f), 1.2e-38f);
         {
-            const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+            const int r = it.rt * kMT + (valid ? row : 0), qi = a.query_of(r), hd = it.h * a.group + r - qi * a.group;
             if (valid) view = row_view(a, it.s, qi);
-            load_query<D, E4M3>(a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid, a.scale < 0.0f, qs + s * C::kQBytes,
-                                lr, c);
+            load_queries<D, E4M3>(a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid, a.scale < 0.0f,
+                                  qs + s * C::kQBytes, c);
             __syncwarp();
-            if (lane == 0 && sr.tiles > 0) mbar_arrive(&sh.q_ready[s]);
+            if (lane == 0 && n > 0) mbar_arrive(&sh.q_ready[s]);
         }
         RowState st{kNegInf, 0.0f, 0.0f};
         {
@@ -655,17 +668,17 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
                 const int j0 = base + i * step;
                 wait(&sh.s_full[s], sp);
                 sp ^= 1;
-                if (warp_on) {
-                    const bool whole = j0 >= wlo && j0 + kKT <= whi;
-                    if (whole && copies == 1)
-                        soft_tile_whole<D, E4M3>(colS, colO, c, i > 0, st);
-                    else
-                        soft_tile_part<D, E4M3>(colS, colO, copy * (span >> 5), span >> 5, c, i > 0, whole, view, draft,
-                                                first, j0, st);
+                const bool whole = j0 >= wlo && j0 + kKT <= whi;
+                if (!warp_on) {
+                    p_done(&sh.p_ready[s]);
+                } else if (whole && copies == 1) {
+                    soft_tile_whole<D, E4M3, 4>(colS, colO, 0, c, i > 0, &sh.p_ready[s], st);
+                } else if (whole && copies == 2) {
+                    soft_tile_whole<D, E4M3, 2>(colS, colO, 2 * copy, c, i > 0, &sh.p_ready[s], st);
+                } else {
+                    soft_tile_part<D, E4M3>(colS, colO, copy * (span >> 5), span >> 5, c, i > 0, whole, view, draft,
+                                            first, j0, &sh.p_ready[s], st);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[s]);
             }
         }
         // --- the item's rows: normalised, or this CTA's piece of them
@@ -690,7 +703,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
             weight = ref == kNegInf ? 0.0f : fast_exp2(ref - top);
         }
         weight *= (E4M3 ? a.kv.v_scale[it.h] : 1.0f) * (piece || top == kNegInf ? 1.0f : 1.0f / sum);
-        const int r = it.rt * kMT + (valid ? row : 0), qi = r / a.group, hd = it.h * a.group + r - qi * a.group;
+        const int r = it.rt * kMT + (valid ? row : 0), qi = a.query_of(r), hd = it.h * a.group + r - qi * a.group;
         const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
         if (valid && (sr.pair || (s == 0 && copy == 0))) {
             if (piece)
@@ -769,7 +782,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
             }
             if (copies > 1) {
                 // thread: a row and every eighth (fourth) piece of four columns
-                const int tr = tid & (span - 1), rr = it.rt * kMT + tr, qj = rr / a.group;
+                const int tr = tid & (span - 1), rr = it.rt * kMT + tr, qj = a.query_of(rr);
                 const int64_t to = int64_t(it.s.q0 + qj) * a.q_heads + it.h * a.group + rr - qj * a.group;
                 if (tr < sr.rows) {
 #pragma unroll 2
@@ -790,9 +803,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         tc_fence_before();
         if (n0 > 0) op0 ^= 1;
         if (n1 > 0) op1 ^= 1;
-        // One row tile: the query tiles' room has been read.  A stream without
-        // tiles must not run an item ahead of the MMA warp's wait for its queries.
-        if (!sr.pair || n1 == 0 || n0 == 0) named_bar(kBarAll, kSoft);
+        if (!sr.pair) named_bar(kBarAll, kSoft);                 // the query tiles' room has been read
         if (tid == 0) note_split(a, it, sr.rows, kMT, sh.plan);
     }
 }
@@ -810,11 +821,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&sh.kv_full[i], 1);
-            mbar_init(&sh.kv_empty[i], 1);
+            mbar_init(&sh.kv_empty[i], 2);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.p_ready[s], 4);
+            mbar_init(&sh.turn[s], 1);
             mbar_init(&sh.o_full[s], 1);
             mbar_init(&sh.q_ready[s], 4);
         }
@@ -839,8 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (warp == 8)
             produce<D, E4M3>(a, maps, sh, ring);
-        else if (warp == 9)
-            multiply<D, E4M3>(a, sh, qs, ring);
+        else if (warp < 11)
+            multiply<D, E4M3>(a, sh, qs, ring, warp - 9);
     }
     tc_fence_before();
     __syncthreads();
@@ -857,7 +869,7 @@ cudaError_t launch(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s
     const int grid = n_sms < kAttnMaxCtas ? n_sms : kAttnMaxCtas;
     e = launch_pdl(attn_tile_kernel<D, E4M3>, dim3(grid), dim3(kThreads), smem, s, a, m);
     if (e == cudaSuccess) e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_attn_join(a, kMT, grid, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, grid, s);
 }
 
 }  // namespace

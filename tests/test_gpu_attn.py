@@ -24,7 +24,7 @@ def _built():
 
 
 def attend(p, causal=True, window=0, draft=None, stream=None):
-    attn = m.Attn(p.hq, p.scale, causal, window)
+    attn = m.Attn(p.hq, p.scale, causal, window, wait_timeout_us=200000)
     # beyond its error word a workspace may hold anything
     ws = torch.full((m.moe_attn_workspace_bytes(attn, p.cache),), 255, dtype=torch.uint8, device="cuda")
     ws[:256] = 0
@@ -226,7 +226,7 @@ def test_key_weights(shape, mask):
     lse[p.t // 3] = float("inf")             # a row that is left out
     g = torch.Generator().manual_seed(6)
     scores = torch.rand(len(p.lens), p.hkv, max(p.lens) + 3, generator=g)
-    attn = m.Attn(p.hq, p.scale, causal, window)
+    attn = m.Attn(p.hq, p.scale, causal, window, wait_timeout_us=200000)
     ws = torch.zeros(m.moe_attn_workspace_bytes(attn, p.cache), dtype=torch.uint8, device="cuda")
     want, tol = ref.key_weights(p, lse, scores, 0.75, causal, window, draft)
     d = None if draft is None else draft.cuda()
