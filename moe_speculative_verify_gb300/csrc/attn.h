@@ -94,6 +94,8 @@ struct KeywArgs {
     const float* scores;
     float* scores_out;
     int64_t score_stride;
+    int32_t tile_heads;      // rows of a tile: the query heads of a kv head (at most 128 at a time)
+    int32_t tile_tokens;     // by so many tokens
 };
 
 struct EvictArgs {
@@ -116,6 +118,12 @@ struct KvMaps {
     CUtensorMap k, v;
 };
 
+// K as above, and q as a 3-D tensor (d, head, token) in boxes of 64 elements,
+// tile_heads heads and tile_tokens tokens.
+struct KeywMaps {
+    CUtensorMap k, q;
+};
+
 // Rows a kv head (new tokens of a sequence times query heads a kv head) up to
 // which the few-rows kernel is taken: one 16-row matrix tile.
 constexpr int kAttnFewRows = 16;
@@ -126,7 +134,7 @@ cudaError_t launch_rope(const RopeArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnArgs& a, int n_notes, cudaStream_t s);
 cudaError_t launch_attn_tile(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
-cudaError_t launch_keyw(const KeywArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_keyw(const KeywArgs& a, const KeywMaps& m, int n_sms, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
 }  // namespace moe

@@ -139,6 +139,44 @@ bool make_kv_maps(const moe_kv_cache_t* c, int box, moe::KvMaps* m) {
     return true;
 }
 
+struct QMapKey {
+    const void* q;
+    int64_t stride;
+    int32_t dim, heads, tokens, box_heads, box_tokens;
+};
+
+// q as a 3-D tensor (d, head, token): boxes of 64 elements x box_heads x
+// box_tokens, 128-byte swizzled; tokens and heads past the end read as zeros.
+bool make_q_map(const void* q, int64_t stride, int dim, int heads, int tokens, int box_heads,
+                int box_tokens, CUtensorMap* m) {
+    QMapKey key;
+    std::memset(&key, 0, sizeof(key));
+    key.q = q;
+    key.stride = stride;
+    key.dim = dim;
+    key.heads = heads;
+    key.tokens = tokens;
+    key.box_heads = box_heads;
+    key.box_tokens = box_tokens;
+    thread_local moe::MapCache<QMapKey, CUtensorMap> cache;
+    if (const CUtensorMap* hit = cache.find(key)) {
+        *m = *hit;
+        return true;
+    }
+    auto fn = moe::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(tokens)};
+    const cuuint64_t strides[2] = {cuuint64_t(dim) * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    cache.put(key, *m);
+    return true;
+}
+
 moe::AttnArgs attn_args(const moe_attn_t* at, const moe_kv_cache_t* c, const moe_seqs_t* s,
                         const void* q, int64_t q_stride, const uint64_t* draft, int32_t tokens,
                         void* ws) {
@@ -296,6 +334,12 @@ moe_status_t moe_key_weights(const moe_attn_t* attn, const moe_kv_cache_t* cache
     if ((st = check_seqs(seqs, true)) != MOE_OK) return st;
     if ((st = check_tokens(n_tokens)) != MOE_OK) return st;
     if (seqs->n_seqs == 0) return n_tokens == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
+    if (n_tokens == 0) {          // no rows: the scores decay; the row arguments are not read
+        q = cache->k;
+        q_stride = int64_t(attn->n_q_heads) * cache->head_dim;
+        lse = static_cast<const float*>(ws);
+        draft_mask = nullptr;
+    }
     if (!rows_ok(q, q_stride, int64_t(attn->n_q_heads) * cache->head_dim) || !lse || !aligned(lse, 4) ||
         !aligned(draft_mask, 8) || !scores || !scores_out || !aligned(scores, 4) ||
         !aligned(scores_out, 4) || score_stride < 1 || !std::isfinite(decay))
@@ -308,7 +352,16 @@ moe_status_t moe_key_weights(const moe_attn_t* attn, const moe_kv_cache_t* cache
     a.scores = scores;
     a.scores_out = scores_out;
     a.score_stride = score_stride;
-    return cuda_status(moe::launch_keyw(a, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
+    a.tile_heads = a.a.group < 128 ? a.a.group : 128;
+    a.tile_tokens = 128 / a.tile_heads < seqs->max_q ? 128 / a.tile_heads : seqs->max_q;
+    moe::KeywMaps maps;
+    moe::KvMaps kv;
+    if (!make_kv_maps(cache, moe::kAttnBigTile, &kv) ||
+        !make_q_map(q, q_stride, cache->head_dim, attn->n_q_heads, n_tokens > 0 ? n_tokens : 1, a.tile_heads,
+                    a.tile_tokens, &maps.q))
+        return MOE_ERR_CUDA;
+    maps.k = kv.k;
+    return cuda_status(moe::launch_keyw(a, maps, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs,

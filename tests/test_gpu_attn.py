@@ -239,3 +239,54 @@ def test_key_weights(shape, mask):
     x = got.cpu().numpy().astype(np.float64)
     bad = ~(np.abs(x - want) <= tol)
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], x[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_key_weights_many_items(dtype):
+    """More items than SMs, many row tiles an item, and rows of other sequences
+    that hold NaN beside those that count."""
+    p = ref.Problem([2600, 900, 1, 257], [40, 3, 1, 9], 64, 16, 64, 32, dtype, seed=21, pads=(2, 2))
+    p.qkv[0], p.qkv[-1] = float("nan"), float("nan")
+    p.cuda()
+    lse = torch.from_numpy(ref.attention(p)[1]).float()
+    scores = torch.rand(4, 16, 2600, generator=torch.Generator().manual_seed(3))
+    want, tol = ref.key_weights(p, lse, scores, 1.0)
+    attn = m.Attn(p.hq, p.scale, wait_timeout_us=200000)
+    ws = torch.zeros(m.moe_attn_workspace_bytes(attn, p.cache), dtype=torch.uint8, device="cuda")
+    got = scores.cuda()
+    m.moe_key_weights(attn, p.cache, p.seqs, p.d_q(), lse.cuda(), got, got, ws)
+    assert m.moe_get_device_error(ws) == 0
+    x = got.cpu().numpy().astype(np.float64)
+    bad = ~(np.abs(x - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], x[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("hq,hkv", [(160, 1), (130, 1), (256, 2), (15, 5)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_wide_groups(hq, hkv, dtype):
+    """More query heads a kv head than a row tile holds, and odd groups."""
+    p = ref.Problem([200, 70], [3, 2], hq, hkv, 64, 64, dtype, seed=22).cuda()
+    out, lse, _ = attend(p)
+    check(p, out, lse)
+    z = torch.from_numpy(ref.attention(p)[1]).float()
+    scores = torch.zeros(2, hkv, 200)
+    want, tol = ref.key_weights(p, z, scores, 1.0)
+    attn = m.Attn(p.hq, p.scale, wait_timeout_us=200000)
+    ws = torch.zeros(m.moe_attn_workspace_bytes(attn, p.cache), dtype=torch.uint8, device="cuda")
+    got = scores.cuda()
+    m.moe_key_weights(attn, p.cache, p.seqs, p.d_q(), z.cuda(), got, got, ws)
+    assert m.moe_get_device_error(ws) == 0
+    assert np.all(np.abs(got.cpu().numpy().astype(np.float64) - want) <= tol)
+
+
+def test_key_weights_without_new_tokens():
+    """Sequences without new tokens only decay."""
+    p = ref.Problem([300, 20], [0, 0], 8, 2, 128, 64, seed=23).cuda()
+    attn = m.Attn(p.hq, p.scale, wait_timeout_us=200000)
+    ws = torch.zeros(m.moe_attn_workspace_bytes(attn, p.cache), dtype=torch.uint8, device="cuda")
+    scores = torch.rand(2, 2, 300, device="cuda")
+    got = scores.clone()
+    m.moe_key_weights(attn, p.cache, p.seqs, p.d_q(), torch.zeros(0, 8, device="cuda"), got, got, ws, decay=0.5)
+    assert m.moe_get_device_error(ws) == 0
+    for b, n in enumerate(p.lens):
+        assert torch.equal(got[b, :, :n], scores[b, :, :n] * 0.5) and torch.equal(got[b, :, n:], scores[b, :, n:])
