@@ -195,6 +195,19 @@ __device__ __forceinline__ float2 unpack_e4m3(uint32_t codes) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Four e4m3 codes as bf16 pairs, exactly, without the conversion unit (which
+// the powers need): a code's exponent and fraction bits moved to where bf16
+// has them give the value times 2^-120, subnormals included.  NaN codes come
+// out as numbers: `nan` collects them (bits 7 of its bytes).
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t codes, uint32_t& lo, uint32_t& hi, uint32_t& nan) {
+    const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);
+    const uint32_t ya = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), yb = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+    constexpr uint32_t k2p120 = 0x7B807B80u;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(ya), "r"(k2p120));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(yb), "r"(k2p120));
+    nan |= (codes & 0x7F7F7F7Fu) + 0x01010101u;
+}
+
 // D[16x8] += A[16x16] B[16x8]: bf16 or f16 operands, fp32 sums.  Lane l = 4g+t
 // holds A rows g, g+8 at columns 2t,2t+1 (a0, a1) and 2t+8,2t+9 (a2, a3), B
 // column g at rows 2t,2t+1 (b0) and 2t+8,2t+9 (b1), D rows g (d0, d1) and g+8

@@ -96,6 +96,13 @@ struct KeywArgs {
     int64_t score_stride;
     int32_t tile_heads;      // rows of a tile: the query heads of a kv head (at most 128 at a time)
     int32_t tile_tokens;     // by so many tokens
+    uint32_t tile_magic;     // ceil(2^32 / tile_tokens), 0 for one token
+
+#ifdef __CUDACC__
+    __device__ __forceinline__ int tile_of(int query) const {
+        return tile_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(query), tile_magic)) : query;
+    }
+#endif
 };
 
 struct EvictArgs {

@@ -354,6 +354,7 @@ moe_status_t moe_key_weights(const moe_attn_t* attn, const moe_kv_cache_t* cache
     a.score_stride = score_stride;
     a.tile_heads = a.a.group < 128 ? a.a.group : 128;
     a.tile_tokens = 128 / a.tile_heads < seqs->max_q ? 128 / a.tile_heads : seqs->max_q;
+    a.tile_magic = a.tile_tokens > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + a.tile_tokens - 1) / a.tile_tokens) : 0u;
     moe::KeywMaps maps;
     moe::KvMaps kv;
     if (!make_kv_maps(cache, moe::kAttnBigTile, &kv) ||

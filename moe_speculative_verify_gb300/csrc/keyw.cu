@@ -16,7 +16,8 @@
 // cycles a 128 x 128 tile on an SM, the powers as many.
 //
 // e4m3 keys are turned to bf16 in shared memory first (exact), which a tile
-// pays once however many rows see it.
+// pays once however many rows see it, by two warpgroups of their own (as part
+// of the powers' warpgroups' round it held up the stream: 16 verify blocks 92 us).
 #include "attn_mma.cuh"
 #include "kernels.h"
 
@@ -25,78 +26,60 @@ namespace moe {
 namespace {
 
 constexpr int kKeys = 128;                  // keys of a tile; two an item
-constexpr int kThreads = 384;               // 2 warpgroups, K warp, Q warp, 2 MMA warps
+// 2 warpgroups for the powers, K warp, Q warp, 2 MMA warps; e4m3: 2 warpgroups that convert
+template <bool E4M3>
+constexpr int kThreads = E4M3 ? 640 : 384;
 constexpr int kQStages = 3;
 
+constexpr int kMaxBufs = 8;                 // K buffers a tile
+constexpr int kItems = 4;                   // items ahead
+
+// Shared memory: the e4m3 keys' bf16 tiles, kQStages query tiles (their rows
+// rounded up to 8, in parts of 64 elements), and as many K buffers a tile as
+// fit: the fewer rows, the more of K in flight.
 template <int D, bool E4M3>
 struct Cfg {
     static constexpr int kRaw = kKeys * (E4M3 ? D : 2 * D);    // a K tile as it is cached
     static constexpr int kTile = kKeys * 2 * D;                // bf16
-    static constexpr int kQTile = 128 * 2 * D;
-    static constexpr int oRaw = 0;                             // [tile][buffer]
-    static constexpr int oK = 4 * kRaw;                        // e4m3: [tile] in bf16
-    static constexpr int oQ = oK + (E4M3 ? 2 * kTile : 0);
-    static constexpr int kBytes = oQ + kQStages * kQTile;      // then Shared
+    static constexpr int oQ = E4M3 ? 2 * kTile : 0;            // (before it, e4m3: [tile] in bf16)
+    static constexpr int kTotal = 232448 - 3072;               // then Shared
+
+    __host__ __device__ __forceinline__ static int part(const KeywArgs& a) {
+        return (a.tile_tokens * a.tile_heads + 7) / 8 * 1024;
+    }
+    __host__ __device__ __forceinline__ static int q_tile(const KeywArgs& a) { return part(a) * (D / 64); }
+    __host__ __device__ __forceinline__ static int raw(const KeywArgs& a) { return oQ + kQStages * q_tile(a); }
+    __host__ __device__ __forceinline__ static int bufs(const KeywArgs& a) {
+        const int n = (kTotal - raw(a)) / (2 * kRaw);
+        return n < kMaxBufs ? n : kMaxBufs;
+    }
 };
 
 struct Shared {
     alignas(16) float off[2][2][128];       // [tile][buffer] -lse log2 e of the columns' rows
     uint32_t live[2][2][4];                 // which columns count
-    uint64_t k_full[2][2], k_empty[2][2];   // [tile][buffer]
-    uint64_t k_bf16[2];
+    alignas(16) int item[kItems][12];       // see Item
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t k_full[2][kMaxBufs], k_empty[2][kMaxBufs];   // [tile][buffer]
+    uint64_t k_bf16[2], k_free[2];          // e4m3: the bf16 tile is there, is no longer read
     uint64_t q_full[kQStages], q_empty[kQStages];
     uint64_t s_full[2][2], s_empty[2][2];   // [tile][buffer]
     uint32_t tmem;
 };
 
-// Items in the order (sequence, key group, head), CTA c taking every
-// gridDim.x-th; every role walks them for itself.
-struct Items {
-    Seq s;
-    int b, h, j0;
-    int t0, t1;                             // row tiles that see some of its keys
-    int64_t idx, base;                      // this item, items before sequence b
-    int64_t count;                          // items of it
-
-    __device__ __forceinline__ void start(const KeywArgs& ka) {
-        b = -1;
-        base = count = 0;
-        idx = int64_t(blockIdx.x) - gridDim.x;
-    }
-    __device__ __forceinline__ bool next(const KeywArgs& ka) {
-        const AttnArgs& a = ka.a;
-        idx += gridDim.x;
-        while (idx >= base + count) {
-            base += count;
-            if (++b >= a.sq.n) return false;
-            s = load_seq(a.sq, a.kv.page, b, a.err);
-            count = int64_t(a.kv.heads) * ((s.len + 2 * kKeys - 1) / (2 * kKeys));
-        }
-        const int in = static_cast<int>(idx - base), g = in / a.kv.heads;
-        h = in - g * a.kv.heads;
-        j0 = g * 2 * kKeys;
-        const int j1 = min(j0 + 2 * kKeys, s.len);
-        int i0 = 0, i1 = s.nq;              // queries that see some of these keys
-        if (!a.draft && a.causal) i0 = max(0, j0 - s.first);
-        if (a.window > 0) i1 = static_cast<int>(min(int64_t(s.nq), max(int64_t(0), int64_t(j1) - 1 - s.first + a.window)));
-        t0 = i0 / ka.tile_tokens;
-        t1 = i1 > i0 ? (i1 + ka.tile_tokens - 1) / ka.tile_tokens : t0;
-        return true;
-    }
+// An item as the roles read it; b < 0: no more.
+struct Item {
+    int b, h, j0, q0;
+    int nq, first, len, t0;                 // row tiles t0 .. t1 - 1 see some of its keys
+    int t1;
 };
 
-// A counted use of a two-buffer resource.
+// A place in a ring of buffers, and the phase of its barriers.
 struct Turn {
-    uint32_t n = 0;
-    __device__ __forceinline__ int buf() const { return n & 1; }
-    __device__ __forceinline__ uint32_t phase() const { return (n >> 1) & 1u; }
-};
-
-struct QSlot {
     int st = 0;
     uint32_t ph = 0;
-    __device__ __forceinline__ void step() {
-        if (++st == kQStages) {
+    __device__ __forceinline__ void step(int n) {
+        if (++st == n) {
             st = 0;
             ph ^= 1u;
         }
@@ -111,42 +94,134 @@ struct Waiter {
     }
 };
 
+// Items in the order (sequence, key group, head), CTA c taking every
+// gridDim.x-th.  The K warp walks them once for the CTA and hands them to the
+// other roles through a small ring (every warp on its own walk: 12 to 20 times
+// the bookkeeping, which then paced the stream of verify blocks).
+struct Scheduler {
+    Seq s;
+    int b, g, h, groups, dg, dh;
+    int64_t skip;                           // items still to pass before this CTA's next, past (g, h)
+
+    __device__ __forceinline__ void start(const KeywArgs& ka) {
+        b = -1;
+        g = h = groups = 0;
+        dg = gridDim.x / ka.a.kv.heads;
+        dh = gridDim.x - dg * ka.a.kv.heads;
+        skip = blockIdx.x;
+    }
+    __device__ __forceinline__ bool next(const KeywArgs& ka, Item& it) {
+        const AttnArgs& a = ka.a;
+        if (b >= 0) {                       // gridDim.x items on
+            g += dg;
+            h += dh;
+            if (h >= a.kv.heads) {
+                h -= a.kv.heads;
+                ++g;
+            }
+            skip = int64_t(g - groups) * a.kv.heads + h;     // past this sequence's end, if it is not below 0
+        }
+        while (b < 0 || g >= groups) {
+            if (++b >= a.sq.n) return false;
+            s = load_seq(a.sq, a.kv.page, b, a.err);
+            groups = (s.len + 2 * kKeys - 1) / (2 * kKeys);
+            const int64_t count = int64_t(groups) * a.kv.heads;
+            if (skip >= count) {
+                skip -= count;
+                g = groups;
+                continue;
+            }
+            g = static_cast<int>(skip / a.kv.heads);
+            h = static_cast<int>(skip - int64_t(g) * a.kv.heads);
+        }
+        const int j0 = g * 2 * kKeys, j1 = min(j0 + 2 * kKeys, s.len);
+        int i0 = 0, i1 = s.nq;              // queries that see some of these keys
+        if (!a.draft && a.causal) i0 = min(max(0, j0 - s.first), s.nq);
+        if (a.window > 0) i1 = static_cast<int>(min(int64_t(s.nq), max(int64_t(0), int64_t(j1) - 1 - s.first + a.window)));
+        const int t0 = ka.tile_of(i0), t1 = i1 > i0 ? ka.tile_of(i1 - 1) + 1 : t0;
+        it = Item{b, h, j0, s.q0, s.nq, s.first, s.len, t0, t1};
+        return true;
+    }
+};
+
+// A role's place in the ring of items; next() copies one out.  One warp each.
+struct Feed {
+    Shared& sh;
+    Waiter& wait;
+    Turn at;
+
+    __device__ __forceinline__ bool next(Item& it) {
+        wait(&sh.item_full[at.st], at.ph);
+        const int4 x = *reinterpret_cast<const int4*>(&sh.item[at.st][0]);
+        const int4 y = *reinterpret_cast<const int4*>(&sh.item[at.st][4]);
+        it = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, sh.item[at.st][8]};
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.item_empty[at.st]);
+        at.step(kItems);
+        return !wait.dead && it.b >= 0;
+    }
+};
+
 template <int D, bool E4M3>
 __device__ __forceinline__ void load_keys(const KeywArgs& ka, const CUtensorMap& map, Shared& sh, uint8_t* smem) {
     using C = Cfg<D, E4M3>;
     constexpr int kBox = E4M3 ? D : 64, kBoxBytes = E4M3 ? D : 128, kParts = D / kBox;
     const AttnArgs& a = ka.a;
     const int lane = threadIdx.x & 31, page = a.kv.page, pl = a.kv.page_log2, np = kKeys >> pl;
-    Items it;
-    it.start(ka);
+    const int bufs = C::bufs(ka), raw = C::raw(ka);
+    Scheduler sc;
+    sc.start(ka);
     Waiter wait{a};
-    Turn use[2];
-    while (it.next(ka)) {
-        const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
-        const int p_hi = (it.s.len + page - 1) >> pl, p0 = it.j0 >> pl, p = p0 + lane;
-        const bool mine = lane < 2 * np && p < p_hi;
-        int pg = mine ? table[p] : 0;
+    Turn use[2], slot;
+    int p0 = 0, p_hi = 0, pg = 0, head = 0;
+    bool mine = false;
+    // the next item, handed on, and its page indices, read a step ahead
+    auto fetch = [&]() {
+        Item it{-1, 0, 0, 0, 0, 0, 0, 0, 0};
+        const bool more = sc.next(ka, it);
+        wait(&sh.item_empty[slot.st], slot.ph ^ 1u);
+        if (lane == 0) {
+            *reinterpret_cast<int4*>(&sh.item[slot.st][0]) = make_int4(it.b, it.h, it.j0, it.q0);
+            *reinterpret_cast<int4*>(&sh.item[slot.st][4]) = make_int4(it.nq, it.first, it.len, it.t0);
+            sh.item[slot.st][8] = it.t1;
+            mbar_arrive(&sh.item_full[slot.st]);
+        }
+        __syncwarp();
+        slot.step(kItems);
+        if (!more) return false;
+        p0 = it.j0 >> pl;
+        p_hi = (it.len + page - 1) >> pl;
+        head = it.h;
+        mine = lane < 2 * np && p0 + lane < p_hi;
+        pg = mine ? a.sq.table[int64_t(it.b) * a.sq.max_pages + p0 + lane] : 0;
+        return true;
+    };
+    bool more = fetch();
+    while (more) {
         if (mine && (pg < 0 || pg >= a.kv.n_pages)) {
             record_error(a.err, MOE_ERR_INVALID_ARG);
             pg = a.kv.n_pages;                                  // out of range: reads as zeros
         }
+        const int c0 = p0, c_hi = p_hi, c_pg = pg, c_head = head;
+        const bool c_mine = mine;
+        more = fetch();
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            const int first = p0 + w * np, boxes = min(first + np, p_hi) - first;
+            const int first = c0 + w * np, boxes = min(first + np, c_hi) - first;
             if (boxes <= 0) continue;
-            const int buf = use[w].buf();
-            wait(&sh.k_empty[w][buf], use[w].phase() ^ 1u);
-            ++use[w].n;
-            uint8_t* dst = smem + C::oRaw + (2 * w + buf) * C::kRaw;
+            const int buf = use[w].st;
+            wait(&sh.k_empty[w][buf], use[w].ph ^ 1u);
+            use[w].step(bufs);
+            uint8_t* dst = smem + raw + (w * bufs + buf) * C::kRaw;
             if (lane == 0)
                 mbar_arrive_expect_tx(&sh.k_full[w][buf], wait.dead ? 0 : boxes * page * (E4M3 ? D : 2 * D));
             __syncwarp();
             for (int k = 0; k < np; ++k) {
-                if (lane == w * np + k && mine && !wait.dead) {
+                if (lane == w * np + k && c_mine && !wait.dead) {
 #pragma unroll
                     for (int x = 0; x < kParts; ++x)
                         tma_load_4d(dst + k * page * kBoxBytes + x * kKeys * 128, &map, &sh.k_full[w][buf], x * kBox, 0,
-                                    it.h, pg);
+                                    c_head, c_pg);
                 }
                 __syncwarp();
             }
@@ -160,11 +235,12 @@ __device__ __forceinline__ void load_rows(const KeywArgs& ka, const CUtensorMap&
     const AttnArgs& a = ka.a;
     const int lane = threadIdx.x & 31;
     const uint32_t bytes = ka.tile_tokens * ka.tile_heads * D * 2;
-    Items it;
-    it.start(ka);
+    const int q_tile = C::q_tile(ka), part = C::part(ka);
+    Item it;
     Waiter wait{a};
-    QSlot q;
-    while (it.next(ka)) {
+    Feed feed{sh, wait};
+    Turn q;
+    while (feed.next(it)) {
         for (int t = it.t0; t < it.t1; ++t)
             for (int hc = 0; hc < a.group; hc += ka.tile_heads) {
                 wait(&sh.q_empty[q.st], q.ph ^ 1u);
@@ -173,12 +249,12 @@ __device__ __forceinline__ void load_rows(const KeywArgs& ka, const CUtensorMap&
                     if (!wait.dead) {
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
-                            tma_load_3d(smem + C::oQ + q.st * C::kQTile + x * 16384, &map, &sh.q_full[q.st], 64 * x,
-                                        it.h * a.group + hc, it.s.q0 + t * ka.tile_tokens);
+                            tma_load_3d(smem + C::oQ + q.st * q_tile + x * part, &map, &sh.q_full[q.st], 64 * x,
+                                        it.h * a.group + hc, it.q0 + t * ka.tile_tokens);
                     }
                 }
                 __syncwarp();
-                q.step();
+                q.step(kQStages);
             }
     }
 }
@@ -188,47 +264,47 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
     using C = Cfg<D, E4M3>;
     const AttnArgs& a = ka.a;
     const uint64_t q_desc = sdesc(smem_u32(smem + C::oQ), 16, 1024, kSw128);
-    Items it;
-    it.start(ka);
+    const int q_tile = C::q_tile(ka), part = C::part(ka), bufs = C::bufs(ka), raw = C::raw(ka);
+    Item it;
     Waiter wait{a};
-    QSlot q;
-    Turn key, buf;
+    Feed feed{sh, wait};
+    Turn q, key, buf;
     uint32_t kp = 0;
-    while (it.next(ka)) {
-        const bool on = it.j0 + w * kKeys < it.s.len;
+    while (feed.next(it)) {
+        const bool on = it.j0 + w * kKeys < it.len;
         int kb = 0;
         uint64_t k_desc = 0;
         if (on) {
             if constexpr (E4M3) {
                 wait(&sh.k_bf16[w], kp);
                 kp ^= 1u;
-                k_desc = sdesc(smem_u32(smem + C::oK + w * C::kTile), 16, 1024, kSw128);
+                k_desc = sdesc(smem_u32(smem + w * C::kTile), 16, 1024, kSw128);
             } else {
-                kb = key.buf();
-                wait(&sh.k_full[w][kb], key.phase());
-                ++key.n;
-                k_desc = sdesc(smem_u32(smem + C::oRaw + (2 * w + kb) * C::kRaw), 16, 1024, kSw128);
+                kb = key.st;
+                wait(&sh.k_full[w][kb], key.ph);
+                key.step(bufs);
+                k_desc = sdesc(smem_u32(smem + raw + (w * bufs + kb) * C::kRaw), 16, 1024, kSw128);
             }
         }
         for (int t = it.t0; t < it.t1; ++t) {
-            const int tokens = min(ka.tile_tokens, it.s.nq - t * ka.tile_tokens);
+            const int tokens = min(ka.tile_tokens, it.nq - t * ka.tile_tokens);
             const uint32_t id = idesc(1, 1, false, (tokens * ka.tile_heads + 15) & ~15);
             for (int hc = 0; hc < a.group; hc += ka.tile_heads) {
                 wait(&sh.q_full[q.st], q.ph);
-                const int sb = buf.buf();
+                const int sb = buf.st;
                 if (on) {
-                    wait(&sh.s_empty[w][sb], buf.phase() ^ 1u);
-                    ++buf.n;
+                    wait(&sh.s_empty[w][sb], buf.ph ^ 1u);
+                    buf.step(2);
                 }
                 tc_fence_after();
-                const uint64_t qd = q_desc + q.st * (C::kQTile >> 4);
+                const uint64_t qd = q_desc + (q.st * q_tile >> 4);
                 const uint32_t d = sh.tmem + (2 * w + sb) * 128;
                 if (elect_one()) {
                     if (on) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                            mma_ss<false>(d, k_desc + off, qd + off, id, k > 0);
+                            mma_ss<false>(d, k_desc + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                                          qd + (((k >> 2) * part + (k & 3) * 32) >> 4), id, k > 0);
                         }
                         mma_commit(&sh.s_full[w][sb]);
                         mma_commit(&sh.q_empty[q.st]);
@@ -237,12 +313,65 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
                     }
                 }
                 __syncwarp();
-                q.step();
+                q.step(kQStages);
             }
         }
-        if (!E4M3 && on) {
-            if (elect_one()) mma_commit(&sh.k_empty[w][kb]);
+        if (on) {
+            if (elect_one()) mma_commit(E4M3 ? &sh.k_free[w] : &sh.k_empty[w][kb]);
             __syncwarp();
+        }
+    }
+}
+
+// e4m3: one tile of the items' pairs to bf16.
+template <int D>
+__device__ __forceinline__ void convert(const KeywArgs& ka, Shared& sh, uint8_t* smem, int w) {
+    using C = Cfg<D, true>;
+    const int lr = threadIdx.x & 127, lane = threadIdx.x & 31;
+    Item it;
+    Waiter wait{ka.a};
+    Feed feed{sh, wait};
+    const int bufs = C::bufs(ka);
+    Turn key;
+    uint32_t fp = 0;
+    while (feed.next(it)) {
+        if (it.j0 + w * kKeys >= it.len) continue;
+        const int kb = key.st;
+        wait(&sh.k_full[w][kb], key.ph);
+        key.step(bufs);
+        const uint8_t* raw = smem + C::raw(ka) + (w * bufs + kb) * C::kRaw;
+        uint8_t* dst = smem + w * C::kTile;
+        uint4 in[D / 16];
+#pragma unroll
+        for (int ch = 0; ch < D / 16; ++ch)
+            in[ch] = *reinterpret_cast<const uint4*>(
+                raw + lr * D + ((D == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3)) << 4));
+        wait(&sh.k_free[w], fp ^ 1u);
+        fp ^= 1u;
+        uint32_t nan = 0;
+#pragma unroll
+        for (int ch = 0; ch < D / 16; ++ch) {
+            const uint4 x = in[ch];
+            uint32_t y[8];
+            e4m3x4_to_bf16(x.x, y[0], y[1], nan);
+            e4m3x4_to_bf16(x.y, y[2], y[3], nan);
+            e4m3x4_to_bf16(x.z, y[4], y[5], nan);
+            e4m3x4_to_bf16(x.w, y[6], y[7], nan);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c2 = 2 * ch + e;
+                *reinterpret_cast<uint4*>(dst + (c2 >> 3) * 16384 + lr * 128 + (((c2 & 7) ^ (lr & 7)) << 4)) =
+                    make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            }
+        }
+        if (nan & 0x80808080u) {             // a NaN code makes its key's scores NaN: one NaN in the row does
+            *reinterpret_cast<uint16_t*>(dst + lr * 128 + ((lr & 7) << 4)) = 0x7FC0u;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sh.k_empty[w][kb]);
+            mbar_arrive(&sh.k_bf16[w]);
         }
     }
 }
@@ -278,102 +407,102 @@ __device__ __forceinline__ void weigh(const KeywArgs& ka, Shared& sh, uint8_t* s
     const bool draft = a.draft != nullptr;
     // the row of column lr: token and head within a tile
     const int r_tok = lr / ka.tile_heads, r_head = lr - r_tok * ka.tile_heads;
-    Items it;
-    it.start(ka);
+    const int heads = a.group;
+    // an item of this tile, its key's place in the scores, the score, and the log-sum-exp of its first
+    // row tile's columns: read an item ahead
     Waiter wait{a};
-    Turn key, buf;
-    while (it.next(ka)) {
-        const int jt = it.j0 + w * kKeys;
-        if (jt >= it.s.len) continue;
-        if constexpr (E4M3) {
-            const int kb = key.buf();
-            wait(&sh.k_full[w][kb], key.phase());
-            ++key.n;
-            const uint8_t* raw = smem + C::oRaw + (2 * w + kb) * C::kRaw;
-            uint8_t* dst = smem + C::oK + w * C::kTile;         // (its last products are done: their S was waited for)
-#pragma unroll
-            for (int ch = 0; ch < D / 16; ++ch) {
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    raw + lr * D + ((D == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3)) << 4));
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                uint32_t y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 f = unpack_e4m3((xs[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-                    y[e] = pack_bf16(f.x, f.y);
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c2 = 2 * ch + e;
-                    *reinterpret_cast<uint4*>(dst + (c2 >> 3) * 16384 + lr * 128 + (((c2 & 7) ^ (lr & 7)) << 4)) =
-                        make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                }
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.k_empty[w][kb]);
-                mbar_arrive(&sh.k_bf16[w]);
-            }
-        }
-        const int j = jt + lr;
-        const int64_t at = (int64_t(it.b) * a.kv.heads + it.h) * ka.score_stride + j;
-        const bool store = j < it.s.len && j < ka.score_stride;
-        const float before = store && j < it.s.first ? ka.decay * ka.scores[at] : 0.0f;
+    Feed feed{sh, wait};
+    struct Ahead {
+        Item it;
+        bool more;
+        int64_t at;
+        bool store;
+        float before, z;
+    };
+    auto row_lse = [&](const Item& it, int t, int hc) {
+        const int i = t * ka.tile_tokens + r_tok, hd = hc + r_head;
+        const bool ok = t < it.t1 && r_tok < ka.tile_tokens && i < it.nq && hd < heads;
+        return ok ? __ldg(a.lse + int64_t(it.q0 + i) * a.q_heads + it.h * heads + hd) : kNegInf;
+    };
+    auto fetch = [&](Ahead& x) {
+        do {
+            x.more = feed.next(x.it);
+        } while (x.more && x.it.j0 + w * kKeys >= x.it.len);
+        if (!x.more) return;
+        const int j = x.it.j0 + w * kKeys + lr;
+        x.at = (int64_t(x.it.b) * a.kv.heads + x.it.h) * ka.score_stride + j;
+        x.store = j < x.it.len && j < ka.score_stride;
+        x.before = x.store && j < x.it.first ? ka.scores[x.at] : 0.0f;
+        x.z = row_lse(x.it, x.it.t0, 0);
+    };
+    Ahead nx;
+    fetch(nx);
+    Turn buf;
+    while (nx.more) {
+        const Item it = nx.it;
+        const int jt = it.j0 + w * kKeys, j = jt + lr;
+        const int64_t at = nx.at;
+        const bool store = nx.store;
+        const float before = ka.decay * nx.before;
+        float z = nx.z, sum = 0.0f;
+        fetch(nx);
         const float c = a.scale * kLog2e * (E4M3 ? a.kv.k_scale[it.h] : 1.0f);
-        const int heads_left = a.group;
-        // the next tile's log-sum-exp of this thread's column, a tile ahead
-        auto row_lse = [&](int t, int hc) {
-            const int i = t * ka.tile_tokens + r_tok, hd = hc + r_head;
-            const bool ok = t < it.t1 && r_tok < ka.tile_tokens && i < it.s.nq && hd < heads_left;
-            return ok ? __ldg(a.lse + int64_t(it.s.q0 + i) * a.q_heads + it.h * a.group + hd) : kNegInf;
-        };
-        float z = row_lse(it.t0, 0), sum = 0.0f;
         for (int t = it.t0; t < it.t1; ++t) {
-            const int i0 = t * ka.tile_tokens, tokens = min(ka.tile_tokens, it.s.nq - i0);
-            const bool seen = (draft ? jt + kKeys <= it.s.first : !a.causal || jt + kKeys <= it.s.first + i0 + 1) &&
-                              !(a.window > 0 && jt <= it.s.first + i0 + tokens - 1 - a.window);
+            const int i0 = t * ka.tile_tokens, tokens = min(ka.tile_tokens, it.nq - i0);
+            const bool seen = (draft ? jt + kKeys <= it.first : !a.causal || jt + kKeys <= it.first + i0 + 1) &&
+                              !(a.window > 0 && jt <= it.first + i0 + tokens - 1 - a.window);
             for (int hc = 0; hc < a.group; hc += ka.tile_heads) {
-                const int sb = buf.buf(), rows = tokens * min(ka.tile_heads, a.group - hc);
+                const int sb = buf.st, rows = tokens * min(ka.tile_heads, a.group - hc);
                 const bool live = fabsf(z) != INFINITY;
                 sh.off[w][sb][lr] = live ? -z * kLog2e : 0.0f;
                 const uint32_t word = __ballot_sync(0xFFFFFFFFu, live);
                 if (lane == 0) sh.live[w][sb][wq] = word;
                 named_bar(1 + w, 128);
-                z = hc + ka.tile_heads < a.group ? row_lse(t, hc + ka.tile_heads) : row_lse(t + 1, 0);
-                wait(&sh.s_full[w][sb], buf.phase());
-                ++buf.n;
+                z = hc + ka.tile_heads < heads ? row_lse(it, t, hc + ka.tile_heads) : row_lse(it, t + 1, 0);
+                wait(&sh.s_full[w][sb], buf.ph);
+                buf.step(2);
                 tc_fence_after();
                 const uint32_t col = tm + sb * 128;
                 const float* off = sh.off[w][sb];
                 const uint32_t* words = sh.live[w][sb];
                 float p0 = 0.0f, p1 = 0.0f;
-                if (seen && rows == 128 && (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) add_powers<32, false>(col + 32 * q, off + 32 * q, c, 0, p0, p1);
-                } else {
-                    // columns of rows that see key j: a range by token, or by the rows' draft masks
-                    int lo = 0, hi = rows;
-                    const int64_t rel = int64_t(j) - it.s.first - i0;         // j's place less the tile's first token's
-                    const int th = ka.tile_heads;
+                // columns of rows that see key j: a range by token, or by the rows' draft masks
+                const int th = ka.tile_heads;
+                int lo = 0, hi = rows;
+                if (!seen) {
+                    const int64_t rel = int64_t(j) - it.first - i0;             // j's place less the tile's first token's
                     if (!draft && a.causal) lo = static_cast<int>(max(int64_t(0), min(rel, int64_t(128)))) * th;
                     if (a.window > 0) hi = min(hi, static_cast<int>(max(int64_t(0), min(rel + a.window, int64_t(128)))) * th);
+                }
+                const bool whole = seen && rows == 128 && (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu;
+                if (whole) {
+#pragma unroll(E4M3 ? 1 : 4)
+                    for (int q = 0; q < 4; ++q) add_powers<32, false>(col + 32 * q, off + 32 * q, c, 0, p0, p1);
+                }
 #pragma unroll 1
-                    for (int n = 0; n < rows; n += 16) {
-                        uint32_t bits = (words[n >> 5] >> (n & 16)) & 0xFFFFu;
+                for (int q = 0; q < 4 && !whole; ++q) {
+                    if (32 * q >= rows) break;
+                    const uint32_t word = words[q];
+                    if (seen && word == 0xFFFFFFFFu) {
+                        add_powers<32, false>(col + 32 * q, off + 32 * q, c, 0, p0, p1);
+                        continue;
+                    }
+#pragma unroll 1
+                    for (int n = 32 * q; n < min(32 * q + 32, rows); n += 16) {
+                        uint32_t bits = (word >> (n & 16)) & 0xFFFFu;
                         if (!seen) {
                             const int l = min(max(lo - n, 0), 16), u = min(max(hi - n, 0), 16);
                             bits &= ((1u << u) - 1u) & ~((1u << l) - 1u);
-                            const int place = j - it.s.first;
+                            const int place = j - it.first;
                             if (draft && place >= 0) {
                                 for (int e = 0; e < 16 && n + e < rows; ++e) {
-                                    const uint64_t m = a.draft[it.s.q0 + i0 + (n + e) / th];
+                                    const uint64_t m = a.draft[it.q0 + i0 + (n + e) / th];
                                     if (place >= 64 || !((m >> place) & 1ull)) bits &= ~(1u << e);
                                 }
                             }
+                            __syncwarp();
                         }
                         add_powers<16, true>(col + n, off + n, c, bits, p0, p1);
-                        __syncwarp();
                     }
                 }
                 sum += p0 + p1;
@@ -387,20 +516,27 @@ __device__ __forceinline__ void weigh(const KeywArgs& ka, Shared& sh, uint8_t* s
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) keyw_kernel(const KeywArgs ka, const __grid_constant__ KeywMaps maps) {
+__global__ void __launch_bounds__(kThreads<E4M3>, 1) keyw_kernel(const KeywArgs ka, const __grid_constant__ KeywMaps maps) {
     using C = Cfg<D, E4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    Shared& sh = *reinterpret_cast<Shared*>(smem + C::kBytes);
+    Shared& sh = *reinterpret_cast<Shared*>(smem + C::kTotal);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int w = 0; w < 2; ++w) {
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < kMaxBufs; ++i) {
                 mbar_init(&sh.k_full[w][i], 1);
                 mbar_init(&sh.k_empty[w][i], E4M3 ? 4 : 1);
+            }
+            for (int i = 0; i < 2; ++i) {
                 mbar_init(&sh.s_full[w][i], 1);
                 mbar_init(&sh.s_empty[w][i], 4);
             }
             mbar_init(&sh.k_bf16[w], 4);
+            mbar_init(&sh.k_free[w], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], kThreads<E4M3> / 32 - 1);   // every warp but the K warp
         }
         for (int i = 0; i < kQStages; ++i) {
             mbar_init(&sh.q_full[i], 1);
@@ -425,8 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1) keyw_kernel(const KeywArgs ka, co
         load_keys<D, E4M3>(ka, maps.k, sh, smem);
     else if (warp == 9)
         load_rows<D, E4M3>(ka, maps.q, sh, smem);
-    else
+    else if (warp < 12)
         multiply<D, E4M3>(ka, sh, smem, warp - 10);
+    else if constexpr (E4M3)
+        convert<D>(ka, sh, smem, (warp - 12) >> 2);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -435,11 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1) keyw_kernel(const KeywArgs ka, co
 
 template <int D, bool E4M3>
 cudaError_t launch(const KeywArgs& a, const KeywMaps& m, int n_sms, cudaStream_t s) {
-    constexpr size_t smem = Cfg<D, E4M3>::kBytes + sizeof(Shared);
+    constexpr size_t smem = Cfg<D, E4M3>::kTotal + sizeof(Shared);
     static_assert(smem <= 232448, "227 KB a CTA");
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(keyw_kernel<D, E4M3>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(keyw_kernel<D, E4M3>, dim3(n_sms), dim3(kThreads), smem, s, a, m);
+    e = launch_pdl(keyw_kernel<D, E4M3>, dim3(n_sms), dim3(kThreads<E4M3>), smem, s, a, m);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -290,3 +290,39 @@ def test_key_weights_without_new_tokens():
     assert m.moe_get_device_error(ws) == 0
     for b, n in enumerate(p.lens):
         assert torch.equal(got[b, :, :n], scores[b, :, :n] * 0.5) and torch.equal(got[b, :, n:], scores[b, :, n:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_key_weights_all_codes_and_nan(dtype):
+    """Every finite e4m3 code (subnormals too) counts with its value, and a NaN
+    key makes its own weight NaN and no other."""
+    p = ref.Problem([256], [1], 8, 1, 128, 64, dtype, seed=24, q_scale=0.2)
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes[[0x7F, 0xFF]] = 0
+    grid = codes[(torch.arange(256)[:, None] + 7 * torch.arange(128)[None]) % 256]
+    vals = grid.view(torch.float8_e4m3fn).float() / 64
+    for j in range(256):
+        pg, o = int(p.table[0, j // 64]), j % 64
+        if dtype == "e4m3":
+            p.k.view(torch.uint8)[pg, 0, o] = grid[j]
+        else:
+            p.k[pg, 0, o] = vals[j].bfloat16()
+    if dtype == "e4m3":
+        p.k_scale[:] = 1 / 64
+    lse = torch.from_numpy(ref.attention(p)[1]).float()
+    scores = torch.zeros(1, 1, 256)
+    want, tol = ref.key_weights(p, lse, scores, 1.0)
+    pg, o = int(p.table[0, 1]), 9
+    if dtype == "e4m3":
+        p.k.view(torch.uint8)[pg, 0, o, 77] = 0xFF
+    else:
+        p.k[pg, 0, o, 77] = float("nan")
+    p.cuda()
+    attn = m.Attn(p.hq, p.scale, wait_timeout_us=200000)
+    ws = torch.zeros(m.moe_attn_workspace_bytes(attn, p.cache), dtype=torch.uint8, device="cuda")
+    got = scores.cuda()
+    m.moe_key_weights(attn, p.cache, p.seqs, p.d_q(), lse.cuda(), got, got, ws)
+    x = got.cpu().numpy().astype(np.float64)[0, 0]
+    assert np.isnan(x[64 + 9])
+    keep = np.arange(256) != 64 + 9
+    assert np.all(np.abs(x - want[0, 0])[keep] <= tol[0, 0][keep])
