@@ -29,26 +29,30 @@ constexpr int kKeys = 128;                  // keys of a tile; two an item
 // 2 warpgroups for the powers, K warp, Q warp, 2 MMA warps; e4m3: 2 warpgroups that convert
 template <bool E4M3>
 constexpr int kThreads = E4M3 ? 640 : 384;
-constexpr int kQStages = 3;
 
 constexpr int kMaxBufs = 8;                 // K buffers a tile
 constexpr int kItems = 4;                   // items ahead
 
-// Shared memory: the e4m3 keys' bf16 tiles, kQStages query tiles (their rows
-// rounded up to 8, in parts of 64 elements), and as many K buffers a tile as
-// fit: the fewer rows, the more of K in flight.
+// Shared memory: the query tiles (their rows rounded up to 8, in parts of 64
+// elements), the e4m3 keys' bf16 tiles (two of each where rows are few: with
+// one, a tile's conversion waits for the products of the one before it), and
+// as many K buffers a tile as fit: the fewer rows, the more of K in flight.
 template <int D, bool E4M3>
 struct Cfg {
+    static constexpr int kQStages = E4M3 ? 2 : 3;
     static constexpr int kRaw = kKeys * (E4M3 ? D : 2 * D);    // a K tile as it is cached
     static constexpr int kTile = kKeys * 2 * D;                // bf16
-    static constexpr int oQ = E4M3 ? 2 * kTile : 0;            // (before it, e4m3: [tile] in bf16)
     static constexpr int kTotal = 232448 - 3072;               // then Shared
 
     __host__ __device__ __forceinline__ static int part(const KeywArgs& a) {
         return (a.tile_tokens * a.tile_heads + 7) / 8 * 1024;
     }
     __host__ __device__ __forceinline__ static int q_tile(const KeywArgs& a) { return part(a) * (D / 64); }
-    __host__ __device__ __forceinline__ static int raw(const KeywArgs& a) { return oQ + kQStages * q_tile(a); }
+    __host__ __device__ __forceinline__ static int conv(const KeywArgs& a) {      // bf16 tiles a key tile
+        return !E4M3 ? 0 : (a.tile_tokens * a.tile_heads <= 64 ? 2 : 1);
+    }
+    __host__ __device__ __forceinline__ static int k16(const KeywArgs& a) { return kQStages * q_tile(a); }
+    __host__ __device__ __forceinline__ static int raw(const KeywArgs& a) { return k16(a) + 2 * conv(a) * kTile; }
     __host__ __device__ __forceinline__ static int bufs(const KeywArgs& a) {
         const int n = (kTotal - raw(a)) / (2 * kRaw);
         return n < kMaxBufs ? n : kMaxBufs;
@@ -61,8 +65,8 @@ struct Shared {
     alignas(16) int item[kItems][12];       // see Item
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t k_full[2][kMaxBufs], k_empty[2][kMaxBufs];   // [tile][buffer]
-    uint64_t k_bf16[2], k_free[2];          // e4m3: the bf16 tile is there, is no longer read
-    uint64_t q_full[kQStages], q_empty[kQStages];
+    uint64_t k_bf16[2][2], k_free[2][2];    // e4m3, [tile][bf16 tile]: it is there, is no longer read
+    uint64_t q_full[3], q_empty[3];
     uint64_t s_full[2][2], s_empty[2][2];   // [tile][buffer]
     uint32_t tmem;
 };
@@ -249,12 +253,12 @@ __device__ __forceinline__ void load_rows(const KeywArgs& ka, const CUtensorMap&
                     if (!wait.dead) {
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
-                            tma_load_3d(smem + C::oQ + q.st * q_tile + x * part, &map, &sh.q_full[q.st], 64 * x,
+                            tma_load_3d(smem + q.st * q_tile + x * part, &map, &sh.q_full[q.st], 64 * x,
                                         it.h * a.group + hc, it.q0 + t * ka.tile_tokens);
                     }
                 }
                 __syncwarp();
-                q.step(kQStages);
+                q.step(C::kQStages);
             }
     }
 }
@@ -263,22 +267,23 @@ template <int D, bool E4M3>
 __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t* smem, int w) {
     using C = Cfg<D, E4M3>;
     const AttnArgs& a = ka.a;
-    const uint64_t q_desc = sdesc(smem_u32(smem + C::oQ), 16, 1024, kSw128);
+    const uint64_t q_desc = sdesc(smem_u32(smem), 16, 1024, kSw128);
     const int q_tile = C::q_tile(ka), part = C::part(ka), bufs = C::bufs(ka), raw = C::raw(ka);
     Item it;
     Waiter wait{a};
     Feed feed{sh, wait};
     Turn q, key, buf;
-    uint32_t kp = 0;
+    const int conv = C::conv(ka), k16 = C::k16(ka);
     while (feed.next(it)) {
         const bool on = it.j0 + w * kKeys < it.len;
         int kb = 0;
         uint64_t k_desc = 0;
         if (on) {
             if constexpr (E4M3) {
-                wait(&sh.k_bf16[w], kp);
-                kp ^= 1u;
-                k_desc = sdesc(smem_u32(smem + w * C::kTile), 16, 1024, kSw128);
+                kb = key.st;
+                wait(&sh.k_bf16[w][kb], key.ph);
+                key.step(conv);
+                k_desc = sdesc(smem_u32(smem + k16 + (w * conv + kb) * C::kTile), 16, 1024, kSw128);
             } else {
                 kb = key.st;
                 wait(&sh.k_full[w][kb], key.ph);
@@ -313,11 +318,11 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
                     }
                 }
                 __syncwarp();
-                q.step(kQStages);
+                q.step(C::kQStages);
             }
         }
         if (on) {
-            if (elect_one()) mma_commit(E4M3 ? &sh.k_free[w] : &sh.k_empty[w][kb]);
+            if (elect_one()) mma_commit(E4M3 ? &sh.k_free[w][kb] : &sh.k_empty[w][kb]);
             __syncwarp();
         }
     }
@@ -331,23 +336,21 @@ __device__ __forceinline__ void convert(const KeywArgs& ka, Shared& sh, uint8_t*
     Item it;
     Waiter wait{ka.a};
     Feed feed{sh, wait};
-    const int bufs = C::bufs(ka);
-    Turn key;
-    uint32_t fp = 0;
+    const int bufs = C::bufs(ka), conv = C::conv(ka);
+    Turn key, out;
     while (feed.next(it)) {
         if (it.j0 + w * kKeys >= it.len) continue;
         const int kb = key.st;
         wait(&sh.k_full[w][kb], key.ph);
         key.step(bufs);
         const uint8_t* raw = smem + C::raw(ka) + (w * bufs + kb) * C::kRaw;
-        uint8_t* dst = smem + w * C::kTile;
+        uint8_t* dst = smem + C::k16(ka) + (w * conv + out.st) * C::kTile;
         uint4 in[D / 16];
 #pragma unroll
         for (int ch = 0; ch < D / 16; ++ch)
             in[ch] = *reinterpret_cast<const uint4*>(
                 raw + lr * D + ((D == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3)) << 4));
-        wait(&sh.k_free[w], fp ^ 1u);
-        fp ^= 1u;
+        wait(&sh.k_free[w][out.st], out.ph ^ 1u);
         uint32_t nan = 0;
 #pragma unroll
         for (int ch = 0; ch < D / 16; ++ch) {
@@ -371,8 +374,9 @@ __device__ __forceinline__ void convert(const KeywArgs& ka, Shared& sh, uint8_t*
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&sh.k_empty[w][kb]);
-            mbar_arrive(&sh.k_bf16[w]);
+            mbar_arrive(&sh.k_bf16[w][out.st]);
         }
+        out.step(conv);
     }
 }
 
@@ -528,17 +532,17 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) keyw_kernel(const KeywArgs 
                 mbar_init(&sh.k_empty[w][i], E4M3 ? 4 : 1);
             }
             for (int i = 0; i < 2; ++i) {
+                mbar_init(&sh.k_bf16[w][i], 4);
+                mbar_init(&sh.k_free[w][i], 1);
                 mbar_init(&sh.s_full[w][i], 1);
                 mbar_init(&sh.s_empty[w][i], 4);
             }
-            mbar_init(&sh.k_bf16[w], 4);
-            mbar_init(&sh.k_free[w], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
             mbar_init(&sh.item_empty[i], kThreads<E4M3> / 32 - 1);   // every warp but the K warp
         }
-        for (int i = 0; i < kQStages; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_empty[i], 2);
         }
