@@ -142,6 +142,6 @@ cudaError_t launch_attn_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cuda
 cudaError_t launch_attn_join(const AttnArgs& a, int n_notes, cudaStream_t s);
 cudaError_t launch_attn_tile(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s);
 cudaError_t launch_keyw(const KeywArgs& a, const KeywMaps& m, int n_sms, cudaStream_t s);
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, int max_len, cudaStream_t s);
 
 }  // namespace moe

@@ -395,7 +395,10 @@ moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs
     a.scores_out = scores_out;
     a.new_len = new_len;
     a.err = static_cast<int32_t*>(ws);
-    return cuda_status(moe::launch_evict(a, reinterpret_cast<cudaStream_t>(stream)));
+    const int64_t places = int64_t(seqs->max_pages) * cache->page_size;
+    const int64_t longest = places < score_stride ? places : score_stride;
+    return cuda_status(moe::launch_evict(a, static_cast<int>(longest < (1 << 30) ? longest : 1 << 30),
+                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

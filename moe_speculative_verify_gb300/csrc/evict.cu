@@ -1,27 +1,29 @@
 // evict.cu -- cuts the cache to a budget of keys per kv head by accumulated
 // attention weight (sm_103a).
 //
-// One cluster of CTAs per (sequence, kv head).  The budget-th largest key is
-// found by radix selection, 8 bits a pass, on the scores' ordered bits: each
-// CTA counts its contiguous slice of the places in shared memory, the counts
-// are added through distributed shared memory, and every CTA finds the same
-// digit.  A key above the threshold is kept, of those equal to it the lowest
-// places; a scan over the slices then gives each kept place its rank, which
-// is the row it moves to.  Integer counts only, so the result does not depend
-// on any order.  The rows then move in 16-byte pieces, the bulk of the bytes.
-#include <cooperative_groups.h>
-
+// Selection: one CTA per (sequence, kv head) finds the budget-th largest key
+// by radix selection on the scores' ordered bits, which it keeps in shared
+// memory: 11, 11 and 10 bits a pass (the first digit has sign, exponent and two
+// fraction bits, so that scores of one magnitude still fall into several bins).  A key above the threshold is kept, of those equal
+// to it the lowest places; a scan over the places gives each kept one its
+// rank, which is the row it moves to.  Integer counts only, so the result does
+// not depend on any order.  (A cluster of 8 or 16 CTAs a pair, with the counts
+// added through distributed shared memory: its five cluster barriers and
+// remote reads took longer, 12 to 16 us for 8192 places.)
+//
+// The move, all but a few percent of the bytes, is a kernel of its own, so
+// that its blocks spread evenly over the card whatever the pairs: a thread
+// has four rows' 16-byte pieces of K and V in flight.
 #include "attn.cuh"
 #include "kernels.h"
-
-namespace cg = cooperative_groups;
 
 namespace moe {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kCluster = 8;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kHeld = 49152;               // places whose keys shared memory holds
 
 // Order of the scores as an unsigned integer: NaN lowest, -0 = +0, the recent
 // keys above every score.
@@ -33,16 +35,13 @@ __device__ __forceinline__ uint32_t score_key(float v, bool recent) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
-    __shared__ int s_hist[2][256];
-    __shared__ int s_sum[256];
+__global__ void __launch_bounds__(kThreads, 1) select_kernel(const EvictArgs a, int held_cap) {
+    extern __shared__ __align__(16) uint32_t s_key[];   // the keys, where they fit
+    __shared__ int s_hist[2048];
     __shared__ int s_digit, s_rest;
-    __shared__ int2 s_count;                    // this CTA's (above, equal)
-    __shared__ int2 s_warp[kThreads / 32];
-    cg::cluster_group cl = cg::this_cluster();
+    __shared__ int2 s_warp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int cr = static_cast<int>(cl.block_rank());
-    const int bh = blockIdx.x / kCluster, b = bh / a.kv.heads, h = bh - b * a.kv.heads;
+    const int bh = blockIdx.x, b = bh / a.kv.heads, h = bh - b * a.kv.heads;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t cap = min(int64_t(a.sq.max_pages) * a.kv.page, a.score_stride);
@@ -53,52 +52,82 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
     const float* sc = a.scores + int64_t(bh) * a.score_stride;
     int32_t* kept = a.kept + int64_t(bh) * a.budget;
     float* so = a.scores_out + int64_t(bh) * a.score_stride;
-    // this CTA's slice of the places, in order
-    const int s0 = static_cast<int>(int64_t(n) * cr / kCluster);
-    const int s1 = static_cast<int>(int64_t(n) * (cr + 1) / kCluster);
+    // each warp's part of the places, in order, a lane four places at a time
+    const int64_t per = (int64_t(n) + 4 * kThreads - 1) / (4 * kThreads) * 128;
+    const int w0 = static_cast<int>(min(int64_t(n), wid * per)), w1 = static_cast<int>(min(int64_t(n), (wid + 1) * per));
+    const bool held = n <= held_cap;
+    // keys of places j .. j + 3, j a multiple of 4 (past the end: whatever)
+    auto keys_at = [&](int j, uint32_t (&k)[4]) {
+        if (held) {
+            const uint4 x = *reinterpret_cast<const uint4*>(s_key + j);
+            k[0] = x.x;
+            k[1] = x.y;
+            k[2] = x.z;
+            k[3] = x.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = j + i < n ? score_key(sc[j + i], j + i >= first_recent) : 0u;
+        }
+    };
 
+    const bool all = n <= keep;
     uint32_t prefix = 0;                         // digits of the threshold so far
     int need = keep;                             // of the keys with that prefix
-    if (n > keep) {
-        for (int pass = 0; pass < 4; ++pass) {
-            const int shift = 24 - 8 * pass;
-            int* hist = s_hist[pass & 1];
-            if (tid < 256) hist[tid] = 0;
+    if (!all) {
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), above = pass == 1 ? 21 : 10;
+            const uint32_t mask = pass == 2 ? 1023u : 2047u;
+            for (int i = tid; i < 2048; i += kThreads) s_hist[i] = 0;
             __syncthreads();
-            for (int j = s0 + tid; j < s1; j += kThreads) {
-                const uint32_t k = score_key(sc[j], j >= first_recent);
-                if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                    atomicAdd(&hist[(k >> shift) & 255u], 1);
-            }
-            cl.sync();
-            if (tid < 256) {
-                int v = 0;
-#pragma unroll
-                for (int c = 0; c < kCluster; ++c) v += cl.map_shared_rank(hist, c)[tid];
-                s_sum[tid] = v;
-            }
-            __syncthreads();
-            if (tid < 32) {                      // the digit whose keys hold the need-th largest
-                int v[8], mine = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mine += v[i] = s_sum[255 - 8 * tid - i];
-                int incl = mine;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                    if (lane >= d) incl += o;
-                }
-                int before = incl - mine;
-                if (before < need && need <= incl) {
+            // (adds of one to one address are added up by the hardware across a warp)
+            if (pass == 0) {
+                for (int j0 = w0; j0 < w1; j0 += 32 * 8) {
+                    float v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if (before < need && need <= before + v[i]) {
-                            s_digit = 255 - 8 * tid - i;
-                            s_rest = need - before;
+                        const int j = j0 + 32 * i + lane;
+                        v[i] = j < w1 ? __ldg(sc + j) : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = j0 + 32 * i + lane;
+                        const uint32_t k = score_key(v[i], j >= first_recent);
+                        if (j < w1) {
+                            if (held) s_key[j] = k;
+                            atomicAdd(&s_hist[k >> 21], 1);
                         }
-                        before += v[i];
                     }
                 }
+            } else {
+#pragma unroll 2
+                for (int j = w0 + 4 * lane; j < w1; j += 128) {
+                    uint32_t k[4];
+                    keys_at(j, k);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j + i < w1 && (k[i] >> above) == (prefix >> above)) atomicAdd(&s_hist[(k[i] >> shift) & mask], 1);
+                }
+            }
+            __syncthreads();
+            // the digit whose keys hold the need-th largest: thread t has digits 2047 - 2t and one below
+            const int c0 = s_hist[2047 - 2 * tid], c1 = s_hist[2046 - 2 * tid];
+            int incl = c0 + c1;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            if (lane == 31) s_warp[wid].x = incl;
+            __syncthreads();
+            int o = lane < wid ? s_warp[lane].x : 0;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) o += __shfl_xor_sync(0xFFFFFFFFu, o, d);
+            const int before = o + incl - c0 - c1;
+            if (before < need && need <= before + c0 + c1) {
+                const bool second = need > before + c0;
+                s_digit = 2047 - 2 * tid - (second ? 1 : 0);
+                s_rest = need - before - (second ? c0 : 0);
             }
             __syncthreads();
             prefix |= static_cast<uint32_t>(s_digit) << shift;
@@ -106,88 +135,138 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
         }
     }
     // --- ranks: keys above the threshold, and the first `need` equal to it
-    const bool all = n <= keep;
-    int2 mine = make_int2(0, 0);
-    // a thread's places are contiguous, so ranks follow the places' order
-    const int len_c = s1 - s0, per = (len_c + kThreads - 1) / kThreads;
-    const int j0 = min(s1, s0 + tid * per), j1 = min(s1, j0 + per);
-    for (int j = j0; j < j1; ++j) {
-        const uint32_t k = score_key(sc[j], j >= first_recent);
-        mine.x += all || k > prefix;
-        mine.y += !all && k == prefix;
-    }
-    int2 incl = mine;
+    // four places' kinds: bit i above, bit 4 + i equal
+    auto kinds_at = [&](int j) {
+        uint32_t k[4], m = 0;
+        if (!all) keys_at(j, k);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, incl.x, d), y = __shfl_up_sync(0xFFFFFFFFu, incl.y, d);
-        if (lane >= d) {
-            incl.x += x;
-            incl.y += y;
-        }
-    }
-    if (lane == 31) s_warp[wid] = incl;
-    __syncthreads();
-    int2 at = make_int2(incl.x - mine.x, incl.y - mine.y);
+        for (int i = 0; i < 4; ++i)
+            if (j + i < w1) m |= all || k[i] > prefix ? 1u << i : (k[i] == prefix ? 16u << i : 0u);
+        return m;
+    };
     int2 sum = make_int2(0, 0);
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < wid) {
-            at.x += s_warp[w].x;
-            at.y += s_warp[w].y;
+    for (int j = w0 + 4 * lane; j < w1; j += 128) {
+        const uint32_t m = kinds_at(j);
+        sum.x += __popc(m & 15u);
+        sum.y += __popc(m >> 4);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        sum.x += __shfl_xor_sync(0xFFFFFFFFu, sum.x, d);
+        sum.y += __shfl_xor_sync(0xFFFFFFFFu, sum.y, d);
+    }
+    if (lane == 0) s_warp[wid] = sum;
+    __syncthreads();
+    int2 at = make_int2(0, 0);
+    {
+        int2 o = s_warp[lane];                   // (32 warps)
+        if (lane >= wid) o = make_int2(0, 0);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            o.x += __shfl_xor_sync(0xFFFFFFFFu, o.x, d);
+            o.y += __shfl_xor_sync(0xFFFFFFFFu, o.y, d);
         }
-        sum.x += s_warp[w].x;
-        sum.y += s_warp[w].y;
+        at = o;
     }
-    if (tid == 0) s_count = sum;
-    cl.sync();
-    for (int c = 0; c < cr; ++c) {
-        const int2 o = *cl.map_shared_rank(&s_count, c);
-        at.x += o.x;
-        at.y += o.y;
-    }
-    for (int j = j0; j < j1; ++j) {
-        const float v = sc[j];
-        const uint32_t k = score_key(v, j >= first_recent);
-        const bool eq = !all && k == prefix;
-        if (all || k > prefix || (eq && at.y < need)) {
-            const int r = at.x + min(at.y, need);
-            kept[r] = j;
-            so[r] = v;
+    for (int j0 = w0; j0 < w1; j0 += 128) {
+        const int j = j0 + 4 * lane;
+        const uint32_t m = j < w1 ? kinds_at(j) : 0u;
+        const uint32_t mine = __popc(m & 15u) | (__popc(m >> 4) << 16);
+        uint32_t incl = mine;                    // counts of the lanes up to this one, packed
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += o;
         }
-        at.x += all || k > prefix;
-        at.y += eq;
+        int gt = at.x + static_cast<int>((incl - mine) & 0xFFFFu), eq = at.y + static_cast<int>((incl - mine) >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool is_gt = (m >> i) & 1u, is_eq = (m >> (4 + i)) & 1u;
+            if (is_gt || (is_eq && eq < need)) {
+                const int r = gt + min(eq, need);
+                kept[r] = j + i;
+                so[r] = sc[j + i];
+            }
+            gt += is_gt;
+            eq += is_eq;
+        }
+        const uint32_t last = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        at.x += last & 0xFFFFu;
+        at.y += last >> 16;
     }
-    for (int r = keep + cr * kThreads + tid; r < a.budget; r += kCluster * kThreads) kept[r] = -1;
-    if (h == 0 && cr == 0 && tid == 0) a.new_len[b] = keep;
-    cl.sync();                                   // the kept list is whole; no CTA's counts are read any more
-    // --- move the rows: a row is rb/16 threads' work, K and V together
-    const int rb = a.kv.dim * (a.kv.e4m3 ? 1 : 2), lanes = rb / 16, es = a.kv.e4m3 ? 1 : 2;
-    const int sub = tid % lanes;
+    for (int r = keep + tid; r < a.budget; r += kThreads) kept[r] = -1;
+    if (h == 0 && tid == 0) a.new_len[b] = keep;
+}
+
+constexpr int kMoveThreads = 256, kFlight = 4;
+
+// LANES threads move a row (16 bytes of K and of V each); a block
+// kFlight * kMoveThreads / LANES rows of one pair.
+template <int LANES, int ES>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
+    constexpr int kRows = kMoveThreads / LANES;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int bh = blockIdx.y, b = bh / a.kv.heads, h = bh - b * a.kv.heads;
+    const int keep = a.new_len[b], r0 = blockIdx.x * kFlight * kRows + threadIdx.x / LANES;
+    const int32_t* kept = a.kept + int64_t(bh) * a.budget;
     const int32_t* from = a.sq.table + int64_t(b) * a.sq.max_pages;
     const int32_t* to = a.to_table + int64_t(b) * a.to_pages;
-    const int rows_c = kThreads / lanes;
-    for (int r = cr * rows_c + tid / lanes; r < keep; r += kCluster * rows_c) {
-        const int j = __ldcg(kept + r);
-        const int ps = from[j >> a.kv.page_log2], pd = to[r >> a.kv.page_log2];
-        if (ps < 0 || ps >= a.kv.n_pages || pd < 0 || pd >= a.kv.n_pages) {
+    const int64_t head = h * a.kv.head_stride;
+    const int sub = 16 * (threadIdx.x % LANES);
+    int j[kFlight], pd[kFlight], ps[kFlight];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+        const int r = r0 + i * kRows;
+        j[i] = r < keep ? kept[r] : -1;
+        pd[i] = r < keep ? to[r >> a.kv.page_log2] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) ps[i] = j[i] >= 0 ? from[j[i] >> a.kv.page_log2] : -1;
+    uint4 x[kFlight], y[kFlight];
+    int64_t dst[kFlight];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+        const int r = r0 + i * kRows;
+        dst[i] = -1;
+        if (j[i] < 0) continue;
+        if (ps[i] < 0 || ps[i] >= a.kv.n_pages || pd[i] < 0 || pd[i] >= a.kv.n_pages) {
             if (sub == 0) record_error(a.err, MOE_ERR_INVALID_ARG);
             continue;
         }
-        const int64_t src = es * (ps * a.kv.page_stride + h * a.kv.head_stride +
-                                  (j & (a.kv.page - 1)) * a.kv.token_stride) + 16 * sub;
-        const int64_t dst = es * (pd * a.kv.page_stride + h * a.kv.head_stride +
-                                  (r & (a.kv.page - 1)) * a.kv.token_stride) + 16 * sub;
-        const uint4 x = *reinterpret_cast<const uint4*>(a.kv.k + src);
-        const uint4 y = *reinterpret_cast<const uint4*>(a.kv.v + src);
-        *reinterpret_cast<uint4*>(a.kv.k + dst) = x;
-        *reinterpret_cast<uint4*>(a.kv.v + dst) = y;
+        const int64_t src = ES * (ps[i] * a.kv.page_stride + head + (j[i] & (a.kv.page - 1)) * a.kv.token_stride) + sub;
+        dst[i] = ES * (pd[i] * a.kv.page_stride + head + (r & (a.kv.page - 1)) * a.kv.token_stride) + sub;
+        x[i] = *reinterpret_cast<const uint4*>(a.kv.k + src);
+        y[i] = *reinterpret_cast<const uint4*>(a.kv.v + src);
     }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i)
+        if (dst[i] >= 0) {
+            *reinterpret_cast<uint4*>(a.kv.k + dst[i]) = x[i];
+            *reinterpret_cast<uint4*>(a.kv.v + dst[i]) = y[i];
+        }
+}
+
+template <int LANES, int ES>
+cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
+    const int rows = kFlight * kMoveThreads / LANES;
+    return launch_pdl(move_kernel<LANES, ES>, dim3((a.budget + rows - 1) / rows, a.sq.n * a.kv.heads),
+                      dim3(kMoveThreads), 0, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-    const cudaError_t e = launch_pdl_cluster(evict_kernel, dim3(a.sq.n * a.kv.heads * kCluster), dim3(kThreads),
-                                             kCluster, 0, s, a);
+cudaError_t launch_evict(const EvictArgs& a, int max_len, cudaStream_t s) {
+    const int cap = max_len < kHeld ? max_len : kHeld;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(select_kernel), kHeld * 4);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(select_kernel, dim3(a.sq.n * a.kv.heads), dim3(kThreads), (size_t(cap) + 3) / 4 * 16, s, a, cap);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.kv.dim == 128)
+        e = a.kv.e4m3 ? launch_move<8, 1>(a, s) : launch_move<16, 2>(a, s);
+    else
+        e = a.kv.e4m3 ? launch_move<4, 1>(a, s) : launch_move<8, 2>(a, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
