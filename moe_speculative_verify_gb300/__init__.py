@@ -414,13 +414,14 @@ def _refuse(ok: bool, where: str) -> None:
 
 
 def _is(t, dtype, *shape) -> bool:
-    return t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == shape
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
 def _heads(t, heads: int, dim: int, tokens: int) -> bool:
     """bf16 [tokens, heads, dim] with a token's heads contiguous."""
-    return (t.dtype == torch.bfloat16 and tuple(t.shape) == (tokens, heads, dim)
-            and (t.stride(2) == 1 or dim == 1) and (t.stride(1) == dim or heads == 1))
+    s = t.stride()
+    return (t.dtype is torch.bfloat16 and t.shape == (tokens, heads, dim) and s[2] == 1
+            and (s[1] == dim or heads == 1))
 
 
 def moe_rope_freqs(rot_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN,
