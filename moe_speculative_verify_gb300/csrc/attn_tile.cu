@@ -698,7 +698,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
             for (int step = 0; step < 2; ++step) {
                 const int c0 = (s ^ step ^ 1) * (D / 2);
                 if (warp_on) {
-#pragma unroll 1
+#pragma unroll 2
                     for (int q = 0; q < D / 32; ++q) {
                         float o[16];
                         tmem_ld16(colO + c0 + 16 * q, o);
@@ -729,10 +729,12 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
                 const int tr = tid & (span - 1), rr = it.rt * kMT + tr, qj = a.query_of(rr);
                 const int64_t to = int64_t(it.s.q0 + qj) * a.q_heads + it.h * a.group + rr - qj * a.group;
                 if (tr < sr.rows) {
-#pragma unroll 2
+#pragma unroll 4
                     for (int d4 = tid / span; d4 < D / 4; d4 += kSoft / span) {
                         float4 y = *cell(tr, d4);
-                        for (int k = 1; k < copies; ++k) {
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) {
+                            if (k >= copies) break;
                             const float4 u = *cell(tr + k * span, d4);
                             y.x += u.x;
                             y.y += u.y;
@@ -785,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     tc_fence_before();
     pdl_wait();
     pdl_launch_dependents();
-    plan_work<kMT, kKT>(a, 2, reinterpret_cast<int64_t*>(sh.ml), &sh.plan);   // (its barriers publish sh.tmem)
+    plan_work<kMT, kKT>(a, 1, reinterpret_cast<int64_t*>(sh.ml), &sh.plan);   // (its barriers publish sh.tmem)
     tc_fence_after();
     zero_pad_rows(a);
     if (warp < 8) {
