@@ -68,6 +68,7 @@ struct Shared {
     uint64_t k_bf16[2][2], k_free[2][2];    // e4m3, [tile][bf16 tile]: it is there, is no longer read
     uint64_t q_full[3], q_empty[3];
     uint64_t s_full[2][2], s_empty[2][2];   // [tile][buffer]
+    uint64_t done[2];
     uint32_t tmem;
 };
 
@@ -148,7 +149,8 @@ struct Scheduler {
     }
 };
 
-// A role's place in the ring of items; next() copies one out.  One warp each.
+// A role's place in the ring of items; next() copies one out, false after the
+// last or once a wait ran out.  One warp each.
 struct Feed {
     Shared& sh;
     Waiter& wait;
@@ -162,7 +164,7 @@ struct Feed {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.item_empty[at.st]);
         at.step(kItems);
-        return !wait.dead && it.b >= 0;
+        return __all_sync(0xFFFFFFFFu, !wait.dead) && it.b >= 0;
     }
 };
 
@@ -231,6 +233,10 @@ __device__ __forceinline__ void load_keys(const KeywArgs& ka, const CUtensorMap&
             }
         }
     }
+    // a CTA ends after its copies, also where a wait ran out: each buffer's last one
+    for (int w = 0; w < 2; ++w)
+        for (int k = 0; k < bufs && mbar_wait(&sh.k_full[w][use[w].st], use[w].ph ^ 1u, a.err, a.timeout_ns); ++k)
+            use[w].step(bufs);
 }
 
 template <int D, bool E4M3>
@@ -261,6 +267,8 @@ __device__ __forceinline__ void load_rows(const KeywArgs& ka, const CUtensorMap&
                 q.step(C::kQStages);
             }
     }
+    for (int k = 0; k < C::kQStages && mbar_wait(&sh.q_full[q.st], q.ph ^ 1u, a.err, a.timeout_ns); ++k)
+        q.step(C::kQStages);
 }
 
 template <int D, bool E4M3>
@@ -326,6 +334,9 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
             __syncwarp();
         }
     }
+    // (also where a wait ran out: the products end before the accumulators are given back)
+    if (elect_one()) mma_commit(&sh.done[w]);
+    mbar_wait(&sh.done[w], 0, a.err, a.timeout_ns);
 }
 
 // e4m3: one tile of the items' pairs to bf16.
@@ -430,7 +441,7 @@ __device__ __forceinline__ void weigh(const KeywArgs& ka, Shared& sh, uint8_t* s
     };
     auto fetch = [&](Ahead& x) {
         do {
-            x.more = feed.next(x.it);
+            x.more = bar_and(1 + w, feed.next(x.it), 128);       // all four warps go on or none: they meet below
         } while (x.more && x.it.j0 + w * kKeys >= x.it.len);
         if (!x.more) return;
         const int j = x.it.j0 + w * kKeys + lr;
@@ -527,6 +538,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) keyw_kernel(const KeywArgs 
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int w = 0; w < 2; ++w) {
+            mbar_init(&sh.done[w], 1);
             for (int i = 0; i < kMaxBufs; ++i) {
                 mbar_init(&sh.k_full[w][i], 1);
                 mbar_init(&sh.k_empty[w][i], E4M3 ? 4 : 1);
