@@ -40,17 +40,23 @@ struct Cfg {
     static constexpr size_t kSmem = 1024 + kRing + kMergeFloats * 4;
 };
 
+constexpr int kItems = 4;                    // items handed on ahead
+
 struct Shared {
-    alignas(8) uint64_t full[10];
+    alignas(16) Item item[kItems];
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t full[10];
     uint64_t empty[10];
     int64_t warp_sum[kConsumers + 1];
     Plan plan;
     float2 ml[kConsumers][kRows];            // maximum (log2) and sum of a warp's keys
 };
 
-// The TMA warp.  A step is a key tile, K and V, a box or two a page, each page
-// issued by a lane of its own, one after the other; the next tile's page
-// indices are read a step ahead.
+// The TMA warp.  It walks the CTA's items and hands them to the other warps,
+// which so need not look up sequences themselves, and prefetches their rows.
+// A step is a key tile, K and V, a box or two a page, each page issued by a
+// lane of its own, one after the other; the next tile's page indices are read
+// a step ahead.
 template <int D, bool E4M3>
 __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, Shared& sh, uint8_t* ring) {
     using C = Cfg<D, E4M3>;
@@ -63,10 +69,31 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
     Walk<kRows, kTile> wk;
     wk.start(a, sh.plan);
     Item it;
-    int st = 0;
-    uint32_t ph = 1;
-    bool dead = false;
-    while (wk.next(a, it)) {
+    int st = 0, slot = 0;
+    uint32_t ph = 1, ip = 1;
+    bool dead = false, more = true;
+    while (more) {
+        more = wk.next(a, it);
+        if (!more) it.b = -1;
+        if (!dead && !mbar_wait(&sh.item_empty[slot], ip, a.err, a.timeout_ns)) dead = true;
+        if (lane == 0) {
+            sh.item[slot] = it;
+            mbar_arrive(&sh.item_full[slot]);
+        }
+        __syncwarp();
+        if (++slot == kItems) {
+            slot = 0;
+            ip ^= 1;
+        }
+        if (!more) break;
+        {
+            const int r = it.rt * kRows + (lane & 15);
+            if (r < it.s.nq * a.group) {
+                const int i = a.query_of(r), hd = it.h * a.group + r - i * a.group;
+                const uint16_t* p = a.q + (it.s.q0 + i) * a.q_stride + hd * D + (lane >> 4) * 64;
+                if (lane < 16 || D > 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+            }
+        }
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
         // pages with a seen key (none where no key is seen)
         const int p_lo = it.lo >> pl, p_hi = it.hi > it.lo ? (it.hi + page - 1) >> pl : p_lo;
@@ -104,6 +131,13 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
             }
             j0 += kTile;
             if (t + 1 < it.t1 && mine()) pg = table[(j0 >> pl) + lane];
+        }
+    }
+    // a CTA ends after its copies, also where a wait ran out: each stage's last one
+    for (int k = 0; k < C::kStages && mbar_wait(&sh.full[st], ph, a.err, a.timeout_ns); ++k) {
+        if (++st == C::kStages) {
+            st = 0;
+            ph ^= 1;
         }
     }
 }
@@ -210,12 +244,21 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
     const int ctid = threadIdx.x;                        // consumers are threads 0 .. 255
     const bool draft = a.draft != nullptr;
     const int slot_floats = kAttnSlotRows * (D + 2);
-    Walk<kRows, kTile> wk;
-    wk.start(a, sh.plan);
-    Item it;
-    int run = 0;
+    int run = 0, slot = 0;
+    uint32_t ip = 0;
     bool dead = false;
-    while (wk.next(a, it)) {
+    for (;;) {
+        if (!dead && !mbar_wait(&sh.item_full[slot], ip, a.err, a.timeout_ns)) dead = true;
+        // all warps go on or none (the merge's barriers); its room has been read
+        if (!bar_and(kBarMerge, !dead, 32 * kConsumers)) break;
+        const Item it = sh.item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
+        if (++slot == kItems) {
+            slot = 0;
+            ip ^= 1;
+        }
+        if (it.b < 0) break;
         QFrag<D, E4M3> q;
         q.load(a, it);
         const int rows = min(kRows, it.s.nq * a.group - it.rt * kRows);
@@ -465,7 +508,6 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
             }
         }
         if (ctid == 0) note_split(a, it, rows, kRows, sh.plan);
-        named_bar(kBarMerge, 32 * kConsumers);
     }
 }
 
@@ -481,6 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], kConsumers / 2);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], kConsumers);
         }
         fence_barrier_init();
         prefetch_tensormap(&maps.k);
@@ -498,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
 
 template <int D, bool E4M3>
 cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s) {
-    using C = Cfg<D, E4M3>;
-    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(attn_rows_kernel<D, E4M3>),
-                                    static_cast<int>(C::kSmem));
+    constexpr size_t smem = Cfg<D, E4M3>::kSmem;
+    static_assert(smem + sizeof(Shared) <= 232448, "227 KB a CTA");
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(attn_rows_kernel<D, E4M3>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int grid = n_sms < kAttnMaxCtas ? n_sms : kAttnMaxCtas;
-    e = launch_pdl(attn_rows_kernel<D, E4M3>, dim3(grid), dim3(kThreads), C::kSmem, s, a, m);
+    e = launch_pdl(attn_rows_kernel<D, E4M3>, dim3(grid), dim3(kThreads), smem, s, a, m);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_join(a, grid, s);
 }

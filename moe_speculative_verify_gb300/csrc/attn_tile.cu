@@ -123,7 +123,7 @@ struct Shared {
     alignas(16) float2 ml[2][128];          // a lane's reference and sum, among a row's sharers
     uint64_t kv_full[10];
     uint64_t kv_empty[10];
-    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], turn[2];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], turn[2], done[2];
     Plan plan;
     Ctx ctx[4];                             // the softmax warpgroups', the TMA warp's, the MMA warps'
     uint32_t tmem;
@@ -199,6 +199,8 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
             if (j + group < T && mine()) pg = table[p];
         }
     }
+    // a CTA ends after its copies, also where a wait ran out: each stage's last one
+    for (int k = 0; k < C::kStages && mbar_wait(&sh.kv_full[at.st], at.ph, a.err, a.timeout_ns); ++k) at.step();
 }
 
 // The MMA warp of stream s: one thread issues, the whole warp waits.  The
@@ -338,6 +340,9 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
             __syncwarp();
         }
     }
+    // (also where a wait ran out: the products end before the accumulators are given back)
+    if (elect_one()) mma_commit(&sh.done[s]);
+    mbar_wait(&sh.done[s], 0, a.err, a.timeout_ns);
 }
 
 // 16 32-bit columns of this thread's TMEM lane.
@@ -497,14 +502,22 @@ __device__ __forceinline__ void soft_tile_part(uint32_t colS, uint32_t colO, int
     p_done(ready);
 }
 
+// The power of two that takes a row's largest element to [128, 256) (e4m3's
+// largest code is 448), or as near as fp32 has it.
+__device__ __forceinline__ float code_factor(float amax) {
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23);
+    return e == 255 ? 1.0f : __uint_as_float(static_cast<uint32_t>(min(261 - e, 253)) << 23);
+}
+
 // A warp's 32 query rows into shared memory, K-major with the 128-byte
 // swizzle: bf16 as they are, or (beside e4m3 codes) as high and low e4m3 codes
 // of the row times a power of two, which goes into the row's c.  `src` is the
 // lane's own row; the warp reads whole rows, D / 8 lanes to one, so that a
-// load touches 4 lines and not 32, eight loads at a time before their use.
+// load touches 4 lines and not 32, a few loads at a time before their use (few,
+// because a short call runs this code from cold instruction caches).
 template <int D, bool E4M3>
 __device__ __forceinline__ void load_queries(const uint16_t* src, bool valid, bool negate, uint8_t* qt, float& c) {
-    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 8;
+    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = E4M3 ? 4 : 8;
     const int lane = threadIdx.x & 31, ch = lane % kLanes, sub = lane / kLanes;
     const int row0 = threadIdx.x & 96;                           // the warp's first row of the tile
     const uint32_t flip = negate ? 0x80008000u : 0u, on = __ballot_sync(0xFFFFFFFFu, valid);
@@ -537,14 +550,12 @@ __device__ __forceinline__ void load_queries(const uint16_t* src, bool valid, bo
                                              fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
 #pragma unroll
                 for (int d = 1; d < kLanes; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-                // the row's largest element to [128, 256): f1 takes it to [1, 2)
-                const float f1 = pow2_norm(amax);
-                const float f2 = f1 == 1.0f && !(amax >= 1.0f && amax < 2.0f) ? 1.0f : 128.0f;
+                const float f = code_factor(amax);
                 uint32_t h[4], l[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f1 * f2;
-                    const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f1 * f2;
+                    const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f;
+                    const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f;
                     h[e] = pack_e4m3(v0, v1);
                     const float2 b = unpack_e4m3(h[e]);
                     l[e] = pack_e4m3(v0 - b.x, v1 - b.y);
@@ -561,10 +572,7 @@ __device__ __forceinline__ void load_queries(const uint16_t* src, bool valid, bo
             }
         }
     }
-    if constexpr (E4M3) {
-        const float f1 = pow2_norm(own), f2 = f1 == 1.0f && !(own >= 1.0f && own < 2.0f) ? 1.0f : 128.0f;
-        c = own < INFINITY ? fmaxf(c / f2 / f1, 1.2e-38f) : __int_as_float(0x7FC00000);
-    }
+    if constexpr (E4M3) c = own < INFINITY ? fmaxf(c / code_factor(own), 1.2e-38f) : __int_as_float(0x7FC00000);
     fence_async_smem();
 }
 
@@ -773,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.p_ready[s], 4);
             mbar_init(&sh.turn[s], 1);
+            mbar_init(&sh.done[s], 1);
             mbar_init(&sh.o_full[s], 1);
             mbar_init(&sh.q_ready[s], 4);
         }
