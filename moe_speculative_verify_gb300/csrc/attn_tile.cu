@@ -21,6 +21,13 @@
 // probability the sum of an e4m3 and an e5m2 code (whose range reaches down to
 // 2^-20 of the reference): two 8-bit products take the time of one 16-bit one,
 // and K and V need no conversion.
+//
+// Measured (64 query heads, 8 kv heads of 128): 2048 tokens over 16,384 keys
+// more 0.80 ms in bf16, 1.46 PFLOP/s where the library's matrix product runs at
+// 1.91 (a step's two products leave the tensor pipe idle between bursts, see
+// multiply), 1.12 ms over e4m3 (the two codes of each probability); 16 verify
+// blocks of up to 8 tokens over 4,099 to 16,411 keys 113 us over e4m3 (2.8 TB/s:
+// the softmax's work a key byte is twice bf16's), 128 over bf16 (4.9 TB/s); one block over 6,011 keys 21 us.
 #include "attn_mma.cuh"
 #include "kernels.h"
 

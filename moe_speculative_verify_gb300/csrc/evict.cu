@@ -4,16 +4,21 @@
 // Selection: one CTA per (sequence, kv head) finds the budget-th largest key
 // by radix selection on the scores' ordered bits, which it keeps in shared
 // memory: 11, 11 and 10 bits a pass (the first digit has sign, exponent and two
-// fraction bits, so that scores of one magnitude still fall into several bins).  A key above the threshold is kept, of those equal
-// to it the lowest places; a scan over the places gives each kept one its
-// rank, which is the row it moves to.  Integer counts only, so the result does
-// not depend on any order.  (A cluster of 8 or 16 CTAs a pair, with the counts
+// fraction bits, so that scores of one magnitude still fall into several
+// bins).  A key above the threshold is kept, of those equal to it the lowest
+// places; a scan over the places gives each kept one its rank, which is the
+// row it moves to.  Integer counts only, so the result does not depend on any
+// order.  (A cluster of 8 or 16 CTAs a pair, with the counts
 // added through distributed shared memory: its five cluster barriers and
 // remote reads took longer, 12 to 16 us for 8192 places.)
 //
 // The move, all but a few percent of the bytes, is a kernel of its own, so
 // that its blocks spread evenly over the card whatever the pairs: a thread
 // has four rows' 16-byte pieces of K and V in flight.
+//
+// Measured (8 kv heads of 128): one sequence of 8,191 keys cut to 4,096 (bf16) 15
+// us, most of it the selection's dependent passes; 16 of 5,003 to 32,003 keys
+// cut to 8,000 (e4m3) 108 us, 4.8 TB/s.
 #include "attn.cuh"
 #include "kernels.h"
 

@@ -18,6 +18,15 @@
 // e4m3 keys are turned to bf16 in shared memory first (exact), which a tile
 // pays once however many rows see it, by two warpgroups of their own (as part
 // of the powers' warpgroups' round it held up the stream: 16 verify blocks 92 us).
+// Queries as two e4m3 codes an element, beside K as it is cached, were no
+// faster (87 us: waiting for instructions was the warps' largest stall) and
+// slower for chunks, where a query tile is coded again for every item.
+//
+// Measured (64 query heads, 8 kv heads of 128): 8 single tokens over 1,021 to
+// 8,209 keys 15 us (4.5 TB/s); 16 verify blocks of up to 8 over 4,099 to 16,411
+// keys 61 us in bf16 (5.3 TB/s of a copy's 6.7), 86 over e4m3 (1.9: the powers'
+// and the conversion's instructions, not bytes); 1024 tokens over
+// 8,192 more 156 us in bf16 (0.94 PFLOP/s), 190 over e4m3.
 #include "attn_mma.cuh"
 #include "kernels.h"
 
