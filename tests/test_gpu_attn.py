@@ -102,6 +102,17 @@ def test_long_split(lens, news, hq, hkv, dtype):
         assert torch.equal(o2, out) and torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 3])
+def test_many_items(news, dtype):
+    """Many short sequences: dozens of items a CTA, some without new tokens."""
+    lens = [1 + (37 * b) % 131 for b in range(500)]
+    p = ref.Problem(lens, [0 if b % 11 == 5 else min(news, n) for b, n in enumerate(lens)], 32, 4, 64, 16, dtype,
+                    seed=17).cuda()
+    out, lse, _ = attend(p)
+    check(p, out, lse)
+
+
 def test_peaked_scores():
     """Scores of +-100s: the running maximum moves and most probabilities vanish."""
     p = ref.Problem([700, 90], [8, 3], 16, 2, 128, 64, seed=4, q_scale=80.0).cuda()
