@@ -26,7 +26,7 @@
 // 8,209 keys 15 us (4.5 TB/s); 16 verify blocks of up to 8 over 4,099 to 16,411
 // keys 61 us in bf16 (5.3 TB/s of a copy's 6.7), 86 over e4m3 (1.9: the powers'
 // and the conversion's instructions, not bytes); 1024 tokens over
-// 8,192 more 156 us in bf16 (0.94 PFLOP/s), 190 over e4m3.
+// 8,192 156 us in bf16 (0.94 PFLOP/s), 162 over e4m3.
 #include "attn_mma.cuh"
 #include "kernels.h"
 
@@ -38,6 +38,13 @@ constexpr int kKeys = 128;                  // keys of a tile; two an item
 // 2 warpgroups for the powers, K warp, Q warp, 2 MMA warps; e4m3: 2 warpgroups that convert
 template <bool E4M3>
 constexpr int kThreads = E4M3 ? 640 : 384;
+
+// e4m3 and more than 64 rows a tile: registers a thread, moved to the powers'
+// warpgroups after the launch at 96: 8 * 128 + 12 * 72 = 1888 a lane column of
+// the 20 * 96 = 1920 launched.  1024 tokens over 8,192 keys 190 -> 162 us with
+// the powers of a full tile unrolled; with fewer rows, whose tiles are never full,
+// both cost more code and the conversion registers (16 verify blocks 86 -> 90).
+constexpr int kRegsPowers = 128, kRegsRest = 72;
 
 constexpr int kMaxBufs = 8;                 // K buffers a tile
 constexpr int kItems = 4;                   // items ahead
@@ -422,7 +429,7 @@ __device__ __forceinline__ void add_powers(uint32_t col, const float* off, float
     }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool MANY>
 __device__ __forceinline__ void weigh(const KeywArgs& ka, Shared& sh, uint8_t* smem) {
     using C = Cfg<D, E4M3>;
     const AttnArgs& a = ka.a;
@@ -498,9 +505,10 @@ __device__ __forceinline__ void weigh(const KeywArgs& ka, Shared& sh, uint8_t* s
                     if (!draft && a.causal) lo = static_cast<int>(max(int64_t(0), min(rel, int64_t(128)))) * th;
                     if (a.window > 0) hi = min(hi, static_cast<int>(max(int64_t(0), min(rel + a.window, int64_t(128)))) * th);
                 }
-                const bool whole = seen && rows == 128 && (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu;
+                const bool whole = MANY && seen && rows == 128 &&
+                                   (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu;
                 if (whole) {
-#pragma unroll(E4M3 ? 1 : 4)
+#pragma unroll
                     for (int q = 0; q < 4; ++q) add_powers<32, false>(col + 32 * q, off + 32 * q, c, 0, p0, p1);
                 }
 #pragma unroll 1
@@ -539,7 +547,8 @@ __device__ __forceinline__ void weigh(const KeywArgs& ka, Shared& sh, uint8_t* s
     }
 }
 
-template <int D, bool E4M3>
+// MANY: tiles of more than 64 rows.
+template <int D, bool E4M3, bool MANY>
 __global__ void __launch_bounds__(kThreads<E4M3>, 1) keyw_kernel(const KeywArgs ka, const __grid_constant__ KeywMaps maps) {
     using C = Cfg<D, E4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -580,37 +589,47 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) keyw_kernel(const KeywArgs 
     tc_fence_after();
     pdl_wait();
     pdl_launch_dependents();
-    if (warp < 8)
-        weigh<D, E4M3>(ka, sh, smem);
-    else if (warp == 8)
-        load_keys<D, E4M3>(ka, maps.k, sh, smem);
-    else if (warp == 9)
-        load_rows<D, E4M3>(ka, maps.q, sh, smem);
-    else if (warp < 12)
-        multiply<D, E4M3>(ka, sh, smem, warp - 10);
-    else if constexpr (E4M3)
-        convert<D>(ka, sh, smem, (warp - 12) >> 2);
+    if (warp < 8) {
+        if constexpr (E4M3 && MANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsPowers));
+        weigh<D, E4M3, MANY>(ka, sh, smem);
+    } else {
+        if constexpr (E4M3 && MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == 8)
+            load_keys<D, E4M3>(ka, maps.k, sh, smem);
+        else if (warp == 9)
+            load_rows<D, E4M3>(ka, maps.q, sh, smem);
+        else if (warp < 12)
+            multiply<D, E4M3>(ka, sh, smem, warp - 10);
+        else if constexpr (E4M3)
+            convert<D>(ka, sh, smem, (warp - 12) >> 2);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 10) tmem_dealloc(sh.tmem, 512);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool MANY>
 cudaError_t launch(const KeywArgs& a, const KeywMaps& m, int n_sms, cudaStream_t s) {
     constexpr size_t smem = Cfg<D, E4M3>::kTotal + sizeof(Shared);
     static_assert(smem <= 232448, "227 KB a CTA");
-    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(keyw_kernel<D, E4M3>), static_cast<int>(smem));
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(keyw_kernel<D, E4M3, MANY>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(keyw_kernel<D, E4M3>, dim3(n_sms), dim3(kThreads<E4M3>), smem, s, a, m);
+    e = launch_pdl(keyw_kernel<D, E4M3, MANY>, dim3(n_sms), dim3(kThreads<E4M3>), smem, s, a, m);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool E4M3>
+cudaError_t launch(const KeywArgs& a, const KeywMaps& m, int n_sms, cudaStream_t s) {
+    const bool many = a.tile_tokens * a.tile_heads > 64;
+    if (a.a.kv.dim == 128) return many ? launch<128, E4M3, true>(a, m, n_sms, s) : launch<128, E4M3, false>(a, m, n_sms, s);
+    return many ? launch<64, E4M3, true>(a, m, n_sms, s) : launch<64, E4M3, false>(a, m, n_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_keyw(const KeywArgs& a, const KeywMaps& m, int n_sms, cudaStream_t s) {
-    if (a.a.kv.dim == 128) return a.a.kv.e4m3 ? launch<128, true>(a, m, n_sms, s) : launch<128, false>(a, m, n_sms, s);
-    return a.a.kv.e4m3 ? launch<64, true>(a, m, n_sms, s) : launch<64, false>(a, m, n_sms, s);
+    return a.a.kv.e4m3 ? launch<true>(a, m, n_sms, s) : launch<false>(a, m, n_sms, s);
 }
 
 }  // namespace moe
