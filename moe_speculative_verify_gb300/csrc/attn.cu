@@ -478,7 +478,7 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
         }
         // --- write: the item's output, or this CTA's piece of it
         const bool piece = it.t0 > 0 || it.t1 < it.n;
-        float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * slot_floats;
+        float* slot = a.partials + (int64_t(it.t0 == 0 ? 0 : kAttnMaxCtas) + blockIdx.x) * slot_floats;
         const float vs = E4M3 ? a.kv.v_scale[it.h] : 1.0f;
         for (int e = ctid; e < rows * (D / 4); e += 32 * kConsumers) {
             const int row = e / (D / 4), d4 = e % (D / 4);
@@ -567,7 +567,10 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
 // A unit is kJoinRows rows of a split item; the blocks share the units of all
 // items out among them (each adds up the notes for itself).  Four threads have
 // four columns of a row, each a quarter of the pieces, so that all pieces are
-// in flight at once.
+// in flight at once.  The first piece is added before the loop over the others,
+// which lie at one distance from each other: with the first one's place chosen
+// inside an unrolled loop, joins of 128 columns whose first quarter counted a
+// multiple of eight pieces ended in a misaligned access.
 constexpr int kJoinRows = 4, kJoinParts = 4;
 
 template <int D>
@@ -609,27 +612,30 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel
             if (i + step <= kAttnMaxCtas - 1 && s_end[i + step - 1] <= u) i += step;
         const SplitNote n = a.notes[i];
         const int row0 = (u - (i > 0 ? s_end[i - 1] : 0)) * kJoinRows;
-        const float* p0 = a.partials + (2 * int64_t(i) + 1) * kSlot;          // the first piece, then
+        // the piece of the CTA where the item begins, and (k >= 1) of the k-th CTA after it
+        const float* head = a.partials + int64_t(i) * kSlot;
+        const float* rest = a.partials + (int64_t(kAttnMaxCtas) + i) * kSlot;
         const int row = min(row0 + rl, n.rows - 1);
         const int ml = kAttnSlotRows * D + 2 * row, od = (d4 * kAttnSlotRows + row) * 4;
-        auto piece = [&](int k) { return p0 + (k == 0 ? 0 : (2 * k - 1) * kSlot); };   // every second slot
-        float top = kNegInf;
+        float top = head[ml];
 #pragma unroll 8
-        for (int k = 0; k < n.pieces; ++k) top = fmaxf(top, piece(k)[ml]);
+        for (int k = 1; k < n.pieces; ++k) top = fmaxf(top, rest[k * kSlot + ml]);
         const float ref = top == kNegInf ? 0.0f : top;
         float sum = 0.0f;
         float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int k = part; k < n.pieces; k += kJoinParts) {
-            const float2 x = *reinterpret_cast<const float2*>(piece(k) + ml);
-            const float4 y = *reinterpret_cast<const float4*>(piece(k) + od);
+        auto add = [&](const float* p) {
+            const float2 x = *reinterpret_cast<const float2*>(p + ml);
+            const float4 y = *reinterpret_cast<const float4*>(p + od);
             const float w = fast_exp2(x.x - ref);
             sum += x.y * w;
             v.x += y.x * w;
             v.y += y.y * w;
             v.z += y.z * w;
             v.w += y.w * w;
-        }
+        };
+        if (part == 0) add(head);
+#pragma unroll 8
+        for (int k = part > 0 ? part : kJoinParts; k < n.pieces; k += kJoinParts) add(rest + k * kSlot);
         s_v[part][cell] = v;
         if (d4 == 0) s_sum[part][rl] = sum;
         __syncthreads();

@@ -269,8 +269,8 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 // some row of the item sees (one unit when none does), and give every CTA an
 // equal run of units in item order.  A CTA so meets at most two items that
 // it shares with its neighbours: it leaves its pieces of those in its two
-// slots (the second slot for an item that begins with it), the CTA where an
-// item begins notes the split, and the join kernel (attn.cu) adds an item's
+// slots (one for an item that begins with it, one for an item that began
+// before), the CTA where an item begins notes the split, and the join kernel (attn.cu) adds an item's
 // pieces up in CTA order.
 struct Item {
     int b, h, rt;          // sequence, kv head, row tile

@@ -36,8 +36,9 @@ struct SplitNote {
 };
 
 // Workspace of the attention calls: the control block (error word), one note
-// per CTA, then the pieces of split items: two slots per CTA, each of
-// kAttnSlotRows rows, fp32: sums [dim/4][row][4], then (reference in log2
+// per CTA, then the pieces of split items: one slot per CTA for an item that
+// begins there, after these one per CTA for an item that began before.  A slot
+// has kAttnSlotRows rows, fp32: sums [dim/4][row][4], then (reference in log2
 // units, sum of powers) [row][2].
 constexpr int kAttnMaxCtas = 160;       // >= SMs of the card; larger grids are cut to it
 constexpr int kAttnSlotRows = 256;

@@ -645,7 +645,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         if (sum != sum) ref = fmaxf(ref, 0.0f);                  // a NaN is a result, not an empty row
         const bool piece = it.t0 > 0 || it.t1 < it.n;
         const int n0 = sr.count(0), n1 = sr.count(1);
-        float* slot = a.partials + (2 * int64_t(blockIdx.x) + (it.t0 == 0 ? 1 : 0)) * kAttnSlotRows * (D + 2);
+        float* slot = a.partials + (int64_t(it.t0 == 0 ? 0 : kAttnMaxCtas) + blockIdx.x) * (kAttnSlotRows * (D + 2));
         // What a row's sums are multiplied with here: its weight among the lanes that share the row (the
         // streams of one row tile, the copies), v_scale and, unless the row goes on elsewhere, 1 / its sum.
         float weight = ref == kNegInf ? 0.0f : 1.0f, top = ref;
