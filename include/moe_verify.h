@@ -451,12 +451,12 @@ moe_status_t moe_greedy_verify(const void* logits, int32_t logits_bf16, int32_t 
  * into it, attention of the step's new tokens over it (single tokens, verify
  * blocks, prefill chunks), and eviction by accumulated attention weight.
  *
- * A page index outside the cache or a sequence whose numbers do not fit (an
- * offset past n_tokens or below the one before it, a length past its block
- * table) is never followed: the call records MOE_ERR_INVALID_ARG in the error
- * word of its workspace (read with moe_get_device_error), takes such a
- * sequence's new tokens as none or its length as what the table holds, and
- * reads such a page as zeros.
+ * A page index outside the cache or a sequence whose numbers do not fit is
+ * never followed: the call records MOE_ERR_INVALID_ARG in the error word of
+ * its workspace (read with moe_get_device_error) and reads such a page as
+ * zeros, a length past the block table as what the table holds.  An offset
+ * past n_tokens or below the one before it leaves its sequence and those after
+ * it without new tokens: the rows from there on are pad rows.
  * ------------------------------------------------------------------------ */
 
 #define MOE_KV_BF16 0          /* cache elements: bf16                            */

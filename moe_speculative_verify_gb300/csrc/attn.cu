@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
     pdl_wait();
     pdl_launch_dependents();
     plan_work<kRows, kTile>(a, 1, sh.warp_sum, &sh.plan);
-    zero_pad_rows(a);
+    zero_pad_rows(a, sh.plan.seqs);
     if (threadIdx.x >= 32 * kConsumers)
         produce<D, E4M3>(a, maps, sh, ring);
     else

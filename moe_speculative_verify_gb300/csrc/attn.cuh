@@ -16,12 +16,14 @@ constexpr float kNegInf = -INFINITY;
 
 // One sequence: its first row of the step's tensors, new tokens, cached keys
 // and the cache place of its first new token.  Numbers that do not fit are
-// cut to what does, and recorded.
+// cut to what does, and recorded.  Rows go by the offsets up to the first pair
+// that does not fit: from that sequence on none has new tokens (a later offset
+// could claim rows of an earlier sequence); `fits` is that sequence's.
 struct Seq {
     int q0, nq, len, first;
 };
 
-__device__ __forceinline__ Seq load_seq(const SeqArgs& s, int page, int b, int32_t* err) {
+__device__ __forceinline__ Seq load_seq(const SeqArgs& s, int page, int b, int32_t* err, bool* fits = nullptr) {
     const int c0 = s.cu_q[b], c1 = s.cu_q[b + 1], len = s.kv_len[b];
     Seq r;
     r.q0 = c0;
@@ -35,6 +37,7 @@ __device__ __forceinline__ Seq load_seq(const SeqArgs& s, int page, int b, int32
     r.len = len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
     r.first = r.len - r.nq;
     if (bad_q || r.len != len) record_error(err, MOE_ERR_INVALID_ARG);
+    if (fits) *fits = !bad_q;
     return r;
 }
 
@@ -323,6 +326,7 @@ struct Plan {
     int64_t off;           // unit u0 lies `off` units into row tile rt of head h of sequence b
     int b, h, rt;
     int ctas;              // CTAs that take part
+    int seqs;              // sequences with rows: those before the first whose offsets do not fit
 
     __device__ __forceinline__ int owner(int64_t u) const {
         const int64_t head = extra * (share + 1);
@@ -337,21 +341,38 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int6
     using W = Work<MT, KT>;
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
     const int per = (a.sq.n + nt - 1) / nt;
-    const int b0 = min(a.sq.n, tid * per), b1 = min(a.sq.n, b0 + per);
-    int64_t mine = 0, head = 0;                // units of the thread's sequences, of a head of the last one
+    int seqs = a.sq.n, b0;
+    int64_t mine, head = 0, incl;              // units of the thread's sequences, of a head of the last one
+    for (;;) {
+        b0 = min(seqs, tid * per);
+        const int b1 = min(seqs, b0 + per);
+        bool fits = true;
+        int bad = b1;
+        mine = 0;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-        head = W::head_units(a, load_seq(a.sq, a.kv.page, b, a.err));
-        mine += a.kv.heads * head;
-    }
-    int64_t incl = mine;
+        for (int b = b0; b < b1; ++b) {
+            head = W::head_units(a, load_seq(a.sq, a.kv.page, b, a.err, &fits));
+            mine += a.kv.heads * head;
+            if (!fits) {
+                bad = b;
+                break;
+            }
+        }
+        incl = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += o;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) s_warp[wid] = incl;
+        if (!__syncthreads_or(!fits)) break;
+        // once more, with the sequences before the first one that does not fit
+        if (tid == 0) s_plan->seqs = seqs;
+        __syncthreads();
+        if (!fits) atomicMin(&s_plan->seqs, bad);
+        __syncthreads();
+        seqs = s_plan->seqs;
     }
-    if (lane == 31) s_warp[wid] = incl;
-    __syncthreads();
     int64_t before = 0, total = 0;
     for (int w = 0; w < (nt >> 5); ++w) {
         const int64_t v = s_warp[w];
@@ -370,6 +391,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int6
         s_plan->share = share;
         s_plan->extra = extra;
         s_plan->ctas = C;
+        s_plan->seqs = seqs;
         a.notes[c].pieces = 0;
     }
     const int64_t pre = before + incl - mine;
@@ -465,10 +487,10 @@ __device__ __forceinline__ void note_split(const AttnArgs& a, const Item& it, in
     a.notes[blockIdx.x] = n;
 }
 
-// Zeroes the output rows that belong to no sequence.
-__device__ __forceinline__ void zero_pad_rows(const AttnArgs& a) {
-    const int first = min(max(a.sq.cu_q[0], 0), a.sq.tokens);
-    const int last = min(max(a.sq.cu_q[a.sq.n], first), a.sq.tokens);
+// Zeroes the output rows that belong to no sequence: those before and after
+// the rows of the sequences that fit, which follow one another.
+__device__ __forceinline__ void zero_pad_rows(const AttnArgs& a, int seqs) {
+    const int first = seqs > 0 ? a.sq.cu_q[0] : a.sq.tokens, last = seqs > 0 ? a.sq.cu_q[seqs] : a.sq.tokens;
     const int n = first + (a.sq.tokens - last);
     for (int p = blockIdx.x; p < n; p += gridDim.x) {
         const int64_t t = p < first ? p : last + (p - first);

@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     pdl_launch_dependents();
     plan_work<kMT, kKT>(a, 1, reinterpret_cast<int64_t*>(sh.ml), &sh.plan);   // (its barriers publish sh.tmem)
     tc_fence_after();
-    zero_pad_rows(a);
+    zero_pad_rows(a, sh.plan.seqs);
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         soften<D, E4M3>(a, sh, qs);

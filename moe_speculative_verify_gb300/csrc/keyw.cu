@@ -123,6 +123,7 @@ struct Scheduler {
     Seq s;
     int b, g, h, groups, dg, dh;
     int64_t skip;                           // items still to pass before this CTA's next, past (g, h)
+    bool rows;                              // no sequence so far whose offsets do not fit
 
     __device__ __forceinline__ void start(const KeywArgs& ka) {
         b = -1;
@@ -130,6 +131,7 @@ struct Scheduler {
         dg = gridDim.x / ka.a.kv.heads;
         dh = gridDim.x - dg * ka.a.kv.heads;
         skip = blockIdx.x;
+        rows = true;
     }
     __device__ __forceinline__ bool next(const KeywArgs& ka, Item& it) {
         const AttnArgs& a = ka.a;
@@ -144,7 +146,13 @@ struct Scheduler {
         }
         while (b < 0 || g >= groups) {
             if (++b >= a.sq.n) return false;
-            s = load_seq(a.sq, a.kv.page, b, a.err);
+            bool fits;
+            s = load_seq(a.sq, a.kv.page, b, a.err, &fits);
+            rows = rows && fits;
+            if (!rows) {
+                s.q0 = s.nq = 0;
+                s.first = s.len;
+            }
             groups = (s.len + 2 * kKeys - 1) / (2 * kKeys);
             const int64_t count = int64_t(groups) * a.kv.heads;
             if (skip >= count) {

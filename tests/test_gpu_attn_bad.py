@@ -1,0 +1,57 @@
+"""Numbers that do not fit, sizes at the documented limits: recorded, refused
+or answered, never left half done."""
+import pytest
+import torch
+
+import attn_ref as ref
+import moe_speculative_verify_gb300 as m
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    m.build()
+    m.load()
+    torch.cuda.set_device(0)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def workspace(attn, cache):
+    return torch.zeros(m.moe_attn_workspace_bytes(attn, cache), dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("news", [1, 6])            # few rows, and a tile of 48
+@pytest.mark.parametrize("cu", ["past", "back", "first", "negative"])
+def test_rows_of_a_bad_sequence_are_pad_rows(news, cu):
+    """Offsets that do not fit: the sequence and those after it have no new
+    tokens, and their rows are +0 and -inf as pad rows are."""
+    p = ref.Problem([70, 50, 90], [news] * 3, 8, 1, 64, 16, seed=31).cuda()
+    offs = {"past": [0, news, 3 * news + 1, 3 * news], "back": [0, news, news - 1, news - 1],
+            "first": [3 * news + 4, 3 * news + 5, 3 * news + 6, 3 * news + 7], "negative": [-2, -1, 0, 1]}[cu]
+    good = {"past": 1, "back": 1, "first": 0, "negative": 0}[cu]
+    attn = m.Attn(8, p.scale, wait_timeout_us=200000)
+    scores = torch.rand(3, 1, 96, generator=torch.Generator().manual_seed(1)).cuda()
+    out, good_z = {}, None
+    for name, c in (("good", [0, news, 2 * news, 3 * news]), ("bad", offs)):
+        ws = workspace(attn, p.cache)
+        o = torch.full((3 * news, 8, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        z = torch.full((3 * news, 8), float("nan"), device="cuda")
+        m.moe_paged_attention(attn, p.cache, m.Seqs.from_tensors(i32(c), p.d_kv_len, p.d_table, news), p.d_q(), o, ws, lse=z)
+        assert m.moe_get_device_error(ws) == (0 if name == "good" else 1)
+        sc = scores.clone()
+        m.moe_key_weights(attn, p.cache, m.Seqs.from_tensors(i32(c), p.d_kv_len, p.d_table, news), p.d_q(), good_z if good_z is not None
+                          else z, sc, sc, ws, decay=0.5)
+        assert m.moe_get_device_error(ws) == (0 if name == "good" else 1)
+        good_z = z if good_z is None else good_z
+        out[name] = o, z, sc
+    n = good * news
+    assert torch.equal(out["bad"][0][:n], out["good"][0][:n]) and torch.equal(out["bad"][1][:n], out["good"][1][:n])
+    rest = out["bad"][0][n:]
+    assert torch.all(rest.view(torch.int16) == 0) and torch.all(torch.isneginf(out["bad"][1][n:]))
+    assert torch.equal(out["bad"][2][:good], out["good"][2][:good])
+    for b in range(good, 3):                 # no new tokens: every key's score decays
+        assert torch.equal(out["bad"][2][b, :, :p.lens[b]], scores[b, :, :p.lens[b]] * 0.5)
