@@ -566,18 +566,18 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
 // SM's rate, here every SM reads some.
 // A unit is kJoinRows rows of a split item; the blocks share the units of all
 // items out among them (each adds up the notes for itself).  Four threads have
-// four columns of a row, each a quarter of the pieces, so that all pieces are
-// in flight at once.  The first piece is added before the loop over the others,
+// four columns of a row, each a quarter of the pieces, kBatch of them in
+// flight at a time.  The first piece is added before the loop over the others,
 // which lie at one distance from each other: with the first one's place chosen
 // inside an unrolled loop, joins of 128 columns whose first quarter counted a
 // multiple of eight pieces ended in a misaligned access.
 constexpr int kJoinRows = 4, kJoinParts = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel(const AttnArgs a, int n_notes) {
+__global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4, 1) attn_join_kernel(const AttnArgs a, int n_notes) {
     constexpr int64_t kSlot = kAttnSlotRows * (D + 2);
     constexpr int kCells = kJoinRows * D / 4;                                  // threads of a part
-    constexpr int kPer = kAttnMaxCtas / 32;
+    constexpr int kPer = kAttnMaxCtas / 32, kBatch = 8;
     __shared__ float4 s_v[kJoinParts][kCells];
     __shared__ float s_sum[kJoinParts][kJoinRows];
     __shared__ int s_end[kAttnMaxCtas];                                        // units up to note i, inclusive
@@ -618,14 +618,17 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel
         const int row = min(row0 + rl, n.rows - 1);
         const int ml = kAttnSlotRows * D + 2 * row, od = (d4 * kAttnSlotRows + row) * 4;
         float top = head[ml];
-#pragma unroll 8
-        for (int k = 1; k < n.pieces; ++k) top = fmaxf(top, rest[k * kSlot + ml]);
+        for (int k0 = 1; k0 < n.pieces; k0 += kBatch) {
+            float t[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) t[j] = k0 + j < n.pieces ? rest[(k0 + j) * kSlot + ml] : kNegInf;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) top = fmaxf(top, t[j]);
+        }
         const float ref = top == kNegInf ? 0.0f : top;
         float sum = 0.0f;
         float4 v = make_float4(0, 0, 0, 0);
-        auto add = [&](const float* p) {
-            const float2 x = *reinterpret_cast<const float2*>(p + ml);
-            const float4 y = *reinterpret_cast<const float4*>(p + od);
+        auto add = [&](const float2& x, const float4& y) {
             const float w = fast_exp2(x.x - ref);
             sum += x.y * w;
             v.x += y.x * w;
@@ -633,9 +636,30 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel
             v.z += y.z * w;
             v.w += y.w * w;
         };
-        if (part == 0) add(head);
-#pragma unroll 8
-        for (int k = part > 0 ? part : kJoinParts; k < n.pieces; k += kJoinParts) add(rest + k * kSlot);
+        float2 hx = make_float2(kNegInf, 0.0f);
+        float4 hy = make_float4(0, 0, 0, 0);
+        if (part == 0) {
+            hx = *reinterpret_cast<const float2*>(head + ml);
+            hy = *reinterpret_cast<const float4*>(head + od);
+        }
+        for (int k0 = part > 0 ? part : kJoinParts; k0 < n.pieces || k0 == kJoinParts; k0 += kBatch * kJoinParts) {
+            float2 x[kBatch];
+            float4 y[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int k = k0 + j * kJoinParts;
+                x[j] = make_float2(kNegInf, 0.0f);
+                y[j] = make_float4(0, 0, 0, 0);
+                if (k < n.pieces) {
+                    x[j] = *reinterpret_cast<const float2*>(rest + k * kSlot + ml);
+                    y[j] = *reinterpret_cast<const float4*>(rest + k * kSlot + od);
+                }
+            }
+            if (k0 == kJoinParts) add(hx, hy);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (k0 + j * kJoinParts < n.pieces) add(x[j], y[j]);
+        }
         s_v[part][cell] = v;
         if (d4 == 0) s_sum[part][rl] = sum;
         __syncthreads();
@@ -665,11 +689,12 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4) attn_join_kernel
 }  // namespace
 
 cudaError_t launch_attn_join(const AttnArgs& a, int n_notes, cudaStream_t s) {
-    // two blocks an SM
+    // one block an SM: with two, their registers leave fewer pieces in flight (one verify block 20.8 -> 22.1 us), and
+    // a call without a split item waits for a second wave (8 keys 9.5 -> 10.4)
     const cudaError_t e =
         a.kv.dim == 128
-            ? launch_pdl(attn_join_kernel<128>, dim3(2 * n_notes), dim3(kJoinRows * kJoinParts * 32), 0, s, a, n_notes)
-            : launch_pdl(attn_join_kernel<64>, dim3(2 * n_notes), dim3(kJoinRows * kJoinParts * 16), 0, s, a, n_notes);
+            ? launch_pdl(attn_join_kernel<128>, dim3(n_notes), dim3(kJoinRows * kJoinParts * 32), 0, s, a, n_notes)
+            : launch_pdl(attn_join_kernel<64>, dim3(n_notes), dim3(kJoinRows * kJoinParts * 16), 0, s, a, n_notes);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
