@@ -132,6 +132,11 @@ struct KeywMaps {
     CUtensorMap k, q;
 };
 
+// The widest window the kernels take, so that the place of a query (at least
+// -MOE_MAX_TOKENS, where new tokens outnumber keys) less the window stays in 32
+// bits; no sequence is long enough for a wider one to matter.
+constexpr int kMaxWindow = 0x7FFFFFFF - 0x10000 - 1;
+
 // Rows a kv head (new tokens of a sequence times query heads a kv head) up to
 // which the few-rows kernel is taken: one 16-row matrix tile.
 constexpr int kAttnFewRows = 16;

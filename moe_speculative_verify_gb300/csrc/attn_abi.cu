@@ -191,7 +191,7 @@ moe::AttnArgs attn_args(const moe_attn_t* at, const moe_kv_cache_t* c, const moe
     a.group_magic = a.group > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + a.group - 1) / a.group) : 0u;
     a.scale = at->scale;
     a.causal = at->causal != 0;
-    a.window = at->window;
+    a.window = at->window < moe::kMaxWindow ? at->window : moe::kMaxWindow;
     uint8_t* base = static_cast<uint8_t*>(ws);
     a.err = reinterpret_cast<int32_t*>(base);
     a.notes = reinterpret_cast<moe::SplitNote*>(base + moe::kAttnNotes);

@@ -1,5 +1,6 @@
 """Numbers that do not fit, sizes at the documented limits: recorded, refused
 or answered, never left half done."""
+import numpy as np
 import pytest
 import torch
 
@@ -55,3 +56,25 @@ def test_rows_of_a_bad_sequence_are_pad_rows(news, cu):
     assert torch.equal(out["bad"][2][:good], out["good"][2][:good])
     for b in range(good, 3):                 # no new tokens: every key's score decays
         assert torch.equal(out["bad"][2][b, :, :p.lens[b]], scores[b, :, :p.lens[b]] * 0.5)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq", [1, 4])              # few rows, and a tile
+def test_window_without_limit_and_more_new_tokens_than_keys(causal, hq):
+    """The largest window is none at all, also where new tokens outnumber keys."""
+    p = ref.Problem([9, 20], [16, 6], hq, 1, 64, 16, seed=32).cuda()
+    got = []
+    for window in (0, 2 ** 31 - 1):
+        attn = m.Attn(hq, p.scale, causal, window, wait_timeout_us=200000)
+        ws = workspace(attn, p.cache)
+        out = torch.empty((p.t, hq, 64), dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty((p.t, hq), device="cuda")
+        m.moe_paged_attention(attn, p.cache, p.seqs, p.d_q(), out, ws, lse=lse)
+        sc = torch.zeros(2, 1, 32, device="cuda")
+        m.moe_key_weights(attn, p.cache, p.seqs, p.d_q(), lse, sc, sc, ws)
+        assert m.moe_get_device_error(ws) == 0
+        got.append((out, lse, sc))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    z = ref.attention(p, causal)[1]
+    assert np.array_equal(np.isneginf(got[1][1].cpu().numpy()), np.isneginf(z))

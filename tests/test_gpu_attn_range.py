@@ -1,0 +1,65 @@
+"""Attention where probabilities and query elements spread over many octaves:
+a first key that takes most of the weight and has value zero, as trained models'
+caches have it, so that the output is the average over thousands of keys of
+small probability each; a query element far above the others."""
+import pytest
+import torch
+
+import moe_speculative_verify_gb300 as m
+from attn_one import One, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    m.build()
+    m.load()
+    torch.cuda.set_device(0)
+
+
+def sink(keys, news, hq, dtype, dim, gap, tail, mean=0.5, seed=1):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = torch.zeros(keys, 1, dim, device="cuda") if tail == "equal" else (randn(g, keys, 1, dim) * 16).round() / 16
+    k[:, :, 0] = 0
+    k[0] = 0
+    k[0, 0, 0] = 16.0
+    v = ((randn(g, keys, 1, dim) + mean) * 16).round() / 16
+    v[0] = 0
+    q = randn(g, news, hq, dim)
+    q[:, :, 0] = gap * dim ** 0.5 / 16.0                    # the first key's score; the others' are 0, or about 1 apart
+    return One(k, v, q, dtype, dim ** -0.5)
+
+
+# rows a kv head: 8 (few rows), 32, 64 (repeated in the tile), 96 (one tile), 320 (two tiles)
+@pytest.mark.parametrize("news,hq", [(1, 8), (4, 8), (8, 8), (12, 8), (40, 8)])
+@pytest.mark.parametrize("keys", [16384, 32768])
+@pytest.mark.parametrize("tail", ["equal", "spread"])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_small_probabilities_behind_a_sink(dtype, tail, keys, news, hq):
+    for gap in (8.0, 10.28, 12.0, 13.0, 14.0, 15.0, 16.0):
+        for dim in (64, 128):
+            sink(keys, news, hq, dtype, dim, gap, tail).check()
+
+
+@pytest.mark.parametrize("news", [1, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_small_probabilities_of_a_million_keys(dtype, news):
+    for gap in (14.0, 16.0, 18.0):
+        sink(1 << 20, news, 8, dtype, 128, gap, "equal").check()
+
+
+@pytest.mark.parametrize("news,hq", [(1, 8), (8, 8), (40, 8)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_outlier_query_channel(dtype, dim, news, hq):
+    """A query element far above the others where the keys have zero: the others
+    alone make the scores."""
+    for size in (1e3, 1e5, 1e6):
+        g = torch.Generator(device="cuda").manual_seed(3)
+        k = (randn(g, 500, 1, dim) * 16).round() / 16
+        k[:, :, 5] = 0
+        v = (randn(g, 500, 1, dim) * 16).round() / 16
+        q = randn(g, news, hq, dim) * 3
+        q[:, :, 5] = size
+        One(k, v, q, dtype, dim ** -0.5).check()
