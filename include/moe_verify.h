@@ -464,6 +464,7 @@ moe_status_t moe_greedy_verify(const void* logits, int32_t logits_bf16, int32_t 
 #define MOE_MAX_HEADS 256      /* query heads                                     */
 #define MOE_MAX_SEQS 4096      /* sequences per call                              */
 #define MOE_MAX_TOKENS 65536   /* new tokens per call                             */
+#define MOE_MAX_KV_LEN 2147352576  /* cached tokens of a sequence: 2^31 - 2^17; a longer length is cut as one past its table */
 
 /*
  * One layer's paged cache: element (page, head, token, d) of K at
@@ -497,7 +498,7 @@ typedef struct {
  * ones included, so new token i lies at cache place kv_len[b] - n_b + i, in
  * page block_table[b, place / page_size].  Rows of no sequence are pad rows.
  *   cu_q         int32 [n_seqs + 1]
- *   kv_len       int32 [n_seqs]
+ *   kv_len       int32 [n_seqs], at most MOE_MAX_KV_LEN
  *   block_table  int32 [n_seqs, max_pages]; entries past a sequence's length are not read
  *   max_q        largest number of new tokens of a sequence; it only picks the
  *                kernel, the results hold for any value >= 1

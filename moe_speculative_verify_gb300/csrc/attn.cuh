@@ -33,7 +33,7 @@ __device__ __forceinline__ Seq load_seq(const SeqArgs& s, int page, int b, int32
         r.q0 = 0;
         r.nq = 0;
     }
-    const int64_t cap = int64_t(s.max_pages) * page;
+    const int64_t cap = min(int64_t(s.max_pages) * page, int64_t(MOE_MAX_KV_LEN));
     r.len = len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
     r.first = r.len - r.nq;
     if (bad_q || r.len != len) record_error(err, MOE_ERR_INVALID_ARG);

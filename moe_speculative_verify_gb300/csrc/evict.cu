@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const EvictArgs a, 
     const int bh = blockIdx.x, b = bh / a.kv.heads, h = bh - b * a.kv.heads;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t cap = min(int64_t(a.sq.max_pages) * a.kv.page, a.score_stride);
+    const int64_t cap = min(min(int64_t(a.sq.max_pages) * a.kv.page, a.score_stride), int64_t(MOE_MAX_KV_LEN));
     const int len = a.sq.kv_len[b];
     const int n = len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
     if (n != len && tid == 0) record_error(a.err, MOE_ERR_INVALID_ARG);

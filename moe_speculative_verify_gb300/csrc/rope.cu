@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     // this token's place in the cache; dst < 0: not stored
     int64_t dst = -1;
     if (b >= 0) {
-        const int at = a.sq.kv_len[b] - (s_end - s_q0) + (t - s_q0);
+        const int64_t at = int64_t(a.sq.kv_len[b]) - (s_end - s_q0) + (t - s_q0);
         if (at >= 0 && (at >> a.kv.page_log2) < a.sq.max_pages) {
             const int pg = a.sq.table[int64_t(b) * a.sq.max_pages + (at >> a.kv.page_log2)];
             if (pg >= 0 && pg < a.kv.n_pages)

@@ -78,3 +78,35 @@ def test_window_without_limit_and_more_new_tokens_than_keys(causal, hq):
         assert torch.equal(a, b)
     z = ref.attention(p, causal)[1]
     assert np.array_equal(np.isneginf(got[1][1].cpu().numpy()), np.isneginf(z))
+
+
+@pytest.mark.parametrize("hq", [1, 20])             # few rows, and a tile
+def test_lengths_near_2_to_31(hq):
+    """The longest sequence's last keys are found; a longer length is cut to it and recorded."""
+    page, dim, pages, longest, window = 128, 64, 8, 2 ** 31 - 2 ** 17, 300
+    g = torch.Generator(device="cuda").manual_seed(41)
+    k, v = (torch.randn(pages, 1, page, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    cache = m.KVCache.from_tensors(k, v)
+    table = torch.randint(0, pages, (1, 2 ** 31 // page), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn(1, hq, dim, generator=g, device="cuda").bfloat16()
+    attn = m.Attn(hq, 0.125, window=window)
+    places = torch.arange(longest - window, longest, device="cuda")
+    rows = table[0, places // page].long()
+    kk, vv = (x[rows, 0, places % page].double() for x in (k, v))
+    s = q[0].double() @ kk.t() * 0.125
+    want, z = torch.softmax(s, 1) @ vv, torch.logsumexp(s, 1)
+    for length in (longest, 2 ** 31 - 1):
+        seqs = m.Seqs.from_tensors(i32([0, 1]), i32([length]), table, hq)   # max_q picks the kernel
+        ws = workspace(attn, cache)
+        out = torch.empty((1, hq, dim), dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty((1, hq), device="cuda")
+        m.moe_paged_attention(attn, cache, seqs, q, out, ws, lse=lse)
+        assert m.moe_get_device_error(ws) == (0 if length == longest else 1)
+        # bf16 probabilities and outputs of unit values: 2^-8 of sum p|v| and of |out|; scores' error below 2^-16
+        assert bool(((out[0].double() - want).abs() <= 2.0 ** -7).all())
+        assert bool(((lse[0].double() - z).abs() <= 2.0 ** -14).all())
+        scores = torch.rand(1, 1, 256, device="cuda")
+        got = scores.clone()
+        m.moe_key_weights(attn, cache, seqs, q, lse, got, got, ws, decay=0.5)
+        assert m.moe_get_device_error(ws) == (0 if length == longest else 1)
+        assert torch.equal(got, scores * 0.5)
