@@ -206,14 +206,15 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const EvictArgs a, 
 constexpr int kMoveThreads = 256, kFlight = 4;
 
 // LANES threads move a row (16 bytes of K and of V each); a block
-// kFlight * kMoveThreads / LANES rows of one pair.
+// kFlight * kMoveThreads / LANES rows of one pair, from row block `block0` on.
+// Pairs are the grid's x, which alone may pass 65,535.
 template <int LANES, int ES>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int block0) {
     constexpr int kRows = kMoveThreads / LANES;
     pdl_wait();
     pdl_launch_dependents();
-    const int bh = blockIdx.y, b = bh / a.kv.heads, h = bh - b * a.kv.heads;
-    const int keep = a.new_len[b], r0 = blockIdx.x * kFlight * kRows + threadIdx.x / LANES;
+    const int bh = blockIdx.x, b = bh / a.kv.heads, h = bh - b * a.kv.heads;
+    const int keep = a.new_len[b], r0 = (block0 + static_cast<int>(blockIdx.y)) * kFlight * kRows + threadIdx.x / LANES;
     const int32_t* kept = a.kept + int64_t(bh) * a.budget;
     const int32_t* from = a.sq.table + int64_t(b) * a.sq.max_pages;
     const int32_t* to = a.to_table + int64_t(b) * a.to_pages;
@@ -254,9 +255,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
 
 template <int LANES, int ES>
 cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
-    const int rows = kFlight * kMoveThreads / LANES;
-    return launch_pdl(move_kernel<LANES, ES>, dim3((a.budget + rows - 1) / rows, a.sq.n * a.kv.heads),
-                      dim3(kMoveThreads), 0, s, a);
+    constexpr int kMost = 65535;                 // row blocks of a launch
+    const int rows = kFlight * kMoveThreads / LANES, most = a.budget < MOE_MAX_KV_LEN ? a.budget : MOE_MAX_KV_LEN;
+    const int blocks = (most + rows - 1) / rows;
+    cudaError_t e = cudaSuccess;
+    for (int k = 0; k < blocks && e == cudaSuccess; k += kMost)
+        e = launch_pdl(move_kernel<LANES, ES>, dim3(a.sq.n * a.kv.heads, blocks - k < kMost ? blocks - k : kMost),
+                       dim3(kMoveThreads), 0, s, a, k);
+    return e;
 }
 
 }  // namespace

@@ -110,3 +110,28 @@ def test_lengths_near_2_to_31(hq):
         m.moe_key_weights(attn, cache, seqs, q, lse, got, got, ws, decay=0.5)
         assert m.moe_get_device_error(ws) == (0 if length == longest else 1)
         assert torch.equal(got, scores * 0.5)
+
+
+@pytest.mark.parametrize("n,h", [(4096, 16), (2100, 32), (300, 256)])
+def test_evict_of_many_pairs(n, h):
+    """More than 65,535 (sequence, kv head) pairs."""
+    page, dim, length, budget = 16, 64, 5, 2
+    g = torch.Generator(device="cuda").manual_seed(33)
+    k = torch.randn(2 * n, h, page, dim, generator=g, device="cuda").bfloat16()
+    v = torch.randn(2 * n, h, page, dim, generator=g, device="cuda").bfloat16()
+    k0, v0 = k.clone(), v.clone()
+    cache = m.KVCache.from_tensors(k, v)
+    ar = torch.arange(n, dtype=torch.int32, device="cuda")
+    seqs = m.Seqs.from_tensors(None, torch.full((n,), length, dtype=torch.int32, device="cuda"), ar[:, None].contiguous())
+    scores = torch.rand(n, h, 8, generator=g, device="cuda")
+    kept = torch.full((n, h, budget), -9, dtype=torch.int32, device="cuda")
+    out, new_len = torch.zeros_like(scores), torch.zeros_like(ar)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    m.moe_cache_evict(cache, seqs, scores, budget, 1, (ar + n)[:, None].contiguous(), kept, out, new_len, ws)
+    assert m.moe_get_device_error(ws) == 0
+    best = scores[:, :, :length - 1].argmax(2, keepdim=True)
+    want = torch.cat([best, torch.full_like(best, length - 1)], 2)
+    assert torch.equal(kept.long(), want) and bool((new_len == budget).all())
+    for x, x0 in ((k, k0), (v, v0)):
+        rows = torch.gather(x0[:n], 2, want[..., None].expand(-1, -1, -1, dim))
+        assert torch.equal(x[n:, :, :budget], rows) and torch.equal(x[:n], x0[:n]) and torch.equal(x[n:, :, budget:], x0[n:, :, budget:])
