@@ -639,6 +639,8 @@ moe_status_t moe_key_weights(const moe_attn_t* attn, const moe_kv_cache_t* cache
  *               pages that any sequence of this call still reads (shared
  *               prefix pages stay as they are); to_pages * page_size >= budget
  * cu_q and max_q of seqs are not read.  budget >= 1, 0 <= n_recent <= budget.
+ * Rows of a source page outside the cache move as zeros; a row whose destination
+ * page lies outside is not written.
  */
 moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs,
                              const float* scores, int64_t score_stride, int32_t budget,

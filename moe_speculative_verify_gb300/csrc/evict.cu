@@ -231,19 +231,31 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
     for (int i = 0; i < kFlight; ++i) ps[i] = j[i] >= 0 ? from[j[i] >> a.kv.page_log2] : -1;
     uint4 x[kFlight], y[kFlight];
     int64_t dst[kFlight];
+    unsigned bad = 0;                            // bit i: row i has no source page; 16: a row has no destination page
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
         const int r = r0 + i * kRows;
         dst[i] = -1;
         if (j[i] < 0) continue;
-        if (ps[i] < 0 || ps[i] >= a.kv.n_pages || pd[i] < 0 || pd[i] >= a.kv.n_pages) {
-            if (sub == 0) record_error(a.err, MOE_ERR_INVALID_ARG);
+        if (pd[i] < 0 || pd[i] >= a.kv.n_pages) {
+            bad |= 16u;
             continue;
+        }
+        if (ps[i] < 0 || ps[i] >= a.kv.n_pages) {        // its own destination is loaded, zeros are stored
+            bad |= 1u << i;
+            ps[i] = pd[i];
+            j[i] = r;
         }
         const int64_t src = ES * (ps[i] * a.kv.page_stride + head + (j[i] & (a.kv.page - 1)) * a.kv.token_stride) + sub;
         dst[i] = ES * (pd[i] * a.kv.page_stride + head + (r & (a.kv.page - 1)) * a.kv.token_stride) + sub;
         x[i] = *reinterpret_cast<const uint4*>(a.kv.k + src);
         y[i] = *reinterpret_cast<const uint4*>(a.kv.v + src);
+    }
+    if (bad) {
+        if (sub == 0) record_error(a.err, MOE_ERR_INVALID_ARG);
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+            if ((bad >> i) & 1u) x[i] = y[i] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kFlight; ++i)

@@ -135,3 +135,27 @@ def test_evict_of_many_pairs(n, h):
     for x, x0 in ((k, k0), (v, v0)):
         rows = torch.gather(x0[:n], 2, want[..., None].expand(-1, -1, -1, dim))
         assert torch.equal(x[n:, :, :budget], rows) and torch.equal(x[:n], x0[:n]) and torch.equal(x[n:, :, budget:], x0[n:, :, budget:])
+
+
+def test_evict_moves_a_bad_page_as_zeros():
+    """A source page outside the cache reads as zeros; a destination outside is
+    not written; both are recorded."""
+    p = ref.Problem([40], [0], 2, 1, 64, 16, seed=34).cuda()
+    total = p.d_k.shape[0]
+    k, v = (torch.cat([x, torch.full_like(x[:3], 7.0)]) for x in (p.d_k, p.d_v))
+    k0 = k.clone()
+    cache = m.KVCache.from_tensors(k, v)
+    table = p.d_table.clone()
+    table[0, 1] = 1 << 29
+    kept = torch.zeros(1, 1, 48, dtype=torch.int32, device="cuda")
+    new_len = i32([0])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    scores = torch.rand(1, 1, 48, device="cuda")
+    m.moe_cache_evict(cache, m.Seqs.from_tensors(None, p.d_kv_len, table), scores, 48, 0, i32([[total, total + 1, -1]]), kept,
+                      torch.empty_like(scores), new_len, ws)
+    assert m.moe_get_device_error(ws) == 1
+    assert int(new_len[0]) == 40 and kept[0, 0].tolist() == list(range(40)) + [-1] * 8
+    for x, x0 in ((k, p.d_k), (v, p.d_v)):
+        assert torch.equal(x[total], x0[int(p.table[0, 0])])
+        assert bool((x[total + 1] == 0).all()) and bool((x[total + 2] == 7.0).all())
+    assert torch.equal(k[:total].view(torch.int16), k0[:total].view(torch.int16))
