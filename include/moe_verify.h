@@ -556,7 +556,8 @@ moe_status_t moe_rope_freqs(int32_t rot_dim, double base, int32_t kind, double f
  * Strides in elements, multiples of 8; pointers 16-byte aligned; q_out and the
  * cache overlap no other argument.  fp32 arithmetic, one rounding: bf16
  * (nearest even), or the e4m3 code of x / scale (nearest even, saturating).
- * A new token whose place is negative or past its block table, or whose page
+ * Tokens of sequences whose offsets do not fit, and of those after them, are
+ * pad rows.  A new token whose place is negative or past its block table, or whose page
  * lies outside the cache, is not stored.  n_tokens == 0 launches nothing.
  */
 moe_status_t moe_rope_append(const moe_rope_t* rope, const moe_kv_cache_t* cache,

@@ -92,20 +92,19 @@ __device__ __forceinline__ Raw load_unit(const Unit& u) {
 
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     __shared__ float2 s_cs[64];
-    __shared__ int s_seq, s_q0, s_end;
+    __shared__ int s_seq, s_bad;                 // lowest sequence with this token; first one that does not fit
     const int t = blockIdx.x, tid = threadIdx.x;
     const int half = a.rot >> 1;
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) s_seq = -1;
+    if (tid == 0) s_seq = s_bad = a.sq.n;
     __syncthreads();
     for (int b = tid; b < a.sq.n; b += kRopeThreads) {
         const int c0 = a.sq.cu_q[b], c1 = a.sq.cu_q[b + 1];
-        if (c0 >= 0 && t >= c0 && t < c1 && c1 <= a.sq.tokens) {
-            s_seq = b;
-            s_q0 = c0;
-            s_end = c1;
-        }
+        if (c0 < 0 || c1 < c0 || c1 > a.sq.tokens)
+            atomicMin(&s_bad, b);
+        else if (t >= c0 && t < c1)
+            atomicMin(&s_seq, b);
     }
     // the thread's first units are on their way while the angles are worked out
     const int D = a.kv.dim, per = D / 16, units = (a.q_heads + 2 * a.kv.heads) * per;
@@ -127,11 +126,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
         s_cs[tid] = make_float2(cs * a.magnitude, sn * a.magnitude);
     }
     __syncthreads();
-    const int b = s_seq;
+    // (from the first sequence on whose offsets do not fit, none has new tokens)
+    const int b = s_seq < s_bad ? s_seq : -1;
     // this token's place in the cache; dst < 0: not stored
     int64_t dst = -1;
     if (b >= 0) {
-        const int64_t at = int64_t(a.sq.kv_len[b]) - (s_end - s_q0) + (t - s_q0);
+        const int64_t at = int64_t(a.sq.kv_len[b]) - a.sq.cu_q[b + 1] + t;
         if (at >= 0 && (at >> a.kv.page_log2) < a.sq.max_pages) {
             const int pg = a.sq.table[int64_t(b) * a.sq.max_pages + (at >> a.kv.page_log2)];
             if (pg >= 0 && pg < a.kv.n_pages)

@@ -159,3 +159,22 @@ def test_evict_moves_a_bad_page_as_zeros():
         assert torch.equal(x[total], x0[int(p.table[0, 0])])
         assert bool((x[total + 1] == 0).all()) and bool((x[total + 2] == 7.0).all())
     assert torch.equal(k[:total].view(torch.int16), k0[:total].view(torch.int16))
+
+
+def test_rope_with_offsets_that_run_backwards():
+    """A token that two sequences claim belongs to the first; the sequences from
+    the first bad offset on have none."""
+    p = ref.Problem([40, 30, 50], [5, 0, 3], 8, 2, 64, 16, seed=35).cuda()
+    freqs, mag = m.moe_rope_freqs(64)
+    rope = m.Rope.from_freqs(freqs.cuda(), False, mag)
+    got = []
+    for offs in ([0, 5, 5, 5], [0, 5, 3, 8], [0, 5, 9, 8]):
+        k, v = p.d_k.clone(), p.d_v.clone()
+        q_out = torch.full((8, 8, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        seqs = m.Seqs.from_tensors(i32(offs), p.d_kv_len, p.d_table, 8)
+        m.moe_rope_append(rope, m.KVCache.from_tensors(k, v), seqs, p.d_qkv[:, :8], p.d_qkv[:, 8:10], p.d_qkv[:, 10:],
+                          torch.arange(8, dtype=torch.int32, device="cuda"), q_out)
+        got.append([x.view(torch.int16) for x in (k, v, q_out)])
+    assert bool((got[0][2][5:] == 0).all())
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
