@@ -68,9 +68,9 @@ class Layer:
         self.kv_len = torch.zeros(1, dtype=torch.int32, device=dev)
         self.scores = torch.zeros(1, n_kv, capacity, device=dev)
         freqs, mag = m.moe_rope_freqs(dim)
-        self.rope = m.Rope.from_freqs(freqs.to(dev), False, mag)
         self.attn = m.Attn(n_q, dim ** -0.5)
         self.ws = torch.zeros(m.moe_attn_workspace_bytes(self.attn, self.cache), dtype=torch.uint8, device=dev)
+        self.rope = m.Rope.from_freqs(freqs.to(dev), False, mag, self.ws)
         self.cached = 0           # host's copy of kv_len
         self.position = 0         # of the next token; it runs on when keys are evicted
 

@@ -453,7 +453,8 @@ moe_status_t moe_greedy_verify(const void* logits, int32_t logits_bf16, int32_t 
  *
  * A page index outside the cache or a sequence whose numbers do not fit is
  * never followed: the call records MOE_ERR_INVALID_ARG in the error word of
- * its workspace (read with moe_get_device_error) and reads such a page as
+ * its workspace (read with moe_get_device_error; moe_rope_append, which has
+ * none, in moe_rope_t.err) and reads such a page as
  * zeros, a length past the block table as what the table holds.  An offset
  * past n_tokens or below the one before it leaves its sequence and those after
  * it without new tokens: the rows from there on are pad rows.
@@ -519,12 +520,16 @@ typedef struct {
  *   freqs      fp32 [rot_dim/2, 2] device: turns per position of pair i as a
  *              sum of two fp32 (moe_rope_freqs fills it)
  *   magnitude  multiplies cos and sin (1 without long-context scaling)
+ *   err        int32 device word, zero at first, where moe_rope_append records
+ *              MOE_ERR_INVALID_ARG; the start of an attention workspace, so that
+ *              moe_get_device_error reads it, or NULL: nothing is recorded
  */
 typedef struct {
     const float* freqs;
     int32_t rot_dim;
     int32_t interleaved;
     float magnitude;
+    int32_t* err;
 } moe_rope_t;
 
 /*
@@ -557,8 +562,10 @@ moe_status_t moe_rope_freqs(int32_t rot_dim, double base, int32_t kind, double f
  * cache overlap no other argument.  fp32 arithmetic, one rounding: bf16
  * (nearest even), or the e4m3 code of x / scale (nearest even, saturating).
  * Tokens of sequences whose offsets do not fit, and of those after them, are
- * pad rows.  A new token whose place is negative or past its block table, or whose page
- * lies outside the cache, is not stored.  n_tokens == 0 launches nothing.
+ * pad rows.  A new token whose place is past its block table or whose page lies
+ * outside the cache is not stored, which is recorded; one whose place is
+ * negative (more new tokens than keys) has no key.  n_tokens == 0 launches
+ * nothing.
  */
 moe_status_t moe_rope_append(const moe_rope_t* rope, const moe_kv_cache_t* cache,
                              const moe_seqs_t* seqs, const void* q, int64_t q_stride,
@@ -653,8 +660,8 @@ moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs
  * moe_get_device_error -- synchronises `stream`, then reads (and clears when
  * `clear` != 0) the device error word at the start of a workspace given to
  * moe_expert_ffn_fp8, moe_layer or one of the attention calls.  Returns MOE_OK, MOE_ERR_TIMEOUT (a bounded
- * wait ran out: the kernel stopped, released its tensor memory and returned)
- * or MOE_ERR_CUDA.
+ * wait ran out: the kernel stopped, released its tensor memory and returned),
+ * MOE_ERR_INVALID_ARG (numbers on the device that do not fit) or MOE_ERR_CUDA.
  */
 moe_status_t moe_get_device_error(void* ws, int32_t clear, moe_stream_t stream);
 

@@ -142,16 +142,19 @@ class Seqs(C.Structure):
 
 class Rope(C.Structure):
     _fields_ = [("freqs", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
-                ("magnitude", C.c_float)]
+                ("magnitude", C.c_float), ("err", C.c_void_p)]
 
     @classmethod
-    def from_freqs(cls, freqs, interleaved: bool = False, magnitude: float = 1.0) -> "Rope":
-        """From moe_rope_freqs' table [rot_dim/2, 2], fp32 on the device."""
+    def from_freqs(cls, freqs, interleaved: bool = False, magnitude: float = 1.0,
+                   ws=None) -> "Rope":
+        """From moe_rope_freqs' table [rot_dim/2, 2], fp32 on the device. ws: an
+        attention workspace in whose error word moe_rope_append records tokens
+        that it could not store (None: nothing is recorded)."""
         if (freqs.dim() != 2 or freqs.shape[1] != 2 or freqs.dtype != torch.float32
                 or not freqs.is_contiguous()):
             raise MoeError(1, "Rope")
-        r = cls(freqs.data_ptr(), 2 * freqs.shape[0], 1 if interleaved else 0, magnitude)
-        r._tensors = (freqs,)
+        r = cls(freqs.data_ptr(), 2 * freqs.shape[0], 1 if interleaved else 0, magnitude, _ptr(ws))
+        r._tensors = (freqs, ws)
         return r
 
 

@@ -62,6 +62,7 @@ struct RopeArgs {
     const int32_t* pos;
     uint16_t* q_out;
     int32_t q_heads;
+    int32_t* err;            // may be NULL
 };
 
 struct AttnArgs {

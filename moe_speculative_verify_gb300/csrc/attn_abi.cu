@@ -268,7 +268,7 @@ moe_status_t moe_rope_append(const moe_rope_t* rope, const moe_kv_cache_t* cache
         !rows_ok(k, k_stride, cache->n_kv_heads * d) || !rows_ok(v, v_stride, cache->n_kv_heads * d))
         return MOE_ERR_INVALID_ARG;
     if (!positions || !aligned(positions, 4) ||
-        (rope->rot_dim > 0 && (!rope->freqs || !aligned(rope->freqs, 4))))
+        (rope->rot_dim > 0 && (!rope->freqs || !aligned(rope->freqs, 4))) || !aligned(rope->err, 4))
         return MOE_ERR_INVALID_ARG;
     moe::RopeArgs a{};
     a.kv = kv_args(cache);
@@ -287,6 +287,7 @@ moe_status_t moe_rope_append(const moe_rope_t* rope, const moe_kv_cache_t* cache
     a.pos = positions;
     a.q_out = static_cast<uint16_t*>(q_out);
     a.q_heads = n_q_heads;
+    a.err = rope->err;
     return cuda_status(moe::launch_rope(a, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     const int b = s_seq < s_bad ? s_seq : -1;
     // this token's place in the cache; dst < 0: not stored
     int64_t dst = -1;
+    bool lost = s_bad < a.sq.n;
     if (b >= 0) {
         const int64_t at = int64_t(a.sq.kv_len[b]) - a.sq.cu_q[b + 1] + t;
         if (at >= 0 && (at >> a.kv.page_log2) < a.sq.max_pages) {
@@ -137,7 +138,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
             if (pg >= 0 && pg < a.kv.n_pages)
                 dst = pg * a.kv.page_stride + (at & (a.kv.page - 1)) * a.kv.token_stride;
         }
+        lost = lost || (at >= 0 && dst < 0);
     }
+    if (lost && tid == 0) record_error(a.err, MOE_ERR_INVALID_ARG);
     for (int u0 = blockIdx.y * kRopeThreads + tid;;) {
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {

@@ -178,3 +178,27 @@ def test_rope_with_offsets_that_run_backwards():
     assert bool((got[0][2][5:] == 0).all())
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("wreck,code", [("none", 0), ("page", 1), ("length", 1), ("offsets", 1), ("fewer keys", 0)])
+def test_rope_records_what_it_could_not_store(wreck, code):
+    p = ref.Problem([40, 30], [5, 3], 8, 2, 64, 16, seed=36).cuda()
+    freqs, mag = m.moe_rope_freqs(64)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    table, kv_len, cu = p.d_table.clone(), p.d_kv_len.clone(), p.d_cu.clone()
+    if wreck == "page":
+        table[1, 1] = p.d_k.shape[0]
+    elif wreck == "length":
+        kv_len[0] = 16 * table.shape[1] + 1
+        table[:] = 0
+    elif wreck == "offsets":
+        cu[2] = 9
+    elif wreck == "fewer keys":
+        kv_len[1] = 2
+    seqs = m.Seqs.from_tensors(cu, kv_len, table, 5)
+    q_out = torch.empty(8, 8, 64, dtype=torch.bfloat16, device="cuda")
+    for rope in (m.Rope.from_freqs(freqs.cuda(), False, mag, ws), m.Rope.from_freqs(freqs.cuda(), False, mag)):
+        m.moe_rope_append(rope, p.cache, seqs, p.d_qkv[:, :8], p.d_qkv[:, 8:10], p.d_qkv[:, 10:],
+                          torch.arange(8, dtype=torch.int32, device="cuda"), q_out)
+        assert m.moe_get_device_error(ws) == code
+        code = 0                             # cleared by the read, and not recorded without a word
