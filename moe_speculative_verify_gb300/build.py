@@ -21,7 +21,7 @@ SOURCES = ["abi.cu", "router.cu", "union.cu", "ffn.cu", "ffn16.cu", "combine.cu"
            "verify.cu", "tile.cu", "attn_abi.cu", "rope.cu", "attn.cu",
            "attn_tile.cu", "keyw.cu", "evict.cu"]
 HEADERS = ["common.cuh", "kernels.h", "layout.h", "select.cuh", "host.h", "attn.h", "attn.cuh",
-           "attn_mma.cuh"]
+           "attn_mma.cuh", "tmem16.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "attn.cuh"
+#include "tmem16.cuh"
 
 namespace moe {
 

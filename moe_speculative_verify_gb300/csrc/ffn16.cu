@@ -36,6 +36,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "layout.h"
+#include "tmem16.cuh"
 
 namespace moe {
 

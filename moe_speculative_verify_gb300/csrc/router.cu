@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "select.cuh"
+#include "tmem16.cuh"
 
 namespace moe {
 
