@@ -567,7 +567,9 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
 // A unit is kJoinRows rows of a split item; the blocks share the units of all
 // items out among them (each adds up the notes for itself).  Four threads have
 // four columns of a row, each a quarter of the pieces, kBatch of them in
-// flight at a time.  The first piece is added before the loop over the others,
+// flight at a time (more take registers from the second block of an SM: with
+// eight, 2048 tokens over 16,384 keys 793 -> 850 us, whose many items are split
+// in two; one verify block, split in 20, 21.5 -> 20.8).  The first piece is added before the loop over the others,
 // which lie at one distance from each other: with the first one's place chosen
 // inside an unrolled loop, joins of 128 columns whose first quarter counted a
 // multiple of eight pieces ended in a misaligned access.
@@ -577,7 +579,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4, 1) attn_join_kernel(const AttnArgs a, int n_notes) {
     constexpr int64_t kSlot = kAttnSlotRows * (D + 2);
     constexpr int kCells = kJoinRows * D / 4;                                  // threads of a part
-    constexpr int kPer = kAttnMaxCtas / 32, kBatch = 8;
+    constexpr int kPer = kAttnMaxCtas / 32, kBatch = 3;
     __shared__ float4 s_v[kJoinParts][kCells];
     __shared__ float s_sum[kJoinParts][kJoinRows];
     __shared__ int s_end[kAttnMaxCtas];                                        // units up to note i, inclusive
@@ -689,12 +691,11 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* D / 4, 1) attn_join_ker
 }  // namespace
 
 cudaError_t launch_attn_join(const AttnArgs& a, int n_notes, cudaStream_t s) {
-    // one block an SM: with two, their registers leave fewer pieces in flight (one verify block 20.8 -> 22.1 us), and
-    // a call without a split item waits for a second wave (8 keys 9.5 -> 10.4)
+    // two blocks an SM: the pieces' loads of one beside the sums of the other
     const cudaError_t e =
         a.kv.dim == 128
-            ? launch_pdl(attn_join_kernel<128>, dim3(n_notes), dim3(kJoinRows * kJoinParts * 32), 0, s, a, n_notes)
-            : launch_pdl(attn_join_kernel<64>, dim3(n_notes), dim3(kJoinRows * kJoinParts * 16), 0, s, a, n_notes);
+            ? launch_pdl(attn_join_kernel<128>, dim3(2 * n_notes), dim3(kJoinRows * kJoinParts * 32), 0, s, a, n_notes)
+            : launch_pdl(attn_join_kernel<64>, dim3(2 * n_notes), dim3(kJoinRows * kJoinParts * 16), 0, s, a, n_notes);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
