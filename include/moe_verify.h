@@ -582,7 +582,8 @@ moe_status_t moe_rope_append(const moe_rope_t* rope, const moe_kv_cache_t* cache
  *   draft_mask:    j < F, or bit j - F of its mask is set (j - F < 64), and
  *   window > 0:    j > F + i - window.
  * A row that sees nothing gives +0 and a log-sum-exp of -inf.
- * wait_timeout_us bounds every device-side wait (0 = 2 000 000 us).
+ * wait_timeout_us bounds every device-side wait (0 = 2 000 000 us); after one
+ * ran out, waits of up to 2 s each see the kernel's copies and products end.
  */
 typedef struct {
     int32_t n_q_heads;

@@ -77,10 +77,11 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
     int st = 0, slot = 0;
     uint32_t ph = 1, ip = 1;
     bool dead = false, more = true;
-    while (more) {
+    while (more && !dead) {
         more = wk.next(a, it);
         if (!more) it.b = -1;
-        if (!dead && !mbar_wait(&sh.item_empty[slot], ip, a.err, a.timeout_ns)) dead = true;
+        // (after a wait that ran out nothing is handed on: the slot may still be read)
+        if (!warp_wait(&sh.item_empty[slot], ip, a.err, a.timeout_ns)) break;
         if (lane == 0) {
             sh.item[slot] = it;
             mbar_arrive(&sh.item_full[slot]);
@@ -116,11 +117,14 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
                 record_error(a.err, MOE_ERR_INVALID_ARG);
                 pg = n_pages;                           // out of range: reads as zeros
             }
-            if (!dead && !mbar_wait(&sh.empty[st], ph, a.err, a.timeout_ns)) dead = true;
-            if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], dead ? 0 : bytes);
+            if (!warp_wait(&sh.empty[st], ph, a.err, a.timeout_ns)) {
+                dead = true;
+                break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], bytes);
             __syncwarp();
             for (int b = 0; b < np; ++b) {
-                if (lane == b && issue && !dead) {
+                if (lane == b && issue) {
 #pragma unroll
                     for (int x = 0; x < kParts; ++x) {
                         uint8_t* dst = box + st * 2 * C::kTileBytes + x * kTile * 128;
@@ -138,8 +142,9 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
             if (t + 1 < it.t1 && mine()) pg = table[(j0 >> pl) + lane];
         }
     }
-    // a CTA ends after its copies, also where a wait ran out: each stage's last one
-    for (int k = 0; k < C::kStages && mbar_wait(&sh.full[st], ph, a.err, a.timeout_ns); ++k) {
+    // each stage's last copy
+    for (int k = 0; k < C::kStages; ++k) {
+        mbar_wait(&sh.full[st], ph, a.err, kDrainNs);
         if (++st == C::kStages) {
             st = 0;
             ph ^= 1;
@@ -290,7 +295,7 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
             if ((run & 1) != grp) continue;
             const int st = run % C::kStages, ph = (run / C::kStages) & 1;
             const uint32_t kb = smem_u32(ring + st * 2 * C::kTileBytes), vb = kb + C::kTileBytes;
-            if (!dead && !mbar_wait(&sh.full[st], ph, a.err, a.timeout_ns)) dead = true;
+            if (!dead && !mbar_wait(&sh.full[st], ph, a.err, a.timeout_ns)) dead = true;   // (all warps leave after this item)
             const int j0 = (it.tile0 + tt) * kTile + key0;
             // --- scores of 16 rows x 16 keys
             float s[2][4] = {};
@@ -440,7 +445,7 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.empty[st]);
+            if (lane == 0 && !dead) mbar_arrive(&sh.empty[st]);
         }
 
         // --- join the eight warps

@@ -266,6 +266,20 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// A CTA ends after its copies and products, also where a wait ran out (they
+// would write into shared or tensor memory that is no longer its own).  The waits
+// for that have a limit of their own, far above what a copy or a burst of products
+// takes, whatever the caller's limit is; they end at once unless the GPU has
+// stopped answering.  A stage is given back only by a thread that saw it full: a
+// second copy into one whose first is still in flight would count into the
+// first one's phase.
+constexpr uint64_t kDrainNs = 2000000000ull;
+
+// A wait of a whole warp whose lanes go on or stop together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, uint64_t timeout_ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, timeout_ns));
+}
+
 // ------------------------------------------------------------ work split ----
 // The attention kernels cut a call into items -- (sequence, kv head, tile of
 // MT query rows), rows r = i * group + g -- of one unit per KT-key tile that

@@ -168,7 +168,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
     ctx.start<32>(a, sh.plan);
     Slot<C::kStages> at{0, 1u};
     bool dead = false;
-    while (ctx.next<32>(a)) {
+    while (!dead && ctx.next<32>(a)) {
         const Item& it = ctx.it;
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
         const int p_lo = it.lo >> pl, p_hi = (it.hi + page - 1) >> pl, head = it.h;
@@ -176,7 +176,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
         int p = (((it.tile0 + it.t0) * kKT) >> pl) + lane;       // this lane's page
         auto mine = [&]() { return lane < group * np && p >= p_lo && p < p_hi; };
         int pg = T > 0 && mine() ? table[p] : 0;
-        for (int j = 0; j < T; j += group) {
+        for (int j = 0; j < T && !dead; j += group) {
             const bool issue = mine() && j + i < T;
             if (issue && (pg < 0 || pg >= n_pages)) {
                 record_error(a.err, MOE_ERR_INVALID_ARG);
@@ -185,13 +185,14 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
             const int p0 = p - lane, m = min(group, T - j);
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-                for (int t = 0; t < m; ++t) {
+                for (int t = 0; t < m && !dead; ++t) {
                     const int bytes = max(0, min(p0 + (t + 1) * np, p_hi) - max(p0 + t * np, p_lo)) * page * C::kRowBytes;
-                    if (!dead && !mbar_wait(&sh.kv_empty[at.st], at.ph, a.err, a.timeout_ns)) dead = true;
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at.st], dead ? 0 : bytes);
+                    dead = !warp_wait(&sh.kv_empty[at.st], at.ph, a.err, a.timeout_ns);
+                    if (dead) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at.st], bytes);
                     __syncwarp();
                     for (int b = t * np; b < (t + 1) * np; ++b) {
-                        if (lane == b && issue && !dead) {
+                        if (lane == b && issue) {
 #pragma unroll
                             for (int x = 0; x < kParts; ++x)
                                 tma_load_4d(box + at.st * C::kTileBytes + x * kKT * 128, v ? &maps.v : &maps.k,
@@ -206,8 +207,8 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
             if (j + group < T && mine()) pg = table[p];
         }
     }
-    // a CTA ends after its copies, also where a wait ran out: each stage's last one
-    for (int k = 0; k < C::kStages && mbar_wait(&sh.kv_full[at.st], at.ph, a.err, a.timeout_ns); ++k) at.step();
+    // each stage's last copy
+    for (int k = 0; k < C::kStages; ++k, at.step()) mbar_wait(&sh.kv_full[at.st], at.ph, a.err, kDrainNs);
 }
 
 // The MMA warp of stream s: one thread issues, the whole warp waits.  The
@@ -256,7 +257,7 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
             for (;; ++op, at.step()) {
                 wait(&sh.kv_full[at.st], at.ph);
                 if (op == to) break;
-                if (lane == 0) mbar_arrive(&sh.kv_empty[at.st]);
+                if (lane == 0 && !dead) mbar_arrive(&sh.kv_empty[at.st]);
                 __syncwarp();
             }
             const int st = at.st;
@@ -300,7 +301,7 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
             tc_fence_after();
             const uint64_t kd = k_desc + ks * (C::kTileBytes >> 4), vd = v_desc + vs * (C::kTileBytes >> 4);
             const uint32_t acc = i - 1 > a0 ? 1u : 0u;
-            if (elect_one()) {
+            if (elect_one() && !dead) {
                 if (do_v) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -343,13 +344,13 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
         // the other stream's last uses
         for (; op < 2 * T; ++op, at.step()) {
             wait(&sh.kv_full[at.st], at.ph);
-            if (lane == 0) mbar_arrive(&sh.kv_empty[at.st]);
+            if (lane == 0 && !dead) mbar_arrive(&sh.kv_empty[at.st]);
             __syncwarp();
         }
     }
-    // (also where a wait ran out: the products end before the accumulators are given back)
+    // the products end before the accumulators are given back
     if (elect_one()) mma_commit(&sh.done[s]);
-    mbar_wait(&sh.done[s], 0, a.err, a.timeout_ns);
+    mbar_wait(&sh.done[s], 0, a.err, kDrainNs);
 }
 
 // 16 32-bit columns of this thread's TMEM lane.

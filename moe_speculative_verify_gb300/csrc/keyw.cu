@@ -107,11 +107,12 @@ struct Turn {
     }
 };
 
+// A warp's waits: after one that ran out the others return at once.
 struct Waiter {
     const AttnArgs& a;
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
+        if (!dead) dead = !warp_wait(bar, parity, a.err, a.timeout_ns);
     }
 };
 
@@ -188,7 +189,7 @@ struct Feed {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.item_empty[at.st]);
         at.step(kItems);
-        return __all_sync(0xFFFFFFFFu, !wait.dead) && it.b >= 0;
+        return !wait.dead && it.b >= 0;
     }
 };
 
@@ -206,10 +207,12 @@ __device__ __forceinline__ void load_keys(const KeywArgs& ka, const CUtensorMap&
     int p0 = 0, p_hi = 0, pg = 0, head = 0;
     bool mine = false;
     // the next item, handed on, and its page indices, read a step ahead
+    // (after a wait that ran out nothing is handed on: the slot may still be read)
     auto fetch = [&]() {
         Item it{-1, 0, 0, 0, 0, 0, 0, 0, 0};
         const bool more = sc.next(ka, it);
         wait(&sh.item_empty[slot.st], slot.ph ^ 1u);
+        if (wait.dead) return false;
         if (lane == 0) {
             *reinterpret_cast<int4*>(&sh.item[slot.st][0]) = make_int4(it.b, it.h, it.j0, it.q0);
             *reinterpret_cast<int4*>(&sh.item[slot.st][4]) = make_int4(it.nq, it.first, it.len, it.t0);
@@ -227,7 +230,7 @@ __device__ __forceinline__ void load_keys(const KeywArgs& ka, const CUtensorMap&
         return true;
     };
     bool more = fetch();
-    while (more) {
+    while (more && !wait.dead) {
         if (mine && (pg < 0 || pg >= a.kv.n_pages)) {
             record_error(a.err, MOE_ERR_INVALID_ARG);
             pg = a.kv.n_pages;                                  // out of range: reads as zeros
@@ -241,13 +244,13 @@ __device__ __forceinline__ void load_keys(const KeywArgs& ka, const CUtensorMap&
             if (boxes <= 0) continue;
             const int buf = use[w].st;
             wait(&sh.k_empty[w][buf], use[w].ph ^ 1u);
+            if (wait.dead) break;
             use[w].step(bufs);
             uint8_t* dst = smem + raw + (w * bufs + buf) * C::kRaw;
-            if (lane == 0)
-                mbar_arrive_expect_tx(&sh.k_full[w][buf], wait.dead ? 0 : boxes * page * (E4M3 ? D : 2 * D));
+            if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[w][buf], boxes * page * (E4M3 ? D : 2 * D));
             __syncwarp();
             for (int k = 0; k < np; ++k) {
-                if (lane == w * np + k && c_mine && !wait.dead) {
+                if (lane == w * np + k && c_mine) {
 #pragma unroll
                     for (int x = 0; x < kParts; ++x)
                         tma_load_4d(dst + k * page * kBoxBytes + x * kKeys * 128, &map, &sh.k_full[w][buf], x * kBox, 0,
@@ -257,10 +260,12 @@ __device__ __forceinline__ void load_keys(const KeywArgs& ka, const CUtensorMap&
             }
         }
     }
-    // a CTA ends after its copies, also where a wait ran out: each buffer's last one
+    // each buffer's last copy
     for (int w = 0; w < 2; ++w)
-        for (int k = 0; k < bufs && mbar_wait(&sh.k_full[w][use[w].st], use[w].ph ^ 1u, a.err, a.timeout_ns); ++k)
+        for (int k = 0; k < bufs; ++k) {
+            mbar_wait(&sh.k_full[w][use[w].st], use[w].ph ^ 1u, a.err, kDrainNs);
             use[w].step(bufs);
+        }
 }
 
 template <int D, bool E4M3>
@@ -278,21 +283,22 @@ __device__ __forceinline__ void load_rows(const KeywArgs& ka, const CUtensorMap&
         for (int t = it.t0; t < it.t1; ++t)
             for (int hc = 0; hc < a.group; hc += ka.tile_heads) {
                 wait(&sh.q_empty[q.st], q.ph ^ 1u);
+                if (wait.dead) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh.q_full[q.st], wait.dead ? 0 : bytes);
-                    if (!wait.dead) {
+                    mbar_arrive_expect_tx(&sh.q_full[q.st], bytes);
 #pragma unroll
-                        for (int x = 0; x < D / 64; ++x)
-                            tma_load_3d(smem + q.st * q_tile + x * part, &map, &sh.q_full[q.st], 64 * x,
-                                        it.h * a.group + hc, it.q0 + t * ka.tile_tokens);
-                    }
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_3d(smem + q.st * q_tile + x * part, &map, &sh.q_full[q.st], 64 * x,
+                                    it.h * a.group + hc, it.q0 + t * ka.tile_tokens);
                 }
                 __syncwarp();
                 q.step(C::kQStages);
             }
     }
-    for (int k = 0; k < C::kQStages && mbar_wait(&sh.q_full[q.st], q.ph ^ 1u, a.err, a.timeout_ns); ++k)
+    for (int k = 0; k < C::kQStages; ++k) {                      // each stage's last copy
+        mbar_wait(&sh.q_full[q.st], q.ph ^ 1u, a.err, kDrainNs);
         q.step(C::kQStages);
+    }
 }
 
 template <int D, bool E4M3>
@@ -333,6 +339,7 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
                     wait(&sh.s_empty[w][sb], buf.ph ^ 1u);
                     buf.step(2);
                 }
+                if (wait.dead) break;
                 tc_fence_after();
                 const uint64_t qd = q_desc + (q.st * q_tile >> 4);
                 const uint32_t d = sh.tmem + (2 * w + sb) * 128;
@@ -353,14 +360,14 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
                 q.step(C::kQStages);
             }
         }
-        if (on) {
+        if (on && !wait.dead) {
             if (elect_one()) mma_commit(E4M3 ? &sh.k_free[w][kb] : &sh.k_empty[w][kb]);
             __syncwarp();
         }
     }
-    // (also where a wait ran out: the products end before the accumulators are given back)
+    // the products end before the accumulators are given back
     if (elect_one()) mma_commit(&sh.done[w]);
-    mbar_wait(&sh.done[w], 0, a.err, a.timeout_ns);
+    mbar_wait(&sh.done[w], 0, a.err, kDrainNs);
 }
 
 // e4m3: one tile of the items' pairs to bf16.
@@ -386,6 +393,7 @@ __device__ __forceinline__ void convert(const KeywArgs& ka, Shared& sh, uint8_t*
             in[ch] = *reinterpret_cast<const uint4*>(
                 raw + lr * D + ((D == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3)) << 4));
         wait(&sh.k_free[w][out.st], out.ph ^ 1u);
+        if (wait.dead) break;
         uint32_t nan = 0;
 #pragma unroll
         for (int ch = 0; ch < D / 16; ++ch) {
