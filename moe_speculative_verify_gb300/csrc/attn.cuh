@@ -117,12 +117,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-__device__ __forceinline__ float fast_log2(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // (d0, d1) = (a0, a1) * b + c, and (d0, d1) += (a0, a1), as one packed
 // instruction each, rounded as the scalar ones.
 __device__ __forceinline__ void fma2_to(float& d0, float& d1, float a0, float a1, float b, float c) {
@@ -179,36 +173,28 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     return r;
 }
 
-// Two fp32 as e4m3 / e5m2 codes in the low 16 bits (nearest even, saturating;
-// NaN stays NaN), `lo` in the low byte; and back.
-__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ float2 unpack_e4m3(uint32_t codes) {
-    const uint32_t h = e4m3x2_to_f16x2(codes);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 // Four e4m3 codes as bf16 pairs, exactly, without the conversion unit (which
 // the powers need): a code's exponent and fraction bits moved to where bf16
 // has them give the value times 2^-120, subnormals included.  NaN codes come
-// out as numbers: `nan` collects them (bits 7 of its bytes).
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t codes, uint32_t& lo, uint32_t& hi, uint32_t& nan) {
+// out as +-480, which no other code does: `most` keeps the largest bits of two
+// columns of codes for e4m3_had_nan, and e4m3_nan_again puts them right.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t codes, uint32_t& lo, uint32_t& hi, uint32_t& most) {
     const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);
-    const uint32_t ya = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), yb = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+    const uint32_t ma = (a >> 4) & 0x07F007F0u, mb = (b >> 4) & 0x07F007F0u;
     constexpr uint32_t k2p120 = 0x7B807B80u;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(ya), "r"(k2p120));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(yb), "r"(k2p120));
-    nan |= (codes & 0x7F7F7F7Fu) + 0x01010101u;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(ma | (a & 0x80008000u)), "r"(k2p120));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(mb | (b & 0x80008000u)), "r"(k2p120));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(ma));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(mb));
+}
+
+__device__ __forceinline__ bool e4m3_had_nan(uint32_t most) { return ((most + 0x00100010u) & 0x08000800u) != 0u; }
+
+// A pair of those results with +-480 as NaN.
+__device__ __forceinline__ uint32_t e4m3_nan_again(uint32_t pair) {
+    if ((pair & 0x7FFFu) == 0x43F0u) pair |= 0x7FC0u;
+    if ((pair & 0x7FFF0000u) == 0x43F00000u) pair |= 0x7FC00000u;
+    return pair;
 }
 
 // D[16x8] += A[16x16] B[16x8]: bf16 or f16 operands, fp32 sums.  Lane l = 4g+t

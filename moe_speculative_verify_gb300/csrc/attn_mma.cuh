@@ -7,52 +7,37 @@
 
 namespace moe {
 
-// Shared-memory matrix descriptor (version 1, 1024-byte aligned tiles): K-major
-// operands with rows of 128 (or 64) bytes swizzled at that width, 8-row groups
-// `sbo` bytes apart; MN-major ones with `lbo` between 128-byte wide parts.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+// Shared-memory matrix descriptor (version 1, 1024-byte aligned tiles): rows of
+// 128 bytes swizzled at that width.  K-major operands: 8-row groups `sbo` bytes
+// apart; MN-major ones: `lbo` between 128-byte wide parts.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(lbo >> 4) << 16;
     d |= static_cast<uint64_t>(sbo >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(swizzle) << 61;
+    d |= static_cast<uint64_t>(2) << 61;
     return d;
 }
 
-constexpr uint32_t kSw128 = 2, kSw64 = 4;
-
-// Instruction descriptor: D fp32, A and B types at bits 7-9 and 10-12, B
-// MN-major at bit 16, N >> 3 at 17-22, M >> 4 at 24-28 (M = 128).
-constexpr uint32_t idesc(uint32_t ta, uint32_t tb, bool b_mn, int N) {
-    return (1u << 4) | (ta << 7) | (tb << 10) | (b_mn ? 1u << 16 : 0u) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+// Instruction descriptor of kind::f16: D fp32, A and B bf16 (1 at bits 7-9 and
+// 10-12), B MN-major at bit 16, N >> 3 at 17-22, M >> 4 at 24-28 (M = 128).
+__device__ constexpr uint32_t idesc(bool b_mn, int N) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-// One step of D[tmem] (+)= A B^T: A in shared (SS) or tensor memory (TS);
-// 16-bit (K = 16) or 8-bit (K = 32) operands.
-template <bool F8>
+// One step (K = 16) of D[tmem] (+)= A B^T: A in shared (SS) or tensor memory (TS).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    if constexpr (F8)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                     "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                     "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
 }
 
-template <bool F8>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    if constexpr (F8)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                     "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                     "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
 }
 
 __device__ __forceinline__ void fence_async_smem() {

@@ -16,18 +16,20 @@
 // that has grown by more than 2^kLag: the rescaling of O in tensor memory is
 // rare then, and every power stays within the 16-bit types.
 //
-// e4m3 caches are multiplied as they are.  A query element (8 significant
-// bits) is the sum of two e4m3 codes of the row scaled by a power of two; a
-// probability the sum of an e4m3 and an e5m2 code (whose range reaches down to
-// 2^-20 of the reference): two 8-bit products take the time of one 16-bit one,
-// and K and V need no conversion.
+// e4m3 tiles are turned to bf16 in shared memory (exactly) by a warpgroup of
+// their own, once for all of an item's rows, and multiplied as a bf16 cache's:
+// queries keep their bits, and a probability its 8 bits at any size.  (8-bit
+// products with a probability as two codes, which need no conversion, lose
+// probabilities far below a row's largest: behind a first key that takes most
+// of the weight the output was 10 % off.)
 //
 // Measured (64 query heads, 8 kv heads of 128): 2048 tokens over 16,384 keys
 // more 0.80 ms in bf16, 1.46 PFLOP/s where the library's matrix product runs at
 // 1.91 (a step's two products leave the tensor pipe idle between bursts, see
-// multiply), 1.12 ms over e4m3 (the two codes of each probability); 16 verify
-// blocks of up to 8 tokens over 4,099 to 16,411 keys 113 us over e4m3 (2.8 TB/s:
-// the softmax's work a key byte is twice bf16's), 128 over bf16 (4.9 TB/s); one block over 6,011 keys 21 us.
+// multiply), 1.00 ms over e4m3 (the conversion's instructions); 16 verify blocks of
+// up to 8 tokens over 4,099 to 16,411 keys 128 us in bf16 (4.9 TB/s), 139 over e4m3
+// (2.3 TB/s: a stage is filled, converted and used in turn); one block over 6,011
+// keys 21.6 us, over e4m3 24.0.
 #include "attn_mma.cuh"
 #include "kernels.h"
 
@@ -37,10 +39,16 @@ namespace {
 
 constexpr int kMT = 256;                 // rows of an item
 constexpr int kKT = 128;                 // keys of a tile
-constexpr int kThreads = 384;            // 2 softmax warpgroups; TMA warp, 2 MMA warps and an idle one
+// 2 softmax warpgroups; TMA warp, 2 MMA warps and an idle one; e4m3: a warpgroup that converts
+template <bool E4M3>
+constexpr int kThreads = E4M3 ? 512 : 384;
 // Registers a thread, moved between the warpgroups after the launch at 168:
-// 8 * 208 + 4 * 80 = 1984 a lane column of the 12 * 168 = 2016 launched.
-constexpr int kRegsSoft = 208, kRegsRest = 80;
+// 8 * 208 + 4 * 80 = 1984 a lane column of the 12 * 168 = 2016 launched; with
+// the converting warps, launched at 128: 8 * 192 + 8 * 64 = 2048 of 16 * 128.
+template <bool E4M3>
+constexpr int kRegsSoft = E4M3 ? 192 : 208;
+template <bool E4M3>
+constexpr int kRegsRest = E4M3 ? 64 : 80;
 constexpr int kSoft = 256;
 constexpr int kBarAll = 1, kBarGroup = 2, kBarMma = 4;   // named barriers: both warpgroups, each, the MMA warps
 constexpr uint32_t kTmemCols = 512;
@@ -48,15 +56,18 @@ constexpr uint32_t kColO = 256;          // S/P of stream s at column 128 s, O a
 
 template <int D, bool E4M3>
 struct Cfg {
-    static constexpr int kRowBytes = E4M3 ? D : 2 * D;             // a cached row
-    static constexpr int kTileBytes = kKT * kRowBytes;
-    static constexpr int kQBytes = 128 * 2 * D;                    // bf16, or e4m3 high and low
-    static constexpr int kStages = kTileBytes == 32768 ? 5 : 10;
+    static constexpr int kTileBytes = kKT * 2 * D;                 // bf16
+    // e4m3: the tile as it is cached lands kRaw bytes into its stage: at D = 128
+    // the upper half, whose rows are also those of the bf16 tile's elements 64 on
+    static constexpr int kRaw = E4M3 ? 16384 : 0;
+    static constexpr int kStageBytes = E4M3 && D == 64 ? kTileBytes + kKT * D : kTileBytes;
+    static constexpr int kQBytes = 128 * 2 * D;
+    static constexpr int kStages = D == 128 || E4M3 ? 5 : 10;
     static constexpr int kMerge = 128 * D * 4;                     // == 2 * kQBytes: stream 1's O
-    static constexpr size_t kSmem = 2 * kQBytes + kStages * kTileBytes;   // then Shared
-    static constexpr float kLag = E4M3 ? 4.0f : 8.0f;
-    static constexpr float kBias = E4M3 ? 4.0f : 0.0f;             // probabilities times 2^kBias
+    static constexpr size_t kSmem = 2 * kQBytes + kStages * kStageBytes;   // then Shared
 };
+
+constexpr float kLag = 8.0f;             // log2 of what powers may grow to
 
 // An item as its CTA works on it: mode, tiles, and each stream's share.
 struct Share {
@@ -128,12 +139,13 @@ struct Ctx {
 
 struct Shared {
     alignas(16) float2 ml[2][128];          // a lane's reference and sum, among a row's sharers
-    uint64_t kv_full[10];
+    uint64_t kv_full[10];                   // e4m3: from kStages on, those of the tiles as they are cached
     uint64_t kv_empty[10];
     uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], turn[2], done[2];
     Plan plan;
     Ctx ctx[4];                             // the softmax warpgroups', the TMA warp's, the MMA warps'
     uint32_t tmem;
+    int raw_end;                            // e4m3: uses of the ring, once all are on their way
 };
 
 // The K/V ring's order: K V of a tile (two row tiles), or K K V V of two tiles
@@ -159,11 +171,13 @@ template <int D, bool E4M3>
 __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, Shared& sh, uint8_t* ring) {
     using C = Cfg<D, E4M3>;
     constexpr int kBox = E4M3 ? D : 64, kBoxBytes = E4M3 ? D : 128, kParts = D / kBox;
+    uint64_t* full = sh.kv_full + (E4M3 ? C::kStages : 0);
+    int uses = 0;
     const int lane = threadIdx.x & 31;
     const int page = a.kv.page, pl = a.kv.page_log2, np = kKT >> pl, n_pages = a.kv.n_pages;
     // lanes 0 .. np-1: the pages of a group's first tile, np .. 2 np - 1: of its second
     const int i = lane >= np ? 1 : 0;
-    uint8_t* box = ring + (lane - i * np) * page * kBoxBytes;
+    uint8_t* box = ring + C::kRaw + (lane - i * np) * page * kBoxBytes;
     Ctx& ctx = sh.ctx[2];
     ctx.start<32>(a, sh.plan);
     Slot<C::kStages> at{0, 1u};
@@ -186,29 +200,90 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 for (int t = 0; t < m && !dead; ++t) {
-                    const int bytes = max(0, min(p0 + (t + 1) * np, p_hi) - max(p0 + t * np, p_lo)) * page * C::kRowBytes;
+                    const int bytes = max(0, min(p0 + (t + 1) * np, p_hi) - max(p0 + t * np, p_lo)) * page * kParts * kBoxBytes;
                     dead = !warp_wait(&sh.kv_empty[at.st], at.ph, a.err, a.timeout_ns);
                     if (dead) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at.st], bytes);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[at.st], bytes);
                     __syncwarp();
                     for (int b = t * np; b < (t + 1) * np; ++b) {
                         if (lane == b && issue) {
 #pragma unroll
                             for (int x = 0; x < kParts; ++x)
-                                tma_load_4d(box + at.st * C::kTileBytes + x * kKT * 128, v ? &maps.v : &maps.k,
-                                            &sh.kv_full[at.st], x * kBox, 0, head, pg);
+                                tma_load_4d(box + at.st * C::kStageBytes + x * kKT * 128, v ? &maps.v : &maps.k,
+                                            &full[at.st], x * kBox, 0, head, pg);
                         }
                         __syncwarp();
                     }
                     at.step();
+                    ++uses;
                 }
             }
             p += group * np;
             if (j + group < T && mine()) pg = table[p];
         }
     }
+    if constexpr (E4M3) {                                        // one more, empty: the converting warps end there
+        if (!dead && warp_wait(&sh.kv_empty[at.st], at.ph, a.err, a.timeout_ns)) {
+            if (lane == 0) {
+                sh.raw_end = uses;
+                mbar_arrive(&full[at.st]);
+            }
+            __syncwarp();
+            at.step();
+        }
+    }
     // each stage's last copy
-    for (int k = 0; k < C::kStages; ++k, at.step()) mbar_wait(&sh.kv_full[at.st], at.ph, a.err, kDrainNs);
+    for (int k = 0; k < C::kStages; ++k, at.step()) mbar_wait(&full[at.st], at.ph, a.err, kDrainNs);
+}
+
+// e4m3: a stage's tile to bf16 where it is, by a warpgroup with a thread a key and
+// without the conversion unit, which the powers need (see e4m3x4_to_bf16).  A
+// thread's 16-byte pieces go in order: the two it writes for piece ch lie in the
+// first half, or over pieces 2 ch - 8 and 2 ch - 7 of its own row, which it has
+// read.  Code size decides: 2048 tokens over 16,384 keys take 1.00 ms with two
+// pieces a turn and 1.04 with one; with all eight, and NaN codes looked for a
+// piece at a time, the code did not fit the instruction caches beside the other
+// roles' (1.9 ms).  A ring of its own for the tiles as they are cached (4 + 2
+// stages for 5) 1.05, a second warpgroup 1.00 (16 verify blocks 139 -> 150 us).
+template <int D>
+__device__ __forceinline__ void convert(const AttnArgs& a, Shared& sh, uint8_t* ring) {
+    using C = Cfg<D, true>;
+    const int lr = threadIdx.x & 127, lane = threadIdx.x & 31;
+    Slot<C::kStages> at{0, 0u};
+    for (int use = 0;; ++use, at.step()) {
+        if (!warp_wait(&sh.kv_full[C::kStages + at.st], at.ph, a.err, a.timeout_ns)) break;
+        if (use == *const_cast<volatile int*>(&sh.raw_end)) break;
+        uint8_t* dst = ring + at.st * C::kStageBytes + lr * 128;
+        const uint8_t* raw = ring + at.st * C::kStageBytes + C::kRaw + lr * D;
+        auto from = [&](int ch) { return raw + ((D == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3)) << 4); };
+        auto to = [&](int c2) { return dst + (c2 >> 3) * 16384 + (((c2 & 7) ^ (lr & 7)) << 4); };
+        uint4 next = *reinterpret_cast<const uint4*>(from(0));
+        uint32_t most = 0;
+#pragma unroll 2
+        for (int ch = 0; ch < D / 16; ++ch) {
+            const uint32_t x[4] = {next.x, next.y, next.z, next.w};
+            next = *reinterpret_cast<const uint4*>(from((ch + 1) & (D / 16 - 1)));
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(x[e], y[2 * e], y[2 * e + 1], most);
+            *reinterpret_cast<uint4*>(to(2 * ch)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(to(2 * ch + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        if (e4m3_had_nan(most)) {
+#pragma unroll 1
+            for (int c2 = 0; c2 < D / 8; ++c2) {
+                uint4 w = *reinterpret_cast<const uint4*>(to(c2));
+                w.x = e4m3_nan_again(w.x);
+                w.y = e4m3_nan_again(w.y);
+                w.z = e4m3_nan_again(w.z);
+                w.w = e4m3_nan_again(w.w);
+                *reinterpret_cast<uint4*>(to(c2)) = w;
+            }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[at.st]);
+    }
 }
 
 // The MMA warp of stream s: one thread issues, the whole warp waits.  The
@@ -223,15 +298,11 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const KvMaps& maps, S
 template <int D, bool E4M3>
 __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t* qs, uint8_t* ring, int s) {
     using C = Cfg<D, E4M3>;
-    constexpr uint32_t kIdQK = E4M3 ? idesc(0, 0, false, kKT) : idesc(1, 1, false, kKT);
-    constexpr uint32_t kIdPV = E4M3 ? idesc(0, 0, true, D) : idesc(1, 1, true, D);
-    constexpr uint32_t kIdPVlow = idesc(1, 0, true, D);          // e5m2 x e4m3
-    constexpr bool kNarrow = E4M3 && D == 64;                    // 64-byte cached rows
-    constexpr uint32_t kSbo = kNarrow ? 512 : 1024, kSw = kNarrow ? kSw64 : kSw128;
+    constexpr uint32_t kIdQK = idesc(false, kKT), kIdPV = idesc(true, D);
     const int lane = threadIdx.x & 31;
     const uint32_t colS = sh.tmem + 128 * s, colO = sh.tmem + kColO + 128 * s;
-    const uint64_t q_desc = sdesc(smem_u32(qs + s * C::kQBytes), 16, 1024, kSw128);
-    const uint64_t k_desc = sdesc(smem_u32(ring), 16, kSbo, kSw), v_desc = sdesc(smem_u32(ring), 16384, kSbo, kSw);
+    const uint64_t q_desc = sdesc(smem_u32(qs + s * C::kQBytes), 16, 1024);
+    const uint64_t k_desc = sdesc(smem_u32(ring), 16, 1024), v_desc = sdesc(smem_u32(ring), 16384, 1024);
     Ctx& ctx = sh.ctx[3];
     ctx.start<64>(a, sh.plan);
     const Item& it = ctx.it;
@@ -279,15 +350,14 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
                 // V rows of keys that no row of the item sees may hold anything: zero them (in a pair both warps do)
                 const int j0 = (pair ? i - 1 : 2 * (i - 1) + s) * kKT;
                 if (j0 < lo || j0 + kKT > hi) {
-                    uint8_t* v = ring + vs * C::kTileBytes;
-                    constexpr int kPitch = E4M3 ? D : 128, kSub = E4M3 ? 1 : D / 64;      // a row's bytes in each part
-                    const int head = min(max(lo - j0, 0), kKT) * kPitch, tail = min(max(hi - j0, 0), kKT) * kPitch;
+                    uint8_t* v = ring + vs * C::kStageBytes;
+                    const int head = min(max(lo - j0, 0), kKT) * 128, tail = min(max(hi - j0, 0), kKT) * 128;
 #pragma unroll
-                    for (int x = 0; x < kSub; ++x) {
+                    for (int x = 0; x < D / 64; ++x) {
                         uint8_t* part = v + x * kKT * 128;
                         for (int e = 16 * lane; e < head; e += 512)
                             *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
-                        for (int e = tail + 16 * lane; e < kKT * kPitch; e += 512)
+                        for (int e = tail + 16 * lane; e < kKT * 128; e += 512)
                             *reinterpret_cast<uint4*>(part + e) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_smem();
@@ -299,18 +369,13 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
             wait(&sh.turn[s], tp);
             tp ^= 1;
             tc_fence_after();
-            const uint64_t kd = k_desc + ks * (C::kTileBytes >> 4), vd = v_desc + vs * (C::kTileBytes >> 4);
+            const uint64_t kd = k_desc + ks * (C::kStageBytes >> 4), vd = v_desc + vs * (C::kStageBytes >> 4);
             const uint32_t acc = i - 1 > a0 ? 1u : 0u;
             if (elect_one() && !dead) {
                 if (do_v) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint32_t ac = k > 0 ? 1u : acc;
-                        if constexpr (!E4M3)
-                            mma_ts<false>(colO, colS + 8 * k, vd + (k * 2048 >> 4), kIdPV, ac);
-                        else                                     // 32 keys' high codes, then low
-                            mma_ts<true>(colO, colS + 8 * k, vd + ((k >> 1) * 32 * C::kRowBytes >> 4),
-                                         k & 1 ? kIdPVlow : kIdPV, ac);
+                        mma_ts(colO, colS + 8 * k, vd + (k * 2048 >> 4), kIdPV, k > 0 ? 1u : acc);
                     }
                     if (i == b0) mma_commit(&sh.o_full[s]);
                     mma_commit(&sh.kv_empty[vs]);
@@ -318,19 +383,10 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Shared& sh, uint8_t*
                     mbar_arrive(&sh.kv_empty[vs]);
                 }
                 if (do_k) {
-                    if constexpr (!E4M3) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                            mma_ss<false>(colS, q_desc + off, kd + off, kIdQK, k > 0);
-                        }
-                    } else {
-                        constexpr int kSteps = D / 32;
-#pragma unroll
-                        for (int k = 0; k < 2 * kSteps; ++k)     // high codes, then low
-                            mma_ss<true>(colS,
-                                         q_desc + ((D == 128 ? (k / kSteps) * 16384 + (k % kSteps) * 32 : k * 32) >> 4),
-                                         kd + ((k % kSteps) * 32 >> 4), kIdQK, k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                        mma_ss(colS, q_desc + off, kd + off, kIdQK, k > 0);
                     }
                     mma_commit(&sh.s_full[s]);
                     mma_commit(&sh.kv_empty[ks]);
@@ -381,10 +437,10 @@ __device__ __forceinline__ float max32(const float (&x)[32]) {
 // Takes a tile's maximum into the reference: the reference follows when it
 // lags by more than kLag, and O in tensor memory with it (its products are
 // complete: S came after them in the MMA thread's order).
-template <int D, bool E4M3>
+template <int D>
 __device__ __forceinline__ void follow(uint32_t colO, float top, bool started, RowState& st) {
     if (!(top > kNegInf)) top = kNegInf;                         // (NaN: the sums carry it)
-    const bool grow = top > st.ref + Cfg<D, E4M3>::kLag || (st.ref == kNegInf && top > kNegInf);
+    const bool grow = top > st.ref + kLag || (st.ref == kNegInf && top > kNegInf);
     if (started && __any_sync(0xFFFFFFFFu, grow)) {
         const float f = !grow ? 1.0f : (st.ref == kNegInf ? 0.0f : fast_exp2(st.ref - top));
         st.sum0 *= f;
@@ -403,9 +459,8 @@ __device__ __forceinline__ void follow(uint32_t colO, float top, bool started, R
     if (grow) st.ref = top;
 }
 
-// 32 scores to powers: summed in fp32, rounded, stored as P of their keys: 16
-// columns, bf16 pairs, or 8 of e4m3 codes and 8 of e5m2 codes of what they leave.
-template <int D, bool E4M3>
+// 32 scores to powers: summed in fp32, rounded to bf16 (the products' type, whose
+// range holds any power), stored as P of their keys: 16 columns of pairs.
 __device__ __forceinline__ void powers(uint32_t colP, const float (&x)[32], float c, float off, RowState& st) {
     uint32_t u[16];
 #pragma unroll
@@ -418,22 +473,14 @@ __device__ __forceinline__ void powers(uint32_t colP, const float (&x)[32], floa
             p[k + 1] = fast_exp2(p[k + 1]);
             add2(st.sum0, st.sum1, p[k], p[k + 1]);
         }
-        if constexpr (!E4M3) {
-            u[e / 2] = pack_bf16(p[0], p[1]);
-            u[e / 2 + 1] = pack_bf16(p[2], p[3]);
-        } else {
-            const uint32_t h0 = pack_e4m3(p[0], p[1]), h1 = pack_e4m3(p[2], p[3]);
-            const float2 b0 = unpack_e4m3(h0), b1 = unpack_e4m3(h1);
-            u[e / 4] = h0 | (h1 << 16);
-            u[8 + e / 4] = pack_e5m2(p[0] - b0.x, p[1] - b0.y) | (pack_e5m2(p[2] - b1.x, p[3] - b1.y) << 16);
-        }
+        u[e / 2] = pack_bf16(p[0], p[1]);
+        u[e / 2 + 1] = pack_bf16(p[2], p[3]);
     }
     tmem_st16(colP, u);
 }
 
-template <int D, bool E4M3>
 __device__ __forceinline__ float power_offset(const RowState& st) {
-    return Cfg<D, E4M3>::kBias - (st.ref == kNegInf ? 0.0f : st.ref);
+    return st.ref == kNegInf ? 0.0f : -st.ref;
 }
 
 // Hands P to the MMA warp.
@@ -447,7 +494,7 @@ __device__ __forceinline__ void p_done(uint64_t* bar) {
 // A key tile that every row sees, N pieces of 32 keys from piece `from` on
 // this copy's (4: all of it) and the others' P zero: the long calls' loops, S
 // held in registers.
-template <int D, bool E4M3, int N>
+template <int D, int N>
 __device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, int from, float c, bool started,
                                                 uint64_t* ready, RowState& st) {
     float x[N][32];
@@ -457,8 +504,8 @@ __device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, in
     float top = max32(x[0]);
 #pragma unroll
     for (int q = 1; q < N; ++q) top = fmaxf(top, max32(x[q]));
-    follow<D, E4M3>(colO, top * c, started, st);
-    const float off = power_offset<D, E4M3>(st);
+    follow<D>(colO, top * c, started, st);
+    const float off = power_offset(st);
     if constexpr (N < 4) {
         const uint32_t z[16] = {};
 #pragma unroll
@@ -466,7 +513,7 @@ __device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, in
     }
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-        powers<D, E4M3>(colS + 16 * (from + q), x[q], c, off, st);
+        powers(colS + 16 * (from + q), x[q], c, off, st);
     }
     p_done(ready);
 }
@@ -474,7 +521,7 @@ __device__ __forceinline__ void soft_tile_whole(uint32_t colS, uint32_t colO, in
 // Any other: `count` pieces of 32 keys from piece `from` on are this copy's,
 // the others' P is zero.  A loop of small code over the pieces, S read twice:
 // a short call runs its code once, from cold instruction caches.
-template <int D, bool E4M3>
+template <int D>
 __device__ __forceinline__ void soft_tile_part(uint32_t colS, uint32_t colO, int from, int count, float c, bool started,
                                                bool whole, const RowView& view, bool draft, int first, int j0,
                                                uint64_t* ready, RowState& st) {
@@ -495,13 +542,13 @@ __device__ __forceinline__ void soft_tile_part(uint32_t colS, uint32_t colO, int
         piece(q);
         top = fmaxf(top, max32(x));
     }
-    follow<D, E4M3>(colO, top * c, started, st);
-    const float off = power_offset<D, E4M3>(st);
+    follow<D>(colO, top * c, started, st);
+    const float off = power_offset(st);
     // P of piece q lies at columns 16 q, in S pieces that have been read
 #pragma unroll 1
     for (int q = from; q < from + count; ++q) {
         if (count > 1) piece(q);
-        powers<D, E4M3>(colS + 16 * q, x, c, off, st);
+        powers(colS + 16 * q, x, c, off, st);
     }
     const uint32_t z[16] = {};
 #pragma unroll 1
@@ -510,27 +557,17 @@ __device__ __forceinline__ void soft_tile_part(uint32_t colS, uint32_t colO, int
     p_done(ready);
 }
 
-// The power of two that takes a row's largest element to [128, 256) (e4m3's
-// largest code is 448), or as near as fp32 has it.
-__device__ __forceinline__ float code_factor(float amax) {
-    const int e = static_cast<int>(__float_as_uint(amax) >> 23);
-    return e == 255 ? 1.0f : __uint_as_float(static_cast<uint32_t>(min(261 - e, 253)) << 23);
-}
-
-// A warp's 32 query rows into shared memory, K-major with the 128-byte
-// swizzle: bf16 as they are, or (beside e4m3 codes) as high and low e4m3 codes
-// of the row times a power of two, which goes into the row's c.  `src` is the
-// lane's own row; the warp reads whole rows, D / 8 lanes to one, so that a
-// load touches 4 lines and not 32, a few loads at a time before their use (few,
-// because a short call runs this code from cold instruction caches).
-template <int D, bool E4M3>
-__device__ __forceinline__ void load_queries(const uint16_t* src, bool valid, bool negate, uint8_t* qt, float& c) {
-    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = E4M3 ? 4 : 8;
+// A warp's 32 query rows into shared memory, K-major with the 128-byte swizzle.
+// `src` is the lane's own row; the warp reads whole rows, D / 8 lanes to one, so
+// that a load touches 4 lines and not 32, a few loads at a time before their use
+// (few, because a short call runs this code from cold instruction caches).
+template <int D>
+__device__ __forceinline__ void load_queries(const uint16_t* src, bool valid, bool negate, uint8_t* qt) {
+    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 8;
     const int lane = threadIdx.x & 31, ch = lane % kLanes, sub = lane / kLanes;
     const int row0 = threadIdx.x & 96;                           // the warp's first row of the tile
     const uint32_t flip = negate ? 0x80008000u : 0u, on = __ballot_sync(0xFFFFFFFFu, valid);
     const unsigned long long mine = reinterpret_cast<unsigned long long>(src);
-    float own = 0.0f;                                            // the largest element of the lane's own row
 #pragma unroll 1
     for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
         uint4 w[kBatch];
@@ -544,43 +581,10 @@ __device__ __forceinline__ void load_queries(const uint16_t* src, bool valid, bo
         for (int k = 0; k < kBatch; ++k) {
             const int rl = (i0 + k) * kRowsAt + sub, r = row0 + rl;
             const uint32_t keep = (on >> rl) & 1u ? 0xFFFFFFFFu : 0u;
-            const uint32_t x[4] = {(w[k].x ^ flip) & keep, (w[k].y ^ flip) & keep, (w[k].z ^ flip) & keep,
-                                   (w[k].w ^ flip) & keep};
-            uint8_t* base = qt + r * 128;
-            if constexpr (!E4M3) {
-                *reinterpret_cast<uint4*>(base + (ch >> 3) * 16384 + (((ch & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(x[0], x[1], x[2], x[3]);
-            } else {
-                float amax = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(x[e] & 0xFFFFu)),
-                                             fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-#pragma unroll
-                for (int d = 1; d < kLanes; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-                const float f = code_factor(amax);
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v0 = bf16_bits_to_f32(x[e] & 0xFFFFu) * f;
-                    const float v1 = __uint_as_float(x[e] & 0xFFFF0000u) * f;
-                    h[e] = pack_e4m3(v0, v1);
-                    const float2 b = unpack_e4m3(h[e]);
-                    l[e] = pack_e4m3(v0 - b.x, v1 - b.y);
-                }
-                const int chunk = ch >> 1, half = 8 * (ch & 1), cl = D == 128 ? chunk : chunk + 4;
-                uint8_t* low = D == 128 ? base + 16384 : base;
-                *reinterpret_cast<uint2*>(base + ((chunk ^ (r & 7)) << 4) + half) =
-                    make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-                *reinterpret_cast<uint2*>(low + ((cl ^ (r & 7)) << 4) + half) =
-                    make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-                // to the row's own lane, from the lanes that read it
-                const float a1 = __shfl_sync(0xFFFFFFFFu, amax, (lane % kRowsAt) * kLanes);
-                own = lane / kRowsAt == i0 + k ? a1 : own;
-            }
+            *reinterpret_cast<uint4*>(qt + r * 128 + (ch >> 3) * 16384 + (((ch & 7) ^ (r & 7)) << 4)) =
+                make_uint4((w[k].x ^ flip) & keep, (w[k].y ^ flip) & keep, (w[k].z ^ flip) & keep, (w[k].w ^ flip) & keep);
         }
     }
-    if constexpr (E4M3) c = own < INFINITY ? fmaxf(c / code_factor(own), 1.2e-38f) : __int_as_float(0x7FC00000);
     fence_async_smem();
 }
 
@@ -611,12 +615,11 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         const int n = sr.count(s);
         RowView view{0, 0, 0ull};
         // (never 0: an unseen key's -inf times it stays -inf)
-        float c = fmaxf(fabsf(a.scale) * kLog2e * (E4M3 ? a.kv.k_scale[it.h] : 1.0f), 1.2e-38f);
+        const float c = fmaxf(fabsf(a.scale) * kLog2e * (E4M3 ? a.kv.k_scale[it.h] : 1.0f), 1.2e-38f);
         {
             const int r = it.rt * kMT + (valid ? row : 0), qi = a.query_of(r), hd = it.h * a.group + r - qi * a.group;
             if (valid) view = row_view(a, it.s, qi);
-            load_queries<D, E4M3>(a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid, a.scale < 0.0f,
-                                  qs + s * C::kQBytes, c);
+            load_queries<D>(a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid, a.scale < 0.0f, qs + s * C::kQBytes);
             __syncwarp();
             if (lane == 0 && n > 0) mbar_arrive(&sh.q_ready[s]);
         }
@@ -632,11 +635,11 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
                 if (!warp_on) {
                     p_done(&sh.p_ready[s]);
                 } else if (whole && copies == 1) {
-                    soft_tile_whole<D, E4M3, 4>(colS, colO, 0, c, i > 0, &sh.p_ready[s], st);
+                    soft_tile_whole<D, 4>(colS, colO, 0, c, i > 0, &sh.p_ready[s], st);
                 } else if (whole && copies == 2) {
-                    soft_tile_whole<D, E4M3, 2>(colS, colO, 2 * copy, c, i > 0, &sh.p_ready[s], st);
+                    soft_tile_whole<D, 2>(colS, colO, 2 * copy, c, i > 0, &sh.p_ready[s], st);
                 } else {
-                    soft_tile_part<D, E4M3>(colS, colO, copy * (span >> 5), span >> 5, c, i > 0, whole, view, draft,
+                    soft_tile_part<D>(colS, colO, copy * (span >> 5), span >> 5, c, i > 0, whole, view, draft,
                                             first, j0, &sh.p_ready[s], st);
                 }
             }
@@ -667,9 +670,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
         if (valid && (sr.pair || (s == 0 && copy == 0))) {
             if (piece)
-                *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(top - C::kBias, sum);
+                *reinterpret_cast<float2*>(slot + kAttnSlotRows * D + 2 * row) = make_float2(top, sum);
             else if (a.lse)
-                a.lse[at] = top == kNegInf ? kNegInf : (top - C::kBias + log2f(sum)) * kLn2;
+                a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
         }
         // four columns of a row, finished
         auto put = [&](int64_t at_, int row_, int d4, const float4& y) {
@@ -771,7 +774,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a,
+__global__ void __launch_bounds__(kThreads<E4M3>, 1) attn_tile_kernel(const AttnArgs a,
                                                                 const __grid_constant__ KvMaps maps) {
     using C = Cfg<D, E4M3>;
     static_assert(C::kMerge == 2 * C::kQBytes, "stream 1's sums fit the two query tiles");
@@ -782,9 +785,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_full[i], E4M3 ? 4 : 1);         // the converting warps, or the TMA warp
             mbar_init(&sh.kv_empty[i], 2);
+            if (E4M3) mbar_init(&sh.kv_full[C::kStages + i], 1);
         }
+        sh.raw_end = -1;
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.p_ready[s], 4);
@@ -808,14 +813,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     tc_fence_after();
     zero_pad_rows(a, sh.plan.seqs);
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft<E4M3>));
         soften<D, E4M3>(a, sh, qs);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest<E4M3>));
         if (warp == 8)
             produce<D, E4M3>(a, maps, sh, ring);
         else if (warp < 11)
             multiply<D, E4M3>(a, sh, qs, ring, warp - 9);
+        else if (E4M3 && warp >= 12)
+            convert<D>(a, sh, ring);
     }
     tc_fence_before();
     __syncthreads();
@@ -830,7 +837,7 @@ cudaError_t launch(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStream_t s
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(attn_tile_kernel<D, E4M3>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int grid = n_sms < kAttnMaxCtas ? n_sms : kAttnMaxCtas;
-    e = launch_pdl(attn_tile_kernel<D, E4M3>, dim3(grid), dim3(kThreads), smem, s, a, m);
+    e = launch_pdl(attn_tile_kernel<D, E4M3>, dim3(grid), dim3(kThreads<E4M3>), smem, s, a, m);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_join(a, grid, s);
 }

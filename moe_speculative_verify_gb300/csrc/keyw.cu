@@ -24,9 +24,9 @@
 //
 // Measured (64 query heads, 8 kv heads of 128): 8 single tokens over 1,021 to
 // 8,209 keys 15 us (4.5 TB/s); 16 verify blocks of up to 8 over 4,099 to 16,411
-// keys 61 us in bf16 (5.3 TB/s of a copy's 6.7), 86 over e4m3 (1.9: the powers'
+// keys 61 us in bf16 (5.3 TB/s of a copy's 6.7), 84 over e4m3 (2.0: the powers'
 // and the conversion's instructions, not bytes); 1024 tokens over
-// 8,192 156 us in bf16 (0.94 PFLOP/s), 162 over e4m3.
+// 8,192 157 us in bf16 (0.93 PFLOP/s), 160 over e4m3.
 #include "attn_mma.cuh"
 #include "kernels.h"
 
@@ -305,7 +305,7 @@ template <int D, bool E4M3>
 __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t* smem, int w) {
     using C = Cfg<D, E4M3>;
     const AttnArgs& a = ka.a;
-    const uint64_t q_desc = sdesc(smem_u32(smem), 16, 1024, kSw128);
+    const uint64_t q_desc = sdesc(smem_u32(smem), 16, 1024);
     const int q_tile = C::q_tile(ka), part = C::part(ka), bufs = C::bufs(ka), raw = C::raw(ka);
     Item it;
     Waiter wait{a};
@@ -321,17 +321,17 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
                 kb = key.st;
                 wait(&sh.k_bf16[w][kb], key.ph);
                 key.step(conv);
-                k_desc = sdesc(smem_u32(smem + k16 + (w * conv + kb) * C::kTile), 16, 1024, kSw128);
+                k_desc = sdesc(smem_u32(smem + k16 + (w * conv + kb) * C::kTile), 16, 1024);
             } else {
                 kb = key.st;
                 wait(&sh.k_full[w][kb], key.ph);
                 key.step(bufs);
-                k_desc = sdesc(smem_u32(smem + raw + (w * bufs + kb) * C::kRaw), 16, 1024, kSw128);
+                k_desc = sdesc(smem_u32(smem + raw + (w * bufs + kb) * C::kRaw), 16, 1024);
             }
         }
         for (int t = it.t0; t < it.t1; ++t) {
             const int tokens = min(ka.tile_tokens, it.nq - t * ka.tile_tokens);
-            const uint32_t id = idesc(1, 1, false, (tokens * ka.tile_heads + 15) & ~15);
+            const uint32_t id = idesc(false, (tokens * ka.tile_heads + 15) & ~15);
             for (int hc = 0; hc < a.group; hc += ka.tile_heads) {
                 wait(&sh.q_full[q.st], q.ph);
                 const int sb = buf.st;
@@ -347,7 +347,7 @@ __device__ __forceinline__ void multiply(const KeywArgs& ka, Shared& sh, uint8_t
                     if (on) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
-                            mma_ss<false>(d, k_desc + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                            mma_ss(d, k_desc + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
                                           qd + (((k >> 2) * part + (k & 3) * 32) >> 4), id, k > 0);
                         }
                         mma_commit(&sh.s_full[w][sb]);
@@ -394,15 +394,15 @@ __device__ __forceinline__ void convert(const KeywArgs& ka, Shared& sh, uint8_t*
                 raw + lr * D + ((D == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3)) << 4));
         wait(&sh.k_free[w][out.st], out.ph ^ 1u);
         if (wait.dead) break;
-        uint32_t nan = 0;
+        uint32_t most = 0;
 #pragma unroll
         for (int ch = 0; ch < D / 16; ++ch) {
             const uint4 x = in[ch];
             uint32_t y[8];
-            e4m3x4_to_bf16(x.x, y[0], y[1], nan);
-            e4m3x4_to_bf16(x.y, y[2], y[3], nan);
-            e4m3x4_to_bf16(x.z, y[4], y[5], nan);
-            e4m3x4_to_bf16(x.w, y[6], y[7], nan);
+            e4m3x4_to_bf16(x.x, y[0], y[1], most);
+            e4m3x4_to_bf16(x.y, y[2], y[3], most);
+            e4m3x4_to_bf16(x.z, y[4], y[5], most);
+            e4m3x4_to_bf16(x.w, y[6], y[7], most);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int c2 = 2 * ch + e;
@@ -410,7 +410,7 @@ __device__ __forceinline__ void convert(const KeywArgs& ka, Shared& sh, uint8_t*
                     make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
             }
         }
-        if (nan & 0x80808080u) {             // a NaN code makes its key's scores NaN: one NaN in the row does
+        if (e4m3_had_nan(most)) {             // a NaN code makes its key's scores NaN: one NaN in the row does
             *reinterpret_cast<uint16_t*>(dst + lr * 128 + ((lr & 7) << 4)) = 0x7FC0u;
         }
         fence_async_smem();

@@ -18,38 +18,38 @@ def _built():
     torch.cuda.set_device(0)
 
 
-def sink(keys, news, hq, dtype, dim, gap, tail, mean=0.5, seed=1):
+def sink(keys, news, hq, hkv, dtype, dim, gap, tail, mean=0.5, seed=1):
     g = torch.Generator(device="cuda").manual_seed(seed)
-    k = torch.zeros(keys, 1, dim, device="cuda") if tail == "equal" else (randn(g, keys, 1, dim) * 16).round() / 16
+    k = torch.zeros(keys, hkv, dim, device="cuda") if tail == "equal" else (randn(g, keys, hkv, dim) * 16).round() / 16
     k[:, :, 0] = 0
     k[0] = 0
-    k[0, 0, 0] = 16.0
-    v = ((randn(g, keys, 1, dim) + mean) * 16).round() / 16
+    k[0, :, 0] = 16.0
+    v = ((randn(g, keys, hkv, dim) + mean) * 16).round() / 16
     v[0] = 0
     q = randn(g, news, hq, dim)
     q[:, :, 0] = gap * dim ** 0.5 / 16.0                    # the first key's score; the others' are 0, or about 1 apart
     return One(k, v, q, dtype, dim ** -0.5)
 
 
-# rows a kv head: 8 (few rows), 32, 64 (repeated in the tile), 96 (one tile), 320 (two tiles)
-@pytest.mark.parametrize("news,hq", [(1, 8), (4, 8), (8, 8), (12, 8), (40, 8)])
-@pytest.mark.parametrize("keys", [16384, 32768])
+# rows a kv head: 8, and 1 with a whole head a CTA (few rows); 32, 64 (repeated in the tile), 96 (one tile), 320 (two)
+@pytest.mark.parametrize("news,hq,hkv,keys", [(1, 8, 1, 32768), (1, 128, 128, 8192), (4, 8, 1, 32768), (8, 8, 1, 16384),
+                                              (8, 256, 32, 8192), (12, 8, 1, 32768), (40, 8, 1, 16384), (40, 8, 1, 32768)])
 @pytest.mark.parametrize("tail", ["equal", "spread"])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-def test_small_probabilities_behind_a_sink(dtype, tail, keys, news, hq):
+def test_small_probabilities_behind_a_sink(dtype, tail, news, hq, hkv, keys):
     for gap in (8.0, 10.28, 12.0, 13.0, 14.0, 15.0, 16.0):
         for dim in (64, 128):
-            sink(keys, news, hq, dtype, dim, gap, tail).check()
+            sink(keys, news, hq, hkv, dtype, dim, gap, tail).check()
 
 
 @pytest.mark.parametrize("news", [1, 8])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_small_probabilities_of_a_million_keys(dtype, news):
     for gap in (14.0, 16.0, 18.0):
-        sink(1 << 20, news, 8, dtype, 128, gap, "equal").check()
+        sink(1 << 20, news, 8, 1, dtype, 128, gap, "equal").check()
 
 
-@pytest.mark.parametrize("news,hq", [(1, 8), (8, 8), (40, 8)])
+@pytest.mark.parametrize("news,hq", [(8, 8), (12, 8), (40, 8)])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_outlier_query_channel(dtype, dim, news, hq):
@@ -63,3 +63,27 @@ def test_outlier_query_channel(dtype, dim, news, hq):
         q = randn(g, news, hq, dim) * 3
         q[:, :, 5] = size
         One(k, v, q, dtype, dim ** -0.5).check()
+
+
+@pytest.mark.parametrize("news,hq", [(1, 8), (8, 8), (40, 8)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_nan_in_the_cache(dtype, dim, news, hq):
+    """A NaN value makes its column NaN and no other; a NaN key every row that sees it."""
+    for code in ((0x7F, 0xFF) if dtype == "e4m3" else (0x7FC0, -0x40)):
+        g = torch.Generator(device="cuda").manual_seed(4)
+        k, v = ((randn(g, 400, 1, dim) * 16).round() / 16 for _ in range(2))
+        p = One(k, v, randn(g, news, hq, dim), dtype, dim ** -0.5)
+        clean, _ = p.run()
+        bits = lambda x: x.view(torch.uint8 if dtype == "e4m3" else torch.int16)
+        before = bits(p.dv)[2, 0, 7, dim - 3].clone()
+        bits(p.dv)[2, 0, 7, dim - 3] = code
+        out, lse = p.run()
+        assert bool(torch.isnan(out[:, :, dim - 3]).all()) and not bool(torch.isnan(lse).any())
+        keep = torch.arange(dim, device="cuda") != dim - 3
+        assert torch.equal(out[:, :, keep], clean[:, :, keep])
+        bits(p.dv)[2, 0, 7, dim - 3] = before
+        bits(p.dk)[6, 0, 15, 3] = code                # key 399: the last row's own
+        out, lse = p.run()
+        assert bool(torch.isnan(out[-1]).all()) and bool(torch.isnan(lse[-1]).all())
+        assert torch.equal(out[:-1], clean[:-1])
