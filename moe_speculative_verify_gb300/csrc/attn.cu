@@ -31,6 +31,13 @@ constexpr int kConsumers = 8;               // warps; four to a tile
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kBarMerge = 1;                // named barrier of the consumer warps
 
+// e4m3: f16 probabilities at 2^15 times their share of a warp's largest, near the
+// end of f16: 8 bits down to 2^-32 of it, some down to 2^-39.  (bf16 ones, which
+// have no such end, need bf16 codes, four times the instructions of f16 ones in a
+// kernel that they bound.)
+template <bool E4M3>
+constexpr float kBias = E4M3 ? 15.0f : 0.0f;
+
 template <int D, bool E4M3>
 struct Cfg {
     static constexpr int kRowBytes = E4M3 ? D : 2 * D;
@@ -369,7 +376,7 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
                 }
             }
             // --- probabilities: summed in fp32, rounded to 16 bits for the product
-            const float ref[2] = {m[0] == kNegInf ? 0.0f : m[0], m[1] == kNegInf ? 0.0f : m[1]};
+            const float ref[2] = {m[0] == kNegInf ? 0.0f : m[0] - kBias<E4M3>, m[1] == kNegInf ? 0.0f : m[1] - kBias<E4M3>};
             float p[2][4];
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -454,6 +461,7 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
             l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
             l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
             if (l[r] != l[r]) m[r] = fmaxf(m[r], 0.0f);   // a NaN is a result, not an empty row
+            m[r] -= kBias<E4M3>;
             if (t == 0) sh.ml[wid][g + 8 * r] = make_float2(m[r], l[r]);
         }
         named_bar(kBarMerge, 32 * kConsumers);

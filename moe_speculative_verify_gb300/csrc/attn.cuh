@@ -218,16 +218,14 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A bf16 query row times 2^-e, e the exponent of its largest element, so that
-// it keeps its bits in f16 beside e4m3 codes (exact in f16 too): the element
-// range below 2^-14 of the largest, which f16 would cut, lies under the
-// product's fp32 rounding of the row's own largest terms.  Zero and
-// non-finite rows stay as they are.
+// The power of two that takes a bf16 query row's largest element to [2^14,
+// 2^15), near the end of f16 (or as near as fp32 has it), where the row
+// multiplies e4m3 codes: elements keep their 8 bits down to 2^-31 of the
+// largest, and below it err by at most 2^-39 of it.  Non-finite rows stay as
+// they are.
 __device__ __forceinline__ float pow2_norm(float amax) {
-    const uint32_t e = __float_as_uint(amax) >> 23;
-    // 2^(127 - e): biased 254 - e (2^-127 is subnormal); e = 0 (zero, subnormal) and 255 stay
-    if (e == 0u || e == 255u) return 1.0f;
-    return e == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - e) << 23);
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23);
+    return e == 255 ? 1.0f : __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
 }
 
 // 4-D tiled bulk tensor load global -> shared; c0 (innermost, elements) starts

@@ -87,3 +87,26 @@ def test_nan_in_the_cache(dtype, dim, news, hq):
         out, lse = p.run()
         assert bool(torch.isnan(out[-1]).all()) and bool(torch.isnan(lse[-1]).all())
         assert torch.equal(out[:-1], clean[:-1])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_outlier_query_channel_of_a_single_token(dim):
+    """As test_outlier_query_channel, in the kernel for few rows."""
+    for dtype in ("bf16", "e4m3"):
+        for size in (1e3, 1e5, 1e6, 1e8):
+            g = torch.Generator(device="cuda").manual_seed(3)
+            k = (randn(g, 500, 1, dim) * 16).round() / 16
+            k[:, :, 5] = 0
+            v = (randn(g, 500, 1, dim) * 16).round() / 16
+            q = randn(g, 1, 8, dim) * 3
+            q[:, :, 5] = size
+            One(k, v, q, dtype, dim ** -0.5).check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_equal_scores_far_below_a_single_token_s_largest(dtype, dim):
+    """Few keys, so that one warp's largest is the heavy key's: the others are
+    21 to 27 octaves below it."""
+    for gap in (14.6, 15.3, 16.3, 17.2, 18.7):
+        sink(16, 1, 8, 1, dtype, dim, gap, "equal").check()
