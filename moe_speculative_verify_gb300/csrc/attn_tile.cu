@@ -614,12 +614,13 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Shared& sh, uint8_t* q
         const bool warp_on = __any_sync(0xFFFFFFFFu, valid);
         const int n = sr.count(s);
         RowView view{0, 0, 0ull};
-        // (never 0: an unseen key's -inf times it stays -inf)
-        const float c = fmaxf(fabsf(a.scale) * kLog2e * (E4M3 ? a.kv.k_scale[it.h] : 1.0f), 1.2e-38f);
+        // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf), or NaN; the sign goes to the queries
+        const float cs = a.scale * kLog2e * (E4M3 ? a.kv.k_scale[it.h] : 1.0f);
+        const float c = cs != cs ? cs : fmaxf(fabsf(cs), 1.2e-38f);
         {
             const int r = it.rt * kMT + (valid ? row : 0), qi = a.query_of(r), hd = it.h * a.group + r - qi * a.group;
             if (valid) view = row_view(a, it.s, qi);
-            load_queries<D>(a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid, a.scale < 0.0f, qs + s * C::kQBytes);
+            load_queries<D>(a.q + (it.s.q0 + qi) * a.q_stride + hd * D, valid, cs < 0.0f, qs + s * C::kQBytes);
             __syncwarp();
             if (lane == 0 && n > 0) mbar_arrive(&sh.q_ready[s]);
         }

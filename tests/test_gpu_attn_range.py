@@ -110,3 +110,19 @@ def test_equal_scores_far_below_a_single_token_s_largest(dtype, dim):
     21 to 27 octaves below it."""
     for gap in (14.6, 15.3, 16.3, 17.2, 18.7):
         sink(16, 1, 8, 1, dtype, dim, gap, "equal").check()
+
+
+@pytest.mark.parametrize("news,hq", [(1, 16), (2, 16), (8, 16), (40, 16)])
+@pytest.mark.parametrize("scale", [0.1, -0.1])
+def test_signs_of_scales(news, hq, scale):
+    """Negative softmax scales and negative scales of a head's codes."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    ks, vs = torch.tensor([1 / 16, -1 / 16], device="cuda"), torch.tensor([-1 / 16, 1 / 16], device="cuda")
+    k, v = ((randn(g, 700, 2, 64) * 16).round() / 16 for _ in range(2))
+    One(k, v, randn(g, news, hq, 64), "e4m3", scale, ks, vs).check()
+    One(k, v, randn(g, news, hq, 64), "bf16", scale).check()
+    p = One(k, v, randn(g, news, hq, 64), "e4m3", scale)
+    p.k_scale[1] = float("nan")
+    out, lse = p.run()
+    assert bool(torch.isnan(out[:, hq // 2:]).all()) and bool(torch.isnan(lse[:, hq // 2:]).all())
+    assert bool(torch.isfinite(out[:, :hq // 2]).all())
