@@ -15,9 +15,10 @@
 // (attn.cuh), so lengths of 1 : 1000 in a batch load them alike.
 //
 // Measured (8 kv heads of 8 query heads of 128, bf16): 48 single tokens over
-// 251 to 32,011 keys 241 us, 5.9 TB/s of a copy's 6.7; one over 60,000 keys
-// 54 us (4.6 TB/s), over 6,011 20.7 and over 8 keys 9.4: a fixed cost of the
-// plan, an item's start and end and the join's launch.
+// 251 to 32,011 keys 241 us, 5.9 TB/s of a copy's 6.7 (over e4m3 281, 2.5 TB/s:
+// the conversions to f16); one over 60,000 keys 53 us (4.6 TB/s), over 6,011 20.8
+// and over 8 keys 9.6: a fixed cost of the plan, an item's start and end and
+// the join's launch.
 #include "attn.cuh"
 #include "kernels.h"
 
@@ -375,7 +376,8 @@ __device__ __forceinline__ void consume(const AttnArgs& a, Shared& sh, uint8_t* 
                     }
                 }
             }
-            // --- probabilities: summed in fp32, rounded to 16 bits for the product
+            // --- probabilities: summed in fp32, rounded for the product to the 16-bit type that the
+            // matrix instruction takes beside V (bf16: 2^-8 of each at most; f16 beside codes: 2^-11)
             const float ref[2] = {m[0] == kNegInf ? 0.0f : m[0] - kBias<E4M3>, m[1] == kNegInf ? 0.0f : m[1] - kBias<E4M3>};
             float p[2][4];
 #pragma unroll

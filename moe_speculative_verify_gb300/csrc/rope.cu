@@ -19,7 +19,7 @@ namespace {
 
 // Small blocks: a block is a token's chain of latencies (its sequence, its
 // page, its angles), and more of them share an SM.  Measured for 4096 tokens,
-// 64 + 16 heads of 128: 128 threads 30.6 us (5.5 TB/s of the 6.7 of a copy), 256
+// 64 + 16 heads of 128: 128 threads 30.8 us (5.4 TB/s of the 6.7 of a copy), 256
 // 34.7, 512 52.6; two units of a thread in flight 32.1, three of 256 threads 37.1.
 constexpr int kRopeThreads = 128;
 constexpr int kFlight = 1;                  // units of a thread in flight
