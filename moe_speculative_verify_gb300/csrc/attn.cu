@@ -574,7 +574,7 @@ cudaError_t launch_rows(const AttnArgs& a, const KvMaps& m, int n_sms, cudaStrea
     return e != cudaSuccess ? e : launch_attn_join(a, grid, s);
 }
 
-// Joins the pieces of the item that begins in CTA blockIdx.x, 8 rows a block:
+// Joins the pieces of the split items:
 // out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k over the pieces in CTA
 // order.  A kernel of its own, not the work of the piece that comes last: that
 // CTA alone would read a verify block's 19 pieces of 64 rows (630 KB) at one
