@@ -657,6 +657,141 @@ moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs
                              int32_t* kept, float* scores_out, int32_t* new_len, void* ws,
                              size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * Attention through a latent cache: one row a token for all heads, a latent
+ * vector whose linear maps are every head's keys and values, and a rotary key
+ * that the heads share.  moe_latent_append writes the rows, moe_latent_attention
+ * attends over them with queries in latent space (absorbed form: single tokens,
+ * verify blocks, chunks), moe_latent_gather reads them back, and
+ * moe_expanded_attention attends over keys and values made from such rows
+ * (expanded form, which takes a third of the work a pair: long prompts).
+ * moe_seqs_t, moe_attn_t, moe_rope_t, the masks and the handling of numbers that
+ * do not fit are those of the attention calls above.
+ * ------------------------------------------------------------------------ */
+
+#define MOE_LATENT_ROPE_DIM 64      /* elements of a row's rotary key            */
+#define MOE_LATENT_MIN_SCALE (-64)  /* least and largest scale_log2              */
+#define MOE_LATENT_MAX_SCALE 7
+
+/*
+ * One layer's paged latent cache: element d of a token's latent vector at
+ * latent + page * latent_page_stride + token * latent_token_stride + d elements,
+ * of its rotary key at rope + page * rope_page_stride + token *
+ * rope_token_stride + d, so both parts fit side by side in one allocation.
+ *   latent_dim   256 or 512        page_size   16, 32, 64 or 128 tokens
+ *   dtype        of the latent: MOE_KV_BF16, or MOE_KV_E4M3, whose values are
+ *                code * 2^scale_log2, bf16 numbers all of them; the rotary key is
+ *                bf16 in both (its rounding would turn with the position)
+ *   strides      multiples of 16 bytes, positive, each below 2^40 bytes
+ *   latent, rope 16-byte aligned device memory
+ */
+typedef struct {
+    void* latent;
+    void* rope;
+    int64_t latent_page_stride;
+    int64_t latent_token_stride;
+    int64_t rope_page_stride;
+    int64_t rope_token_stride;
+    int32_t dtype;
+    int32_t scale_log2;      /* e4m3 only */
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t latent_dim;
+} moe_latent_cache_t;
+
+/*
+ * moe_latent_append -- the step's new tokens: latents normalised, rotary
+ * positions on the shared keys and on the queries' rotary parts, rows stored at
+ * their places in the cache.
+ *   kv         bf16 [n_tokens, latent_dim + 64], token stride kv_stride: the latent,
+ *              then the rotary key
+ *   gamma      fp32 [latent_dim], 16-byte aligned: the latent x is stored as
+ *              x / sqrt(sum x^2 / latent_dim + eps) * gamma; NULL: as it is
+ *   q_rope     bf16 [n_tokens, n_q_heads, 64], strides q_token_stride, q_head_stride
+ *   q_out      the same with strides of its own (may be q_rope itself with equal
+ *              strides), so that it can lie in the query rows that
+ *              moe_latent_attention reads; pad rows are +0
+ *   positions  int32 [n_tokens];  rope->rot_dim is 64
+ * Strides in elements, positive multiples of 8 (tokens' at least a token's
+ * width), below 2^32; pointers 16-byte aligned; q_out and the cache overlap no
+ * other argument.
+ * fp32 arithmetic, one rounding: bf16, or the saturating e4m3 code of
+ * x / 2^scale_log2.  Tokens without a place and numbers that do not fit: as
+ * moe_rope_append.  n_tokens == 0 launches nothing.
+ */
+moe_status_t moe_latent_append(const moe_rope_t* rope, const moe_latent_cache_t* cache,
+                               const moe_seqs_t* seqs, const void* kv, int64_t kv_stride,
+                               const float* gamma, float eps, const void* q_rope,
+                               int64_t q_token_stride, int64_t q_head_stride,
+                               const int32_t* positions, int32_t n_tokens, int32_t n_q_heads,
+                               void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                               moe_stream_t stream);
+
+/* Bytes of a workspace that serves moe_latent_attention and moe_latent_gather
+ * for this shape, whatever the batch (0 for a shape that is refused); its first
+ * 256 bytes as those of moe_attn_workspace_bytes. */
+size_t moe_latent_workspace_bytes(const moe_attn_t* attn, const moe_latent_cache_t* cache);
+
+/*
+ * moe_latent_attention -- softmax attention of the new tokens over the cache,
+ * every query head over the same rows: scores scale * q . (latent, rotary key),
+ * values the latents.
+ *   q          bf16 [n_tokens, n_q_heads, latent_dim + 64], token stride q_stride
+ *              (elements): a head's query times its key map, then its rotary part
+ *   draft_mask uint64 [n_tokens] or NULL
+ *   out        bf16 [n_tokens, n_q_heads, latent_dim] contiguous; pad rows +0
+ *   lse        fp32 [n_tokens, n_q_heads] or NULL, as moe_paged_attention's
+ * n_q_heads is free (1 .. MOE_MAX_HEADS).  The rest as moe_paged_attention.
+ */
+moe_status_t moe_latent_attention(const moe_attn_t* attn, const moe_latent_cache_t* cache,
+                                  const moe_seqs_t* seqs, const void* q, int64_t q_stride,
+                                  const uint64_t* draft_mask, int32_t n_tokens, void* out,
+                                  float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_latent_gather -- cached rows read back as bf16 (exactly):
+ *   out[cu_k[b] + j] = (latent, rotary key) at place j of sequence b, for
+ *   j < min(kv_len[b], cu_k[b + 1] - cu_k[b]); the other rows of out are +0.
+ *   cu_k       int32 [n_seqs + 1], rows of out; from the first offset on that is
+ *              past n_rows or below the one before it, no sequence has rows
+ *   out        bf16 [n_rows, latent_dim + 64], row stride out_stride (elements, a
+ *              multiple of 8)
+ *   ws         at least 256 bytes: the error word
+ * cu_q and max_q of seqs are not read.  n_rows == 0 launches nothing.
+ */
+moe_status_t moe_latent_gather(const moe_latent_cache_t* cache, const moe_seqs_t* seqs,
+                               const int32_t* cu_k, int32_t n_rows, void* out, int64_t out_stride,
+                               void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Bytes of a workspace for moe_expanded_attention with values of v_dim elements
+ * a head (64 or 128); 0 for a shape that is refused. */
+size_t moe_expanded_workspace_bytes(const moe_attn_t* attn, int32_t v_dim);
+
+/*
+ * moe_expanded_attention -- softmax attention of the new tokens over keys and
+ * values of their own for every head, in rows one sequence after another: key j
+ * of sequence b, j < kv_len[b], is row cu_k[b] + j; its own part for head h is
+ * k[row, h], its rotary part k_rope[row], its values v[row, h].
+ *   q          bf16 [n_tokens, n_q_heads, v_dim + 64], token stride q_stride: a head's
+ *              own part, then its rotary part
+ *   k, v       bf16 [n_keys, n_q_heads, v_dim], token and head strides of their own
+ *   k_rope     bf16 [n_keys, 64], token stride rope_stride
+ *   out        bf16 [n_tokens, n_q_heads, v_dim] contiguous; pad rows +0
+ *   lse        fp32 [n_tokens, n_q_heads] or NULL, as moe_paged_attention's
+ * Strides in elements, positive multiples of 8, below 2^32; pointers 16-byte
+ * aligned.  block_table and max_pages of seqs are not read; no draft masks.  A
+ * length past n_keys is cut to it, a row outside 0 .. n_keys - 1 reads as zeros;
+ * both are recorded (MOE_ERR_INVALID_ARG).
+ */
+moe_status_t moe_expanded_attention(const moe_attn_t* attn, const moe_seqs_t* seqs,
+                                    const int32_t* cu_k, int32_t n_keys, int32_t v_dim,
+                                    const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_token_stride, int64_t k_head_stride,
+                                    const void* k_rope, int64_t rope_stride, const void* v,
+                                    int64_t v_token_stride, int64_t v_head_stride,
+                                    int32_t n_tokens, void* out, float* lse, void* ws,
+                                    size_t ws_bytes, moe_stream_t stream);
+
 /*
  * moe_get_device_error -- synchronises `stream`, then reads (and clears when
  * `clear` != 0) the device error word at the start of a workspace given to

@@ -30,6 +30,9 @@ __all__ = [
     "KVCache", "Seqs", "Rope", "Attn", "KV_BF16", "KV_E4M3", "ROPE_PLAIN", "ROPE_LINEAR",
     "ROPE_RAMP", "moe_rope_freqs", "moe_rope_append", "moe_attn_workspace_bytes",
     "moe_paged_attention", "moe_key_weights", "moe_cache_evict",
+    "LatentCache", "LATENT_ROPE_DIM", "moe_latent_append", "moe_latent_workspace_bytes",
+    "moe_latent_attention", "moe_latent_gather", "moe_expanded_workspace_bytes",
+    "moe_expanded_attention",
 ]
 
 LAYOUT_ROW_MAJOR = 0
@@ -39,6 +42,7 @@ KV_E4M3 = 1
 ROPE_PLAIN = 0
 ROPE_LINEAR = 1
 ROPE_RAMP = 2
+LATENT_ROPE_DIM = 64         # elements of a latent cache row's rotary key
 CODE_KEYS = ("w_gate", "w_up", "w_down", "sh_gate", "sh_up", "sh_down")
 
 MOE_MAX_ROWS = 4096
@@ -115,6 +119,33 @@ class KVCache(C.Structure):
                 _ptr(v_scale) if e4m3 else None, st[0], st[1], st[2],
                 KV_E4M3 if e4m3 else KV_BF16, n, p, h, d)
         c._tensors = (k, v, k_scale, v_scale)
+        return c
+
+
+class LatentCache(C.Structure):
+    _fields_ = [("latent", C.c_void_p), ("rope", C.c_void_p), ("latent_page_stride", C.c_int64),
+                ("latent_token_stride", C.c_int64), ("rope_page_stride", C.c_int64),
+                ("rope_token_stride", C.c_int64), ("dtype", C.c_int32), ("scale_log2", C.c_int32),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("latent_dim", C.c_int32)]
+
+    @classmethod
+    def from_tensors(cls, latent, rope, scale_log2: int = 0) -> "LatentCache":
+        """From latent [pages, page size, latent dim], bf16 or e4m3
+        (torch.float8_e4m3fn or uint8 codes of value code * 2^scale_log2), and
+        rope [pages, page size, 64] bf16; any page and token strides, so slices
+        of one [pages, page size, latent dim + 64] tensor fit.  The result holds
+        references to the tensors."""
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        if (latent.dim() != 3 or rope.shape != (*latent.shape[:2], LATENT_ROPE_DIM)
+                or latent.dtype not in codes + (torch.bfloat16,) or rope.dtype != torch.bfloat16
+                or latent.stride(2) != 1 or rope.stride(2) != 1):
+            raise MoeError(1, "LatentCache")
+        n, p, d = latent.shape
+        def st(t, i):
+            return t.stride(i) if t.shape[i] > 1 else t.shape[2]
+        c = cls(latent.data_ptr(), rope.data_ptr(), st(latent, 0), st(latent, 1), st(rope, 0),
+                st(rope, 1), KV_E4M3 if latent.dtype in codes else KV_BF16, scale_log2, n, p, d)
+        c._tensors = (latent, rope)
         return c
 
 
@@ -218,6 +249,20 @@ def load() -> C.CDLL:
     L.moe_paged_attention.argtypes = [at, kv, sq, P, I64, P, I32, P, P, P, SZ, P]
     L.moe_key_weights.argtypes = [at, kv, sq, P, I64, P, I32, P, C.c_float, P, P, I64, P, SZ, P]
     L.moe_cache_evict.argtypes = [kv, sq, P, I64, I32, I32, P, I32, P, P, P, P, SZ, P]
+    lc = C.POINTER(LatentCache)
+    L.moe_latent_append.argtypes = [C.POINTER(Rope), lc, sq, P, I64, P, C.c_float, P, I64, I64, P,
+                                    I32, I32, P, I64, I64, P]
+    L.moe_latent_workspace_bytes.restype = SZ
+    L.moe_latent_workspace_bytes.argtypes = [at, lc]
+    L.moe_latent_attention.argtypes = [at, lc, sq, P, I64, P, I32, P, P, P, SZ, P]
+    L.moe_latent_gather.argtypes = [lc, sq, P, I32, P, I64, P, SZ, P]
+    L.moe_expanded_workspace_bytes.restype = SZ
+    L.moe_expanded_workspace_bytes.argtypes = [at, I32]
+    L.moe_expanded_attention.argtypes = [at, sq, P, I32, I32, P, I64, P, I64, I64, P, I64, P, I64,
+                                         I64, I32, P, P, P, SZ, P]
+    for n in ("moe_latent_append", "moe_latent_attention", "moe_latent_gather",
+              "moe_expanded_attention"):
+        getattr(L, n).restype = C.c_int
     for n in ("moe_rope_freqs", "moe_rope_append", "moe_paged_attention", "moe_key_weights",
               "moe_cache_evict"):
         getattr(L, n).restype = C.c_int
@@ -520,6 +565,109 @@ def moe_cache_evict(cache: KVCache, seqs: Seqs, scores, budget: int, n_recent: i
                                   _ptr(kept), _ptr(scores_out), _ptr(new_len), _ptr(ws),
                                   ws.numel() * ws.element_size(), _stream(stream)),
            "moe_cache_evict")
+
+
+# ------------------------------------------------------------ latent cache --
+def _here(*tensors) -> bool:
+    """All of them (None aside) on the current device, on whose stream a call runs."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return all(t is None or t.get_device() == dev for t in tensors)
+
+
+def _strided(t, tokens: int, heads: int, dim: int) -> bool:
+    """bf16 [tokens, heads, dim] with free strides of token and head."""
+    return t.dtype is torch.bfloat16 and t.shape == (tokens, heads, dim) and t.stride(2) == 1
+
+
+def _stride(t, i: int) -> int:
+    """The stride of axis i; where the axis has one place, one that is fit for any check."""
+    return t.stride(i) if t.shape[i] > 1 else (t.shape[1:].numel() if i == 0 else t.shape[-1])
+
+
+def moe_latent_append(rope: Rope, cache: LatentCache, seqs: Seqs, kv, q_rope, positions, q_out,
+                      gamma=None, eps: float = 1e-6, stream=None) -> None:
+    """kv bf16 [T, latent_dim + 64] (free token stride); q_rope, q_out bf16
+    [T, n_q_heads, 64] (free strides of token and head, so that q_out can be the
+    last 64 elements of moe_latent_attention's query rows); gamma fp32
+    [latent_dim] or None: the latents are stored without normalisation."""
+    T, H = q_rope.shape[:2]
+    L = cache.latent_dim
+    _refuse(kv.dtype is torch.bfloat16 and kv.shape == (T, L + LATENT_ROPE_DIM) and kv.stride(1) == 1
+            and _strided(q_rope, T, H, LATENT_ROPE_DIM) and _strided(q_out, T, H, LATENT_ROPE_DIM)
+            and _is(positions, torch.int32, T)
+            and (gamma is None or _is(gamma, torch.float32, L))
+            and _here(kv, q_rope, q_out, positions, gamma), "moe_latent_append")
+    _check(load().moe_latent_append(C.byref(rope), C.byref(cache), C.byref(seqs), kv.data_ptr(),
+                                    _stride(kv, 0), _ptr(gamma), eps, q_rope.data_ptr(),
+                                    _stride(q_rope, 0), _stride(q_rope, 1), positions.data_ptr(),
+                                    T, H, q_out.data_ptr(), _stride(q_out, 0), _stride(q_out, 1),
+                                    _stream(stream)), "moe_latent_append")
+
+
+def moe_latent_workspace_bytes(attn: Attn, cache: LatentCache) -> int:
+    """Bytes of a workspace, zeroed once by the caller, for moe_latent_attention
+    and moe_latent_gather."""
+    return load().moe_latent_workspace_bytes(C.byref(attn), C.byref(cache))
+
+
+def moe_latent_attention(attn: Attn, cache: LatentCache, seqs: Seqs, q, out, ws, lse=None,
+                         draft_mask=None, stream=None) -> None:
+    """q bf16 [T, n_q_heads, latent_dim + 64] (free token stride); out bf16
+    [T, n_q_heads, latent_dim], contiguous; lse fp32 [T, n_q_heads] or None;
+    draft_mask int64 [T] (the bits of a uint64) or None."""
+    T, H, L = q.shape[0], attn.n_q_heads, cache.latent_dim
+    W = L + LATENT_ROPE_DIM
+    _refuse(q.dim() == 3 and _heads(q, H, W, T) and _is(out, torch.bfloat16, T, H, L)
+            and (lse is None or _is(lse, torch.float32, T, H))
+            and (draft_mask is None or _is(draft_mask, torch.int64, T))
+            and _here(q, out, lse, draft_mask, ws), "moe_latent_attention")
+    _check(load().moe_latent_attention(C.byref(attn), C.byref(cache), C.byref(seqs), _ptr(q),
+                                       q.stride(0) if T > 1 else H * W, _ptr(draft_mask), T,
+                                       _ptr(out), _ptr(lse), _ptr(ws),
+                                       ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_latent_attention")
+
+
+def moe_latent_gather(cache: LatentCache, seqs: Seqs, cu_k, out, ws, stream=None) -> None:
+    """cu_k int32 [n_seqs + 1]: rows of out, bf16 [N, latent_dim + 64] (free row
+    stride), where each sequence's cached rows go; rows of none are zeroed."""
+    N, W = out.shape[0], cache.latent_dim + LATENT_ROPE_DIM
+    _refuse(out.dtype is torch.bfloat16 and out.shape == (N, W) and out.stride(1) == 1
+            and _is(cu_k, torch.int32, seqs.n_seqs + 1) and _here(out, cu_k, ws),
+            "moe_latent_gather")
+    _check(load().moe_latent_gather(C.byref(cache), C.byref(seqs), _ptr(cu_k), N, _ptr(out),
+                                    _stride(out, 0), _ptr(ws), ws.numel() * ws.element_size(),
+                                    _stream(stream)), "moe_latent_gather")
+
+
+def moe_expanded_workspace_bytes(attn: Attn, v_dim: int) -> int:
+    """Bytes of a workspace, zeroed once by the caller, for moe_expanded_attention."""
+    return load().moe_expanded_workspace_bytes(C.byref(attn), v_dim)
+
+
+def moe_expanded_attention(attn: Attn, seqs: Seqs, cu_k, q, k, k_rope, v, out, ws, lse=None,
+                           stream=None) -> None:
+    """q bf16 [T, n_q_heads, D + 64] (free token stride); k, v bf16
+    [N, n_q_heads, D] (free strides of token and head, so that both can be halves
+    of one projection's output), k_rope bf16 [N, 64] (free token stride); out bf16
+    [T, n_q_heads, D], contiguous; cu_k int32 [n_seqs + 1] (or [n_seqs]): first row
+    of each sequence; lse fp32 [T, n_q_heads] or None.  D is 64 or 128."""
+    T, H = q.shape[0], attn.n_q_heads
+    N, D = k.shape[0], v.shape[-1]
+    _refuse(q.dim() == 3 and _heads(q, H, D + LATENT_ROPE_DIM, T) and _strided(k, N, H, D)
+            and _strided(v, N, H, D) and k_rope.dtype is torch.bfloat16
+            and k_rope.shape == (N, LATENT_ROPE_DIM) and k_rope.stride(1) == 1
+            and cu_k.dim() == 1 and cu_k.shape[0] >= seqs.n_seqs
+            and _is(cu_k, torch.int32, cu_k.shape[0]) and _is(out, torch.bfloat16, T, H, D)
+            and (lse is None or _is(lse, torch.float32, T, H))
+            and _here(q, k, k_rope, v, out, cu_k, lse, ws), "moe_expanded_attention")
+    _check(load().moe_expanded_attention(C.byref(attn), C.byref(seqs), _ptr(cu_k), N, D, _ptr(q),
+                                         q.stride(0) if T > 1 else H * (D + LATENT_ROPE_DIM),
+                                         _ptr(k), _stride(k, 0), _stride(k, 1), _ptr(k_rope),
+                                         _stride(k_rope, 0), _ptr(v), _stride(v, 0), _stride(v, 1),
+                                         T, _ptr(out), _ptr(lse), _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_expanded_attention")
 
 
 def moe_get_device_error(ws, clear: bool = True, stream=None) -> int:

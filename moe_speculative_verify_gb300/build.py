@@ -19,9 +19,10 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libmoe_verify.so")
 SOURCES = ["abi.cu", "router.cu", "union.cu", "ffn.cu", "ffn16.cu", "combine.cu", "noalloc.cu",
            "verify.cu", "tile.cu", "attn_abi.cu", "rope.cu", "attn.cu",
-           "attn_tile.cu", "keyw.cu", "evict.cu"]
+           "attn_tile.cu", "keyw.cu", "evict.cu", "latent_abi.cu", "latent_rows.cu", "latent_attn.cu",
+           "expanded.cu"]
 HEADERS = ["common.cuh", "kernels.h", "layout.h", "select.cuh", "host.h", "attn.h", "attn.cuh",
-           "attn_mma.cuh", "tmem16.cuh"]
+           "attn_mma.cuh", "tmem16.cuh", "latent.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -1,0 +1,88 @@
+// latent.h -- arguments, workspace layout and launch entry points of the
+// operators over a latent cache (latent_rows.cu, latent_attn.cu) and of the
+// expanded form's attention (expanded.cu), used by their host ABI
+// (latent_abi.cu).
+#pragma once
+
+#include "attn.h"
+
+namespace moe {
+
+constexpr int kLatentRot = MOE_LATENT_ROPE_DIM;   // 64: the rotary part of a row
+
+// The latent cache as the kernels see it (strides in elements).
+struct LatentArgs {
+    uint8_t* latent;
+    uint16_t* rope;
+    int64_t lat_page, lat_token, rope_page, rope_token;
+    int32_t e4m3, scale_log2;
+    int32_t n_pages, page, page_log2, dim;
+};
+
+// 2^e, exactly, for the exponents that a cache may have and their opposites.
+#ifdef __CUDACC__
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+#endif
+
+struct LatentAppendArgs {
+    LatentArgs c;
+    SeqArgs sq;
+    const float* freqs;
+    int32_t interleaved;
+    float magnitude;
+    const float* gamma;      // NULL: no normalisation
+    float eps;
+    const uint16_t* kv;
+    int64_t kv_stride;
+    const uint16_t* q;
+    int64_t q_token, q_head;
+    uint16_t* q_out;
+    int64_t out_token, out_head;
+    const int32_t* pos;
+    int32_t q_heads;
+    int32_t* err;            // may be NULL
+};
+
+struct LatentGatherArgs {
+    LatentArgs c;
+    SeqArgs sq;              // cu_q unused
+    const int32_t* cu_k;
+    int32_t rows;
+    uint16_t* out;
+    int64_t out_stride;
+    int32_t* err;
+};
+
+// Workspace of absorbed attention: as that of the other attention calls
+// (attn.h), a slot for the pieces of kLatentRows rows of `dim` elements.
+constexpr int kLatentRows = 128;
+
+inline int64_t latent_workspace_bytes(int dim) {
+    return kAttnPartials + int64_t(2) * kAttnMaxCtas * kLatentRows * (dim + 2) * 4;
+}
+
+// Absorbed attention: `a` with one kv head of the latent's width and its rows the
+// query heads of a token; q has the latent part and the rotary one side by side.
+struct LatentAttnArgs {
+    AttnArgs a;
+    LatentArgs c;
+};
+
+// Expanded attention: `a` with a kv head of its own for every query head, and
+// pages of one token, so that lengths are cut to the n_keys rows there are.
+struct ExpandedArgs {
+    AttnArgs a;
+    const int32_t* cu_k;
+    int32_t n_keys, dim;     // dim: a head's own part of q and k, and v
+    const uint16_t* k;
+    const uint16_t* rope;
+    const uint16_t* v;
+    int64_t k_token, k_head, rope_token, v_token, v_head;
+};
+
+cudaError_t launch_latent_append(const LatentAppendArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_latent_gather(const LatentGatherArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_latent_attn(const LatentAttnArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_expanded(const ExpandedArgs& a, int n_sms, cudaStream_t s);
+
+}  // namespace moe
