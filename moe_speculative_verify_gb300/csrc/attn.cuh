@@ -332,10 +332,13 @@ struct Plan {
     }
 };
 
-// All threads of the block.  s_warp: one int64 per warp, s_plan: shared.
+// All threads of the block.  s_warp: one int64 per warp, s_plan: shared.  The
+// block is worker c of `workers` (a CTA, or one CTA of a pair that works as one, of
+// which one clears the note).
 template <int MT, int KT>
 __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int64_t* s_warp,
-                                          Plan* s_plan) {
+                                          Plan* s_plan, int c = blockIdx.x, int workers = gridDim.x,
+                                          bool notes = true) {
     using W = Work<MT, KT>;
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
     const int per = (a.sq.n + nt - 1) / nt;
@@ -378,8 +381,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int6
         total += v;
     }
     const int64_t want = div64(total + min_units - 1, min_units);
-    const int C = static_cast<int>(want < int64_t(gridDim.x) ? (want > 0 ? want : 1) : gridDim.x);
-    const int c = blockIdx.x;
+    const int C = static_cast<int>(want < int64_t(workers) ? (want > 0 ? want : 1) : workers);
     const int64_t share = div64(total, C), extra = total - share * C;
     const int64_t u0 = c < C ? c * share + min(int64_t(c), extra) : total;
     const int64_t u1 = c < C ? u0 + share + (c < extra ? 1 : 0) : total;
@@ -390,7 +392,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, int min_units, int6
         s_plan->extra = extra;
         s_plan->ctas = C;
         s_plan->seqs = seqs;
-        a.notes[c].pieces = 0;
+        if (notes) a.notes[c].pieces = 0;
     }
     const int64_t pre = before + incl - mine;
     if (u0 < u1 && pre <= u0 && u0 < pre + mine) {
@@ -472,17 +474,18 @@ struct Walk {
     }
 };
 
-// One thread, for each item of the CTA: notes the split item that begins here.
-__device__ __forceinline__ void note_split(const AttnArgs& a, const Item& it, int rows, int mt, const Plan& p) {
+// One thread, for each item of worker c: notes the split item that begins here.
+__device__ __forceinline__ void note_split(const AttnArgs& a, const Item& it, int rows, int mt, const Plan& p,
+                                           int c = blockIdx.x) {
     if (it.t0 != 0 || it.t1 >= it.n) return;
     // the last item of the CTA's run, so its note is not written over
     SplitNote n;
-    n.pieces = p.owner(it.u + it.n - 1) - static_cast<int>(blockIdx.x) + 1;
+    n.pieces = p.owner(it.u + it.n - 1) - c + 1;
     n.rows = rows;
     n.row0 = it.rt * mt;
     n.q0 = it.s.q0;
     n.head = it.h;
-    a.notes[blockIdx.x] = n;
+    a.notes[c] = n;
 }
 
 // Zeroes the output rows that belong to no sequence: those before and after

@@ -53,13 +53,25 @@ struct LatentGatherArgs {
     int32_t* err;
 };
 
-// Workspace of absorbed attention: as that of the other attention calls
-// (attn.h), a slot for the pieces of kLatentRows rows of `dim` elements.
-constexpr int kLatentRows = 128;
+// Workspace of absorbed attention: the control block, one note per pair of CTAs
+// (attn.h), then the pieces of split items, two slots a pair as there.  A slot has
+// kLatentRows rows, fp32: sums [dim/4][row][4], then (reference in log2 units, sum
+// of powers) [row][2].
+constexpr int kLatentRows = 128;        // rows of an item
+constexpr int kLatentKeys = 128;        // keys of a tile
+constexpr int kLatentMaxPairs = kAttnMaxCtas / 2;
 
 inline int64_t latent_workspace_bytes(int dim) {
-    return kAttnPartials + int64_t(2) * kAttnMaxCtas * kLatentRows * (dim + 2) * 4;
+    return kAttnPartials + int64_t(2) * kLatentMaxPairs * kLatentRows * (dim + 2) * 4;
 }
+
+// Tensor maps of the cache: latent as a 4-D tensor (64 elements or 128 codes of a
+// row, token, such part of the row, page) in boxes of min(page, 64) tokens, as
+// many parts as one box may have (bf16 pages of 64 tokens and more: two); the
+// rotary key as a 3-D one (element, token, page).  128-byte swizzled.
+struct LatentMaps {
+    CUtensorMap latent, rope;
+};
 
 // Absorbed attention: `a` with one kv head of the latent's width and its rows the
 // query heads of a token; q has the latent part and the rotary one side by side.
@@ -82,7 +94,7 @@ struct ExpandedArgs {
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_latent_gather(const LatentGatherArgs& a, int n_sms, cudaStream_t s);
-cudaError_t launch_latent_attn(const LatentAttnArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_latent_attn(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cudaStream_t s);
 cudaError_t launch_expanded(const ExpandedArgs& a, int n_sms, cudaStream_t s);
 
 }  // namespace moe
