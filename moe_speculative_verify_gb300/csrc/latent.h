@@ -58,19 +58,20 @@ struct LatentGatherArgs {
 // kLatentRows rows, fp32: sums [dim/4][row][4], then (reference in log2 units, sum
 // of powers) [row][2].
 constexpr int kLatentRows = 128;        // rows of an item
-constexpr int kLatentKeys = 128;        // keys of a tile
+constexpr int kLatentKeys = 64;         // keys of a tile
 constexpr int kLatentMaxPairs = kAttnMaxCtas / 2;
 
 inline int64_t latent_workspace_bytes(int dim) {
     return kAttnPartials + int64_t(2) * kLatentMaxPairs * kLatentRows * (dim + 2) * 4;
 }
 
-// Tensor maps of the cache: latent as a 4-D tensor (64 elements or 128 codes of a
-// row, token, such part of the row, page) in boxes of min(page, 64) tokens, as
-// many parts as one box may have (bf16 pages of 64 tokens and more: two); the
-// rotary key as a 3-D one (element, token, page).  128-byte swizzled.
+// Tensor maps of the cache: the latent as a 4-D tensor (64 elements or 128 codes of a
+// row, token, such part of the row, page), keys in boxes of min(page, 32) tokens
+// and values of min(page, 64), of one part, or where that is the whole box of a bf16
+// tile all of a row's, or half of it; the rotary key as a 3-D one (element, token,
+// page) in boxes as the keys'.  128-byte swizzled.
 struct LatentMaps {
-    CUtensorMap latent, rope;
+    CUtensorMap keys, values, rope;
 };
 
 // Absorbed attention: `a` with one kv head of the latent's width and its rows the

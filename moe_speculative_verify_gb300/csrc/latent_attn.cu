@@ -5,20 +5,20 @@
 // sum_j p_j c_j / sum_j p_j: a cached row is key and value of every head, so a
 // row of C + 64 elements takes 2 (2 C + 64) operations a query row.  An item is up to
 // 128 query rows (tokens times heads) of one sequence, worked on by a cluster
-// of two CTAs, 64 rows each, over tiles of 128 keys:
-//   S = Q K^T     one tcgen05.mma of the pair, M = N = 128: each CTA holds its rows
-//                 of Q and 64 of the keys, all C + 64 elements;
-//   softmax       a warpgroup a CTA; tensor memory has a row's keys 0 .. 63 in lane
-//                 r and 64 .. 127 in lane 64 + r;
-//   O += P V      M = 128, N = 256: each CTA holds its rows of P, all 128 keys'
+// of two CTAs, 64 rows each, over tiles of 64 keys:
+//   S = Q K^T     one tcgen05.mma of the pair, M = 128, N = 64: each CTA holds its
+//                 rows of Q and 32 of the keys, all C + 64 elements;
+//   softmax       a warpgroup a CTA; tensor memory has a row's keys 0 .. 31 in lane
+//                 r and 32 .. 63 in lane 64 + r;
+//   O += P V      M = 128, N = 256: each CTA holds its rows of P, all 64 keys'
 //                 elements of its half of C, and its rows of all of O.
 // Why pairs: O of 128 rows would fill an SM's tensor memory and Q its shared
 // memory; a single SM with 64 rows runs its matrix instructions at less than
-// half rate (measured, 64 rows by 64 keys by 16: 61 clocks), while the pair's
-// 128 x 128 x 16 takes the ideal 32 and 128 x 256 x 16 64.  The price is that keys
-// are held twice, once by key and once by element: 17 panels of 64 x 64 an SM for a
-// tile's 9.  They are copied by group and given back by group, so that a group's
-// copy has a tile's time to land.
+// half rate (measured, 64 rows by 64 keys by 16: 61 clocks, by 256: 147), while the pair's
+// 128 x 64 x 16 takes 25 and 128 x 256 x 16 the ideal 64.  The price is that a key is
+// held twice, whole in one CTA and by halves in both, and copied for each from L2.
+// (The halves copied from shared memory to shared memory instead: such copies run at
+// some 14 bytes a clock, 60 clocks a key.)
 //
 // A row's sums use a reference that follows the running maximum only when that has
 // grown by more than 2^kLag (see attn_tile.cu).  e4m3 rows are turned to bf16 in
@@ -32,27 +32,30 @@ namespace moe {
 namespace {
 
 constexpr int kMT = kLatentRows, kKT = kLatentKeys;
-constexpr int kHalf = 64;                // rows and keys of a CTA
-constexpr int kPanel = kHalf * 128;      // 64 rows of 64 bf16 elements
+constexpr int kRows = 64;                // rows of a CTA
+constexpr int kKeys = kKT / 2;           // whole keys of a CTA
+constexpr int kRowPanel = kRows * 128;   // 64 elements of its rows (Q, P)
+constexpr int kKeyPanel = kKeys * 128;   // and of its keys
+constexpr int kTilePanel = kKT * 128;    // and of a tile's
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 128;          // S of tile g at column 64 (g & 1), O behind
+constexpr uint32_t kColO = 64;           // S of tile g at column 32 (g & 1), O behind
 constexpr float kLag = 8.0f;             // log2 of what powers may grow to
-// 4 softmax warps; copies of K, of V, MMA, a warp that passes K on; 4 warps that
-// pass V on; e4m3: 4 warps that convert K, 4 that convert V
+// 4 softmax warps; copies of keys, MMA, copies of values, one that passes keys on; 4
+// that pass values on; e4m3: 4 that convert keys and pass them on
 template <bool E4M3>
 constexpr int kThreads = E4M3 ? 512 : 384;
 constexpr int kBarSoft = 1, kBarV = 2, kBarK = 3;                // named barriers, 128 threads each
 
 template <int C>
 struct Cfg {
-    static constexpr int kGroups = C / 128;                      // of two panels of K, beside the rotary one
-    static constexpr int kVPanels = C / 128;                     // of a CTA's half of C, for 64 keys
+    static constexpr int kParts = C / 128;                       // of two panels each: of a key, beside the rotary one
+    static constexpr int kVPanels = C / 128;                     // of a CTA's half of C
     static constexpr int kNV = C / 256;                          // MMAs of P V a step
-    static constexpr int kQBytes = (C / 64 + 1) * kPanel;
-    static constexpr int kPBytes = 2 * kPanel;
-    static constexpr int kKBytes = kQBytes;
-    static constexpr int kVBytes = 2 * kVPanels * kPanel;
-    static constexpr size_t kSmem = kQBytes + kPBytes + kKBytes + kVBytes;   // then Shared
+    static constexpr int kQBytes = (C / 64 + 1) * kRowPanel;
+    static constexpr int kPBytes = kRowPanel;
+    static constexpr int kKBytes = (C / 64 + 1) * kKeyPanel;
+    static constexpr int kVBytes = kVPanels * kTilePanel;
+    static constexpr size_t kSmem = kQBytes + 2 * (kPBytes + kKBytes + kVBytes);   // then Shared
 };
 
 // A role's place in the pair's work, in shared memory; THREADS threads share it, at
@@ -96,18 +99,19 @@ struct Ctx {
     __device__ __forceinline__ int key0(int tile) const { return (it.tile0 + it.t0 + tile) * kKT; }
 };
 
+// Barriers of the two stages of K, V, S and P, a tile each in turn.
 struct Shared {
-    float top[2][2][kHalf];                 // a row's maximum by half of a tile's keys, two tiles in turn
-    float sum[2][kHalf];
+    float top[2][2][kRows];                 // a row's maximum by half of a tile's keys, two tiles in turn
+    float sum[2][kRows];
     int64_t scan[16];                       // plan_work's
-    // of this CTA: copies that landed, room that the pair's products gave back
-    uint64_t k_full[5], k_empty[5], v_full[2], v_empty[2];
+    // of this CTA: what landed, and the room that the products gave back
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     // of the pair, in its first CTA: operands in place in both
-    uint64_t k_ready[5], v_ready[2], p_ready, q_ready;
+    uint64_t k_ready[2], v_ready[2], p_ready[2], q_ready;
     // of this CTA: the pair's products are done
-    uint64_t s_full[2], pv_done, done;
+    uint64_t s_full[2], pv_done[2], done;
     Plan plan;
-    Ctx ctx[6];                             // softmax, copies of K and V, MMA, K and V passed on
+    Ctx ctx[6];                             // softmax, copies of keys, MMA, keys and values passed on, copies of values
     uint32_t tmem;
 };
 
@@ -177,134 +181,76 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 }
 
 // ----------------------------------------------------------------- copies ----
-// The boxes of 64 keys from k0 on: lane p has the p-th, of `tokens` keys.
-struct Boxes {
-    int tokens, n, bytes;    // bytes: of those of the 64 keys' boxes that are read, for one panel
-    bool mine;
-    int page, slot;
-
-    __device__ __forceinline__ void set(const LatentArgs& c, const AttnArgs& a, const Item& it, int k0) {
-        tokens = min(c.page, kHalf);
-        n = kHalf / tokens;
-        const int lane = threadIdx.x & 31, k = k0 + lane * tokens;
-        mine = lane < n && k < it.hi && k + tokens > it.lo;
-        slot = k & (c.page - 1);
-        page = 0;
-        if (mine) page = a.sq.table[int64_t(it.b) * a.sq.max_pages + (k >> c.page_log2)];
-        if (page < 0 || page >= c.n_pages) {
-            record_error(a.err, MOE_ERR_INVALID_ARG);
-            page = c.n_pages;                                    // out of range: reads as zeros
-        }
-        bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * tokens * 128;
-    }
-};
-
-// Copies `panels` (bf16) or panels / 2 parts of codes (e4m3: into the second of each two
-// panels, see convert_row) of the boxes' rows, from panel p0 on.
-template <bool E4M3>
-__device__ __forceinline__ void copy_panels(const Boxes& b, const LatentMaps& maps, uint8_t* dst, int p0, int panels, uint64_t* full) {
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) mbar_arrive_expect_tx(full, b.bytes * (E4M3 ? panels / 2 : panels));
-    __syncwarp();
-    if (b.mine) {
-        uint8_t* at = dst + lane * b.tokens * 128;
-        if constexpr (E4M3) {
-            for (int x = 0; x < panels; x += 2) tma_load_4d(at + (x + 1) * kPanel, &maps.latent, full, 0, b.slot, (p0 + x) / 2, b.page);
-        } else {
-            const int step = b.tokens == kHalf ? 2 : 1;
-            for (int x = 0; x < panels; x += step) tma_load_4d(at + x * kPanel, &maps.latent, full, 0, b.slot, p0 + x, b.page);
-        }
-    }
-    __syncwarp();
-}
-
-// This CTA's 64 keys of each tile, all elements: the rotary part, then the groups.
-template <int C, bool E4M3>
-__device__ __forceinline__ void produce_k(const LatentAttnArgs& la, const LatentMaps& maps, Shared& sh, uint8_t* ks, uint32_t rank) {
+// The two warps that copy from memory: keys (this CTA's 32 of each tile, all elements
+// and the rotary part) and values (all 64 keys, this CTA's half of the elements).  A
+// box a page (for small pages and for codes, a box a page and panel), each page by a
+// lane of its own.
+template <int C, bool E4M3, bool V>
+__device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMaps& maps, Shared& sh, uint8_t* ring, uint32_t rank) {
     using F = Cfg<C>;
+    constexpr int kN = V ? kKT : kKeys, kPanel = V ? kTilePanel : kKeyPanel, kPanels = V ? F::kVPanels : C / 64;
     const AttnArgs& a = la.a;
-    Ctx& ctx = sh.ctx[1];
+    uint64_t* fulls = V ? sh.v_full : sh.k_full;
+    uint64_t* empties = V ? sh.v_empty : sh.k_empty;
+    const CUtensorMap* map = V ? &maps.values : &maps.keys;
+    const int lane = threadIdx.x & 31, p0 = V ? static_cast<int>(rank) * kPanels : 0;
+    const int tokens = min(la.c.page, kN), boxes = kN / tokens;
+    Ctx& ctx = sh.ctx[V ? 5 : 1];
     ctx.start<32>(a, sh.plan);
     int uses = 0;
-    uint32_t ph = 1u;
     bool dead = false;
     while (!dead && ctx.next<32>(a)) {
-        const int T = ctx.tiles;
-        for (int j = 0; j < T && !dead; ++j, ph ^= 1u) {
-            Boxes b;
-            b.set(la.c, a, ctx.it, ctx.key0(j) + static_cast<int>(rank) * kHalf);
-            for (int g = 0; g <= F::kGroups; ++g) {              // g = 0: the rotary part
-                dead = !warp_wait(&sh.k_empty[g], ph, a.err, a.timeout_ns);
-                if (dead) break;
-                if (g == 0) {
-                    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&sh.k_full[0], b.bytes);
-                    __syncwarp();
-                    if (b.mine)
-                        tma_load_3d(ks + (C / 64) * kPanel + (threadIdx.x & 31) * b.tokens * 128, &maps.rope, &sh.k_full[0], 0, b.slot, b.page);
-                    __syncwarp();
+        const Item& it = ctx.it;
+        const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
+        for (int j = 0; j < ctx.tiles; ++j, ++uses) {
+            const int k = ctx.key0(j) + (V ? 0 : static_cast<int>(rank) * kKeys) + lane * tokens, slot = k & (la.c.page - 1), st = uses & 1;
+            const bool mine = lane < boxes && k < it.hi && k + tokens > it.lo;
+            int page = mine ? table[k >> la.c.page_log2] : 0;
+            if (page < 0 || page >= la.c.n_pages) {
+                record_error(a.err, MOE_ERR_INVALID_ARG);
+                page = la.c.n_pages;                             // out of range: reads as zeros
+            }
+            const int rows = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * tokens;
+            dead = !warp_wait(&empties[st], ((uses >> 1) & 1) ^ 1, a.err, a.timeout_ns);
+            if (dead) break;
+            uint64_t* full = &fulls[st];
+            if (lane == 0) mbar_arrive_expect_tx(full, rows * (kPanels * (E4M3 ? 64 : 128) + (V ? 0 : 2 * kLatentRot)));
+            __syncwarp();
+            if (mine) {
+                uint8_t* at = ring + st * (V ? F::kVBytes : F::kKBytes) + lane * tokens * 128;
+                if (!V) tma_load_3d(at + kPanels * kPanel, &maps.rope, full, 0, slot, page);
+                if constexpr (E4M3) {                            // into the second of each two panels, see convert_row
+                    for (int x = 0; x < kPanels; x += 2) tma_load_4d(at + (x + 1) * kPanel, map, full, 0, slot, (p0 + x) / 2, page);
+                } else if (tokens == kN) {
+                    tma_load_4d(at, map, full, 0, slot, p0, page);
                 } else {
-                    copy_panels<E4M3>(b, maps, ks + (g - 1) * 2 * kPanel, (g - 1) * 2, 2, &sh.k_full[g]);
+                    for (int x = 0; x < kPanels; ++x) tma_load_4d(at + x * kPanel, map, full, 0, slot, p0 + x, page);
                 }
-                ++uses;
             }
+            __syncwarp();
         }
     }
-    // each group's last copy
-    for (int g = 0; g <= F::kGroups; ++g) {
-        const int n = (uses + F::kGroups - g) / (F::kGroups + 1);
-        if (n > 0) mbar_wait(&sh.k_full[g], (n - 1) & 1, a.err, kDrainNs);
-    }
-}
-
-// All 128 keys of each tile, this CTA's half of the elements: by half of the keys.
-template <int C, bool E4M3>
-__device__ __forceinline__ void produce_v(const LatentAttnArgs& la, const LatentMaps& maps, Shared& sh, uint8_t* vs, uint32_t rank) {
-    using F = Cfg<C>;
-    const AttnArgs& a = la.a;
-    Ctx& ctx = sh.ctx[2];
-    ctx.start<32>(a, sh.plan);
-    int uses = 0;
-    uint32_t ph = 1u;
-    bool dead = false;
-    while (!dead && ctx.next<32>(a)) {
-        const int T = ctx.tiles;
-        for (int j = 0; j < T && !dead; ++j, ph ^= 1u) {
-            for (int h = 0; h < 2; ++h) {
-                Boxes b;
-                b.set(la.c, a, ctx.it, ctx.key0(j) + h * kHalf);
-                dead = !warp_wait(&sh.v_empty[h], ph, a.err, a.timeout_ns);
-                if (dead) break;
-                copy_panels<E4M3>(b, maps, vs + h * F::kVPanels * kPanel, static_cast<int>(rank) * F::kVPanels, F::kVPanels, &sh.v_full[h]);
-                ++uses;
-            }
-        }
-    }
-    for (int h = 0; h < 2; ++h) {
-        const int n = (uses + 1 - h) / 2;
-        if (n > 0) mbar_wait(&sh.v_full[h], (n - 1) & 1, a.err, kDrainNs);
+    // each stage's last copy
+    for (int st = 0; st < 2; ++st) {
+        const int n = (uses + 1 - st) / 2;
+        if (n > 0) mbar_wait(&fulls[st], (n - 1) & 1, a.err, kDrainNs);
     }
 }
 
 // ------------------------------------------------------------ passing on ----
 // What landed in this CTA is told to the first one, whose MMA warp waits for both.
-// Values of keys that no row of the item sees may be anything: they are zeroed here,
-// as are, in tiles where some row does not see some key, those of a key with an
-// element that is not finite (its score is not finite for the rows that do see it, so
-// that they become NaN all the same; a probability of 0 would make the others NaN).
 template <int C>
 __device__ __forceinline__ void pass_k(const LatentAttnArgs& la, Shared& sh) {
     const AttnArgs& a = la.a;
-    Ctx& ctx = sh.ctx[4];
+    Ctx& ctx = sh.ctx[3];
     ctx.start<32>(a, sh.plan);
-    uint32_t ph = 0;
+    int n = 0;
     bool dead = false;
     while (!dead && ctx.next<32>(a)) {
-        for (int j = 0; j < ctx.tiles && !dead; ++j, ph ^= 1u) {
-            for (int g = 0; g <= Cfg<C>::kGroups; ++g) {
-                dead = !warp_wait(&sh.k_full[g], ph, a.err, a.timeout_ns);
-                if (dead) break;
-                if ((threadIdx.x & 31) == 0) arrive_first(&sh.k_ready[g]);
-            }
+        for (int j = 0; j < ctx.tiles; ++j, ++n) {
+            dead = !warp_wait(&sh.k_full[n & 1], (n >> 1) & 1, a.err, a.timeout_ns);
+            if (dead) break;
+            if ((threadIdx.x & 31) == 0) arrive_first(&sh.k_ready[n & 1]);
         }
     }
 }
@@ -317,45 +263,50 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& w) {
     return bad;
 }
 
+// Four warps.  Values of keys that no row of the item sees may be anything: they are
+// zeroed, as are, in tiles where some row does not see some key, those of a key with an
+// element that is not finite (its score is not finite for the rows that do see it,
+// which so become NaN all the same; a probability of 0 would make the others NaN).
 template <int C>
 __device__ __forceinline__ void pass_v(const LatentAttnArgs& la, Shared& sh, uint8_t* vs) {
     using F = Cfg<C>;
     const AttnArgs& a = la.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-    Ctx& ctx = sh.ctx[5];
+    Ctx& ctx = sh.ctx[4];
     ctx.start<128>(a, sh.plan);
-    uint32_t ph = 0;
+    int n = 0;
     bool dead = false;
     while (ctx.next<128>(a, kBarV)) {
-        for (int j = 0; j < ctx.tiles && !dead; ++j, ph ^= 1u) {
-            for (int h = 0; h < 2; ++h) {
-                dead = !warp_wait(&sh.v_full[h], ph, a.err, a.timeout_ns);
-                if (dead) break;
-                const int j0 = ctx.key0(j) + h * kHalf, lo = max(ctx.it.lo, ctx.wlo), hi = min(ctx.it.hi, ctx.whi);
-                if (j0 < lo || j0 + kHalf > hi) {
-                    // a key's elements, 16 bytes a lane
-                    uint8_t* v = vs + h * F::kVPanels * kPanel + (lane >> 3) * kPanel + (lane & 7) * 16;
-                    for (int r = warp; r < kHalf; r += 4) {
-                        uint4* p = reinterpret_cast<uint4*>(v + r * 128);
-                        bool bad = j0 + r < ctx.it.lo || j0 + r >= ctx.it.hi;
-                        if (lane < 8 * F::kVPanels) bad = bad || any_nonfinite(*p);
-                        if (__any_sync(0xFFFFFFFFu, bad) && lane < 8 * F::kVPanels) *p = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
+        for (int j = 0; j < ctx.tiles && !dead; ++j, ++n) {
+            const int st = n & 1;
+            dead = !warp_wait(&sh.v_full[st], (n >> 1) & 1, a.err, a.timeout_ns);
+            if (dead) break;
+            const int j0 = ctx.key0(j), lo = max(ctx.it.lo, ctx.wlo), hi = min(ctx.it.hi, ctx.whi);
+            if (j0 < lo || j0 + kKT > hi) {
+                // a key's elements, 16 bytes a lane
+                uint8_t* v = vs + st * F::kVBytes + (lane >> 3) * kTilePanel + (lane & 7) * 16;
+                for (int r = warp; r < kKT; r += 4) {
+                    uint4* p = reinterpret_cast<uint4*>(v + r * 128);
+                    bool bad = j0 + r < ctx.it.lo || j0 + r >= ctx.it.hi;
+                    if (lane < 8 * F::kVPanels) bad = bad || any_nonfinite(*p);
+                    if (__any_sync(0xFFFFFFFFu, bad) && lane < 8 * F::kVPanels) *p = make_uint4(0, 0, 0, 0);
                 }
-                if (lane == 0) arrive_first(&sh.v_ready[h]);
+                fence_async_smem();
+                __syncwarp();
             }
+            if (lane == 0) arrive_first(&sh.v_ready[st]);
         }
     }
 }
 
 // e4m3: 128 codes of a key, which landed in row r of the second of two panels, to
-// bf16 in row r of both, by one thread: all are read before any is written.
-__device__ __forceinline__ void convert_row(uint8_t* two, int r, uint32_t factor, bool nan_again, uint32_t nan_bits, bool zero,
-                                            bool zero_nan) {
+// bf16 in row r of both, by one thread: all are read before any is written.  A NaN
+// code comes out as `nan_bits`, which no other does; `zero` and, where it has NaN
+// codes, `zero_nan` make the row zeros (see pass_v).
+template <int PANEL>
+__device__ __forceinline__ void convert_row(uint8_t* two, int r, uint32_t factor, uint32_t nan_bits, bool zero, bool zero_nan) {
     uint8_t* first = two + r * 128;
-    uint8_t* second = first + kPanel;
+    uint8_t* second = first + PANEL;
     uint4 raw[8];
 #pragma unroll
     for (int ch = 0; ch < 8; ++ch) raw[ch] = *reinterpret_cast<const uint4*>(second + ((ch ^ (r & 7)) << 4));
@@ -366,7 +317,7 @@ __device__ __forceinline__ void convert_row(uint8_t* two, int r, uint32_t factor
         uint32_t y[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // as e4m3x4_to_bf16, with the row's power of two in the factor
+            // as e4m3x4_to_bf16, with the cache's power of two in the factor
             const uint32_t p = __byte_perm(x[e], 0, 0x1404), q = __byte_perm(x[e], 0, 0x3424);
             const uint32_t mp = (p >> 4) & 0x07F007F0u, mq = (q >> 4) & 0x07F007F0u;
             asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y[2 * e]) : "r"(mp | (p & 0x80008000u)), "r"(factor));
@@ -384,10 +335,10 @@ __device__ __forceinline__ void convert_row(uint8_t* two, int r, uint32_t factor
 #pragma unroll 1
         for (int ch = 0; ch < 16; ++ch)
             *reinterpret_cast<uint4*>((ch < 8 ? first : second) + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
-    } else if (had_nan && nan_again) {
+    } else if (had_nan) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i) {
-            uint32_t* w = reinterpret_cast<uint32_t*>((i < 32 ? first : second)) + (i & 31);
+            uint32_t* w = reinterpret_cast<uint32_t*>(i < 32 ? first : second) + (i & 31);
             uint32_t v = *w;
             if ((v & 0x7FFFu) == nan_bits) v |= 0x7FC0u;
             if ((v & 0x7FFF0000u) == nan_bits << 16) v |= 0x7FC00000u;
@@ -396,72 +347,41 @@ __device__ __forceinline__ void convert_row(uint8_t* two, int r, uint32_t factor
     }
 }
 
-// The factor of convert_row and what a NaN code comes out as: 480 times the scale.
-__device__ __forceinline__ uint32_t code_factor(int scale_log2) {
-    const uint32_t f = static_cast<uint32_t>(127 + 120 + scale_log2) << 7;
-    return f | (f << 16);
-}
-__device__ __forceinline__ uint32_t code_nan(int scale_log2) { return 0x43F0u + static_cast<uint32_t>(scale_log2 * 128); }
-
-// K: two warps a group, two groups at a time.
-template <int C>
-__device__ __forceinline__ void convert_k(const LatentAttnArgs& la, Shared& sh, uint8_t* ks) {
-    const AttnArgs& a = la.a;
-    const int lane = threadIdx.x & 31, t = threadIdx.x & 127, side = t >> 6;
-    const uint32_t factor = code_factor(la.c.scale_log2), nan_bits = code_nan(la.c.scale_log2);
-    Ctx& ctx = sh.ctx[4];
-    ctx.start<128>(a, sh.plan);
-    uint32_t ph = 0;
-    bool dead = false;
-    while (ctx.next<128>(a, kBarK)) {
-        for (int j = 0; j < ctx.tiles && !dead; ++j, ph ^= 1u) {
-            if (t < 32) {
-                dead = !warp_wait(&sh.k_full[0], ph, a.err, a.timeout_ns);
-                if (dead) break;
-                if (lane == 0) arrive_first(&sh.k_ready[0]);
-            }
-            for (int g = side; g < Cfg<C>::kGroups; g += 2) {
-                dead = !warp_wait(&sh.k_full[g + 1], ph, a.err, a.timeout_ns);
-                if (dead) break;
-                convert_row(ks + g * 2 * kPanel, t & 63, factor, true, nan_bits, false, false);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_first(&sh.k_ready[g + 1]);
-            }
-        }
-    }
-}
-
-// V: a thread a key and 128 elements.
-template <int C>
-__device__ __forceinline__ void convert_v(const LatentAttnArgs& la, Shared& sh, uint8_t* vs) {
+// e4m3: four warps each for keys and values, a thread a key and 128 codes.
+template <int C, bool V>
+__device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, uint8_t* ring) {
     using F = Cfg<C>;
+    constexpr int kN = V ? kKT : kKeys, kPanel = V ? kTilePanel : kKeyPanel, kUnits = V ? F::kVPanels / 2 : F::kParts;
+    static_assert(kN * kUnits <= 128, "a row's part a thread");
     const AttnArgs& a = la.a;
-    const int lane = threadIdx.x & 31, t = threadIdx.x & 127, r = t & 63, side = t >> 6;
-    const uint32_t factor = code_factor(la.c.scale_log2), nan_bits = code_nan(la.c.scale_log2);
-    Ctx& ctx = sh.ctx[5];
+    const int lane = threadIdx.x & 31, t = threadIdx.x & 127, r = t % kN, part = t / kN;
+    // 2^120 times the cache's power of two (see e4m3x4_to_bf16), and 480 times it
+    const uint32_t f = static_cast<uint32_t>(127 + 120 + la.c.scale_log2) << 7, factor = f | (f << 16);
+    const uint32_t nan_bits = 0x43F0u + static_cast<uint32_t>(la.c.scale_log2 * 128);
+    Ctx& ctx = sh.ctx[V ? 4 : 3];
     ctx.start<128>(a, sh.plan);
-    uint32_t ph = 0;
+    int n = 0;
     bool dead = false;
-    while (ctx.next<128>(a, kBarV)) {
-        for (int j = 0; j < ctx.tiles && !dead; ++j, ph ^= 1u) {
-            for (int h = 0; h < 2; ++h) {
-                dead = !warp_wait(&sh.v_full[h], ph, a.err, a.timeout_ns);
-                if (dead) break;
-                const int j0 = ctx.key0(j) + h * kHalf, key = j0 + r;
-                const bool part = j0 < ctx.wlo || j0 + kHalf > ctx.whi;
-                if (2 * side < F::kVPanels)
-                    convert_row(vs + (h * F::kVPanels + 2 * side) * kPanel, r, factor, true, nan_bits,
-                                key < ctx.it.lo || key >= ctx.it.hi, part);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_first(&sh.v_ready[h]);
+    while (ctx.next<128>(a, V ? kBarV : kBarK)) {
+        for (int j = 0; j < ctx.tiles && !dead; ++j, ++n) {
+            const int st = n & 1;
+            dead = !warp_wait(V ? &sh.v_full[st] : &sh.k_full[st], (n >> 1) & 1, a.err, a.timeout_ns);
+            if (dead) break;
+            if (part < kUnits) {
+                const int j0 = ctx.key0(j), key = j0 + r;
+                convert_row<kPanel>(ring + st * (V ? F::kVBytes : F::kKBytes) + part * 2 * kPanel, r, factor, nan_bits,
+                                    V && (key < ctx.it.lo || key >= ctx.it.hi), V && (j0 < ctx.wlo || j0 + kKT > ctx.whi));
             }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_first(V ? &sh.v_ready[st] : &sh.k_ready[st]);
         }
     }
 }
 
 // --------------------------------------------------------------- products ----
+// The MMA warp of the first CTA: Q K^T of a tile, then P V of the one before, so
+// that one tile's softmax runs beside another's products.
 // The MMA warp of the first CTA: Q K^T of a tile, then P V of the one before, so
 // that one tile's softmax runs beside another's products.
 template <int C>
@@ -471,10 +391,10 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
     const AttnArgs& a = la.a;
     const uint32_t colS = sh.tmem, colO = sh.tmem + kColO;
     const uint64_t qd = sdesc(smem_u32(qs), 16, 1024), pd = sdesc(smem_u32(ps), 16, 1024);
-    const uint64_t kd = sdesc(smem_u32(ks), 16, 1024), vd = sdesc(smem_u32(vs), kPanel, 1024);
-    Ctx& ctx = sh.ctx[3];
+    const uint64_t kd = sdesc(smem_u32(ks), 16, 1024), vd = sdesc(smem_u32(vs), kTilePanel, 1024);
+    Ctx& ctx = sh.ctx[2];
     ctx.start<32>(a, sh.plan);
-    uint32_t qp = 0, pp = 0, kp = 0, vp = 0, g = 0;              // phases; tiles so far
+    uint32_t qp = 0, g = 0;                                      // phase of q_ready; tiles begun
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead) dead = !__all_sync(0xFFFFFFFFu, pair_wait(bar, parity, a.err, a.timeout_ns));
@@ -486,50 +406,42 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
         qp ^= 1u;
         for (int i = 0; i <= T && !dead; ++i) {
             if (i < T) {
-#pragma unroll 1
-                for (int x = 0; x <= F::kGroups; ++x) {
-                    wait(&sh.k_ready[x], kp);
-                    if (dead) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const int p0 = x == 0 ? C / 64 : 2 * (x - 1), n = x == 0 ? 4 : 8;
+                const uint32_t st = g & 1u;
+                wait(&sh.k_ready[st], (g >> 1) & 1u);
+                if (dead) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t kk = kd + (st * F::kKBytes >> 4);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            if (k >= n) break;
-                            const uint32_t off = ((p0 + (k >> 2)) * kPanel + (k & 3) * 32) >> 4;
-                            pair_mma(colS + 64 * (g & 1u), qd + off, kd + off, kIdQK, x > 0 || k > 0);
-                        }
-                        pair_commit(&sh.k_empty[x]);
-                        if (x == F::kGroups) pair_commit(&sh.s_full[g & 1u]);
-                    }
-                    __syncwarp();
+                    for (int x = 0; x <= C / 64; ++x)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            pair_mma(colS + 32 * st, qd + ((x * kRowPanel + k * 32) >> 4), kk + ((x * kKeyPanel + k * 32) >> 4), kIdQK,
+                                     x > 0 || k > 0);
+                    pair_commit(&sh.s_full[st]);
+                    pair_commit(&sh.k_empty[st]);
                 }
-                kp ^= 1u;
+                __syncwarp();
                 ++g;
             }
-            if (i > 0 && !dead) {
-                wait(&sh.p_ready, pp);
-                pp ^= 1u;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    wait(&sh.v_ready[h], vp);
-                    if (dead) break;
-                    tc_fence_after();
-                    if (elect_one()) {
+            if (i > 0) {
+                const uint32_t v = g - (i < T ? 2u : 1u), st = v & 1u, ph = (v >> 1) & 1u;
+                wait(&sh.v_ready[st], ph);
+                wait(&sh.p_ready[st], ph);
+                if (dead) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t pp = pd + (st * F::kPBytes >> 4), vv = vd + (st * F::kVBytes >> 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                            for (int n = 0; n < F::kNV; ++n)
-                                pair_mma(colO + 128 * n, pd + ((h * kPanel + k * 32) >> 4),
-                                         vd + (((h * F::kVPanels + 2 * n) * kPanel + k * 2048) >> 4), kIdPV,
-                                         i > 1 || h > 0 || k > 0);
-                        }
-                        pair_commit(&sh.v_empty[h]);
-                        if (h == 1) pair_commit(&sh.pv_done);
-                    }
-                    __syncwarp();
+                        for (int n = 0; n < F::kNV; ++n)
+                            pair_mma(colO + 128 * n, pp + (k * 32 >> 4), vv + ((2 * n * kTilePanel + k * 2048) >> 4), kIdPV,
+                                     i > 1 || k > 0);
+                    pair_commit(&sh.v_empty[st]);
+                    pair_commit(&sh.pv_done[st]);
                 }
-                vp ^= 1u;
+                __syncwarp();
             }
         }
     }
@@ -556,7 +468,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
     constexpr int kChunks = (C + kLatentRot) / 8, kBatch = 9;
     const uint32_t flip = negate ? 0x80008000u : 0u;
 #pragma unroll 1
-    for (int e0 = 0; e0 < kHalf * kChunks; e0 += 128 * kBatch) {
+    for (int e0 = 0; e0 < kRows * kChunks; e0 += 128 * kBatch) {
         uint4 w[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -571,7 +483,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int e = e0 + 128 * k + static_cast<int>(threadIdx.x), r = e / kChunks, ch = e - r * kChunks;
-            if (r < kHalf) *reinterpret_cast<uint4*>(qs + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[k];
+            if (r < kRows) *reinterpret_cast<uint4*>(qs + (ch >> 3) * kRowPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[k];
         }
     }
     fence_async_smem();
@@ -584,22 +496,19 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
     const int tid = threadIdx.x, lr = tid & 63, half = tid >> 6, lane = tid & 31;
     const uint32_t tm = sh.tmem + (static_cast<uint32_t>(tid & 96) << 16);
     const uint32_t colO = tm + kColO;
-    uint8_t* p_row = ps + half * kPanel + lr * 128;
+    uint8_t* p_row = ps + lr * 128;
     const bool draft = a.draft != nullptr;
     Ctx& ctx = sh.ctx[0];
     ctx.start<128>(a, sh.plan);
     const Item& it = ctx.it;
-    uint32_t g = 0, pv = 0;                                      // tiles so far; phase of pv_done
-    bool pending = false, dead = false;                          // a P V that has not been waited for
+    uint32_t g = 0, waited = 0;                                  // tiles so far; products P V waited for
+    bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
         tc_fence_after();
     };
-    auto wait_pv = [&]() {
-        if (!pending) return;
-        wait(&sh.pv_done, pv);
-        pv ^= 1u;
-        pending = false;
+    auto wait_pv = [&](uint32_t upto) {                          // the first `upto` of them (at most two are under way)
+        for (; waited < upto; ++waited) wait(&sh.pv_done[waited & 1u], (waited >> 1) & 1u);
     };
     // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf), or NaN; the sign goes to the queries
     const float cs = a.scale * kLog2e;
@@ -620,26 +529,20 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
         for (int j = 0; j < T; ++j, ++g) {
             const int j0 = ctx.key0(j);
             wait(&sh.s_full[g & 1u], (g >> 1) & 1u);
-            float x[2][32];
-            tmem_ld32(tm + 64 * (g & 1u), x[0]);
-            tmem_ld32(tm + 64 * (g & 1u) + 32, x[1]);
+            float x[32];
+            tmem_ld32(tm + 32 * (g & 1u), x);
             tmem_wait_ld();
             if (j0 < ctx.wlo || j0 + kKT > ctx.whi) {
+                const uint32_t bits = row_bits(view, draft, it.s.first, j0 + half * kKeys);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t bits = row_bits(view, draft, it.s.first, j0 + half * kHalf + 32 * q);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((bits >> e) & 1u)) x[q][e] = kNegInf;
-                }
+                for (int e = 0; e < 32; ++e)
+                    if (!((bits >> e) & 1u)) x[e] = kNegInf;
             }
             float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int e = 0; e < 32; e += 4)
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[q][e + k]);
+                for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[e + k]);
             float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             sh.top[g & 1u][half][lr] = top;
             named_bar(kBarSoft, 128);
@@ -647,7 +550,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
             if (!(top > kNegInf)) top = kNegInf;                 // (NaN: the sums carry it)
             const bool grow = top > ref + kLag || (ref == kNegInf && top > kNegInf);
             if (j > 0 && __any_sync(0xFFFFFFFFu, grow)) {
-                wait_pv();
+                wait_pv(g);
                 const float f = !grow ? 1.0f : (ref == kNegInf ? 0.0f : fast_exp2(ref - top));
                 sum0 *= f;
                 sum1 *= f;
@@ -665,28 +568,25 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
             }
             if (grow) ref = top;
             const float off = ref == kNegInf ? 0.0f : -ref;
-            uint32_t u[32];
+            uint32_t u[16];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int e = 0; e < 32; e += 2) {
+                float p0, p1;
+                fma2_to(p0, p1, x[e], x[e + 1], c, off);
+                p0 = fast_exp2(p0);
+                p1 = fast_exp2(p1);
+                add2(sum0, sum1, p0, p1);
+                u[e / 2] = pack_bf16(p0, p1);
+            }
+            if (g >= 2) wait_pv(g - 1);                          // P's room has been read
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float p0, p1;
-                    fma2_to(p0, p1, x[q][e], x[q][e + 1], c, off);
-                    p0 = fast_exp2(p0);
-                    p1 = fast_exp2(p1);
-                    add2(sum0, sum1, p0, p1);
-                    u[16 * q + e / 2] = pack_bf16(p0, p1);
-                }
-            wait_pv();                                           // P's room has been read
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-                *reinterpret_cast<uint4*>(p_row + ((ch ^ (lr & 7)) << 4)) =
+            for (int ch = 0; ch < 4; ++ch)
+                *reinterpret_cast<uint4*>(p_row + (g & 1u) * F::kPBytes + (((4 * half + ch) ^ (lr & 7)) << 4)) =
                     make_uint4(u[4 * ch], u[4 * ch + 1], u[4 * ch + 2], u[4 * ch + 3]);
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_first(&sh.p_ready);
-            pending = true;
+            if (lane == 0) arrive_first(&sh.p_ready[g & 1u]);
         }
         // --- the item's rows: normalised, or this pair's piece of them
         sh.sum[half][lr] = sum0 + sum1;
@@ -703,7 +603,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
             else if (a.lse)
                 a.lse[at] = ref == kNegInf ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
-        wait_pv();
+        wait_pv(g);
         if (__any_sync(0xFFFFFFFFu, valid)) {
 #pragma unroll 1
             for (int q = 0; q < F::kNV * 8; ++q) {
@@ -741,30 +641,29 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     extern __shared__ __align__(1024) uint8_t dyn[];
     uint8_t* qs = dyn;
     uint8_t* ps = qs + F::kQBytes;
-    uint8_t* ks = ps + F::kPBytes;
-    uint8_t* vs = ks + F::kKBytes;
+    uint8_t* ks = ps + 2 * F::kPBytes;
+    uint8_t* vs = ks + 2 * F::kKBytes;
     Shared& sh = *reinterpret_cast<Shared*>(dyn + F::kSmem);
     const AttnArgs& a = la.a;
     const int warp = threadIdx.x >> 5, pair = blockIdx.x >> 1;
     const uint32_t rank = cta_rank();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 5; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.k_empty[i], 1);
-            mbar_init(&sh.k_ready[i], E4M3 && i > 0 ? 4 : 2);    // both CTAs: the passing warp, or the group's two that convert
-        }
-        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.k_ready[i], E4M3 ? 8 : 2);             // both CTAs' passing warps
             mbar_init(&sh.v_full[i], 1);
             mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.v_ready[i], 8);
             mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_ready[i], 8);
+            mbar_init(&sh.pv_done[i], 1);
         }
-        mbar_init(&sh.p_ready, 8);
         mbar_init(&sh.q_ready, 8);
-        mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.done, 1);
         fence_barrier_init();
-        prefetch_tensormap(&maps.latent);
+        prefetch_tensormap(&maps.keys);
+        prefetch_tensormap(&maps.values);
         prefetch_tensormap(&maps.rope);
     }
     if (warp == 6) pair_alloc(&sh.tmem);
@@ -779,17 +678,17 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     if (warp < 4)
         soften<C>(la, sh, qs, ps, pair, rank);
     else if (warp == 4)
-        produce_k<C, E4M3>(la, maps, sh, ks, rank);
-    else if (warp == 5)
-        produce_v<C, E4M3>(la, maps, sh, vs, rank);
-    else if (warp == 6) {
+        produce<C, E4M3, false>(la, maps, sh, ks, rank);
+    else if (warp == 5) {
         if (rank == 0) multiply<C>(la, sh, qs, ps, ks, vs);
-    } else if (warp >= 8) {
+    } else if (warp == 6)
+        produce<C, E4M3, true>(la, maps, sh, vs, rank);
+    else if (warp >= 8) {
         if constexpr (E4M3) {
             if (warp < 12)
-                convert_k<C>(la, sh, ks);
+                convert<C, true>(la, sh, vs);
             else
-                convert_v<C>(la, sh, vs);
+                convert<C, false>(la, sh, ks);
         } else {
             pass_v<C>(la, sh, vs);
         }
