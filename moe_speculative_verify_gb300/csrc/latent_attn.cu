@@ -126,31 +126,15 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Arrives on the barrier at this address of the pair's first CTA.
+// Arrives on the barrier at this address of the pair's first CTA.  What was written
+// before lies in this CTA's shared memory and is read by its own tensor core, so the
+// CTA's order does; a release to the cluster would wait for memory (1000 to 2500
+// clocks, a third of a tile's time).
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+        "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
-}
-
-// mbar_wait for arrivals of either CTA.
-__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, int32_t* err, uint64_t timeout_ns) {
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 0; it < (1u << 30); ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if ((it & 63u) == 63u && globaltimer_ns() - t0 > timeout_ns) break;
-    }
-    record_error(err, MOE_ERR_TIMEOUT);
-    return false;
 }
 
 __device__ __forceinline__ void pair_alloc(uint32_t* dst) {
@@ -397,7 +381,7 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
     uint32_t qp = 0, g = 0;                                      // phase of q_ready; tiles begun
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead) dead = !__all_sync(0xFFFFFFFFu, pair_wait(bar, parity, a.err, a.timeout_ns));
+        if (!dead) dead = !warp_wait(bar, parity, a.err, a.timeout_ns);
     };
     while (!dead && ctx.next<32>(a)) {
         const int T = ctx.tiles;
