@@ -75,9 +75,20 @@ struct Ctx {
         else
             named_bar(bar, THREADS);
     }
+    // wk.start with the first sequence as it was loaded once for all roles
     template <int THREADS>
-    __device__ __forceinline__ void start(const AttnArgs& a, const Plan& p) {
-        if (threadIdx.x % THREADS == 0) wk.start(a, p);
+    __device__ __forceinline__ void start(const AttnArgs& a, const Plan& p, const Seq& first) {
+        if (threadIdx.x % THREADS) return;
+        wk.left = p.u1 - p.u0;
+        wk.u = p.u0;
+        wk.b = wk.h = wk.rt = wk.rts = 0;
+        wk.off = 0;
+        if (wk.left <= 0) return;
+        wk.b = p.b;
+        wk.rt = p.rt;
+        wk.off = p.off;
+        wk.s = first;
+        wk.rts = Work<kMT, kKT>::row_tiles(a, first);
     }
     template <int THREADS>
     __device__ __forceinline__ bool next(const AttnArgs& a, int bar = 0) {
@@ -111,6 +122,7 @@ struct Shared {
     // of this CTA: the pair's products are done
     uint64_t s_full[2], pv_done[2], done;
     Plan plan;
+    Seq first;                              // of the pair's units
     Ctx ctx[6];                             // softmax, copies of keys, MMA, keys and values passed on, copies of values
     uint32_t tmem;
 };
@@ -180,7 +192,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMa
     const int lane = threadIdx.x & 31, p0 = V ? static_cast<int>(rank) * kPanels : 0;
     const int tokens = min(la.c.page, kN), boxes = kN / tokens;
     Ctx& ctx = sh.ctx[V ? 5 : 1];
-    ctx.start<32>(a, sh.plan);
+    ctx.start<32>(a, sh.plan, sh.first);
     int uses = 0;
     bool dead = false;
     while (!dead && ctx.next<32>(a)) {
@@ -227,7 +239,7 @@ template <int C>
 __device__ __forceinline__ void pass_k(const LatentAttnArgs& la, Shared& sh) {
     const AttnArgs& a = la.a;
     Ctx& ctx = sh.ctx[3];
-    ctx.start<32>(a, sh.plan);
+    ctx.start<32>(a, sh.plan, sh.first);
     int n = 0;
     bool dead = false;
     while (!dead && ctx.next<32>(a)) {
@@ -257,7 +269,7 @@ __device__ __forceinline__ void pass_v(const LatentAttnArgs& la, Shared& sh, uin
     const AttnArgs& a = la.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
     Ctx& ctx = sh.ctx[4];
-    ctx.start<128>(a, sh.plan);
+    ctx.start<128>(a, sh.plan, sh.first);
     int n = 0;
     bool dead = false;
     while (ctx.next<128>(a, kBarV)) {
@@ -343,7 +355,7 @@ __device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, ui
     const uint32_t f = static_cast<uint32_t>(127 + 120 + la.c.scale_log2) << 7, factor = f | (f << 16);
     const uint32_t nan_bits = 0x43F0u + static_cast<uint32_t>(la.c.scale_log2 * 128);
     Ctx& ctx = sh.ctx[V ? 4 : 3];
-    ctx.start<128>(a, sh.plan);
+    ctx.start<128>(a, sh.plan, sh.first);
     int n = 0;
     bool dead = false;
     while (ctx.next<128>(a, V ? kBarV : kBarK)) {
@@ -377,7 +389,7 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
     const uint64_t qd = sdesc(smem_u32(qs), 16, 1024), pd = sdesc(smem_u32(ps), 16, 1024);
     const uint64_t kd = sdesc(smem_u32(ks), 16, 1024), vd = sdesc(smem_u32(vs), kTilePanel, 1024);
     Ctx& ctx = sh.ctx[2];
-    ctx.start<32>(a, sh.plan);
+    ctx.start<32>(a, sh.plan, sh.first);
     uint32_t qp = 0, g = 0;                                      // phase of q_ready; tiles begun
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -445,30 +457,33 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// The CTA's rows of Q into shared memory, K-major with the 128-byte swizzle, by 128
-// threads in whole rows; rows past the last are zeros.
+// The CTA's rows of Q into shared memory, K-major with the 128-byte swizzle: a warp
+// copies whole rows, all of its 16 on their way at once; rows past the last are zeros.
+// (By registers, nine pieces a thread at a time, an item's start took 18,000 clocks.)
 template <int C>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int row0, int count, bool negate, uint8_t* qs) {
-    constexpr int kChunks = (C + kLatentRot) / 8, kBatch = 9;
-    const uint32_t flip = negate ? 0x80008000u : 0u;
+    constexpr int kChunks = (C + kLatentRot) / 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto place = [&](int r, int ch) { return qs + (ch >> 3) * kRowPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+#pragma unroll 4
+    for (int r = warp; r < kRows; r += 4) {
+        const int row = row0 + min(r, count - 1), qi = a.query_of(row), hd = row - qi * a.group;
+        const uint16_t* src = a.q + int64_t(it.s.q0 + qi) * a.q_stride + hd * (C + kLatentRot);
+        const uint32_t bytes = r < count ? 16u : 0u;
+#pragma unroll
+        for (int ch = lane; ch < kChunks; ch += 32)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(r, ch))), "l"(src + 8 * ch), "r"(bytes)
+                         : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (negate) {
 #pragma unroll 1
-    for (int e0 = 0; e0 < kRows * kChunks; e0 += 128 * kBatch) {
-        uint4 w[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int e = e0 + 128 * k + static_cast<int>(threadIdx.x), r = e / kChunks, ch = e - r * kChunks;
-            w[k] = make_uint4(0, 0, 0, 0);
-            if (r < count) {
-                const int row = row0 + r, qi = a.query_of(row), hd = row - qi * a.group;
-                w[k] = __ldg(reinterpret_cast<const uint4*>(a.q + int64_t(it.s.q0 + qi) * a.q_stride + hd * (C + kLatentRot) + 8 * ch));
-                w[k] = make_uint4(w[k].x ^ flip, w[k].y ^ flip, w[k].z ^ flip, w[k].w ^ flip);
+        for (int r = warp; r < kRows; r += 4)
+            for (int ch = lane; ch < kChunks; ch += 32) {
+                uint4* p = reinterpret_cast<uint4*>(place(r, ch));
+                const uint4 w = *p;
+                *p = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
             }
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int e = e0 + 128 * k + static_cast<int>(threadIdx.x), r = e / kChunks, ch = e - r * kChunks;
-            if (r < kRows) *reinterpret_cast<uint4*>(qs + (ch >> 3) * kRowPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[k];
-        }
     }
     fence_async_smem();
 }
@@ -483,7 +498,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
     uint8_t* p_row = ps + lr * 128;
     const bool draft = a.draft != nullptr;
     Ctx& ctx = sh.ctx[0];
-    ctx.start<128>(a, sh.plan);
+    ctx.start<128>(a, sh.plan, sh.first);
     const Item& it = ctx.it;
     uint32_t g = 0, waited = 0;                                  // tiles so far; products P V waited for
     bool dead = false;
@@ -590,22 +605,22 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
         wait_pv(g);
         if (__any_sync(0xFFFFFFFFu, valid)) {
 #pragma unroll 1
-            for (int q = 0; q < F::kNV * 8; ++q) {
-                float o[16];
-                tmem_ld16(colO + 16 * q, o);
+            for (int q = 0; q < F::kNV * 4; ++q) {
+                float o[32];
+                tmem_ld32(colO + 32 * q, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = weight != 0.0f ? o[e] * weight : 0.0f;
-                const int d0 = half * (C / 2) + 16 * q;
+                for (int e = 0; e < 32; ++e) o[e] = weight != 0.0f ? o[e] * weight : 0.0f;
+                const int d0 = half * (C / 2) + 32 * q;
                 if (valid) {
                     if (piece) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 8; ++e)
                             *reinterpret_cast<float4*>(slot + ((d0 / 4 + e) * kLatentRows + row0 + lr) * 4) =
                                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
+                        for (int e = 0; e < 4; ++e)
                             *reinterpret_cast<uint4*>(a.out + at * C + d0 + 8 * e) =
                                 make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
                                            pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
@@ -657,6 +672,8 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     pdl_wait();
     pdl_launch_dependents();
     plan_work<kMT, kKT>(a, 1, sh.scan, &sh.plan, pair, gridDim.x >> 1, rank == 0);   // (its barriers publish sh.tmem)
+    if (threadIdx.x == 0 && sh.plan.u0 < sh.plan.u1) sh.first = load_seq(a.sq, a.kv.page, sh.plan.b, nullptr);
+    __syncthreads();
     tc_fence_after();
     zero_pad_rows(a, sh.plan.seqs);
     if (warp < 4)
@@ -688,26 +705,28 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
 }
 
 // Joins the pieces of the split items, out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k
-// in pair order.  A unit is two rows of a split item; the blocks share the units
-// of all items out.  Four threads have four columns of a row, each a quarter of the pieces.
-constexpr int kJoinRows = 2, kJoinParts = 4;
+// in pair order.  A unit is kJoinRows rows and kJoinDims columns of a split item; the
+// blocks share the units of all items out.  A thread has four columns of a row, and
+// of the pieces every kJoinParts-th; eight rows beside each other make whole lines of
+// the pieces' layout, four threads' columns whole sectors of the output.
+constexpr int kJoinRows = 8, kJoinDims = 64, kJoinParts = 4, kJoinThreads = kJoinRows * kJoinDims / 4 * kJoinParts;
 
 template <int C>
-__global__ void __launch_bounds__(kJoinRows* kJoinParts* C / 4, 1) latent_join_kernel(const AttnArgs a, int n_notes) {
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArgs a, int n_notes) {
     constexpr int64_t kSlot = kLatentRows * (C + 2);
-    constexpr int kCells = kJoinRows * C / 4, kBatch = 3;
+    constexpr int kCells = kJoinRows * kJoinDims / 4, kBatch = 4, kCuts = C / kJoinDims;
     __shared__ float4 s_v[kJoinParts][kCells];
-    __shared__ float s_sum[kJoinParts][kJoinRows];
-    __shared__ int s_end[96];                                    // units up to note i, inclusive
-    static_assert(kLatentMaxPairs <= 96, "three notes a lane");
+    __shared__ float2 s_ml[kJoinParts][kJoinRows];
+    __shared__ int s_end[128];                                   // units up to note i, inclusive
+    static_assert(kLatentMaxPairs <= 128, "four notes a lane");
     pdl_wait();
     pdl_launch_dependents();
     if (threadIdx.x < 32) {
-        int u[3], sum = 0;
+        int u[4], sum = 0;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const int i = threadIdx.x * 3 + k;
-            u[k] = i < n_notes && a.notes[i].pieces > 0 ? (a.notes[i].rows + kJoinRows - 1) / kJoinRows : 0;
+        for (int k = 0; k < 4; ++k) {
+            const int i = threadIdx.x * 4 + k;
+            u[k] = i < n_notes && a.notes[i].pieces > 0 ? (a.notes[i].rows + kJoinRows - 1) / kJoinRows * kCuts : 0;
             sum += u[k];
         }
         int before = sum;
@@ -718,72 +737,82 @@ __global__ void __launch_bounds__(kJoinRows* kJoinParts* C / 4, 1) latent_join_k
         }
         before -= sum;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) s_end[threadIdx.x * 3 + k] = before += u[k];
+        for (int k = 0; k < 4; ++k) s_end[threadIdx.x * 4 + k] = before += u[k];
     }
     __syncthreads();
-    const int total = s_end[95];
+    const int total = s_end[127];
     const int cell = threadIdx.x % kCells, part = threadIdx.x / kCells;
-    const int rl = cell % kJoinRows, d4 = cell / kJoinRows;
+    const int rl = cell % kJoinRows;
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
         int i = 0;
-        while (s_end[i] <= u) ++i;
+#pragma unroll
+        for (int step = 64; step > 0; step >>= 1)
+            if (s_end[i + step - 1] <= u) i += step;
         const SplitNote n = a.notes[i];
-        const int row0 = (u - (i > 0 ? s_end[i - 1] : 0)) * kJoinRows;
+        const int v = u - (i > 0 ? s_end[i - 1] : 0), row = v / kCuts * kJoinRows + rl;
+        const int d4 = v % kCuts * (kJoinDims / 4) + cell / kJoinRows;
         // the piece of the pair where the item begins, and (k >= 1) of the k-th pair after it
         const float* head = a.partials + int64_t(i) * kSlot;
         const float* rest = a.partials + (int64_t(kLatentMaxPairs) + i) * kSlot;
-        const int row = min(row0 + rl, n.rows - 1);
         const int ml = kLatentRows * C + 2 * row, od = (d4 * kLatentRows + row) * 4;
-        float top = head[ml];
-        for (int k = 1; k < n.pieces; ++k) top = fmaxf(top, rest[k * kSlot + ml]);
-        const float ref = top == kNegInf ? 0.0f : top;
-        float sum = 0.0f;
-        float4 v = make_float4(0, 0, 0, 0);
-        auto add = [&](const float2& x, const float4& y) {
-            const float w = fast_exp2(x.x - ref);
-            sum += x.y * w;
-            v.x += y.x * w;
-            v.y += y.y * w;
-            v.z += y.z * w;
-            v.w += y.w * w;
-        };
-        if (part == 0) add(*reinterpret_cast<const float2*>(head + ml), *reinterpret_cast<const float4*>(head + od));
-        for (int k0 = part > 0 ? part : kJoinParts; k0 < n.pieces; k0 += kBatch * kJoinParts) {
+        // this part's pieces, with a reference of its own
+        float top = kNegInf, sum = 0.0f;
+        float4 s = make_float4(0, 0, 0, 0);
+        for (int k0 = part; k0 < n.pieces && row < n.rows; k0 += kBatch * kJoinParts) {
             float2 x[kBatch];
             float4 y[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const int k = k0 + j * kJoinParts;
+                const float* p = k == 0 ? head : rest + k * kSlot;
                 x[j] = make_float2(kNegInf, 0.0f);
                 y[j] = make_float4(0, 0, 0, 0);
                 if (k < n.pieces) {
-                    x[j] = *reinterpret_cast<const float2*>(rest + k * kSlot + ml);
-                    y[j] = *reinterpret_cast<const float4*>(rest + k * kSlot + od);
+                    x[j] = *reinterpret_cast<const float2*>(p + ml);
+                    y[j] = *reinterpret_cast<const float4*>(p + od);
                 }
             }
+            float now = top;
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (k0 + j * kJoinParts < n.pieces) add(x[j], y[j]);
+            for (int j = 0; j < kBatch; ++j) now = fmaxf(now, x[j].x);
+            const float ref = now == kNegInf ? 0.0f : now, keep = fast_exp2(top - ref);
+            sum *= keep;
+            s = make_float4(s.x * keep, s.y * keep, s.z * keep, s.w * keep);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const float w = fast_exp2(x[j].x - ref);
+                sum = fmaf(x[j].y, w, sum);
+                s.x = fmaf(y[j].x, w, s.x);
+                s.y = fmaf(y[j].y, w, s.y);
+                s.z = fmaf(y[j].z, w, s.z);
+                s.w = fmaf(y[j].w, w, s.w);
+            }
+            top = now;
         }
-        s_v[part][cell] = v;
-        if (d4 == 0) s_sum[part][rl] = sum;
+        s_v[part][cell] = s;
+        if (cell < kJoinRows) s_ml[part][rl] = make_float2(top, sum);
         __syncthreads();
-        if (part == 0 && row0 + rl < n.rows) {
+        if (part == 0 && row < n.rows) {
+            top = kNegInf;
+#pragma unroll
+            for (int p = 0; p < kJoinParts; ++p) top = fmaxf(top, s_ml[p][rl].x);
+            const float ref = top == kNegInf ? 0.0f : top;
             sum = 0.0f;
-            v = make_float4(0, 0, 0, 0);
+            s = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int p = 0; p < kJoinParts; ++p) {
+                const float w = fast_exp2(s_ml[p][rl].x - ref);
                 const float4 y = s_v[p][cell];
-                sum += s_sum[p][rl];
-                v.x += y.x;
-                v.y += y.y;
-                v.z += y.z;
-                v.w += y.w;
+                sum = fmaf(s_ml[p][rl].y, w, sum);
+                s.x = fmaf(y.x, w, s.x);
+                s.y = fmaf(y.y, w, s.y);
+                s.z = fmaf(y.z, w, s.z);
+                s.w = fmaf(y.w, w, s.w);
             }
             const int r = n.row0 + row, q = a.query_of(r), hd = r - q * a.group;
             const int64_t at = int64_t(n.q0 + q) * a.q_heads + hd;
             const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
-            *reinterpret_cast<uint2*>(a.out + at * C + 4 * d4) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+            *reinterpret_cast<uint2*>(a.out + at * C + 4 * d4) = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
             if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
         }
         __syncthreads();
@@ -800,7 +829,7 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cuda
     e = launch_pdl_cluster(latent_attn_kernel<C, E4M3>, dim3(2 * pairs), dim3(kThreads<E4M3>), 2, smem, s, a, m);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(latent_join_kernel<C>, dim3(n_sms), dim3(kJoinRows * kJoinParts * C / 4), 0, s, a.a, pairs);
+    e = launch_pdl(latent_join_kernel<C>, dim3(3 * n_sms), dim3(kJoinThreads), 0, s, a.a, pairs);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
