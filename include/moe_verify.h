@@ -682,7 +682,7 @@ moe_status_t moe_cache_evict(const moe_kv_cache_t* cache, const moe_seqs_t* seqs
  *   dtype        of the latent: MOE_KV_BF16, or MOE_KV_E4M3, whose values are
  *                code * 2^scale_log2, bf16 numbers all of them; the rotary key is
  *                bf16 in both (its rounding would turn with the position)
- *   strides      multiples of 16 bytes, positive, each below 2^40 bytes
+ *   strides      multiples of 16 bytes, positive, each below 2^37 bytes
  *   latent, rope 16-byte aligned device memory
  */
 typedef struct {

@@ -65,11 +65,10 @@ inline int64_t latent_workspace_bytes(int dim) {
     return kAttnPartials + int64_t(2) * kLatentMaxPairs * kLatentRows * (dim + 2) * 4;
 }
 
-// Tensor maps of the cache: the latent as a 4-D tensor (64 elements or 128 codes of a
-// row, token, such part of the row, page), keys in boxes of min(page, 32) tokens
-// and values of min(page, 64), of one part, or where that is the whole box of a bf16
-// tile all of a row's, or half of it; the rotary key as a 3-D one (element, token,
-// page) in boxes as the keys'.  128-byte swizzled.
+// Tensor maps of the cache: the latent as a 5-D tensor (64 elements or 128 codes of a
+// row, eight tokens, such part of the row, such eight tokens, page), keys in boxes of
+// whole rows of min(page, 32) tokens, values of half rows of min(page, 64); the rotary
+// key as a 3-D one (element, token, page) in boxes as the keys'.  128-byte swizzled.
 struct LatentMaps {
     CUtensorMap keys, values, rope;
 };

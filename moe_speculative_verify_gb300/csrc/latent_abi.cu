@@ -12,8 +12,9 @@ using moe::aligned;
 using moe::cuda_status;
 using moe::device_info;
 
+// (a tensor map's strides are below 2^40 bytes, that of eight tokens among them)
 bool stride_ok(int64_t elems, int64_t es, int64_t least) {
-    return elems >= least && elems <= (int64_t(1) << 40) / es - 1 && (elems * es) % 16 == 0;
+    return elems >= least && elems <= (int64_t(1) << 37) / es - 1 && (elems * es) % 16 == 0;
 }
 
 // Strides of rows of bf16 elements that are read in 16-byte pieces.
@@ -118,14 +119,14 @@ bool make_maps(const moe_latent_cache_t* c, moe::LatentMaps* m) {
     if (!fn) return false;
     const bool e4m3 = c->dtype == MOE_KV_E4M3;
     const cuuint64_t es = e4m3 ? 1 : 2, part = 128 / es;         // 128 bytes
-    const cuuint64_t dims[4] = {part, cuuint64_t(c->page_size), c->latent_dim / part, cuuint64_t(c->n_pages)};
-    const cuuint64_t strides[3] = {c->latent_token_stride * es, 128, c->latent_page_stride * es};
-    const cuuint32_t one[4] = {1, 1, 1, 1};
-    auto latent = [&](CUtensorMap* map, int tokens, int parts) {
-        const bool all = !e4m3 && c->page_size >= tokens;
-        const cuuint32_t box[4] = {cuuint32_t(part), cuuint32_t(c->page_size < tokens ? c->page_size : tokens),
-                                   cuuint32_t(all ? parts : 1), 1};
-        return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c->latent, dims, strides, box, one,
+    const cuuint64_t dims[5] = {part, 8, c->latent_dim / part, cuuint64_t(c->page_size) / 8, cuuint64_t(c->n_pages)};
+    const cuuint64_t token = c->latent_token_stride * es;
+    const cuuint64_t strides[4] = {token, 128, 8 * token, c->latent_page_stride * es};
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    auto latent = [&](CUtensorMap* map, int tokens, int dim) {
+        const cuuint32_t box[5] = {cuuint32_t(part), 8, cuuint32_t(dim / part),
+                                   cuuint32_t(c->page_size < tokens ? c->page_size : tokens) / 8, 1};
+        return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, c->latent, dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
@@ -133,7 +134,7 @@ bool make_maps(const moe_latent_cache_t* c, moe::LatentMaps* m) {
     const cuuint64_t rdims[3] = {moe::kLatentRot, cuuint64_t(c->page_size), cuuint64_t(c->n_pages)};
     const cuuint64_t rstrides[2] = {cuuint64_t(c->rope_token_stride) * 2, cuuint64_t(c->rope_page_stride) * 2};
     const cuuint32_t rbox[3] = {moe::kLatentRot, cuuint32_t(c->page_size < keys ? c->page_size : keys), 1};
-    return latent(&m->keys, keys, c->latent_dim / 64) && latent(&m->values, moe::kLatentKeys, c->latent_dim / 128) &&
+    return latent(&m->keys, keys, c->latent_dim) && latent(&m->values, moe::kLatentKeys, c->latent_dim / 2) &&
            fn(&m->rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->rope, rdims, rstrides, rbox, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

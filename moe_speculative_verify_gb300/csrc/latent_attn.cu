@@ -35,8 +35,10 @@ constexpr int kMT = kLatentRows, kKT = kLatentKeys;
 constexpr int kRows = 64;                // rows of a CTA
 constexpr int kKeys = kKT / 2;           // whole keys of a CTA
 constexpr int kRowPanel = kRows * 128;   // 64 elements of its rows (Q, P)
-constexpr int kKeyPanel = kKeys * 128;   // and of its keys
-constexpr int kTilePanel = kKT * 128;    // and of a tile's
+// K and V lie in atoms of 8 keys by 64 elements (1 KB, swizzled), eight keys' atoms
+// beside each other, so that a copy reads eight whole rows at a time (element by
+// element of all rows, memory gave 4.7 TB/s).  The rotary part of K has its own place.
+constexpr int kAtom = 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 64;           // S of tile g at column 32 (g & 1), O behind
 constexpr float kLag = 8.0f;             // log2 of what powers may grow to
@@ -53,8 +55,11 @@ struct Cfg {
     static constexpr int kNV = C / 256;                          // MMAs of P V a step
     static constexpr int kQBytes = (C / 64 + 1) * kRowPanel;
     static constexpr int kPBytes = kRowPanel;
-    static constexpr int kKBytes = (C / 64 + 1) * kKeyPanel;
-    static constexpr int kVBytes = kVPanels * kTilePanel;
+    static constexpr int kKGroup = C / 64 * kAtom;               // of eight keys
+    static constexpr int kVGroup = kVPanels * kAtom;
+    static constexpr int kRope = kKeys / 8 * kKGroup;            // offset of the rotary part in a stage
+    static constexpr int kKBytes = kRope + kKeys / 8 * kAtom;
+    static constexpr int kVBytes = kKT / 8 * kVGroup;
     static constexpr size_t kSmem = kQBytes + 2 * (kPBytes + kKBytes + kVBytes);   // then Shared
 };
 
@@ -177,19 +182,30 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 }
 
 // ----------------------------------------------------------------- copies ----
+// 5-D tiled bulk tensor load global -> shared; c0 (innermost, elements) starts on a
+// 16-byte boundary.  A coordinate out of range reads as zeros.
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3, int32_t c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
 // The two warps that copy from memory: keys (this CTA's 32 of each tile, all elements
 // and the rotary part) and values (all 64 keys, this CTA's half of the elements).  A
-// box a page (for small pages and for codes, a box a page and panel), each page by a
-// lane of its own.
+// box a page, each page by a lane of its own.  e4m3: the codes land in the second half
+// of their stage, see convert.
 template <int C, bool E4M3, bool V>
 __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMaps& maps, Shared& sh, uint8_t* ring, uint32_t rank) {
     using F = Cfg<C>;
-    constexpr int kN = V ? kKT : kKeys, kPanel = V ? kTilePanel : kKeyPanel, kPanels = V ? F::kVPanels : C / 64;
+    constexpr int kN = V ? kKT : kKeys, kGroup = (V ? F::kVGroup : F::kKGroup) / (E4M3 ? 2 : 1);   // eight keys' bytes
     const AttnArgs& a = la.a;
     uint64_t* fulls = V ? sh.v_full : sh.k_full;
     uint64_t* empties = V ? sh.v_empty : sh.k_empty;
     const CUtensorMap* map = V ? &maps.values : &maps.keys;
-    const int lane = threadIdx.x & 31, p0 = V ? static_cast<int>(rank) * kPanels : 0;
+    const int lane = threadIdx.x & 31, p0 = V ? static_cast<int>(rank) * F::kVPanels / (E4M3 ? 2 : 1) : 0;
     const int tokens = min(la.c.page, kN), boxes = kN / tokens;
     Ctx& ctx = sh.ctx[V ? 5 : 1];
     ctx.start<32>(a, sh.plan, sh.first);
@@ -199,7 +215,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMa
         const Item& it = ctx.it;
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
         for (int j = 0; j < ctx.tiles; ++j, ++uses) {
-            const int k = ctx.key0(j) + (V ? 0 : static_cast<int>(rank) * kKeys) + lane * tokens, slot = k & (la.c.page - 1), st = uses & 1;
+            const int k = ctx.key0(j) + (V ? 0 : static_cast<int>(rank) * kKeys) + lane * tokens, st = uses & 1;
             const bool mine = lane < boxes && k < it.hi && k + tokens > it.lo;
             int page = mine ? table[k >> la.c.page_log2] : 0;
             if (page < 0 || page >= la.c.n_pages) {
@@ -210,18 +226,14 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMa
             dead = !warp_wait(&empties[st], ((uses >> 1) & 1) ^ 1, a.err, a.timeout_ns);
             if (dead) break;
             uint64_t* full = &fulls[st];
-            if (lane == 0) mbar_arrive_expect_tx(full, rows * (kPanels * (E4M3 ? 64 : 128) + (V ? 0 : 2 * kLatentRot)));
+            if (lane == 0) mbar_arrive_expect_tx(full, rows / 8 * (kGroup + (V ? 0 : kAtom)));
             __syncwarp();
             if (mine) {
-                uint8_t* at = ring + st * (V ? F::kVBytes : F::kKBytes) + lane * tokens * 128;
-                if (!V) tma_load_3d(at + kPanels * kPanel, &maps.rope, full, 0, slot, page);
-                if constexpr (E4M3) {                            // into the second of each two panels, see convert_row
-                    for (int x = 0; x < kPanels; x += 2) tma_load_4d(at + (x + 1) * kPanel, map, full, 0, slot, (p0 + x) / 2, page);
-                } else if (tokens == kN) {
-                    tma_load_4d(at, map, full, 0, slot, p0, page);
-                } else {
-                    for (int x = 0; x < kPanels; ++x) tma_load_4d(at + x * kPanel, map, full, 0, slot, p0 + x, page);
-                }
+                const int slot = k & (la.c.page - 1);
+                uint8_t* stage = ring + st * (V ? F::kVBytes : F::kKBytes);
+                uint8_t* to = stage + (E4M3 ? kN / 8 * kGroup : 0) + lane * (tokens / 8) * kGroup;
+                if (!V) tma_load_3d(stage + F::kRope + lane * (tokens / 8) * kAtom, &maps.rope, full, 0, slot, page);
+                tma_load_5d(to, map, full, 0, 0, p0, slot / 8, page);
             }
             __syncwarp();
         }
@@ -280,9 +292,9 @@ __device__ __forceinline__ void pass_v(const LatentAttnArgs& la, Shared& sh, uin
             const int j0 = ctx.key0(j), lo = max(ctx.it.lo, ctx.wlo), hi = min(ctx.it.hi, ctx.whi);
             if (j0 < lo || j0 + kKT > hi) {
                 // a key's elements, 16 bytes a lane
-                uint8_t* v = vs + st * F::kVBytes + (lane >> 3) * kTilePanel + (lane & 7) * 16;
+                uint8_t* v = vs + st * F::kVBytes + (lane >> 3) * kAtom + (lane & 7) * 16;
                 for (int r = warp; r < kKT; r += 4) {
-                    uint4* p = reinterpret_cast<uint4*>(v + r * 128);
+                    uint4* p = reinterpret_cast<uint4*>(v + (r >> 3) * F::kVGroup + (r & 7) * 128);
                     bool bad = j0 + r < ctx.it.lo || j0 + r >= ctx.it.hi;
                     if (lane < 8 * F::kVPanels) bad = bad || any_nonfinite(*p);
                     if (__any_sync(0xFFFFFFFFu, bad) && lane < 8 * F::kVPanels) *p = make_uint4(0, 0, 0, 0);
@@ -295,17 +307,12 @@ __device__ __forceinline__ void pass_v(const LatentAttnArgs& la, Shared& sh, uin
     }
 }
 
-// e4m3: 128 codes of a key, which landed in row r of the second of two panels, to
-// bf16 in row r of both, by one thread: all are read before any is written.  A NaN
+// e4m3: 128 codes of a key, as read, to bf16 in the key's row of two atoms.  A NaN
 // code comes out as `nan_bits`, which no other does; `zero` and, where it has NaN
 // codes, `zero_nan` make the row zeros (see pass_v).
-template <int PANEL>
-__device__ __forceinline__ void convert_row(uint8_t* two, int r, uint32_t factor, uint32_t nan_bits, bool zero, bool zero_nan) {
-    uint8_t* first = two + r * 128;
-    uint8_t* second = first + PANEL;
-    uint4 raw[8];
-#pragma unroll
-    for (int ch = 0; ch < 8; ++ch) raw[ch] = *reinterpret_cast<const uint4*>(second + ((ch ^ (r & 7)) << 4));
+__device__ __forceinline__ void convert_row(const uint4 (&raw)[8], uint8_t* first, int r, uint32_t factor, uint32_t nan_bits, bool zero,
+                                            bool zero_nan) {
+    uint8_t* second = first + kAtom;
     uint32_t most = 0;
 #pragma unroll
     for (int ch = 0; ch < 8; ++ch) {
@@ -343,11 +350,12 @@ __device__ __forceinline__ void convert_row(uint8_t* two, int r, uint32_t factor
     }
 }
 
-// e4m3: four warps each for keys and values, a thread a key and 128 codes.
+// e4m3: four warps each for keys and values, a thread a key and 128 codes.  All codes
+// are read before any atom is written over them.
 template <int C, bool V>
 __device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, uint8_t* ring) {
     using F = Cfg<C>;
-    constexpr int kN = V ? kKT : kKeys, kPanel = V ? kTilePanel : kKeyPanel, kUnits = V ? F::kVPanels / 2 : F::kParts;
+    constexpr int kN = V ? kKT : kKeys, kGroup = V ? F::kVGroup : F::kKGroup, kUnits = V ? F::kVPanels / 2 : F::kParts;
     static_assert(kN * kUnits <= 128, "a row's part a thread");
     const AttnArgs& a = la.a;
     const int lane = threadIdx.x & 31, t = threadIdx.x & 127, r = t % kN, part = t / kN;
@@ -361,12 +369,20 @@ __device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, ui
     while (ctx.next<128>(a, V ? kBarV : kBarK)) {
         for (int j = 0; j < ctx.tiles && !dead; ++j, ++n) {
             const int st = n & 1;
-            dead = !warp_wait(V ? &sh.v_full[st] : &sh.k_full[st], (n >> 1) & 1, a.err, a.timeout_ns);
+            uint8_t* stage = ring + st * (V ? F::kVBytes : F::kKBytes);
+            const bool ok = mbar_wait(V ? &sh.v_full[st] : &sh.k_full[st], (n >> 1) & 1, a.err, a.timeout_ns);
+            uint4 raw[8];
+            if (part < kUnits) {
+                const uint8_t* from = stage + kN / 8 * (kGroup / 2) + (r >> 3) * (kGroup / 2) + part * kAtom + (r & 7) * 128;
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) raw[ch] = *reinterpret_cast<const uint4*>(from + ((ch ^ (r & 7)) << 4));
+            }
+            dead = !bar_and(V ? kBarV : kBarK, ok, 128);
             if (dead) break;
             if (part < kUnits) {
                 const int j0 = ctx.key0(j), key = j0 + r;
-                convert_row<kPanel>(ring + st * (V ? F::kVBytes : F::kKBytes) + part * 2 * kPanel, r, factor, nan_bits,
-                                    V && (key < ctx.it.lo || key >= ctx.it.hi), V && (j0 < ctx.wlo || j0 + kKT > ctx.whi));
+                convert_row(raw, stage + (r >> 3) * kGroup + 2 * part * kAtom + (r & 7) * 128, r, factor, nan_bits,
+                            V && (key < ctx.it.lo || key >= ctx.it.hi), V && (j0 < ctx.wlo || j0 + kKT > ctx.whi));
             }
             fence_async_smem();
             __syncwarp();
@@ -387,7 +403,8 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
     const AttnArgs& a = la.a;
     const uint32_t colS = sh.tmem, colO = sh.tmem + kColO;
     const uint64_t qd = sdesc(smem_u32(qs), 16, 1024), pd = sdesc(smem_u32(ps), 16, 1024);
-    const uint64_t kd = sdesc(smem_u32(ks), 16, 1024), vd = sdesc(smem_u32(vs), kTilePanel, 1024);
+    const uint64_t kd = sdesc(smem_u32(ks), 16, F::kKGroup), rd = sdesc(smem_u32(ks) + F::kRope, 16, kAtom);
+    const uint64_t vd = sdesc(smem_u32(vs), kAtom, F::kVGroup);
     Ctx& ctx = sh.ctx[2];
     ctx.start<32>(a, sh.plan, sh.first);
     uint32_t qp = 0, g = 0;                                      // phase of q_ready; tiles begun
@@ -407,13 +424,13 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
                 if (dead) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t kk = kd + (st * F::kKBytes >> 4);
+                    const uint64_t kk = kd + (st * F::kKBytes >> 4), rr = rd + (st * F::kKBytes >> 4);
 #pragma unroll
                     for (int x = 0; x <= C / 64; ++x)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            pair_mma(colS + 32 * st, qd + ((x * kRowPanel + k * 32) >> 4), kk + ((x * kKeyPanel + k * 32) >> 4), kIdQK,
-                                     x > 0 || k > 0);
+                            pair_mma(colS + 32 * st, qd + ((x * kRowPanel + k * 32) >> 4),
+                                     x < C / 64 ? kk + ((x * kAtom + k * 32) >> 4) : rr + (k * 32 >> 4), kIdQK, x > 0 || k > 0);
                     pair_commit(&sh.s_full[st]);
                     pair_commit(&sh.k_empty[st]);
                 }
@@ -432,7 +449,7 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int n = 0; n < F::kNV; ++n)
-                            pair_mma(colO + 128 * n, pp + (k * 32 >> 4), vv + ((2 * n * kTilePanel + k * 2048) >> 4), kIdPV,
+                            pair_mma(colO + 128 * n, pp + (k * 32 >> 4), vv + ((2 * n * kAtom + 2 * k * F::kVGroup) >> 4), kIdPV,
                                      i > 1 || k > 0);
                     pair_commit(&sh.v_empty[st]);
                     pair_commit(&sh.pv_done[st]);
