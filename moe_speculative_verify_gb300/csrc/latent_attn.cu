@@ -47,6 +47,7 @@ constexpr float kLag = 8.0f;             // log2 of what powers may grow to
 template <bool E4M3>
 constexpr int kThreads = E4M3 ? 512 : 384;
 constexpr int kBarSoft = 1, kBarV = 2, kBarK = 3;                // named barriers, 128 threads each
+constexpr int kBarTop = 4;                                       // and two of the 64 that share 32 rows
 
 template <int C>
 struct Cfg {
@@ -517,15 +518,13 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
     Ctx& ctx = sh.ctx[0];
     ctx.start<128>(a, sh.plan, sh.first);
     const Item& it = ctx.it;
-    uint32_t g = 0, waited = 0;                                  // tiles so far; products P V waited for
+    uint32_t g = 0;                                              // tiles so far
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
         tc_fence_after();
     };
-    auto wait_pv = [&](uint32_t upto) {                          // the first `upto` of them (at most two are under way)
-        for (; waited < upto; ++waited) wait(&sh.pv_done[waited & 1u], (waited >> 1) & 1u);
-    };
+    auto wait_pv = [&](uint32_t tile) { wait(&sh.pv_done[tile & 1u], (tile >> 1) & 1u); };
     // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf), or NaN; the sign goes to the queries
     const float cs = a.scale * kLog2e;
     const float c = fmaxf(fabsf(cs), 1.2e-38f);
@@ -561,40 +560,52 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
                 for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[e + k]);
             float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             sh.top[g & 1u][half][lr] = top;
-            named_bar(kBarSoft, 128);
+            // powers by the reference so far, while the row's other half says its maximum
+            uint32_t u[16];
+            float s0, s1;
+            auto powers = [&]() {
+                const float off = ref == kNegInf ? 0.0f : -ref;
+                s0 = sum0;
+                s1 = sum1;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float p0, p1;
+                    fma2_to(p0, p1, x[e], x[e + 1], c, off);
+                    p0 = fast_exp2(p0);
+                    p1 = fast_exp2(p1);
+                    add2(s0, s1, p0, p1);
+                    u[e / 2] = pack_bf16(p0, p1);
+                }
+            };
+            if (j > 0) powers();
+            named_bar(kBarTop + ((tid >> 5) & 1), 64);
             top = fmaxf(top, sh.top[g & 1u][half ^ 1][lr]) * c;
             if (!(top > kNegInf)) top = kNegInf;                 // (NaN: the sums carry it)
             const bool grow = top > ref + kLag || (ref == kNegInf && top > kNegInf);
-            if (j > 0 && __any_sync(0xFFFFFFFFu, grow)) {
-                wait_pv(g);
+            if (__any_sync(0xFFFFFFFFu, grow) || j == 0) {
                 const float f = !grow ? 1.0f : (ref == kNegInf ? 0.0f : fast_exp2(ref - top));
                 sum0 *= f;
                 sum1 *= f;
+                if (grow) ref = top;
+                if (j > 0) {
+                    wait_pv(g - 1);
 #pragma unroll 1
-                for (int q = 0; q < F::kNV * 8; ++q) {
-                    float o[16];
-                    tmem_ld16(colO + 16 * q, o);
-                    tmem_wait_ld();
-                    uint32_t u[16];
+                    for (int q = 0; q < F::kNV * 8; ++q) {
+                        float o[16];
+                        tmem_ld16(colO + 16 * q, o);
+                        tmem_wait_ld();
+                        uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
-                    tmem_st16(colO + 16 * q, u);
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+                        tmem_st16(colO + 16 * q, w);
+                    }
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
+                powers();
             }
-            if (grow) ref = top;
-            const float off = ref == kNegInf ? 0.0f : -ref;
-            uint32_t u[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float p0, p1;
-                fma2_to(p0, p1, x[e], x[e + 1], c, off);
-                p0 = fast_exp2(p0);
-                p1 = fast_exp2(p1);
-                add2(sum0, sum1, p0, p1);
-                u[e / 2] = pack_bf16(p0, p1);
-            }
-            if (g >= 2) wait_pv(g - 1);                          // P's room has been read
+            sum0 = s0;
+            sum1 = s1;
+            // (P's room has been read: S of this tile came after P V of two before)
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch)
                 *reinterpret_cast<uint4*>(p_row + (g & 1u) * F::kPBytes + (((4 * half + ch) ^ (lr & 7)) << 4)) =
@@ -619,7 +630,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
             else if (a.lse)
                 a.lse[at] = ref == kNegInf ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
-        wait_pv(g);
+        if (T > 0) wait_pv(g - 1);
         if (__any_sync(0xFFFFFFFFu, valid)) {
 #pragma unroll 1
             for (int q = 0; q < F::kNV * 4; ++q) {
@@ -722,28 +733,29 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
 }
 
 // Joins the pieces of the split items, out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k
-// in pair order.  A unit is kJoinRows rows and kJoinDims columns of a split item; the
-// blocks share the units of all items out.  A thread has four columns of a row, and
-// of the pieces every kJoinParts-th; eight rows beside each other make whole lines of
-// the pieces' layout, four threads' columns whole sectors of the output.
-constexpr int kJoinRows = 8, kJoinDims = 64, kJoinParts = 4, kJoinThreads = kJoinRows * kJoinDims / 4 * kJoinParts;
+// in pair order.  A thread has four columns of a row, kBatch pieces of them in flight; a
+// warp has eight rows, which are a line of the pieces' layout, by four such columns, a
+// sector of the output.  (Rows as units of whole blocks, the pieces shared out among
+// their threads: 76 us behind a chunk whose 76 pairs share 40 MB, 12 now.)
+constexpr int kJoinRows = 8, kJoinThreads = 512;
 
 template <int C>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArgs a, int n_notes) {
+__global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const AttnArgs a, int n_notes) {
     constexpr int64_t kSlot = kLatentRows * (C + 2);
-    constexpr int kCells = kJoinRows * kJoinDims / 4, kBatch = 4, kCuts = C / kJoinDims;
-    __shared__ float4 s_v[kJoinParts][kCells];
-    __shared__ float2 s_ml[kJoinParts][kJoinRows];
+    constexpr int kBatch = 4, kUnit = kJoinRows * C / 4;         // threads' work of eight rows
+    __shared__ SplitNote s_note[kLatentMaxPairs];
     __shared__ int s_end[128];                                   // units up to note i, inclusive
     static_assert(kLatentMaxPairs <= 128, "four notes a lane");
     pdl_wait();
     pdl_launch_dependents();
+    for (int i = threadIdx.x; i < n_notes; i += kJoinThreads) s_note[i] = a.notes[i];
+    __syncthreads();
     if (threadIdx.x < 32) {
         int u[4], sum = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int i = threadIdx.x * 4 + k;
-            u[k] = i < n_notes && a.notes[i].pieces > 0 ? (a.notes[i].rows + kJoinRows - 1) / kJoinRows * kCuts : 0;
+            u[k] = i < n_notes && s_note[i].pieces > 0 ? (s_note[i].rows + kJoinRows - 1) / kJoinRows : 0;
             sum += u[k];
         }
         int before = sum;
@@ -757,34 +769,32 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArg
         for (int k = 0; k < 4; ++k) s_end[threadIdx.x * 4 + k] = before += u[k];
     }
     __syncthreads();
-    const int total = s_end[127];
-    const int cell = threadIdx.x % kCells, part = threadIdx.x / kCells;
-    const int rl = cell % kJoinRows;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const int total = s_end[127] * kUnit;
+    for (int w = blockIdx.x * kJoinThreads + threadIdx.x; w < total; w += gridDim.x * kJoinThreads) {
+        const int u = w / kUnit, cell = w - u * kUnit;
         int i = 0;
 #pragma unroll
         for (int step = 64; step > 0; step >>= 1)
             if (s_end[i + step - 1] <= u) i += step;
-        const SplitNote n = a.notes[i];
-        const int v = u - (i > 0 ? s_end[i - 1] : 0), row = v / kCuts * kJoinRows + rl;
-        const int d4 = v % kCuts * (kJoinDims / 4) + cell / kJoinRows;
+        const SplitNote& n = s_note[i];
+        const int row = (u - (i > 0 ? s_end[i - 1] : 0)) * kJoinRows + cell % kJoinRows, d4 = cell / kJoinRows;
+        if (row >= n.rows) continue;
         // the piece of the pair where the item begins, and (k >= 1) of the k-th pair after it
         const float* head = a.partials + int64_t(i) * kSlot;
         const float* rest = a.partials + (int64_t(kLatentMaxPairs) + i) * kSlot;
-        const int ml = kLatentRows * C + 2 * row, od = (d4 * kLatentRows + row) * 4;
-        // this part's pieces, with a reference of its own
+        const int ml = kLatentRows * C + 2 * row, od = (d4 * kLatentRows + row) * 4, pieces = n.pieces;
         float top = kNegInf, sum = 0.0f;
         float4 s = make_float4(0, 0, 0, 0);
-        for (int k0 = part; k0 < n.pieces && row < n.rows; k0 += kBatch * kJoinParts) {
+        for (int k0 = 0; k0 < pieces; k0 += kBatch) {
             float2 x[kBatch];
             float4 y[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int k = k0 + j * kJoinParts;
+                const int k = k0 + j;
                 const float* p = k == 0 ? head : rest + k * kSlot;
                 x[j] = make_float2(kNegInf, 0.0f);
                 y[j] = make_float4(0, 0, 0, 0);
-                if (k < n.pieces) {
+                if (k < pieces) {
                     x[j] = *reinterpret_cast<const float2*>(p + ml);
                     y[j] = *reinterpret_cast<const float4*>(p + od);
                 }
@@ -797,42 +807,20 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArg
             s = make_float4(s.x * keep, s.y * keep, s.z * keep, s.w * keep);
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const float w = fast_exp2(x[j].x - ref);
-                sum = fmaf(x[j].y, w, sum);
-                s.x = fmaf(y[j].x, w, s.x);
-                s.y = fmaf(y[j].y, w, s.y);
-                s.z = fmaf(y[j].z, w, s.z);
-                s.w = fmaf(y[j].w, w, s.w);
+                const float f = fast_exp2(x[j].x - ref);
+                sum = fmaf(x[j].y, f, sum);
+                s.x = fmaf(y[j].x, f, s.x);
+                s.y = fmaf(y[j].y, f, s.y);
+                s.z = fmaf(y[j].z, f, s.z);
+                s.w = fmaf(y[j].w, f, s.w);
             }
             top = now;
         }
-        s_v[part][cell] = s;
-        if (cell < kJoinRows) s_ml[part][rl] = make_float2(top, sum);
-        __syncthreads();
-        if (part == 0 && row < n.rows) {
-            top = kNegInf;
-#pragma unroll
-            for (int p = 0; p < kJoinParts; ++p) top = fmaxf(top, s_ml[p][rl].x);
-            const float ref = top == kNegInf ? 0.0f : top;
-            sum = 0.0f;
-            s = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int p = 0; p < kJoinParts; ++p) {
-                const float w = fast_exp2(s_ml[p][rl].x - ref);
-                const float4 y = s_v[p][cell];
-                sum = fmaf(s_ml[p][rl].y, w, sum);
-                s.x = fmaf(y.x, w, s.x);
-                s.y = fmaf(y.y, w, s.y);
-                s.z = fmaf(y.z, w, s.z);
-                s.w = fmaf(y.w, w, s.w);
-            }
-            const int r = n.row0 + row, q = a.query_of(r), hd = r - q * a.group;
-            const int64_t at = int64_t(n.q0 + q) * a.q_heads + hd;
-            const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
-            *reinterpret_cast<uint2*>(a.out + at * C + 4 * d4) = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
-            if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
-        }
-        __syncthreads();
+        const int r = n.row0 + row, q = a.query_of(r), hd = r - q * a.group;
+        const int64_t at = int64_t(n.q0 + q) * a.q_heads + hd;
+        const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
+        *reinterpret_cast<uint2*>(a.out + at * C + 4 * d4) = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
+        if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -846,7 +834,7 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cuda
     e = launch_pdl_cluster(latent_attn_kernel<C, E4M3>, dim3(2 * pairs), dim3(kThreads<E4M3>), 2, smem, s, a, m);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(latent_join_kernel<C>, dim3(3 * n_sms), dim3(kJoinThreads), 0, s, a.a, pairs);
+    e = launch_pdl(latent_join_kernel<C>, dim3(2 * n_sms), dim3(kJoinThreads), 0, s, a.a, pairs);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
