@@ -1,86 +1,618 @@
-// expanded.cu -- attention of the expanded form of a latent cache's layer
-// (sm_103a): a head's key is a part of its own beside the rotary part that the
-// heads share, its values have the own part's width.
+// expanded.cu -- attention of the expanded form of a latent cache's layer, on tensor
+// memory of pairs of SMs (sm_103a): a head's key is a part of D elements of its own
+// beside the 64 of the rotary part that the heads share, its values have D elements.
 //
-// A warp takes a token's head, one pass over the keys with a running maximum
-// and sum.
-#include "attn.cuh"
-#include "latent.h"
+// An item is up to 512 query rows of one sequence and head, worked on by a cluster
+// of two CTAs as two streams of 256 rows, 128 a CTA, over tiles of 128 keys:
+//   S = Q K^T     one tcgen05.mma of the pair, M = 256, N = 128: each CTA holds its
+//                 rows of Q and 64 of the keys;
+//   softmax       of each stream by a warpgroup a CTA, a thread a row;
+//   O += P V      M = 256, N = D, P from tensor memory: each CTA holds its rows of P,
+//                 all keys' values of its half of D, and its rows of all of O.
+// So a tile's keys and values are read by one CTA each (half by half), and one stream's
+// products run while the other's softmax does.  Pairs, because their products run at
+// the tensor core's full rate (256 x 128 x 16 in 64 clocks) where a single SM's from
+// shared memory, 128 x 128 x 16, takes 102 for its 64.
+//
+// The reference of a row's sums lags as in attn_tile.cu.
+#include "kernels.h"
+#include "pair.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMT = kExpandedRows, kKT = kExpandedKeys;
+constexpr int kStream = kMT / 2;         // rows of a stream
+constexpr int kKeys = kKT / 2;           // keys of a CTA
+constexpr int kPanel = 128 * 128;        // 128 rows of 64 elements
+constexpr int kThreads = 384;            // 8 softmax warps; copies, an MMA warp a stream, one that passes on what landed
+constexpr int kStages = 3;
+// Registers a thread, moved between the warpgroups after the launch at 168:
+// 8 * 208 + 4 * 80 = 1984 a lane column of the 12 * 168 = 2016 launched.
+constexpr int kRegsSoft = 208, kRegsRest = 80;
+constexpr int kBarGroup = 1, kBarMma = 3;                        // named barriers: each softmax warpgroup, the MMA warps
+constexpr uint32_t kColO = 256;          // S/P of stream s at column 128 s, O at 256 + 128 s
+constexpr float kLag = 8.0f;             // log2 of what powers may grow to
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) expanded_kernel(const ExpandedArgs x) {
-    constexpr int kOwn = D / 32;
+struct Cfg {
+    static constexpr int kQBytes = (D / 64 + 1) * kPanel;        // of a stream: 128 rows
+    static constexpr int kKPanel = kKeys * 128;
+    static constexpr int kKBytes = (D / 64 + 1) * kKPanel;
+    static constexpr int kVBytes = kPanel;                       // 128 keys, D / 2 elements used of 64
+    static constexpr size_t kSmem = 2 * kQBytes + kStages * (kKBytes + kVBytes);   // then Shared
+};
+
+// A role's place in the pair's work, in shared memory; THREADS threads share it, at
+// named barrier `bar`.
+struct Ctx {
+    Walk<kMT, kKT> wk;
+    Item it;
+    int more;
+    int rows;                // rows of the item
+    int tiles;               // key tiles of this pair (0: nothing seen)
+    int a[2], b[2];          // stream s takes local tiles a .. b-1
+    int wlo[2], whi[2];      // keys that every row of the stream sees
+    int lo_all, hi_all;      // and of the item
+
+    template <int THREADS>
+    __device__ __forceinline__ void sync(int bar) {
+        if constexpr (THREADS == 32)
+            __syncwarp();
+        else
+            named_bar(bar, THREADS);
+    }
+    template <int THREADS>
+    __device__ __forceinline__ void start(const AttnArgs& at, const Plan& p) {
+        if (threadIdx.x % THREADS == 0) wk.start(at, p);
+    }
+    template <int THREADS>
+    __device__ __forceinline__ bool next(const AttnArgs& at, int bar = 0) {
+        sync<THREADS>(bar);
+        if (threadIdx.x % THREADS == 0) {
+            more = wk.next(at, it);
+            if (more) set(at);
+        }
+        sync<THREADS>(bar);
+        return more != 0;
+    }
+    __device__ __forceinline__ void set(const AttnArgs& at) {
+        const int r0 = it.rt * kMT;
+        rows = min(kMT, it.s.nq - r0);
+        tiles = it.hi > it.lo ? it.t1 - it.t0 : 0;
+        const int2 all = rows_whole(at, it.s, r0, r0 + rows - 1);
+        lo_all = all.x;
+        hi_all = all.y;
+        const int base = it.tile0 + it.t0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int i0 = r0 + s * kStream, i1 = min(i0 + kStream, r0 + rows) - 1;
+            a[s] = b[s] = 0;
+            wlo[s] = whi[s] = 0;
+            if (i1 < i0) continue;
+            const int2 k = rows_range(at, it.s, i0, i1), w = rows_whole(at, it.s, i0, i1);
+            wlo[s] = w.x;
+            whi[s] = w.y;
+            a[s] = min(max(k.x / kKT - base, 0), tiles);
+            b[s] = k.y > k.x ? max(min((k.y + kKT - 1) / kKT - base, tiles), a[s]) : a[s];
+        }
+    }
+    __device__ __forceinline__ int key0(int tile) const { return (it.tile0 + it.t0 + tile) * kKT; }
+};
+
+struct Shared {
+    int64_t scan[16];                       // plan_work's
+    // of this CTA: what landed, and the room that both streams' products gave back
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    // of the pair, in its first CTA: operands in place in both; the streams' turns
+    uint64_t k_ready[kStages], v_ready[kStages], q_ready[2], p_ready[2], turn[2];
+    // of this CTA: the pair's products are done
+    uint64_t s_full[2], o_full[2], done[2];
+    Plan plan;
+    Ctx ctx[5];                             // the softmax warpgroups', copies, MMA, passing on
+    uint32_t tmem;
+    int bad;                                // some masked tile had values that are not finite
+};
+
+struct Slot {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void step() {
+        if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+// The warp that copies: this CTA's 64 keys of each tile, then its half of the tile's
+// values.  Rows past the sequence's are read as they lie there, or as zeros past the last.
+template <int D>
+__device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMaps& maps, Shared& sh, uint8_t* ks, uint8_t* vs, int rank) {
+    using F = Cfg<D>;
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 31;
-    const int64_t u = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    Ctx& ctx = sh.ctx[2];
+    ctx.start<32>(a, sh.plan);
+    Slot at;
+    int uses = 0;
+    bool dead = false;
+    while (!dead && ctx.next<32>(a)) {
+        const Item& it = ctx.it;
+        const int64_t k0 = x.cu_k[it.b];
+        if (lane == 0 && (k0 < 0 || k0 + it.s.len > x.n_keys)) record_error(a.err, MOE_ERR_INVALID_ARG);
+        for (int j = 0; j < ctx.tiles; ++j, at.step(), ++uses) {
+            // (a place far outside stays outside, whatever 32 bits make of the sum)
+            const int row = static_cast<int>(min(max(k0 + ctx.key0(j), int64_t(-(1 << 30))), int64_t(x.n_keys)));
+            dead = !warp_wait(&sh.k_empty[at.st], at.ph ^ 1u, a.err, a.timeout_ns);
+            if (dead) break;
+            if (lane == 0) {
+                uint8_t* k = ks + at.st * F::kKBytes;
+                mbar_arrive_expect_tx(&sh.k_full[at.st], F::kKBytes);
+                tma_load_4d(k, &maps.k, &sh.k_full[at.st], 0, row + rank * kKeys, 0, it.h);
+                tma_load_2d(k + (D / 64) * F::kKPanel, &maps.rope, &sh.k_full[at.st], 0, row + rank * kKeys);
+            }
+            __syncwarp();
+            dead = !warp_wait(&sh.v_empty[at.st], at.ph ^ 1u, a.err, a.timeout_ns);
+            if (lane == 0 && !dead) {
+                mbar_arrive_expect_tx(&sh.v_full[at.st], F::kVBytes);
+                tma_load_3d(vs + at.st * F::kVBytes, &maps.v, &sh.v_full[at.st], rank * (D / 2), row, it.h);
+            }
+            __syncwarp();
+            if (dead) {                                          // this stage's K alone
+                mbar_wait(&sh.k_full[at.st], at.ph, a.err, kDrainNs);
+                break;
+            }
+        }
+    }
+    // each stage's last copies
+    for (int st = 0; st < kStages; ++st) {
+        const int n = (uses + kStages - 1 - st) / kStages;
+        if (n > 0) {
+            mbar_wait(&sh.k_full[st], (n - 1) & 1, a.err, kDrainNs);
+            mbar_wait(&sh.v_full[st], (n - 1) & 1, a.err, kDrainNs);
+        }
+    }
+}
+
+// The warp that tells the first CTA, whose MMA warps wait for both, what landed here.
+// Values of keys that no row of the item sees may be anything: they are zeroed.  So are,
+// in tiles where some row does not see some key, elements that are not finite (a
+// probability of 0 would make them NaN for that row); the rows that do see such a key
+// get them when the item ends.
+template <int D>
+__device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8_t* vs) {
+    using F = Cfg<D>;
+    const AttnArgs& a = x.a;
+    const int lane = threadIdx.x & 31;
+    Ctx& ctx = sh.ctx[4];
+    ctx.start<32>(a, sh.plan);
+    Slot at;
+    bool dead = false;
+    while (!dead && ctx.next<32>(a)) {
+        for (int j = 0; j < ctx.tiles; ++j, at.step()) {
+            dead = !warp_wait(&sh.k_full[at.st], at.ph, a.err, a.timeout_ns);
+            if (dead) break;
+            if (lane == 0) arrive_first(&sh.k_ready[at.st]);
+            dead = !warp_wait(&sh.v_full[at.st], at.ph, a.err, a.timeout_ns);
+            if (dead) break;
+            const int j0 = ctx.key0(j), lo = max(ctx.it.lo, ctx.lo_all), hi = min(ctx.it.hi, ctx.hi_all);
+            if (j0 < lo || j0 + kKT > hi) {
+                bool any = false;
+                uint8_t* v = vs + at.st * F::kVBytes;
+                for (int e = lane; e < kKT * 8; e += 32) {       // 16 bytes of key e / 8
+                    uint4* p = reinterpret_cast<uint4*>(v + e * 16);
+                    const int key = j0 + (e >> 3);
+                    uint32_t w[4] = {p->x, p->y, p->z, p->w};
+                    bool put = key < ctx.it.lo || key >= ctx.it.hi;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (put) w[i] = 0;
+                        if ((w[i] & 0x7F80u) == 0x7F80u) {
+                            w[i] &= 0xFFFF0000u;
+                            any = true;
+                        }
+                        if ((w[i] & 0x7F800000u) == 0x7F800000u) {
+                            w[i] &= 0xFFFFu;
+                            any = true;
+                        }
+                    }
+                    if (put || any) *p = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (any) {                                       // in both CTAs: each has all columns of its rows
+                    for (uint32_t r = 0; r < 2; ++r)
+                        asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.u32 [p], %2;\n\t}" ::"r"(
+                                         smem_u32(&sh.bad)),
+                                     "r"(r), "r"(1)
+                                     : "memory");
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                }
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) arrive_first(&sh.v_ready[at.st]);
+        }
+    }
+}
+
+// The MMA warp of stream s, in the first CTA.  The streams' warps take turns, a burst each: PV of
+// a tile, then QK of the next (which writes S over that P); a warp's waits run beside
+// the other's burst (see attn_tile.cu).
+template <int D>
+__device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint8_t* qs, uint8_t* ks, uint8_t* vs, int s) {
+    using F = Cfg<D>;
+    constexpr uint32_t kM256 = static_cast<uint32_t>(128 >> 4) << 24;   // beyond idesc's M = 128
+    constexpr uint32_t kIdQK = idesc(false, kKT) + kM256, kIdPV = idesc(true, D) + kM256;
+    const AttnArgs& a = x.a;
+    const uint32_t colS = sh.tmem + 128 * s, colO = sh.tmem + kColO + 128 * s;
+    const uint64_t qd = sdesc(smem_u32(qs + s * F::kQBytes), 16, 1024);
+    const uint64_t kd = sdesc(smem_u32(ks), 16, 1024), vd = sdesc(smem_u32(vs), kPanel, 1024);
+    Ctx& ctx = sh.ctx[3];
+    ctx.start<64>(a, sh.plan);
+    Slot ka, va;
+    uint32_t qp = 0, pp = 0, tp = 0;
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !warp_wait(bar, parity, a.err, a.timeout_ns);
+    };
+    if (s == 1 && (threadIdx.x & 31) == 0) mbar_arrive(&sh.turn[0]);   // stream 0 begins
+    while (ctx.next<64>(a, kBarMma)) {
+        const int T = ctx.tiles, a0 = s ? ctx.a[1] : ctx.a[0], b0 = s ? ctx.b[1] : ctx.b[0];
+        if (T == 0) continue;
+        if (b0 > a0) {
+            wait(&sh.q_ready[s], qp);
+            qp ^= 1u;
+        }
+        for (int i = 0; i <= T; ++i) {
+            const bool do_v = i > a0 && i <= b0, do_k = i >= a0 && i < b0, has_v = i > 0, has_k = i < T;
+            const int vst = va.st, kst = ka.st;
+            if (has_v) {
+                wait(&sh.v_ready[vst], va.ph);
+                va.step();
+            }
+            if (has_k) {
+                wait(&sh.k_ready[kst], ka.ph);
+                ka.step();
+            }
+            if (do_v) {
+                wait(&sh.p_ready[s], pp);
+                pp ^= 1u;
+            }
+            wait(&sh.turn[s], tp);
+            tp ^= 1u;
+            tc_fence_after();
+            if (elect_one() && !dead) {
+                if (do_v) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        pair_mma_ts(colO, colS + 8 * k, vd + ((vst * F::kVBytes + k * 2048) >> 4), kIdPV, i - 1 > a0 || k > 0);
+                    if (i == b0) pair_commit(&sh.o_full[s]);
+                }
+                if (has_v) pair_commit(&sh.v_empty[vst]);
+                if (do_k) {
+#pragma unroll
+                    for (int k = 0; k < D / 16 + 4; ++k)
+                        pair_mma(colS, qd + (((k >> 2) * kPanel + (k & 3) * 32) >> 4),
+                                 kd + ((kst * F::kKBytes + (k >> 2) * F::kKPanel + (k & 3) * 32) >> 4), kIdQK, k > 0);
+                    pair_commit(&sh.s_full[s]);
+                }
+                if (has_k) pair_commit(&sh.k_empty[kst]);
+                mbar_arrive(&sh.turn[s ^ 1]);
+            }
+            __syncwarp();
+        }
+    }
+    // the products end before the accumulators are given back
+    if (elect_one()) pair_commit(&sh.done[s]);
+    __syncwarp();
+    mbar_wait(&sh.done[s], 0, a.err, kDrainNs);
+}
+
+// What a softmax thread carries through an item: its row's reference (log2 units)
+// and sum of powers, in two parts.
+struct RowState {
+    float ref, sum0, sum1;
+};
+
+__device__ __forceinline__ float max32(const float (&x)[32]) {
+    float t[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], fmaxf(x[e + 2 * k], x[e + 2 * k + 1]));
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// Takes a tile's maximum into the reference, and O with it where the reference moves
+// (its products are complete: S came after them in the MMA thread's order).
+template <int D>
+__device__ __forceinline__ void follow(uint32_t colO, float top, bool started, RowState& st) {
+    if (!(top > kNegInf)) top = kNegInf;                         // (NaN: the sums carry it)
+    const bool grow = top > st.ref + kLag || (st.ref == kNegInf && top > kNegInf);
+    if (started && __any_sync(0xFFFFFFFFu, grow)) {
+        const float f = !grow ? 1.0f : (st.ref == kNegInf ? 0.0f : fast_exp2(st.ref - top));
+        st.sum0 *= f;
+        st.sum1 *= f;
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+            float o[16];
+            tmem_ld16(colO + 16 * q, o);
+            tmem_wait_ld();
+            uint32_t u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+            tmem_st16(colO + 16 * q, u);
+        }
+    }
+    if (grow) st.ref = top;
+}
+
+// 32 scores to powers: summed in fp32, rounded to bf16 (the products' type, whose
+// range holds any power), stored as P of their keys: 16 columns of pairs.
+__device__ __forceinline__ void powers(uint32_t colP, const float (&x)[32], float c, float off, RowState& st) {
+    uint32_t u[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float p0, p1;
+        fma2_to(p0, p1, x[e], x[e + 1], c, off);
+        p0 = fast_exp2(p0);
+        p1 = fast_exp2(p1);
+        add2(st.sum0, st.sum1, p0, p1);
+        u[e / 2] = pack_bf16(p0, p1);
+    }
+    tmem_st16(colP, u);
+}
+
+// The CTA's 128 rows of a stream into shared memory, K-major with the 128-byte swizzle:
+// a warp copies whole rows; rows past the last are zeros.
+template <int D>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int row0, int count, bool negate, uint8_t* qt) {
+    constexpr int kChunks = (D + kLatentRot) / 8;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+    auto place = [&](int r, int ch) { return qt + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+#pragma unroll 4
+    for (int r = warp; r < 128; r += 4) {
+        const uint16_t* src = a.q + int64_t(it.s.q0 + row0 + (r < count ? r : 0)) * a.q_stride + it.h * (D + kLatentRot);
+        if (lane < kChunks)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(r, lane))), "l"(src + 8 * lane),
+                         "r"(r < count ? 16u : 0u)
+                         : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (negate) {
+#pragma unroll 1
+        for (int r = warp; r < 128; r += 4)
+            if (lane < kChunks) {
+                uint4* p = reinterpret_cast<uint4*>(place(r, lane));
+                const uint4 w = *p;
+                *p = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
+            }
+    }
+    fence_async_smem();
+}
+
+template <int D>
+__device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, uint8_t* qs, int pair, int rank) {
+    using F = Cfg<D>;
+    const AttnArgs& a = xa.a;
+    const int tid = threadIdx.x, s = tid >> 7, lr = tid & 127, lane = tid & 31;
+    const uint32_t tm = sh.tmem + (static_cast<uint32_t>(tid & 96) << 16);
+    const uint32_t colS = tm + 128 * s, colO = tm + kColO + 128 * s;
+    Ctx& ctx = sh.ctx[s];
+    ctx.start<128>(a, sh.plan);
+    const Item& it = ctx.it;
+    uint32_t sp = 0, op = 0;
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
+        tc_fence_after();
+    };
+    // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf); the sign goes to the queries
+    const float cs = a.scale * kLog2e;
+    const float c = fmaxf(fabsf(cs), 1.2e-38f);
+    while (ctx.next<128>(a, kBarGroup + s)) {
+        const int row0 = s * kStream + rank * 128, count = min(max(ctx.rows - row0, 0), 128);
+        const int t0 = s ? ctx.a[1] : ctx.a[0], n = (s ? ctx.b[1] : ctx.b[0]) - t0;
+        const int wlo = s ? ctx.wlo[1] : ctx.wlo[0], whi = s ? ctx.whi[1] : ctx.whi[0];
+        const bool valid = lr < count, warp_on = __any_sync(0xFFFFFFFFu, valid);
+        const int qi = it.rt * kMT + row0 + (valid ? lr : 0);
+        RowView view{0, 0, 0ull};
+        if (valid) view = row_view(a, it.s, qi);
+        if (n > 0) {
+            load_queries<D>(a, it, it.rt * kMT + row0, count, cs < 0.0f, qs + s * F::kQBytes);
+            __syncwarp();
+            if (lane == 0) arrive_first(&sh.q_ready[s]);
+        }
+        RowState st{kNegInf, 0.0f, 0.0f};
+        for (int i = 0; i < n; ++i) {
+            const int j0 = ctx.key0(t0 + i);
+            wait(&sh.s_full[s], sp);
+            sp ^= 1u;
+            if (warp_on) {
+                const bool whole = j0 >= wlo && j0 + kKT <= whi;
+                if (whole) {
+                    float x[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(colS + 32 * q, x[q]);
+                    tmem_wait_ld();
+                    const float top = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3])));
+                    follow<D>(colO, top * c, i > 0, st);
+                    const float off = st.ref == kNegInf ? 0.0f : -st.ref;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) powers(colS + 16 * q, x[q], c, off, st);
+                } else {
+                    float x[32], top = kNegInf;
+                    auto piece = [&](int q) {
+                        tmem_ld32(colS + 32 * q, x);
+                        tmem_wait_ld();
+                        const uint32_t bits = row_bits(view, false, it.s.first, j0 + 32 * q);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) x[e] = kNegInf;
+                    };
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        piece(q);
+                        top = fmaxf(top, max32(x));
+                    }
+                    follow<D>(colO, top * c, i > 0, st);
+                    const float off = st.ref == kNegInf ? 0.0f : -st.ref;
+                    // P of piece q lies at columns 16 q, in S pieces that have been read
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        piece(q);
+                        powers(colS + 16 * q, x, c, off, st);
+                    }
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_first(&sh.p_ready[s]);
+        }
+        // --- the item's rows: normalised, or this pair's piece of them
+        const float sum = st.sum0 + st.sum1;
+        float ref = st.ref;
+        if (sum != sum) ref = fmaxf(ref, 0.0f);                  // a NaN is a result, not an empty row
+        const bool piece = it.t0 > 0 || it.t1 < it.n;
+        float* slot = a.partials + (int64_t(it.t0 == 0 ? 0 : kMaxPairs) + pair) * (kMT * (D + 2));
+        const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + it.h;
+        const float weight = ref == kNegInf || n == 0 ? 0.0f : (piece ? 1.0f : 1.0f / sum);
+        if (valid) {
+            if (piece)
+                *reinterpret_cast<float2*>(slot + kMT * D + 2 * (row0 + lr)) = make_float2(ref, sum);
+            else if (a.lse)
+                a.lse[at] = ref == kNegInf ? kNegInf : (ref + log2f(sum)) * kLn2;
+        }
+        if (n > 0) {
+            wait(&sh.o_full[s], op);
+            op ^= 1u;
+        }
+        const bool bad = *const_cast<volatile int*>(&sh.bad) != 0;
+        if (warp_on) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                tmem_ld32(colO + 32 * q, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = weight != 0.0f ? o[e] * weight : 0.0f;
+                if (bad && valid) {
+                    // values that are not finite, of the masked tiles' keys that this row sees
+                    const int64_t k0 = xa.cu_k[it.b];
+                    for (int j = max(view.lo, ctx.key0(0)); j < min(view.hi, ctx.key0(ctx.tiles)); ++j) {
+                        const int tile = j - j % kKT;
+                        if (tile >= ctx.lo_all && tile + kKT <= min(ctx.it.hi, ctx.hi_all)) continue;
+                        if (k0 + j < 0 || k0 + j >= xa.n_keys) continue;
+                        const uint16_t* v = xa.v + (k0 + j) * xa.v_token + it.h * xa.v_head + 32 * q;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const uint32_t w = v[e];
+                            if ((w & 0x7F80u) == 0x7F80u) o[e] += bf16_bits_to_f32(w);
+                        }
+                    }
+                }
+                if (valid) {
+                    if (piece) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4*>(slot + ((8 * q + e) * kMT + row0 + lr) * 4) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4*>(a.out + at * D + 32 * q + 8 * e) =
+                                make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                           pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+        if (tid == 0 && rank == 0) note_split(a, it, ctx.rows, kMT, sh.plan, pair);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArgs x, const __grid_constant__ ExpandedMaps maps) {
+    using F = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    uint8_t* qs = dyn;
+    uint8_t* ks = qs + 2 * F::kQBytes;
+    uint8_t* vs = ks + kStages * F::kKBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(dyn + F::kSmem);
+    const AttnArgs& a = x.a;
+    const int warp = threadIdx.x >> 5, pair = blockIdx.x >> 1, rank = static_cast<int>(cta_rank());
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.v_full[i], 1);
+            mbar_init(&sh.k_empty[i], 2);                        // both streams' products
+            mbar_init(&sh.v_empty[i], 2);
+            mbar_init(&sh.k_ready[i], 2);                        // both CTAs' passing warps
+            mbar_init(&sh.v_ready[i], 2);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.q_ready[s], 8);
+            mbar_init(&sh.p_ready[s], 8);
+            mbar_init(&sh.turn[s], 1);
+            mbar_init(&sh.s_full[s], 1);
+            mbar_init(&sh.o_full[s], 1);
+            mbar_init(&sh.done[s], 1);
+        }
+        sh.bad = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.rope);
+        prefetch_tensormap(&maps.v);
+    }
+    if (warp == 8) pair_alloc(&sh.tmem);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                              // both CTAs' barriers are there
     pdl_wait();
     pdl_launch_dependents();
-    if (u >= int64_t(a.sq.tokens) * a.q_heads) return;
-    const int t = static_cast<int>(u / a.q_heads), h = static_cast<int>(u % a.q_heads);
-    Seq s;
-    int b = -1;
-    for (int i = 0; i < a.sq.n; ++i) {
-        bool fits;
-        s = load_seq(a.sq, 1, i, a.err, &fits);
-        if (!fits) break;
-        if (t >= s.q0 && t < s.q0 + s.nq) {
-            b = i;
-            break;
-        }
+    plan_work<kMT, kKT>(a, 1, sh.scan, &sh.plan, pair, gridDim.x >> 1, rank == 0);   // (its barriers publish sh.tmem)
+    tc_fence_after();
+    zero_pad_rows(a, sh.plan.seqs);
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        soften<D>(x, sh, qs, pair, rank);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == 8)
+            produce<D>(x, maps, sh, ks, vs, rank);
+        else if (warp == 11)
+            pass_on<D>(x, sh, vs);
+        else if (rank == 0)
+            multiply<D>(x, sh, qs, ks, vs, warp - 9);
     }
-    uint16_t* out = a.out + u * D;
-    float o[kOwn] = {};
-    float top = kNegInf, sum = 0.0f;
-    if (b >= 0) {
-        const uint16_t* q = a.q + t * a.q_stride + h * (D + kLatentRot);
-        float qc[kOwn], qr[2];
-        for (int i = 0; i < kOwn; ++i) qc[i] = bf16_bits_to_f32(q[lane + 32 * i]);
-        for (int i = 0; i < 2; ++i) qr[i] = bf16_bits_to_f32(q[D + lane + 32 * i]);
-        const RowView v = row_view(a, s, t - s.q0);
-        const int k0 = x.cu_k[b];
-        for (int j = max(v.lo, 0); j < v.hi; ++j) {
-            float kx[kOwn] = {}, r[2] = {}, vx[kOwn] = {};
-            const int64_t row = int64_t(k0) + j;
-            if (row < 0 || row >= x.n_keys) {
-                record_error(a.err, MOE_ERR_INVALID_ARG);
-            } else {
-                for (int i = 0; i < kOwn; ++i) {
-                    kx[i] = bf16_bits_to_f32(x.k[row * x.k_token + h * x.k_head + lane + 32 * i]);
-                    vx[i] = bf16_bits_to_f32(x.v[row * x.v_token + h * x.v_head + lane + 32 * i]);
-                }
-                for (int i = 0; i < 2; ++i) r[i] = bf16_bits_to_f32(x.rope[row * x.rope_token + lane + 32 * i]);
-            }
-            float d = qr[0] * r[0] + qr[1] * r[1];
-            for (int i = 0; i < kOwn; ++i) d = fmaf(qc[i], kx[i], d);
-            for (int k = 16; k > 0; k >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, k);
-            const float z = d * a.scale * kLog2e;
-            const float now = fmaxf(top, z);
-            const float keep = top == kNegInf ? 0.0f : exp2f(top - now), p = now == kNegInf && z == z ? 0.0f : exp2f(z - now);
-            sum = sum * keep + p;
-            for (int i = 0; i < kOwn; ++i) o[i] = o[i] * keep + p * vx[i];
-            top = now;
-        }
-    }
-    const bool none = top == kNegInf && !(sum != sum);
-    for (int i = 0; i < kOwn; ++i)
-        out[lane + 32 * i] = static_cast<uint16_t>(pack_bf16(none ? 0.0f : o[i] / sum, 0.0f));
-    if (lane == 0 && a.lse) a.lse[u] = none ? kNegInf : (top + log2f(sum)) * kLn2;
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                              // nothing of the pair is in flight
+    tc_fence_after();
+    if (warp == 8) pair_dealloc(sh.tmem);
+}
+
+template <int D>
+cudaError_t launch(const ExpandedArgs& a, const ExpandedMaps& m, int n_sms, cudaStream_t s) {
+    constexpr size_t smem = Cfg<D>::kSmem + sizeof(Shared);
+    static_assert(smem <= 232448, "227 KB a CTA");
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(expanded_kernel<D>), static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int pairs = n_sms / 2 < kMaxPairs ? n_sms / 2 : kMaxPairs;
+    e = launch_pdl_cluster(expanded_kernel<D>, dim3(2 * pairs), dim3(kThreads), 2, smem, s, a, m);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_pair_join<D, kMT>(a.a, pairs, n_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_expanded(const ExpandedArgs& a, int n_sms, cudaStream_t s) {
-    const int64_t warps = int64_t(a.a.sq.tokens) * a.a.q_heads;
-    const dim3 grid(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)));
-    cudaError_t e = a.dim == 128 ? launch_pdl(expanded_kernel<128>, grid, dim3(kThreads), 0, s, a)
-                                 : launch_pdl(expanded_kernel<64>, grid, dim3(kThreads), 0, s, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+cudaError_t launch_expanded(const ExpandedArgs& a, const ExpandedMaps& m, int n_sms, cudaStream_t s) {
+    return a.dim == 128 ? launch<128>(a, m, n_sms, s) : launch<64>(a, m, n_sms, s);
 }
 
 }  // namespace moe

@@ -53,16 +53,22 @@ struct LatentGatherArgs {
     int32_t* err;
 };
 
-// Workspace of absorbed attention: the control block, one note per pair of CTAs
-// (attn.h), then the pieces of split items, two slots a pair as there.  A slot has
-// kLatentRows rows, fp32: sums [dim/4][row][4], then (reference in log2 units, sum
+// Workspaces: the control block, one note per pair of CTAs (attn.h), then the pieces
+// of split items, two slots a pair as there.  A slot has an item's rows, fp32: sums [dim/4][row][4], then (reference in log2 units, sum
 // of powers) [row][2].
 constexpr int kLatentRows = 128;        // rows of an item
 constexpr int kLatentKeys = 64;         // keys of a tile
-constexpr int kLatentMaxPairs = kAttnMaxCtas / 2;
+constexpr int kMaxPairs = kAttnMaxCtas / 2;
+
+constexpr int kExpandedRows = 512;      // rows of an item of the expanded form
+constexpr int kExpandedKeys = 128;
 
 inline int64_t latent_workspace_bytes(int dim) {
-    return kAttnPartials + int64_t(2) * kLatentMaxPairs * kLatentRows * (dim + 2) * 4;
+    return kAttnPartials + int64_t(2) * kMaxPairs * kLatentRows * (dim + 2) * 4;
+}
+
+inline int64_t expanded_workspace_bytes(int dim) {
+    return kAttnPartials + int64_t(2) * kMaxPairs * kExpandedRows * (dim + 2) * 4;
 }
 
 // Tensor maps of the cache: the latent as a 5-D tensor (64 elements or 128 codes of a
@@ -80,6 +86,14 @@ struct LatentAttnArgs {
     LatentArgs c;
 };
 
+// Tensor maps of the expanded form: k as a 4-D tensor (64 elements, token, such part
+// of the head, head) in boxes of 64 tokens and the whole head; the rotary key (element,
+// token) in boxes of 64 tokens; v (element, token, head) in boxes of 64 elements and 128
+// tokens.  128-byte swizzled; what lies outside reads as zeros.
+struct ExpandedMaps {
+    CUtensorMap k, rope, v;
+};
+
 // Expanded attention: `a` with a kv head of its own for every query head, and
 // pages of one token, so that lengths are cut to the n_keys rows there are.
 struct ExpandedArgs {
@@ -95,6 +109,6 @@ struct ExpandedArgs {
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_latent_gather(const LatentGatherArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_latent_attn(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cudaStream_t s);
-cudaError_t launch_expanded(const ExpandedArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_expanded(const ExpandedArgs& a, const ExpandedMaps& m, int n_sms, cudaStream_t s);
 
 }  // namespace moe

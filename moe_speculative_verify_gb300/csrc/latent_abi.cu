@@ -139,6 +139,25 @@ bool make_maps(const moe_latent_cache_t* c, moe::LatentMaps* m) {
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_maps(const moe::ExpandedArgs& a, moe::ExpandedMaps* m) {
+    auto fn = moe::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t n = a.n_keys, h = a.a.q_heads;
+    const cuuint32_t one[4] = {1, 1, 1, 1}, rows = moe::kExpandedKeys / 2;
+    auto map = [&](CUtensorMap* to, const uint16_t* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+        return fn(to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t kd[4] = {64, n, cuuint64_t(a.dim) / 64, h}, ks[3] = {cuuint64_t(a.k_token) * 2, 128, cuuint64_t(a.k_head) * 2};
+    const cuuint32_t kb[4] = {64, rows, cuuint32_t(a.dim) / 64, 1};
+    const cuuint64_t rd[2] = {moe::kLatentRot, n}, rs[1] = {cuuint64_t(a.rope_token) * 2};
+    const cuuint32_t rb[2] = {moe::kLatentRot, rows};
+    const cuuint64_t vd[3] = {cuuint64_t(a.dim), n, h}, vs[2] = {cuuint64_t(a.v_token) * 2, cuuint64_t(a.v_head) * 2};
+    const cuuint32_t vb[3] = {64, moe::kExpandedKeys, 1};
+    return map(&m->k, a.k, 4, kd, ks, kb) && map(&m->rope, a.rope, 2, rd, rs, rb) && map(&m->v, a.v, 3, vd, vs, vb);
+}
+
 }  // namespace
 
 extern "C" {
@@ -242,7 +261,7 @@ moe_status_t moe_latent_gather(const moe_latent_cache_t* cache, const moe_seqs_t
 
 size_t moe_expanded_workspace_bytes(const moe_attn_t* attn, int32_t v_dim) {
     if (check_attn(attn) != MOE_OK || (v_dim != 64 && v_dim != 128)) return 0;
-    return static_cast<size_t>(moe::attn_workspace_bytes(v_dim));
+    return static_cast<size_t>(moe::expanded_workspace_bytes(v_dim));
 }
 
 moe_status_t moe_expanded_attention(const moe_attn_t* attn, const moe_seqs_t* seqs,
@@ -283,7 +302,9 @@ moe_status_t moe_expanded_attention(const moe_attn_t* attn, const moe_seqs_t* se
     a.rope_token = rope_stride;
     a.v_token = v_token_stride;
     a.v_head = v_head_stride;
-    return cuda_status(moe::launch_expanded(a, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
+    moe::ExpandedMaps maps;
+    if (!make_maps(a, &maps)) return MOE_ERR_CUDA;
+    return cuda_status(moe::launch_expanded(a, maps, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
