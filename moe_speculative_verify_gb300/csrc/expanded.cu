@@ -105,6 +105,7 @@ struct Shared {
     int64_t scan[16];                       // plan_work's
     // of this CTA: what landed, and the room that both streams' products gave back
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t q_full[2], q_empty[2];
     // of the pair, in its first CTA: operands in place in both; the streams' turns
     uint64_t k_ready[kStages], v_ready[kStages], q_ready[2], p_ready[2], turn[2];
     // of this CTA: the pair's products are done
@@ -127,22 +128,25 @@ struct Slot {
 };
 
 // The warp that copies: this CTA's 64 keys of each tile, then its half of the tile's
-// values.  Rows past the sequence's are read as they lie there, or as zeros past the last.
+// values; an item's queries after its first tile, as soon as the last one's have been
+// used, beside that item's end.  Rows past the sequence's are read as they lie there,
+// or as zeros past the last.
 template <int D>
-__device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMaps& maps, Shared& sh, uint8_t* ks, uint8_t* vs, int rank) {
+__device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMaps& maps, Shared& sh, uint8_t* qs, uint8_t* ks, uint8_t* vs,
+                                        int rank) {
     using F = Cfg<D>;
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 31;
     Ctx& ctx = sh.ctx[2];
     ctx.start<32>(a, sh.plan);
     Slot at;
-    int uses = 0;
+    int uses = 0, used[2] = {0, 0};                              // tiles begun; items of a stream
     bool dead = false;
     while (!dead && ctx.next<32>(a)) {
         const Item& it = ctx.it;
         const int64_t k0 = x.cu_k[it.b];
         if (lane == 0 && (k0 < 0 || k0 + it.s.len > x.n_keys)) record_error(a.err, MOE_ERR_INVALID_ARG);
-        for (int j = 0; j < ctx.tiles; ++j, at.step(), ++uses) {
+        for (int j = 0; j < ctx.tiles && !dead; ++j) {
             // (a place far outside stays outside, whatever 32 bits make of the sum)
             const int row = static_cast<int>(min(max(k0 + ctx.key0(j), int64_t(-(1 << 30))), int64_t(x.n_keys)));
             dead = !warp_wait(&sh.k_empty[at.st], at.ph ^ 1u, a.err, a.timeout_ns);
@@ -155,18 +159,31 @@ __device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMap
             }
             __syncwarp();
             dead = !warp_wait(&sh.v_empty[at.st], at.ph ^ 1u, a.err, a.timeout_ns);
-            if (lane == 0 && !dead) {
-                mbar_arrive_expect_tx(&sh.v_full[at.st], F::kVBytes);
-                tma_load_3d(vs + at.st * F::kVBytes, &maps.v, &sh.v_full[at.st], rank * (D / 2), row, it.h);
-            }
-            __syncwarp();
             if (dead) {                                          // this stage's K alone
                 mbar_wait(&sh.k_full[at.st], at.ph, a.err, kDrainNs);
                 break;
             }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh.v_full[at.st], F::kVBytes);
+                tma_load_3d(vs + at.st * F::kVBytes, &maps.v, &sh.v_full[at.st], rank * (D / 2), row, it.h);
+            }
+            __syncwarp();
+            at.step();
+            ++uses;
+            for (int s = 0; s < 2 && j == 0; ++s) {
+                if ((s ? ctx.b[1] - ctx.a[1] : ctx.b[0] - ctx.a[0]) <= 0) continue;
+                dead = dead || !warp_wait(&sh.q_empty[s], (used[s] & 1) ^ 1, a.err, a.timeout_ns);
+                if (dead) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.q_full[s], F::kQBytes);
+                    tma_load_4d(qs + s * F::kQBytes, &maps.q, &sh.q_full[s], 0, it.s.q0 + it.rt * kMT + s * kStream + rank * 128, 0, it.h);
+                }
+                __syncwarp();
+                ++used[s];
+            }
         }
     }
-    // each stage's last copies
+    // the last copies
     for (int st = 0; st < kStages; ++st) {
         const int n = (uses + kStages - 1 - st) / kStages;
         if (n > 0) {
@@ -174,6 +191,16 @@ __device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMap
             mbar_wait(&sh.v_full[st], (n - 1) & 1, a.err, kDrainNs);
         }
     }
+    for (int s = 0; s < 2; ++s)
+        if (used[s] > 0) mbar_wait(&sh.q_full[s], (used[s] - 1) & 1, a.err, kDrainNs);
+}
+
+// Whether a pair of bf16 has one that is not finite (its sign bit or, in the upper one,
+// a carry into it tells), and the pair with such as zeros.
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    const uint32_t n = nonfinite2(w);
+    return w & ((n & 0x8000u ? 0u : 0xFFFFu) | (n & 0x80000000u ? 0u : 0xFFFF0000u));
 }
 
 // The warp that tells the first CTA, whose MMA warps wait for both, what landed here.
@@ -189,6 +216,7 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
     Ctx& ctx = sh.ctx[4];
     ctx.start<32>(a, sh.plan);
     Slot at;
+    uint32_t qp[2] = {0, 0};
     bool dead = false;
     while (!dead && ctx.next<32>(a)) {
         for (int j = 0; j < ctx.tiles; ++j, at.step()) {
@@ -200,25 +228,24 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
             const int j0 = ctx.key0(j), lo = max(ctx.it.lo, ctx.lo_all), hi = min(ctx.it.hi, ctx.hi_all);
             if (j0 < lo || j0 + kKT > hi) {
                 bool any = false;
-                uint8_t* v = vs + at.st * F::kVBytes;
-                for (int e = lane; e < kKT * 8; e += 32) {       // 16 bytes of key e / 8
-                    uint4* p = reinterpret_cast<uint4*>(v + e * 16);
-                    const int key = j0 + (e >> 3);
-                    uint32_t w[4] = {p->x, p->y, p->z, p->w};
-                    bool put = key < ctx.it.lo || key >= ctx.it.hi;
+                uint8_t* v = vs + at.st * F::kVBytes + lane * 16;
+                const int key0 = j0 + (lane >> 3), see0 = ctx.it.lo, see1 = ctx.it.hi;
+#pragma unroll 1
+                for (int e0 = 0; e0 < kKT / 4; e0 += 8) {        // 16 bytes of eight keys at a time
+                    uint4 w[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (put) w[i] = 0;
-                        if ((w[i] & 0x7F80u) == 0x7F80u) {
-                            w[i] &= 0xFFFF0000u;
-                            any = true;
-                        }
-                        if ((w[i] & 0x7F800000u) == 0x7F800000u) {
-                            w[i] &= 0xFFFFu;
+                    for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint4*>(v + (e0 + e) * 512);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int key = key0 + 4 * (e0 + e);
+                        uint4* p = reinterpret_cast<uint4*>(v + (e0 + e) * 512);
+                        if (key < see0 || key >= see1) {
+                            *p = make_uint4(0, 0, 0, 0);
+                        } else if (nonfinite2(w[e].x) | nonfinite2(w[e].y) | nonfinite2(w[e].z) | nonfinite2(w[e].w)) {
+                            *p = make_uint4(finite2(w[e].x), finite2(w[e].y), finite2(w[e].z), finite2(w[e].w));
                             any = true;
                         }
                     }
-                    if (put || any) *p = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 if (any) {                                       // in both CTAs: each has all columns of its rows
                     for (uint32_t r = 0; r < 2; ++r)
@@ -232,6 +259,13 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
                 __syncwarp();
             }
             if (lane == 0) arrive_first(&sh.v_ready[at.st]);
+            for (int s = 0; s < 2 && j == 0; ++s) {
+                if ((s ? ctx.b[1] - ctx.a[1] : ctx.b[0] - ctx.a[0]) <= 0) continue;
+                dead = dead || !warp_wait(&sh.q_full[s], s ? qp[1] : qp[0], a.err, a.timeout_ns);
+                if (lane == 0 && !dead) arrive_first(&sh.q_ready[s]);
+                qp[s] ^= 1u;
+            }
+            if (dead) break;
         }
     }
 }
@@ -296,6 +330,7 @@ __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint
                         pair_mma(colS, qd + (((k >> 2) * kPanel + (k & 3) * 32) >> 4),
                                  kd + ((kst * F::kKBytes + (k >> 2) * F::kKPanel + (k & 3) * 32) >> 4), kIdQK, k > 0);
                     pair_commit(&sh.s_full[s]);
+                    if (i == b0 - 1) pair_commit(&sh.q_empty[s]);
                 }
                 if (has_k) pair_commit(&sh.k_empty[kst]);
                 mbar_arrive(&sh.turn[s ^ 1]);
@@ -364,37 +399,8 @@ __device__ __forceinline__ void powers(uint32_t colP, const float (&x)[32], floa
     tmem_st16(colP, u);
 }
 
-// The CTA's 128 rows of a stream into shared memory, K-major with the 128-byte swizzle:
-// a warp copies whole rows; rows past the last are zeros.
 template <int D>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int row0, int count, bool negate, uint8_t* qt) {
-    constexpr int kChunks = (D + kLatentRot) / 8;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-    auto place = [&](int r, int ch) { return qt + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
-#pragma unroll 4
-    for (int r = warp; r < 128; r += 4) {
-        const uint16_t* src = a.q + int64_t(it.s.q0 + row0 + (r < count ? r : 0)) * a.q_stride + it.h * (D + kLatentRot);
-        if (lane < kChunks)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(r, lane))), "l"(src + 8 * lane),
-                         "r"(r < count ? 16u : 0u)
-                         : "memory");
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (negate) {
-#pragma unroll 1
-        for (int r = warp; r < 128; r += 4)
-            if (lane < kChunks) {
-                uint4* p = reinterpret_cast<uint4*>(place(r, lane));
-                const uint4 w = *p;
-                *p = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
-            }
-    }
-    fence_async_smem();
-}
-
-template <int D>
-__device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, uint8_t* qs, int pair, int rank) {
-    using F = Cfg<D>;
+__device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int pair, int rank) {
     const AttnArgs& a = xa.a;
     const int tid = threadIdx.x, s = tid >> 7, lr = tid & 127, lane = tid & 31;
     const uint32_t tm = sh.tmem + (static_cast<uint32_t>(tid & 96) << 16);
@@ -408,7 +414,7 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, uint8
         if (!dead && !mbar_wait(bar, parity, a.err, a.timeout_ns)) dead = true;
         tc_fence_after();
     };
-    // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf); the sign goes to the queries
+    // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf); the sign goes to the scores
     const float cs = a.scale * kLog2e;
     const float c = fmaxf(fabsf(cs), 1.2e-38f);
     while (ctx.next<128>(a, kBarGroup + s)) {
@@ -419,11 +425,6 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, uint8
         const int qi = it.rt * kMT + row0 + (valid ? lr : 0);
         RowView view{0, 0, 0ull};
         if (valid) view = row_view(a, it.s, qi);
-        if (n > 0) {
-            load_queries<D>(a, it, it.rt * kMT + row0, count, cs < 0.0f, qs + s * F::kQBytes);
-            __syncwarp();
-            if (lane == 0) arrive_first(&sh.q_ready[s]);
-        }
         RowState st{kNegInf, 0.0f, 0.0f};
         for (int i = 0; i < n; ++i) {
             const int j0 = ctx.key0(t0 + i);
@@ -431,40 +432,30 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, uint8
             sp ^= 1u;
             if (warp_on) {
                 const bool whole = j0 >= wlo && j0 + kKT <= whi;
-                if (whole) {
-                    float x[4][32];
+                float x[4][32];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(colS + 32 * q, x[q]);
-                    tmem_wait_ld();
-                    const float top = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3])));
-                    follow<D>(colO, top * c, i > 0, st);
-                    const float off = st.ref == kNegInf ? 0.0f : -st.ref;
+                for (int q = 0; q < 4; ++q) tmem_ld32(colS + 32 * q, x[q]);
+                tmem_wait_ld();
+                if (cs < 0.0f) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) powers(colS + 16 * q, x[q], c, off, st);
-                } else {
-                    float x[32], top = kNegInf;
-                    auto piece = [&](int q) {
-                        tmem_ld32(colS + 32 * q, x);
-                        tmem_wait_ld();
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[q][e] = -x[q][e];
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
                         const uint32_t bits = row_bits(view, false, it.s.first, j0 + 32 * q);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!((bits >> e) & 1u)) x[e] = kNegInf;
-                    };
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        piece(q);
-                        top = fmaxf(top, max32(x));
-                    }
-                    follow<D>(colO, top * c, i > 0, st);
-                    const float off = st.ref == kNegInf ? 0.0f : -st.ref;
-                    // P of piece q lies at columns 16 q, in S pieces that have been read
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        piece(q);
-                        powers(colS + 16 * q, x, c, off, st);
+                            if (!((bits >> e) & 1u)) x[q][e] = kNegInf;
                     }
                 }
+                const float top = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3])));
+                follow<D>(colO, top * c, i > 0, st);
+                const float off = st.ref == kNegInf ? 0.0f : -st.ref;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) powers(colS + 16 * q, x[q], c, off, st);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -555,7 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             mbar_init(&sh.v_ready[i], 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sh.q_ready[s], 8);
+            mbar_init(&sh.q_full[s], 1);
+            mbar_init(&sh.q_empty[s], 1);
+            mbar_init(&sh.q_ready[s], 2);
             mbar_init(&sh.p_ready[s], 8);
             mbar_init(&sh.turn[s], 1);
             mbar_init(&sh.s_full[s], 1);
@@ -564,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
         }
         sh.bad = 0;
         fence_barrier_init();
+        prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.rope);
         prefetch_tensormap(&maps.v);
@@ -579,11 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
     zero_pad_rows(a, sh.plan.seqs);
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        soften<D>(x, sh, qs, pair, rank);
+        soften<D>(x, sh, pair, rank);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (warp == 8)
-            produce<D>(x, maps, sh, ks, vs, rank);
+            produce<D>(x, maps, sh, qs, ks, vs, rank);
         else if (warp == 11)
             pass_on<D>(x, sh, vs);
         else if (rank == 0)

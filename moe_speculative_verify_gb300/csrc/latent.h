@@ -86,12 +86,12 @@ struct LatentAttnArgs {
     LatentArgs c;
 };
 
-// Tensor maps of the expanded form: k as a 4-D tensor (64 elements, token, such part
-// of the head, head) in boxes of 64 tokens and the whole head; the rotary key (element,
+// Tensor maps of the expanded form: q and k as 4-D tensors (64 elements, token, such
+// part of the head, head) in boxes of 128 and 64 tokens and the whole head; the rotary key (element,
 // token) in boxes of 64 tokens; v (element, token, head) in boxes of 64 elements and 128
 // tokens.  128-byte swizzled; what lies outside reads as zeros.
 struct ExpandedMaps {
-    CUtensorMap k, rope, v;
+    CUtensorMap q, k, rope, v;
 };
 
 // Expanded attention: `a` with a kv head of its own for every query head, and

@@ -149,13 +149,16 @@ bool make_maps(const moe::ExpandedArgs& a, moe::ExpandedMaps* m) {
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
+    const cuuint64_t qd[4] = {64, cuuint64_t(a.a.sq.tokens), cuuint64_t(a.dim) / 64 + 1, h};
+    const cuuint64_t qs[3] = {cuuint64_t(a.a.q_stride) * 2, 128, (cuuint64_t(a.dim) + moe::kLatentRot) * 2};
+    const cuuint32_t qb[4] = {64, 128, cuuint32_t(a.dim) / 64 + 1, 1};
     const cuuint64_t kd[4] = {64, n, cuuint64_t(a.dim) / 64, h}, ks[3] = {cuuint64_t(a.k_token) * 2, 128, cuuint64_t(a.k_head) * 2};
     const cuuint32_t kb[4] = {64, rows, cuuint32_t(a.dim) / 64, 1};
     const cuuint64_t rd[2] = {moe::kLatentRot, n}, rs[1] = {cuuint64_t(a.rope_token) * 2};
     const cuuint32_t rb[2] = {moe::kLatentRot, rows};
     const cuuint64_t vd[3] = {cuuint64_t(a.dim), n, h}, vs[2] = {cuuint64_t(a.v_token) * 2, cuuint64_t(a.v_head) * 2};
     const cuuint32_t vb[3] = {64, moe::kExpandedKeys, 1};
-    return map(&m->k, a.k, 4, kd, ks, kb) && map(&m->rope, a.rope, 2, rd, rs, rb) && map(&m->v, a.v, 3, vd, vs, vb);
+    return map(&m->q, a.a.q, 4, qd, qs, qb) && map(&m->k, a.k, 4, kd, ks, kb) && map(&m->rope, a.rope, 2, rd, rs, rb) && map(&m->v, a.v, 3, vd, vs, vb);
 }
 
 }  // namespace
