@@ -31,7 +31,7 @@ constexpr int kStages = 3;
 // Registers a thread, moved between the warpgroups after the launch at 168:
 // 8 * 208 + 4 * 80 = 1984 a lane column of the 12 * 168 = 2016 launched.
 constexpr int kRegsSoft = 208, kRegsRest = 80;
-constexpr int kBarGroup = 1, kBarMma = 3;                        // named barriers: each softmax warpgroup, the MMA warps
+constexpr int kAhead = 4;                // items that the copying warp may be ahead by
 constexpr uint32_t kColO = 256;          // S/P of stream s at column 128 s, O at 256 + 128 s
 constexpr float kLag = 8.0f;             // log2 of what powers may grow to
 
@@ -44,39 +44,17 @@ struct Cfg {
     static constexpr size_t kSmem = 2 * kQBytes + kStages * (kKBytes + kVBytes);   // then Shared
 };
 
-// A role's place in the pair's work, in shared memory; THREADS threads share it, at
-// named barrier `bar`.
-struct Ctx {
-    Walk<kMT, kKT> wk;
+// An item as the CTA's warps work on it.  The copying warp walks the pair's items and
+// queues them here; each other role takes its own way through the queue.
+struct Job {
     Item it;
-    int more;
+    int more;                // 0: none; no other field holds
     int rows;                // rows of the item
     int tiles;               // key tiles of this pair (0: nothing seen)
     int a[2], b[2];          // stream s takes local tiles a .. b-1
     int wlo[2], whi[2];      // keys that every row of the stream sees
     int lo_all, hi_all;      // and of the item
 
-    template <int THREADS>
-    __device__ __forceinline__ void sync(int bar) {
-        if constexpr (THREADS == 32)
-            __syncwarp();
-        else
-            named_bar(bar, THREADS);
-    }
-    template <int THREADS>
-    __device__ __forceinline__ void start(const AttnArgs& at, const Plan& p) {
-        if (threadIdx.x % THREADS == 0) wk.start(at, p);
-    }
-    template <int THREADS>
-    __device__ __forceinline__ bool next(const AttnArgs& at, int bar = 0) {
-        sync<THREADS>(bar);
-        if (threadIdx.x % THREADS == 0) {
-            more = wk.next(at, it);
-            if (more) set(at);
-        }
-        sync<THREADS>(bar);
-        return more != 0;
-    }
     __device__ __forceinline__ void set(const AttnArgs& at) {
         const int r0 = it.rt * kMT;
         rows = min(kMT, it.s.nq - r0);
@@ -98,6 +76,8 @@ struct Ctx {
             b[s] = k.y > k.x ? max(min((k.y + kKT - 1) / kKT - base, tiles), a[s]) : a[s];
         }
     }
+    __device__ __forceinline__ int first(int s) const { return s ? a[1] : a[0]; }
+    __device__ __forceinline__ int last(int s) const { return s ? b[1] : b[0]; }
     __device__ __forceinline__ int key0(int tile) const { return (it.tile0 + it.t0 + tile) * kKT; }
 };
 
@@ -106,12 +86,16 @@ struct Shared {
     // of this CTA: what landed, and the room that both streams' products gave back
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_full[2], q_empty[2];
-    // of the pair, in its first CTA: operands in place in both; the streams' turns
-    uint64_t k_ready[kStages], v_ready[kStages], q_ready[2], p_ready[2], turn[2];
+    // of the pair, in its first CTA: operands in place in both
+    uint64_t k_ready[kStages], v_ready[kStages], q_ready[2];
+    uint64_t p_ready[2][2];                 // by half of a tile's keys
     // of this CTA: the pair's products are done
     uint64_t s_full[2], o_full[2], done[2];
     Plan plan;
-    Ctx ctx[5];                             // the softmax warpgroups', copies, MMA, passing on
+    Walk<kMT, kKT> walk;                    // the copying warp's
+    Job job[kAhead];
+    uint64_t job_full[kAhead], job_empty[kAhead];
+    int lock;                               // whether a stream's products are being issued
     uint32_t tmem;
     int bad;                                // some masked tile had values that are not finite
 };
@@ -127,6 +111,18 @@ struct Slot {
     }
 };
 
+// A warp's way through the queue.
+struct Jobs {
+    int n = 0;
+    __device__ __forceinline__ const Job* next(Shared& sh, const AttnArgs& a) {
+        if (!warp_wait(&sh.job_full[n % kAhead], (n / kAhead) & 1, a.err, a.timeout_ns)) return nullptr;
+        const Job* j = &sh.job[n % kAhead];
+        return j->more ? j : nullptr;
+    }
+    // by one thread of the warp, once all have read what they need of the item
+    __device__ __forceinline__ void done(Shared& sh) { mbar_arrive(&sh.job_empty[n % kAhead]); }
+};
+
 // The warp that copies: this CTA's 64 keys of each tile, then its half of the tile's
 // values; an item's queries after its first tile, as soon as the last one's have been
 // used, beside that item's end.  Rows past the sequence's are read as they lie there,
@@ -137,18 +133,27 @@ __device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMap
     using F = Cfg<D>;
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 31;
-    Ctx& ctx = sh.ctx[2];
-    ctx.start<32>(a, sh.plan);
+    if (lane == 0) sh.walk.start(a, sh.plan);
     Slot at;
     int uses = 0, used[2] = {0, 0};                              // tiles begun; items of a stream
     bool dead = false;
-    while (!dead && ctx.next<32>(a)) {
-        const Item& it = ctx.it;
+    for (int n = 0;; ++n) {
+        Job& job = sh.job[n % kAhead];
+        dead = dead || !warp_wait(&sh.job_empty[n % kAhead], ((n / kAhead) & 1) ^ 1, a.err, a.timeout_ns);
+        if (dead) break;                                         // (the others' waits for it run out too)
+        if (lane == 0) {
+            job.more = sh.walk.next(a, job.it);
+            if (job.more) job.set(a);
+            mbar_arrive(&sh.job_full[n % kAhead]);
+        }
+        __syncwarp();
+        if (!job.more) break;
+        const Item& it = job.it;
         const int64_t k0 = x.cu_k[it.b];
         if (lane == 0 && (k0 < 0 || k0 + it.s.len > x.n_keys)) record_error(a.err, MOE_ERR_INVALID_ARG);
-        for (int j = 0; j < ctx.tiles && !dead; ++j) {
+        for (int j = 0; j < job.tiles && !dead; ++j) {
             // (a place far outside stays outside, whatever 32 bits make of the sum)
-            const int row = static_cast<int>(min(max(k0 + ctx.key0(j), int64_t(-(1 << 30))), int64_t(x.n_keys)));
+            const int row = static_cast<int>(min(max(k0 + job.key0(j), int64_t(-(1 << 30))), int64_t(x.n_keys)));
             dead = !warp_wait(&sh.k_empty[at.st], at.ph ^ 1u, a.err, a.timeout_ns);
             if (dead) break;
             if (lane == 0) {
@@ -171,7 +176,7 @@ __device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMap
             at.step();
             ++uses;
             for (int s = 0; s < 2 && j == 0; ++s) {
-                if ((s ? ctx.b[1] - ctx.a[1] : ctx.b[0] - ctx.a[0]) <= 0) continue;
+                if (job.last(s) <= job.first(s)) continue;
                 dead = dead || !warp_wait(&sh.q_empty[s], (used[s] & 1) ^ 1, a.err, a.timeout_ns);
                 if (dead) break;
                 if (lane == 0) {
@@ -213,23 +218,22 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
     using F = Cfg<D>;
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 31;
-    Ctx& ctx = sh.ctx[4];
-    ctx.start<32>(a, sh.plan);
     Slot at;
+    Jobs jobs;
     uint32_t qp[2] = {0, 0};
     bool dead = false;
-    while (!dead && ctx.next<32>(a)) {
-        for (int j = 0; j < ctx.tiles; ++j, at.step()) {
+    while (const Job* job = dead ? nullptr : jobs.next(sh, a)) {
+        for (int j = 0; j < job->tiles; ++j, at.step()) {
             dead = !warp_wait(&sh.k_full[at.st], at.ph, a.err, a.timeout_ns);
             if (dead) break;
             if (lane == 0) arrive_first(&sh.k_ready[at.st]);
             dead = !warp_wait(&sh.v_full[at.st], at.ph, a.err, a.timeout_ns);
             if (dead) break;
-            const int j0 = ctx.key0(j), lo = max(ctx.it.lo, ctx.lo_all), hi = min(ctx.it.hi, ctx.hi_all);
+            const int j0 = job->key0(j), lo = max(job->it.lo, job->lo_all), hi = min(job->it.hi, job->hi_all);
             if (j0 < lo || j0 + kKT > hi) {
                 bool any = false;
                 uint8_t* v = vs + at.st * F::kVBytes + lane * 16;
-                const int key0 = j0 + (lane >> 3), see0 = ctx.it.lo, see1 = ctx.it.hi;
+                const int key0 = j0 + (lane >> 3), see0 = job->it.lo, see1 = job->it.hi;
 #pragma unroll 1
                 for (int e0 = 0; e0 < kKT / 4; e0 += 8) {        // 16 bytes of eight keys at a time
                     uint4 w[8];
@@ -260,45 +264,61 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
             }
             if (lane == 0) arrive_first(&sh.v_ready[at.st]);
             for (int s = 0; s < 2 && j == 0; ++s) {
-                if ((s ? ctx.b[1] - ctx.a[1] : ctx.b[0] - ctx.a[0]) <= 0) continue;
+                if (job->last(s) <= job->first(s)) continue;
                 dead = dead || !warp_wait(&sh.q_full[s], s ? qp[1] : qp[0], a.err, a.timeout_ns);
                 if (lane == 0 && !dead) arrive_first(&sh.q_ready[s]);
                 qp[s] ^= 1u;
             }
             if (dead) break;
         }
+        __syncwarp();
+        if (lane == 0) jobs.done(sh);
+        ++jobs.n;
     }
 }
 
-// The MMA warp of stream s, in the first CTA.  The streams' warps take turns, a burst each: PV of
-// a tile, then QK of the next (which writes S over that P); a warp's waits run beside
-// the other's burst (see attn_tile.cu).
+// The MMA warp of stream s, in the first CTA.  The streams go their own ways, through
+// items too, and issue a burst at a time, which a lock keeps whole: PV of a tile, then
+// QK of the next (which writes S over that P); a warp's waits run beside the other's
+// burst.  (Bursts in strict turns left the one stream waiting for the other's last
+// tiles under a causal mask, and both for each other's items.)
 template <int D>
 __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint8_t* qs, uint8_t* ks, uint8_t* vs, int s) {
     using F = Cfg<D>;
     constexpr uint32_t kM256 = static_cast<uint32_t>(128 >> 4) << 24;   // beyond idesc's M = 128
     constexpr uint32_t kIdQK = idesc(false, kKT) + kM256, kIdPV = idesc(true, D) + kM256;
     const AttnArgs& a = x.a;
+    const int lane = threadIdx.x & 31;
     const uint32_t colS = sh.tmem + 128 * s, colO = sh.tmem + kColO + 128 * s;
     const uint64_t qd = sdesc(smem_u32(qs + s * F::kQBytes), 16, 1024);
     const uint64_t kd = sdesc(smem_u32(ks), 16, 1024), vd = sdesc(smem_u32(vs), kPanel, 1024);
-    Ctx& ctx = sh.ctx[3];
-    ctx.start<64>(a, sh.plan);
     Slot ka, va;
-    uint32_t qp = 0, pp = 0, tp = 0;
+    Jobs jobs;
+    uint32_t qp = 0, pp = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead) dead = !warp_wait(bar, parity, a.err, a.timeout_ns);
     };
-    if (s == 1 && (threadIdx.x & 31) == 0) mbar_arrive(&sh.turn[0]);   // stream 0 begins
-    while (ctx.next<64>(a, kBarMma)) {
-        const int T = ctx.tiles, a0 = s ? ctx.a[1] : ctx.a[0], b0 = s ? ctx.b[1] : ctx.b[0];
-        if (T == 0) continue;
+    auto lock = [&]() {
+        bool ok = true;
+        if (lane == 0 && !dead) {
+            const uint64_t t0 = globaltimer_ns();
+            while (atomicCAS(&sh.lock, 0, 1) != 0)
+                if (globaltimer_ns() - t0 > a.timeout_ns) {
+                    record_error(a.err, MOE_ERR_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+        }
+        dead = !__all_sync(0xFFFFFFFFu, ok) || dead;
+    };
+    while (const Job* job = dead ? nullptr : jobs.next(sh, a)) {
+        const int T = job->tiles, a0 = job->first(s), b0 = job->last(s);
         if (b0 > a0) {
             wait(&sh.q_ready[s], qp);
             qp ^= 1u;
         }
-        for (int i = 0; i <= T; ++i) {
+        for (int i = 0; i <= T && T > 0; ++i) {
             const bool do_v = i > a0 && i <= b0, do_k = i >= a0 && i < b0, has_v = i > 0, has_k = i < T;
             const int vst = va.st, kst = ka.st;
             if (has_v) {
@@ -309,18 +329,27 @@ __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint
                 wait(&sh.k_ready[kst], ka.ph);
                 ka.step();
             }
-            if (do_v) {
-                wait(&sh.p_ready[s], pp);
-                pp ^= 1u;
-            }
-            wait(&sh.turn[s], tp);
-            tp ^= 1u;
+            if (do_v) wait(&sh.p_ready[s][0], pp);
+            if (do_v || do_k) lock();
             tc_fence_after();
+            // (a base and constants: each operand worked out on its own would cost as much as its product)
+            const uint64_t kk = kd + kst * (F::kKBytes >> 4), vv = vd + vst * (F::kVBytes >> 4);
+            const uint32_t more = i - 1 > a0;
+            auto pv = [&](int k) { pair_mma_ts(colO, colS + 8 * k, vv + (k * 2048 >> 4), kIdPV, k > 0 ? 1u : more); };
+            if (do_v) {                                          // the second half's powers are worked out beside the first's products
+                if (elect_one() && !dead) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) pv(k);
+                }
+                __syncwarp();
+                wait(&sh.p_ready[s][1], pp);
+                pp ^= 1u;
+                tc_fence_after();
+            }
             if (elect_one() && !dead) {
                 if (do_v) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        pair_mma_ts(colO, colS + 8 * k, vd + ((vst * F::kVBytes + k * 2048) >> 4), kIdPV, i - 1 > a0 || k > 0);
+                    for (int k = 4; k < 8; ++k) pv(k);
                     if (i == b0) pair_commit(&sh.o_full[s]);
                 }
                 if (has_v) pair_commit(&sh.v_empty[vst]);
@@ -328,15 +357,17 @@ __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint
 #pragma unroll
                     for (int k = 0; k < D / 16 + 4; ++k)
                         pair_mma(colS, qd + (((k >> 2) * kPanel + (k & 3) * 32) >> 4),
-                                 kd + ((kst * F::kKBytes + (k >> 2) * F::kKPanel + (k & 3) * 32) >> 4), kIdQK, k > 0);
+                                 kk + (((k >> 2) * F::kKPanel + (k & 3) * 32) >> 4), kIdQK, k > 0);
                     pair_commit(&sh.s_full[s]);
                     if (i == b0 - 1) pair_commit(&sh.q_empty[s]);
                 }
                 if (has_k) pair_commit(&sh.k_empty[kst]);
-                mbar_arrive(&sh.turn[s ^ 1]);
+                if (do_v || do_k) atomicExch(&sh.lock, 0);
             }
             __syncwarp();
         }
+        if (lane == 0) jobs.done(sh);
+        ++jobs.n;
     }
     // the products end before the accumulators are given back
     if (elect_one()) pair_commit(&sh.done[s]);
@@ -399,15 +430,21 @@ __device__ __forceinline__ void powers(uint32_t colP, const float (&x)[32], floa
     tmem_st16(colP, u);
 }
 
+// Tells the MMA warp of the P stored so far.
+__device__ __forceinline__ void hand_over(uint64_t* bar) {
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive_first(bar);
+}
+
 template <int D>
 __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int pair, int rank) {
     const AttnArgs& a = xa.a;
-    const int tid = threadIdx.x, s = tid >> 7, lr = tid & 127, lane = tid & 31;
+    const int tid = threadIdx.x, s = tid >> 7, lr = tid & 127;
     const uint32_t tm = sh.tmem + (static_cast<uint32_t>(tid & 96) << 16);
     const uint32_t colS = tm + 128 * s, colO = tm + kColO + 128 * s;
-    Ctx& ctx = sh.ctx[s];
-    ctx.start<128>(a, sh.plan);
-    const Item& it = ctx.it;
+    Jobs jobs;
     uint32_t sp = 0, op = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -417,17 +454,18 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
     // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf); the sign goes to the scores
     const float cs = a.scale * kLog2e;
     const float c = fmaxf(fabsf(cs), 1.2e-38f);
-    while (ctx.next<128>(a, kBarGroup + s)) {
-        const int row0 = s * kStream + rank * 128, count = min(max(ctx.rows - row0, 0), 128);
-        const int t0 = s ? ctx.a[1] : ctx.a[0], n = (s ? ctx.b[1] : ctx.b[0]) - t0;
-        const int wlo = s ? ctx.wlo[1] : ctx.wlo[0], whi = s ? ctx.whi[1] : ctx.whi[0];
+    while (const Job* job = jobs.next(sh, a)) {
+        const Item& it = job->it;
+        const int row0 = s * kStream + rank * 128, count = min(max(job->rows - row0, 0), 128);
+        const int t0 = job->first(s), n = job->last(s) - t0;
+        const int wlo = s ? job->wlo[1] : job->wlo[0], whi = s ? job->whi[1] : job->whi[0];
         const bool valid = lr < count, warp_on = __any_sync(0xFFFFFFFFu, valid);
         const int qi = it.rt * kMT + row0 + (valid ? lr : 0);
         RowView view{0, 0, 0ull};
         if (valid) view = row_view(a, it.s, qi);
         RowState st{kNegInf, 0.0f, 0.0f};
         for (int i = 0; i < n; ++i) {
-            const int j0 = ctx.key0(t0 + i);
+            const int j0 = job->key0(t0 + i);
             wait(&sh.s_full[s], sp);
             sp ^= 1u;
             if (warp_on) {
@@ -454,13 +492,15 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
                 const float top = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3])));
                 follow<D>(colO, top * c, i > 0, st);
                 const float off = st.ref == kNegInf ? 0.0f : -st.ref;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) powers(colS + 16 * q, x[q], c, off, st);
+                powers(colS, x[0], c, off, st);
+                powers(colS + 16, x[1], c, off, st);
+                hand_over(&sh.p_ready[s][0]);
+                powers(colS + 32, x[2], c, off, st);
+                powers(colS + 48, x[3], c, off, st);
+            } else {
+                hand_over(&sh.p_ready[s][0]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_first(&sh.p_ready[s]);
+            hand_over(&sh.p_ready[s][1]);
         }
         // --- the item's rows: normalised, or this pair's piece of them
         const float sum = st.sum0 + st.sum1;
@@ -492,9 +532,9 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
                 if (bad && valid) {
                     // values that are not finite, of the masked tiles' keys that this row sees
                     const int64_t k0 = xa.cu_k[it.b];
-                    for (int j = max(view.lo, ctx.key0(0)); j < min(view.hi, ctx.key0(ctx.tiles)); ++j) {
+                    for (int j = max(view.lo, job->key0(0)); j < min(view.hi, job->key0(job->tiles)); ++j) {
                         const int tile = j - j % kKT;
-                        if (tile >= ctx.lo_all && tile + kKT <= min(ctx.it.hi, ctx.hi_all)) continue;
+                        if (tile >= job->lo_all && tile + kKT <= min(it.hi, job->hi_all)) continue;
                         if (k0 + j < 0 || k0 + j >= xa.n_keys) continue;
                         const uint16_t* v = xa.v + (k0 + j) * xa.v_token + it.h * xa.v_head + 32 * q;
 #pragma unroll
@@ -522,7 +562,10 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
             }
         }
         tc_fence_before();
-        if (tid == 0 && rank == 0) note_split(a, it, ctx.rows, kMT, sh.plan, pair);
+        if (tid == 0 && rank == 0) note_split(a, it, job->rows, kMT, sh.plan, pair);
+        __syncwarp();
+        if ((tid & 31) == 0) jobs.done(sh);
+        ++jobs.n;
     }
 }
 
@@ -549,13 +592,18 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             mbar_init(&sh.q_full[s], 1);
             mbar_init(&sh.q_empty[s], 1);
             mbar_init(&sh.q_ready[s], 2);
-            mbar_init(&sh.p_ready[s], 8);
-            mbar_init(&sh.turn[s], 1);
+            mbar_init(&sh.p_ready[s][0], 8);
+            mbar_init(&sh.p_ready[s][1], 8);
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.o_full[s], 1);
             mbar_init(&sh.done[s], 1);
         }
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(&sh.job_full[i], 1);
+            mbar_init(&sh.job_empty[i], 8 + 1 + (rank == 0 ? 2 : 0));   // softmax warps, passing on, MMA
+        }
         sh.bad = 0;
+        sh.lock = 0;
         fence_barrier_init();
         prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.k);
