@@ -55,25 +55,27 @@ struct Job {
     int wlo[2], whi[2];      // keys that every row of the stream sees
     int lo_all, hi_all;      // and of the item
 
-    __device__ __forceinline__ void set(const AttnArgs& at) {
+    __device__ __forceinline__ void set(const AttnArgs& at, const Item& it) {
         const int r0 = it.rt * kMT;
-        rows = min(kMT, it.s.nq - r0);
-        tiles = it.hi > it.lo ? it.t1 - it.t0 : 0;
-        const int2 all = rows_whole(at, it.s, r0, r0 + rows - 1);
+        const int n = min(kMT, it.s.nq - r0), m = it.hi > it.lo ? it.t1 - it.t0 : 0;
+        const int2 all = rows_whole(at, it.s, r0, r0 + n - 1);
+        rows = n;
+        tiles = m;
         lo_all = all.x;
         hi_all = all.y;
         const int base = it.tile0 + it.t0;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int i0 = r0 + s * kStream, i1 = min(i0 + kStream, r0 + rows) - 1;
+            const int i0 = r0 + s * kStream, i1 = min(i0 + kStream, r0 + n) - 1;
             a[s] = b[s] = 0;
             wlo[s] = whi[s] = 0;
             if (i1 < i0) continue;
             const int2 k = rows_range(at, it.s, i0, i1), w = rows_whole(at, it.s, i0, i1);
             wlo[s] = w.x;
             whi[s] = w.y;
-            a[s] = min(max(k.x / kKT - base, 0), tiles);
-            b[s] = k.y > k.x ? max(min((k.y + kKT - 1) / kKT - base, tiles), a[s]) : a[s];
+            const int first = min(max(k.x / kKT - base, 0), m);
+            a[s] = first;
+            b[s] = k.y > k.x ? max(min((k.y + kKT - 1) / kKT - base, m), first) : first;
         }
     }
     __device__ __forceinline__ int first(int s) const { return s ? a[1] : a[0]; }
@@ -87,15 +89,12 @@ struct Shared {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_full[2], q_empty[2];
     // of the pair, in its first CTA: operands in place in both
-    uint64_t k_ready[kStages], v_ready[kStages], q_ready[2];
-    uint64_t p_ready[2][2];                 // by half of a tile's keys
+    uint64_t k_ready[kStages], v_ready[kStages], q_ready[2], p_ready[2];
     // of this CTA: the pair's products are done
     uint64_t s_full[2], o_full[2], done[2];
     Plan plan;
-    Walk<kMT, kKT> walk;                    // the copying warp's
     Job job[kAhead];
     uint64_t job_full[kAhead], job_empty[kAhead];
-    int lock;                               // whether a stream's products are being issued
     uint32_t tmem;
     int bad;                                // some masked tile had values that are not finite
 };
@@ -133,7 +132,8 @@ __device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMap
     using F = Cfg<D>;
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) sh.walk.start(a, sh.plan);
+    Walk<kMT, kKT> walk;                                         // every lane's own, in registers
+    walk.start(a, sh.plan);
     Slot at;
     int uses = 0, used[2] = {0, 0};                              // tiles begun; items of a stream
     bool dead = false;
@@ -141,13 +141,18 @@ __device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMap
         Job& job = sh.job[n % kAhead];
         dead = dead || !warp_wait(&sh.job_empty[n % kAhead], ((n / kAhead) & 1) ^ 1, a.err, a.timeout_ns);
         if (dead) break;                                         // (the others' waits for it run out too)
+        Item next;
+        const bool more = walk.next(a, next);
         if (lane == 0) {
-            job.more = sh.walk.next(a, job.it);
-            if (job.more) job.set(a);
+            job.more = more;
+            if (more) {
+                job.it = next;
+                job.set(a, next);
+            }
             mbar_arrive(&sh.job_full[n % kAhead]);
         }
         __syncwarp();
-        if (!job.more) break;
+        if (!more) break;
         const Item& it = job.it;
         const int64_t k0 = x.cu_k[it.b];
         if (lane == 0 && (k0 < 0 || k0 + it.s.len > x.n_keys)) record_error(a.err, MOE_ERR_INVALID_ARG);
@@ -200,19 +205,56 @@ __device__ __forceinline__ void produce(const ExpandedArgs& x, const ExpandedMap
         if (used[s] > 0) mbar_wait(&sh.q_full[s], (used[s] - 1) & 1, a.err, kDrainNs);
 }
 
-// Whether a pair of bf16 has one that is not finite (its sign bit or, in the upper one,
-// a carry into it tells), and the pair with such as zeros.
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+// Of a pair of bf16: bits 15 and 31 are set where one is not finite (its exponent
+// carries into them), and the pair with such as zeros.
+__device__ __forceinline__ uint32_t carry2(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
-    const uint32_t n = nonfinite2(w);
+    const uint32_t n = carry2(w);
     return w & ((n & 0x8000u ? 0u : 0xFFFFu) | (n & 0x80000000u ? 0u : 0xFFFF0000u));
 }
 
+// Puts a tile's values right, keys from j0 on of which the item's rows see see0 .. see1 - 1 and
+// all of them wlo .. whi - 1: where some row does not see some key, elements that are not
+// finite become zeros (a probability of 0 would make them NaN for that row).  The rows
+// that do see such a key get them when the item ends.
+__device__ __forceinline__ void mend_values(Shared& sh, uint8_t* tile, int j0, int see0, int see1, int wlo, int whi) {
+    if (j0 >= max(see0, wlo) && j0 + kKT <= min(see1, whi)) return;
+    // 16 bytes of eight keys at a time: in all but few tiles all is finite and nothing to be put right
+    const int lane = threadIdx.x & 31;
+    uint8_t* v = tile + lane * 16;
+    uint32_t odd = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < kKT / 4; e0 += 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint4*>(v + (e0 + e) * 512);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) odd |= carry2(w[e].x) | carry2(w[e].y) | carry2(w[e].z) | carry2(w[e].w);
+    }
+    if (!__any_sync(0xFFFFFFFFu, (odd & 0x80008000u) != 0)) return;
+    bool any = false;
+#pragma unroll 1
+    for (int e = 0; e < kKT / 4; ++e) {
+        const int key = j0 + (lane >> 3) + 4 * e;
+        uint4* p = reinterpret_cast<uint4*>(v + e * 512);
+        const uint4 w = *p;
+        if (((carry2(w.x) | carry2(w.y) | carry2(w.z) | carry2(w.w)) & 0x80008000u) == 0) continue;
+        *p = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+        any = any || (key >= see0 && key < see1);
+    }
+    if (any) {                                                   // in both CTAs: each has all columns of its rows
+        for (uint32_t r = 0; r < 2; ++r)
+            asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.u32 [p], %2;\n\t}" ::"r"(
+                             smem_u32(&sh.bad)),
+                         "r"(r), "r"(1)
+                         : "memory");
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
 // The warp that tells the first CTA, whose MMA warps wait for both, what landed here.
-// Values of keys that no row of the item sees may be anything: they are zeroed.  So are,
-// in tiles where some row does not see some key, elements that are not finite (a
-// probability of 0 would make them NaN for that row); the rows that do see such a key
-// get them when the item ends.
 template <int D>
 __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8_t* vs) {
     using F = Cfg<D>;
@@ -229,39 +271,7 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
             if (lane == 0) arrive_first(&sh.k_ready[at.st]);
             dead = !warp_wait(&sh.v_full[at.st], at.ph, a.err, a.timeout_ns);
             if (dead) break;
-            const int j0 = job->key0(j), lo = max(job->it.lo, job->lo_all), hi = min(job->it.hi, job->hi_all);
-            if (j0 < lo || j0 + kKT > hi) {
-                bool any = false;
-                uint8_t* v = vs + at.st * F::kVBytes + lane * 16;
-                const int key0 = j0 + (lane >> 3), see0 = job->it.lo, see1 = job->it.hi;
-#pragma unroll 1
-                for (int e0 = 0; e0 < kKT / 4; e0 += 8) {        // 16 bytes of eight keys at a time
-                    uint4 w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint4*>(v + (e0 + e) * 512);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int key = key0 + 4 * (e0 + e);
-                        uint4* p = reinterpret_cast<uint4*>(v + (e0 + e) * 512);
-                        if (key < see0 || key >= see1) {
-                            *p = make_uint4(0, 0, 0, 0);
-                        } else if (nonfinite2(w[e].x) | nonfinite2(w[e].y) | nonfinite2(w[e].z) | nonfinite2(w[e].w)) {
-                            *p = make_uint4(finite2(w[e].x), finite2(w[e].y), finite2(w[e].z), finite2(w[e].w));
-                            any = true;
-                        }
-                    }
-                }
-                if (any) {                                       // in both CTAs: each has all columns of its rows
-                    for (uint32_t r = 0; r < 2; ++r)
-                        asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.u32 [p], %2;\n\t}" ::"r"(
-                                         smem_u32(&sh.bad)),
-                                     "r"(r), "r"(1)
-                                     : "memory");
-                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                }
-                fence_async_smem();
-                __syncwarp();
-            }
+            mend_values(sh, vs + at.st * F::kVBytes, job->key0(j), job->it.lo, job->it.hi, job->lo_all, job->hi_all);
             if (lane == 0) arrive_first(&sh.v_ready[at.st]);
             for (int s = 0; s < 2 && j == 0; ++s) {
                 if (job->last(s) <= job->first(s)) continue;
@@ -278,17 +288,16 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
 }
 
 // The MMA warp of stream s, in the first CTA.  The streams go their own ways, through
-// items too, and issue a burst at a time, which a lock keeps whole: PV of a tile, then
-// QK of the next (which writes S over that P); a warp's waits run beside the other's
-// burst.  (Bursts in strict turns left the one stream waiting for the other's last
-// tiles under a causal mask, and both for each other's items.)
+// items too; a burst is PV of a tile, then QK of the next (which writes S over that
+// P).  A warp's waits run beside the other's burst.  (Bursts in strict turns left the one
+// stream waiting for the other's last tiles under a causal mask, and both for each
+// other's items: 573 us where this takes 539; a lock about a burst 552.)
 template <int D>
 __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint8_t* qs, uint8_t* ks, uint8_t* vs, int s) {
     using F = Cfg<D>;
     constexpr uint32_t kM256 = static_cast<uint32_t>(128 >> 4) << 24;   // beyond idesc's M = 128
     constexpr uint32_t kIdQK = idesc(false, kKT) + kM256, kIdPV = idesc(true, D) + kM256;
     const AttnArgs& a = x.a;
-    const int lane = threadIdx.x & 31;
     const uint32_t colS = sh.tmem + 128 * s, colO = sh.tmem + kColO + 128 * s;
     const uint64_t qd = sdesc(smem_u32(qs + s * F::kQBytes), 16, 1024);
     const uint64_t kd = sdesc(smem_u32(ks), 16, 1024), vd = sdesc(smem_u32(vs), kPanel, 1024);
@@ -298,19 +307,6 @@ __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead) dead = !warp_wait(bar, parity, a.err, a.timeout_ns);
-    };
-    auto lock = [&]() {
-        bool ok = true;
-        if (lane == 0 && !dead) {
-            const uint64_t t0 = globaltimer_ns();
-            while (atomicCAS(&sh.lock, 0, 1) != 0)
-                if (globaltimer_ns() - t0 > a.timeout_ns) {
-                    record_error(a.err, MOE_ERR_TIMEOUT);
-                    ok = false;
-                    break;
-                }
-        }
-        dead = !__all_sync(0xFFFFFFFFu, ok) || dead;
     };
     while (const Job* job = dead ? nullptr : jobs.next(sh, a)) {
         const int T = job->tiles, a0 = job->first(s), b0 = job->last(s);
@@ -329,27 +325,18 @@ __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint
                 wait(&sh.k_ready[kst], ka.ph);
                 ka.step();
             }
-            if (do_v) wait(&sh.p_ready[s][0], pp);
-            if (do_v || do_k) lock();
+            if (do_v) {
+                wait(&sh.p_ready[s], pp);
+                pp ^= 1u;
+            }
             tc_fence_after();
             // (a base and constants: each operand worked out on its own would cost as much as its product)
             const uint64_t kk = kd + kst * (F::kKBytes >> 4), vv = vd + vst * (F::kVBytes >> 4);
             const uint32_t more = i - 1 > a0;
-            auto pv = [&](int k) { pair_mma_ts(colO, colS + 8 * k, vv + (k * 2048 >> 4), kIdPV, k > 0 ? 1u : more); };
-            if (do_v) {                                          // the second half's powers are worked out beside the first's products
-                if (elect_one() && !dead) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) pv(k);
-                }
-                __syncwarp();
-                wait(&sh.p_ready[s][1], pp);
-                pp ^= 1u;
-                tc_fence_after();
-            }
             if (elect_one() && !dead) {
                 if (do_v) {
 #pragma unroll
-                    for (int k = 4; k < 8; ++k) pv(k);
+                    for (int k = 0; k < 8; ++k) pair_mma_ts(colO, colS + 8 * k, vv + (k * 2048 >> 4), kIdPV, k > 0 ? 1u : more);
                     if (i == b0) pair_commit(&sh.o_full[s]);
                 }
                 if (has_v) pair_commit(&sh.v_empty[vst]);
@@ -362,11 +349,10 @@ __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint
                     if (i == b0 - 1) pair_commit(&sh.q_empty[s]);
                 }
                 if (has_k) pair_commit(&sh.k_empty[kst]);
-                if (do_v || do_k) atomicExch(&sh.lock, 0);
             }
             __syncwarp();
         }
-        if (lane == 0) jobs.done(sh);
+        if ((threadIdx.x & 31) == 0) jobs.done(sh);
         ++jobs.n;
     }
     // the products end before the accumulators are given back
@@ -494,13 +480,10 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
                 const float off = st.ref == kNegInf ? 0.0f : -st.ref;
                 powers(colS, x[0], c, off, st);
                 powers(colS + 16, x[1], c, off, st);
-                hand_over(&sh.p_ready[s][0]);
                 powers(colS + 32, x[2], c, off, st);
                 powers(colS + 48, x[3], c, off, st);
-            } else {
-                hand_over(&sh.p_ready[s][0]);
             }
-            hand_over(&sh.p_ready[s][1]);
+            hand_over(&sh.p_ready[s]);
         }
         // --- the item's rows: normalised, or this pair's piece of them
         const float sum = st.sum0 + st.sum1;
@@ -522,13 +505,14 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
         }
         const bool bad = *const_cast<volatile int*>(&sh.bad) != 0;
         if (warp_on) {
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-                float o[32];
-                tmem_ld32(colO + 32 * q, o);
-                tmem_wait_ld();
+            float o[D / 32][32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = weight != 0.0f ? o[e] * weight : 0.0f;
+            for (int q = 0; q < D / 32; ++q) tmem_ld32(colO + 32 * q, o[q]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[q][e] = weight != 0.0f ? o[q][e] * weight : 0.0f;
                 if (bad && valid) {
                     // values that are not finite, of the masked tiles' keys that this row sees
                     const int64_t k0 = xa.cu_k[it.b];
@@ -539,8 +523,8 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
                         const uint16_t* v = xa.v + (k0 + j) * xa.v_token + it.h * xa.v_head + 32 * q;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const uint32_t w = v[e];
-                            if ((w & 0x7F80u) == 0x7F80u) o[e] += bf16_bits_to_f32(w);
+                            const uint32_t b = v[e];
+                            if ((b & 0x7F80u) == 0x7F80u) o[q][e] += bf16_bits_to_f32(b);
                         }
                     }
                 }
@@ -549,16 +533,15 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             *reinterpret_cast<float4*>(slot + ((8 * q + e) * kMT + row0 + lr) * 4) =
-                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                                make_float4(o[q][4 * e], o[q][4 * e + 1], o[q][4 * e + 2], o[q][4 * e + 3]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             *reinterpret_cast<uint4*>(a.out + at * D + 32 * q + 8 * e) =
-                                make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                           pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                                make_uint4(pack_bf16(o[q][8 * e], o[q][8 * e + 1]), pack_bf16(o[q][8 * e + 2], o[q][8 * e + 3]),
+                                           pack_bf16(o[q][8 * e + 4], o[q][8 * e + 5]), pack_bf16(o[q][8 * e + 6], o[q][8 * e + 7]));
                     }
                 }
-                __syncwarp();
             }
         }
         tc_fence_before();
@@ -592,8 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             mbar_init(&sh.q_full[s], 1);
             mbar_init(&sh.q_empty[s], 1);
             mbar_init(&sh.q_ready[s], 2);
-            mbar_init(&sh.p_ready[s][0], 8);
-            mbar_init(&sh.p_ready[s][1], 8);
+            mbar_init(&sh.p_ready[s], 8);
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.o_full[s], 1);
             mbar_init(&sh.done[s], 1);
@@ -603,7 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             mbar_init(&sh.job_empty[i], 8 + 1 + (rank == 0 ? 2 : 0));   // softmax warps, passing on, MMA
         }
         sh.bad = 0;
-        sh.lock = 0;
         fence_barrier_init();
         prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.k);
