@@ -568,20 +568,24 @@ def moe_cache_evict(cache: KVCache, seqs: Seqs, scores, budget: int, n_recent: i
 
 
 # ------------------------------------------------------------ latent cache --
+# (Each attribute of a tensor that is asked for costs some 0.1 us of the host, of a
+# call's 6 to 9; shapes and strides are asked for once.)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _here(*tensors) -> bool:
     """All of them (None aside) on the current device, on whose stream a call runs."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    return all(t is None or t.get_device() == dev for t in tensors)
+    dev = tensors[0].get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        return False
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            return False
+    return True
 
 
-def _strided(t, tokens: int, heads: int, dim: int) -> bool:
-    """bf16 [tokens, heads, dim] with free strides of token and head."""
-    return t.dtype is torch.bfloat16 and t.shape == (tokens, heads, dim) and t.stride(2) == 1
-
-
-def _stride(t, i: int) -> int:
-    """The stride of axis i; where the axis has one place, one that is fit for any check."""
-    return t.stride(i) if t.shape[i] > 1 else (t.shape[1:].numel() if i == 0 else t.shape[-1])
+def _flat(t, dtype, shape) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
 def moe_latent_append(rope: Rope, cache: LatentCache, seqs: Seqs, kv, q_rope, positions, q_out,
@@ -590,17 +594,24 @@ def moe_latent_append(rope: Rope, cache: LatentCache, seqs: Seqs, kv, q_rope, po
     [T, n_q_heads, 64] (free strides of token and head, so that q_out can be the
     last 64 elements of moe_latent_attention's query rows); gamma fp32
     [latent_dim] or None: the latents are stored without normalisation."""
-    T, H = q_rope.shape[:2]
-    L = cache.latent_dim
-    _refuse(kv.dtype is torch.bfloat16 and kv.shape == (T, L + LATENT_ROPE_DIM) and kv.stride(1) == 1
-            and _strided(q_rope, T, H, LATENT_ROPE_DIM) and _strided(q_out, T, H, LATENT_ROPE_DIM)
-            and _is(positions, torch.int32, T)
-            and (gamma is None or _is(gamma, torch.float32, L))
+    shape, L = q_rope.shape, cache.latent_dim
+    _refuse(len(shape) == 3 and shape[2] == 64 and q_out.shape == shape
+            and kv.shape == (shape[0], L + 64) and kv.dtype is _BF16 and q_rope.dtype is _BF16
+            and q_out.dtype is _BF16 and _flat(positions, _I32, shape[:1])
+            and (gamma is None or _flat(gamma, _F32, (L,)))
             and _here(kv, q_rope, q_out, positions, gamma), "moe_latent_append")
-    _check(load().moe_latent_append(C.byref(rope), C.byref(cache), C.byref(seqs), kv.data_ptr(),
-                                    _stride(kv, 0), _ptr(gamma), eps, q_rope.data_ptr(),
-                                    _stride(q_rope, 0), _stride(q_rope, 1), positions.data_ptr(),
-                                    T, H, q_out.data_ptr(), _stride(q_out, 0), _stride(q_out, 1),
+    T, H, _ = shape
+    kt, k1 = kv.stride()
+    qt, qh, q1 = q_rope.stride()
+    ot, oh, o1 = q_out.stride()
+    _refuse(k1 == 1 and q1 == 1 and o1 == 1, "moe_latent_append")
+    if T == 1:                   # (the stride of an axis with one place is not followed)
+        kt, qt, ot = L + 64, 64 * H, 64 * H
+    if H == 1:
+        qh = oh = 64
+    _check(load().moe_latent_append(C.byref(rope), C.byref(cache), C.byref(seqs), kv.data_ptr(), kt,
+                                    _ptr(gamma), eps, q_rope.data_ptr(), qt, qh,
+                                    positions.data_ptr(), T, H, q_out.data_ptr(), ot, oh,
                                     _stream(stream)), "moe_latent_append")
 
 
@@ -615,28 +626,30 @@ def moe_latent_attention(attn: Attn, cache: LatentCache, seqs: Seqs, q, out, ws,
     """q bf16 [T, n_q_heads, latent_dim + 64] (free token stride); out bf16
     [T, n_q_heads, latent_dim], contiguous; lse fp32 [T, n_q_heads] or None;
     draft_mask int64 [T] (the bits of a uint64) or None."""
-    T, H, L = q.shape[0], attn.n_q_heads, cache.latent_dim
-    W = L + LATENT_ROPE_DIM
-    _refuse(q.dim() == 3 and _heads(q, H, W, T) and _is(out, torch.bfloat16, T, H, L)
-            and (lse is None or _is(lse, torch.float32, T, H))
-            and (draft_mask is None or _is(draft_mask, torch.int64, T))
+    H, L = attn.n_q_heads, cache.latent_dim
+    W, T = L + 64, q.shape[0]
+    _refuse(q.shape == (T, H, W) and q.dtype is _BF16 and _flat(out, _BF16, (T, H, L))
+            and (lse is None or _flat(lse, _F32, (T, H)))
+            and (draft_mask is None or _flat(draft_mask, torch.int64, (T,)))
             and _here(q, out, lse, draft_mask, ws), "moe_latent_attention")
-    _check(load().moe_latent_attention(C.byref(attn), C.byref(cache), C.byref(seqs), _ptr(q),
-                                       q.stride(0) if T > 1 else H * W, _ptr(draft_mask), T,
-                                       _ptr(out), _ptr(lse), _ptr(ws),
-                                       ws.numel() * ws.element_size(), _stream(stream)),
+    qt, qh, q1 = q.stride()
+    _refuse(q1 == 1 and (qh == W or H == 1), "moe_latent_attention")
+    _check(load().moe_latent_attention(C.byref(attn), C.byref(cache), C.byref(seqs), q.data_ptr(),
+                                       qt if T > 1 else H * W, _ptr(draft_mask), T, out.data_ptr(),
+                                       _ptr(lse), ws.data_ptr(), ws.nbytes, _stream(stream)),
            "moe_latent_attention")
 
 
 def moe_latent_gather(cache: LatentCache, seqs: Seqs, cu_k, out, ws, stream=None) -> None:
     """cu_k int32 [n_seqs + 1]: rows of out, bf16 [N, latent_dim + 64] (free row
     stride), where each sequence's cached rows go; rows of none are zeroed."""
-    N, W = out.shape[0], cache.latent_dim + LATENT_ROPE_DIM
-    _refuse(out.dtype is torch.bfloat16 and out.shape == (N, W) and out.stride(1) == 1
-            and _is(cu_k, torch.int32, seqs.n_seqs + 1) and _here(out, cu_k, ws),
-            "moe_latent_gather")
-    _check(load().moe_latent_gather(C.byref(cache), C.byref(seqs), _ptr(cu_k), N, _ptr(out),
-                                    _stride(out, 0), _ptr(ws), ws.numel() * ws.element_size(),
+    N, W = out.shape[0], cache.latent_dim + 64
+    _refuse(out.shape == (N, W) and out.dtype is _BF16 and _flat(cu_k, _I32, (seqs.n_seqs + 1,))
+            and _here(out, cu_k, ws), "moe_latent_gather")
+    rows, r1 = out.stride()
+    _refuse(r1 == 1, "moe_latent_gather")
+    _check(load().moe_latent_gather(C.byref(cache), C.byref(seqs), cu_k.data_ptr(), N, out.data_ptr(),
+                                    rows if N > 1 else W, ws.data_ptr(), ws.nbytes,
                                     _stream(stream)), "moe_latent_gather")
 
 
@@ -652,22 +665,29 @@ def moe_expanded_attention(attn: Attn, seqs: Seqs, cu_k, q, k, k_rope, v, out, w
     of one projection's output), k_rope bf16 [N, 64] (free token stride); out bf16
     [T, n_q_heads, D], contiguous; cu_k int32 [n_seqs + 1] (or [n_seqs]): first row
     of each sequence; lse fp32 [T, n_q_heads] or None.  D is 64 or 128."""
-    T, H = q.shape[0], attn.n_q_heads
-    N, D = k.shape[0], v.shape[-1]
-    _refuse(q.dim() == 3 and _heads(q, H, D + LATENT_ROPE_DIM, T) and _strided(k, N, H, D)
-            and _strided(v, N, H, D) and k_rope.dtype is torch.bfloat16
-            and k_rope.shape == (N, LATENT_ROPE_DIM) and k_rope.stride(1) == 1
-            and cu_k.dim() == 1 and cu_k.shape[0] >= seqs.n_seqs
-            and _is(cu_k, torch.int32, cu_k.shape[0]) and _is(out, torch.bfloat16, T, H, D)
-            and (lse is None or _is(lse, torch.float32, T, H))
+    H, T = attn.n_q_heads, q.shape[0]
+    N, _, D = shape = k.shape
+    _refuse(shape == (N, H, D) and v.shape == shape and q.shape == (T, H, D + 64)
+            and k_rope.shape == (N, 64) and q.dtype is _BF16 and k.dtype is _BF16
+            and v.dtype is _BF16 and k_rope.dtype is _BF16 and _flat(out, _BF16, (T, H, D))
+            and cu_k.dim() == 1 and cu_k.shape[0] >= seqs.n_seqs and _flat(cu_k, _I32, cu_k.shape)
+            and (lse is None or _flat(lse, _F32, (T, H)))
             and _here(q, k, k_rope, v, out, cu_k, lse, ws), "moe_expanded_attention")
-    _check(load().moe_expanded_attention(C.byref(attn), C.byref(seqs), _ptr(cu_k), N, D, _ptr(q),
-                                         q.stride(0) if T > 1 else H * (D + LATENT_ROPE_DIM),
-                                         _ptr(k), _stride(k, 0), _stride(k, 1), _ptr(k_rope),
-                                         _stride(k_rope, 0), _ptr(v), _stride(v, 0), _stride(v, 1),
-                                         T, _ptr(out), _ptr(lse), _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream(stream)),
-           "moe_expanded_attention")
+    qt, qh, q1 = q.stride()
+    kt, kh, k1 = k.stride()
+    vt, vh, v1 = v.stride()
+    rt, r1 = k_rope.stride()
+    _refuse(q1 == 1 and k1 == 1 and v1 == 1 and r1 == 1 and (qh == D + 64 or H == 1),
+            "moe_expanded_attention")
+    if N == 1:
+        kt, vt, rt = H * D, H * D, 64
+    if H == 1:
+        kh = vh = D
+    _check(load().moe_expanded_attention(C.byref(attn), C.byref(seqs), cu_k.data_ptr(), N, D,
+                                         q.data_ptr(), qt if T > 1 else H * (D + 64), k.data_ptr(),
+                                         kt, kh, k_rope.data_ptr(), rt, v.data_ptr(), vt, vh, T,
+                                         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes,
+                                         _stream(stream)), "moe_expanded_attention")
 
 
 def moe_get_device_error(ws, clear: bool = True, stream=None) -> int:
