@@ -108,7 +108,8 @@ struct ExpandedArgs {
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int n_sms, cudaStream_t s);
 cudaError_t launch_latent_gather(const LatentGatherArgs& a, int n_sms, cudaStream_t s);
-cudaError_t launch_latent_attn(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cudaStream_t s);
+// few: up to half of kLatentRows query rows a sequence (it only picks the kernel)
+cudaError_t launch_latent_attn(const LatentAttnArgs& a, const LatentMaps& m, bool few, int n_sms, cudaStream_t s);
 cudaError_t launch_expanded(const ExpandedArgs& a, const ExpandedMaps& m, int n_sms, cudaStream_t s);
 
 }  // namespace moe

@@ -237,7 +237,8 @@ moe_status_t moe_latent_attention(const moe_attn_t* attn, const moe_latent_cache
     a.a.kv.n_pages = a.c.n_pages;
     moe::LatentMaps maps;
     if (!make_maps(cache, &maps)) return MOE_ERR_CUDA;
-    return cuda_status(moe::launch_latent_attn(a, maps, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
+    const bool few = int64_t(seqs->max_q) * attn->n_q_heads <= moe::kLatentRows / 2;
+    return cuda_status(moe::launch_latent_attn(a, maps, few, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_latent_gather(const moe_latent_cache_t* cache, const moe_seqs_t* seqs,

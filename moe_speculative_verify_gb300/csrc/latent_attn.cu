@@ -30,10 +30,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kMT = kLatentRows, kKT = kLatentKeys;
-constexpr int kRows = 64;                // rows of a CTA
+constexpr int kKT = kLatentKeys;
+constexpr int kRows = 64;                // rows of a CTA, as the products take them
 constexpr int kKeys = kKT / 2;           // whole keys of a CTA
-constexpr int kRowPanel = kRows * 128;   // 64 elements of its rows (Q, P)
+constexpr int kRowPanel = kRows * 128;   // 64 elements of its rows
 // K and V lie in atoms of 8 keys by 64 elements (1 KB, swizzled), eight keys' atoms
 // beside each other, so that a copy reads eight whole rows at a time (element by
 // element of all rows, memory gave 4.7 TB/s).  The rotary part of K has its own place.
@@ -47,88 +47,105 @@ constexpr int kThreads = E4M3 ? 512 : 384;
 constexpr int kBarSoft = 1, kBarV = 2, kBarK = 3;                // named barriers, 128 threads each
 constexpr int kBarTop = 4;                                       // and two of the 64 that share 32 rows
 
-template <int C>
+constexpr int kAhead = 3;                // items that the copying warp may be ahead by
+
+// FEW: items of up to 64 rows, 32 a CTA (single tokens of up to 64 heads). Their
+// queries take half the room, which a third stage of keys gets: such calls are bound by
+// memory, and two stages of keys are too few bytes on their way (48 single tokens over
+// 251 to 32,011 rows: 103 -> 97 us). The products still take 64 rows a CTA: those
+// past the 32 are whatever lies behind a panel, and reach no other row.
+template <int C, bool FEW>
 struct Cfg {
+    static constexpr int kItem = FEW ? kLatentRows / 2 : kLatentRows;   // rows of an item
+    static constexpr int kHeld = kItem / 2;                      // of them a CTA's
+    static constexpr int kQPanel = kHeld * 128;
+    static constexpr int kKStages = FEW ? 3 : 2;
     static constexpr int kParts = C / 128;                       // of two panels each: of a key, beside the rotary one
     static constexpr int kVPanels = C / 128;                     // of a CTA's half of C
     static constexpr int kNV = C / 256;                          // MMAs of P V a step
-    static constexpr int kQBytes = (C / 64 + 1) * kRowPanel;
+    static constexpr int kQBytes = (C / 64 + 1) * kQPanel;
     static constexpr int kPBytes = kRowPanel;
     static constexpr int kKGroup = C / 64 * kAtom;               // of eight keys
     static constexpr int kVGroup = kVPanels * kAtom;
     static constexpr int kRope = kKeys / 8 * kKGroup;            // offset of the rotary part in a stage
     static constexpr int kKBytes = kRope + kKeys / 8 * kAtom;
     static constexpr int kVBytes = kKT / 8 * kVGroup;
-    static constexpr size_t kSmem = kQBytes + 2 * (kPBytes + kKBytes + kVBytes);   // then Shared
+    static constexpr size_t kSmem = kQBytes + kKStages * kKBytes + 2 * (kPBytes + kVBytes);   // then Shared
 };
 
-// A role's place in the pair's work, in shared memory; THREADS threads share it, at
-// named barrier `bar`.
-struct Ctx {
-    Walk<kMT, kKT> wk;
+// An item as the CTA's warps work on it.  The warp that copies keys walks the pair's
+// items and queues them here; each other role takes its own way through the queue.
+struct Job {
     Item it;
-    int more;
+    int more;                // 0: none; no other field holds
     int rows, half;          // rows of the item, and of its first CTA
     int tiles;               // of this pair (0: nothing seen)
     int wlo, whi;            // keys that every row of the item sees
 
-    template <int THREADS>
-    __device__ __forceinline__ void sync(int bar) {
-        if constexpr (THREADS == 32)
-            __syncwarp();
-        else
-            named_bar(bar, THREADS);
-    }
-    // wk.start with the first sequence as it was loaded once for all roles
-    template <int THREADS>
-    __device__ __forceinline__ void start(const AttnArgs& a, const Plan& p, const Seq& first) {
-        if (threadIdx.x % THREADS) return;
-        wk.left = p.u1 - p.u0;
-        wk.u = p.u0;
-        wk.b = wk.h = wk.rt = wk.rts = 0;
-        wk.off = 0;
-        if (wk.left <= 0) return;
-        wk.b = p.b;
-        wk.rt = p.rt;
-        wk.off = p.off;
-        wk.s = first;
-        wk.rts = Work<kMT, kKT>::row_tiles(a, first);
-    }
-    template <int THREADS>
-    __device__ __forceinline__ bool next(const AttnArgs& a, int bar = 0) {
-        sync<THREADS>(bar);
-        if (threadIdx.x % THREADS == 0) {
-            more = wk.next(a, it);
-            if (more) {
-                rows = min(kMT, it.s.nq * a.group - it.rt * kMT);
-                half = (rows + 1) / 2;
-                tiles = it.hi > it.lo ? it.t1 - it.t0 : 0;
-                const int2 w = rows_whole(a, it.s, a.query_of(it.rt * kMT), a.query_of(it.rt * kMT + rows - 1));
-                wlo = w.x;
-                whi = w.y;
-            }
-        }
-        sync<THREADS>(bar);
-        return more != 0;
+    template <int MT>
+    __device__ __forceinline__ void set(const AttnArgs& a, const Item& i) {
+        const int n = min(MT, i.s.nq * a.group - i.rt * MT);
+        const int2 w = rows_whole(a, i.s, a.query_of(i.rt * MT), a.query_of(i.rt * MT + n - 1));
+        it = i;
+        rows = n;
+        half = (n + 1) / 2;
+        tiles = i.hi > i.lo ? i.t1 - i.t0 : 0;
+        wlo = w.x;
+        whi = w.y;
     }
     __device__ __forceinline__ int key0(int tile) const { return (it.tile0 + it.t0 + tile) * kKT; }
 };
 
-// Barriers of the two stages of K, V, S and P, a tile each in turn.
+// Barriers of the stages of K and of the two of V, S and P, a tile each in turn.
 struct Shared {
     float top[2][2][kRows];                 // a row's maximum by half of a tile's keys, two tiles in turn
     float sum[2][kRows];
     int64_t scan[16];                       // plan_work's
     // of this CTA: what landed, and the room that the products gave back
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
     // of the pair, in its first CTA: operands in place in both
-    uint64_t k_ready[2], v_ready[2], p_ready[2], q_ready;
+    uint64_t k_ready[3], v_ready[2], p_ready[2], q_ready;
     // of this CTA: the pair's products are done
     uint64_t s_full[2], pv_done[2], done;
     Plan plan;
-    Seq first;                              // of the pair's units
-    Ctx ctx[6];                             // softmax, copies of keys, MMA, keys and values passed on, copies of values
+    Job job[kAhead];
+    uint64_t job_full[kAhead], job_empty[kAhead];
     uint32_t tmem;
+};
+
+// A warp's way through the queue.
+struct Jobs {
+    int n = 0;
+    __device__ __forceinline__ const Job* next(Shared& sh, const AttnArgs& a) {
+        if (!warp_wait(&sh.job_full[n % kAhead], (n / kAhead) & 1, a.err, a.timeout_ns)) return nullptr;
+        const Job* j = &sh.job[n % kAhead];
+        return j->more ? j : nullptr;
+    }
+    // by all of the warp, once it has read what it needs of the item
+    __device__ __forceinline__ void done(Shared& sh) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.job_empty[n % kAhead]);
+        ++n;
+    }
+};
+
+// A warpgroup's next item: all of it goes on or stops, at the named barrier `id`.
+__device__ __forceinline__ const Job* next_of_group(Jobs& jobs, Shared& sh, const AttnArgs& a, int id, bool dead) {
+    const Job* j = dead ? nullptr : jobs.next(sh, a);
+    return bar_and(id, j != nullptr, 128) ? j : nullptr;
+}
+
+// A place in a ring of N stages.
+template <int N>
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void step() {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
 };
 
 // ----------------------------------------------------------------- copies ----
@@ -147,25 +164,47 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
 // and the rotary part) and values (all 64 keys, this CTA's half of the elements).  A
 // box a page, each page by a lane of its own.  e4m3: the codes land in the second half
 // of their stage, see convert.
-template <int C, bool E4M3, bool V>
+template <int C, bool FEW, bool E4M3, bool V>
 __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMaps& maps, Shared& sh, uint8_t* ring, uint32_t rank) {
-    using F = Cfg<C>;
+    using F = Cfg<C, FEW>;
     constexpr int kN = V ? kKT : kKeys, kGroup = (V ? F::kVGroup : F::kKGroup) / (E4M3 ? 2 : 1);   // eight keys' bytes
+    constexpr int kStages = V ? 2 : F::kKStages;
     const AttnArgs& a = la.a;
     uint64_t* fulls = V ? sh.v_full : sh.k_full;
     uint64_t* empties = V ? sh.v_empty : sh.k_empty;
     const CUtensorMap* map = V ? &maps.values : &maps.keys;
     const int lane = threadIdx.x & 31, p0 = V ? static_cast<int>(rank) * F::kVPanels / (E4M3 ? 2 : 1) : 0;
     const int tokens = min(la.c.page, kN), boxes = kN / tokens;
-    Ctx& ctx = sh.ctx[V ? 5 : 1];
-    ctx.start<32>(a, sh.plan, sh.first);
+    Walk<F::kItem, kKT> walk;                                    // keys: every lane's own, in registers
+    if (!V) walk.start(a, sh.plan);
+    Jobs jobs;
+    Ring<kStages> at;
     int uses = 0;
     bool dead = false;
-    while (!dead && ctx.next<32>(a)) {
-        const Item& it = ctx.it;
+    while (!dead) {
+        const Job* job;
+        if constexpr (V) {
+            job = jobs.next(sh, a);
+            if (!job) break;
+        } else {
+            Job& next = sh.job[jobs.n % kAhead];
+            if (!warp_wait(&sh.job_empty[jobs.n % kAhead], ((jobs.n / kAhead) & 1) ^ 1, a.err, a.timeout_ns)) break;
+            Item it;                                             // (the others' waits for it run out too)
+            const bool more = walk.next(a, it);
+            if (lane == 0) {
+                next.more = more;
+                if (more) next.set<F::kItem>(a, it);
+                mbar_arrive(&sh.job_full[jobs.n % kAhead]);
+            }
+            __syncwarp();
+            if (!more) break;
+            job = &next;
+            ++jobs.n;
+        }
+        const Item& it = job->it;
         const int32_t* table = a.sq.table + int64_t(it.b) * a.sq.max_pages;
-        for (int j = 0; j < ctx.tiles; ++j, ++uses) {
-            const int k = ctx.key0(j) + (V ? 0 : static_cast<int>(rank) * kKeys) + lane * tokens, st = uses & 1;
+        for (int j = 0; j < job->tiles; ++j, ++uses, at.step()) {
+            const int k = job->key0(j) + (V ? 0 : static_cast<int>(rank) * kKeys) + lane * tokens;
             const bool mine = lane < boxes && k < it.hi && k + tokens > it.lo;
             int page = mine ? table[k >> la.c.page_log2] : 0;
             if (page < 0 || page >= la.c.n_pages) {
@@ -173,43 +212,44 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMa
                 page = la.c.n_pages;                             // out of range: reads as zeros
             }
             const int rows = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * tokens;
-            dead = !warp_wait(&empties[st], ((uses >> 1) & 1) ^ 1, a.err, a.timeout_ns);
+            dead = !warp_wait(&empties[at.st], at.ph ^ 1u, a.err, a.timeout_ns);
             if (dead) break;
-            uint64_t* full = &fulls[st];
+            uint64_t* full = &fulls[at.st];
             if (lane == 0) mbar_arrive_expect_tx(full, rows / 8 * (kGroup + (V ? 0 : kAtom)));
             __syncwarp();
             if (mine) {
                 const int slot = k & (la.c.page - 1);
-                uint8_t* stage = ring + st * (V ? F::kVBytes : F::kKBytes);
+                uint8_t* stage = ring + at.st * (V ? F::kVBytes : F::kKBytes);
                 uint8_t* to = stage + (E4M3 ? kN / 8 * kGroup : 0) + lane * (tokens / 8) * kGroup;
                 if (!V) tma_load_3d(stage + F::kRope + lane * (tokens / 8) * kAtom, &maps.rope, full, 0, slot, page);
                 tma_load_5d(to, map, full, 0, 0, p0, slot / 8, page);
             }
             __syncwarp();
         }
+        if constexpr (V) jobs.done(sh);
     }
     // each stage's last copy
-    for (int st = 0; st < 2; ++st) {
-        const int n = (uses + 1 - st) / 2;
+    for (int st = 0; st < kStages; ++st) {
+        const int n = (uses + kStages - 1 - st) / kStages;
         if (n > 0) mbar_wait(&fulls[st], (n - 1) & 1, a.err, kDrainNs);
     }
 }
 
 // ------------------------------------------------------------ passing on ----
 // What landed in this CTA is told to the first one, whose MMA warp waits for both.
-template <int C>
+template <int C, bool FEW>
 __device__ __forceinline__ void pass_k(const LatentAttnArgs& la, Shared& sh) {
     const AttnArgs& a = la.a;
-    Ctx& ctx = sh.ctx[3];
-    ctx.start<32>(a, sh.plan, sh.first);
-    int n = 0;
+    Jobs jobs;
+    Ring<Cfg<C, FEW>::kKStages> at;
     bool dead = false;
-    while (!dead && ctx.next<32>(a)) {
-        for (int j = 0; j < ctx.tiles; ++j, ++n) {
-            dead = !warp_wait(&sh.k_full[n & 1], (n >> 1) & 1, a.err, a.timeout_ns);
+    while (const Job* job = dead ? nullptr : jobs.next(sh, a)) {
+        for (int j = 0; j < job->tiles; ++j, at.step()) {
+            dead = !warp_wait(&sh.k_full[at.st], at.ph, a.err, a.timeout_ns);
             if (dead) break;
-            if ((threadIdx.x & 31) == 0) arrive_first(&sh.k_ready[n & 1]);
+            if ((threadIdx.x & 31) == 0) arrive_first(&sh.k_ready[at.st]);
         }
+        jobs.done(sh);
     }
 }
 
@@ -225,35 +265,34 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& w) {
 // zeroed, as are, in tiles where some row does not see some key, those of a key with an
 // element that is not finite (its score is not finite for the rows that do see it,
 // which so become NaN all the same; a probability of 0 would make the others NaN).
-template <int C>
+template <int C, bool FEW>
 __device__ __forceinline__ void pass_v(const LatentAttnArgs& la, Shared& sh, uint8_t* vs) {
-    using F = Cfg<C>;
+    using F = Cfg<C, FEW>;
     const AttnArgs& a = la.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-    Ctx& ctx = sh.ctx[4];
-    ctx.start<128>(a, sh.plan, sh.first);
-    int n = 0;
+    Jobs jobs;
+    Ring<2> at;
     bool dead = false;
-    while (ctx.next<128>(a, kBarV)) {
-        for (int j = 0; j < ctx.tiles && !dead; ++j, ++n) {
-            const int st = n & 1;
-            dead = !warp_wait(&sh.v_full[st], (n >> 1) & 1, a.err, a.timeout_ns);
+    while (const Job* job = dead ? nullptr : jobs.next(sh, a)) {
+        for (int j = 0; j < job->tiles; ++j, at.step()) {
+            dead = !warp_wait(&sh.v_full[at.st], at.ph, a.err, a.timeout_ns);
             if (dead) break;
-            const int j0 = ctx.key0(j), lo = max(ctx.it.lo, ctx.wlo), hi = min(ctx.it.hi, ctx.whi);
+            const int j0 = job->key0(j), lo = max(job->it.lo, job->wlo), hi = min(job->it.hi, job->whi);
             if (j0 < lo || j0 + kKT > hi) {
                 // a key's elements, 16 bytes a lane
-                uint8_t* v = vs + st * F::kVBytes + (lane >> 3) * kAtom + (lane & 7) * 16;
+                uint8_t* v = vs + at.st * F::kVBytes + (lane >> 3) * kAtom + (lane & 7) * 16;
                 for (int r = warp; r < kKT; r += 4) {
                     uint4* p = reinterpret_cast<uint4*>(v + (r >> 3) * F::kVGroup + (r & 7) * 128);
-                    bool bad = j0 + r < ctx.it.lo || j0 + r >= ctx.it.hi;
+                    bool bad = j0 + r < job->it.lo || j0 + r >= job->it.hi;
                     if (lane < 8 * F::kVPanels) bad = bad || any_nonfinite(*p);
                     if (__any_sync(0xFFFFFFFFu, bad) && lane < 8 * F::kVPanels) *p = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) arrive_first(&sh.v_ready[st]);
+            if (lane == 0) arrive_first(&sh.v_ready[at.st]);
         }
+        jobs.done(sh);
     }
 }
 
@@ -302,9 +341,9 @@ __device__ __forceinline__ void convert_row(const uint4 (&raw)[8], uint8_t* firs
 
 // e4m3: four warps each for keys and values, a thread a key and 128 codes.  All codes
 // are read before any atom is written over them.
-template <int C, bool V>
+template <int C, bool FEW, bool V>
 __device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, uint8_t* ring) {
-    using F = Cfg<C>;
+    using F = Cfg<C, FEW>;
     constexpr int kN = V ? kKT : kKeys, kGroup = V ? F::kVGroup : F::kKGroup, kUnits = V ? F::kVPanels / 2 : F::kParts;
     static_assert(kN * kUnits <= 128, "a row's part a thread");
     const AttnArgs& a = la.a;
@@ -312,15 +351,13 @@ __device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, ui
     // 2^120 times the cache's power of two (see e4m3x4_to_bf16), and 480 times it
     const uint32_t f = static_cast<uint32_t>(127 + 120 + la.c.scale_log2) << 7, factor = f | (f << 16);
     const uint32_t nan_bits = 0x43F0u + static_cast<uint32_t>(la.c.scale_log2 * 128);
-    Ctx& ctx = sh.ctx[V ? 4 : 3];
-    ctx.start<128>(a, sh.plan, sh.first);
-    int n = 0;
+    Jobs jobs;
+    Ring<V ? 2 : F::kKStages> at;
     bool dead = false;
-    while (ctx.next<128>(a, V ? kBarV : kBarK)) {
-        for (int j = 0; j < ctx.tiles && !dead; ++j, ++n) {
-            const int st = n & 1;
-            uint8_t* stage = ring + st * (V ? F::kVBytes : F::kKBytes);
-            const bool ok = mbar_wait(V ? &sh.v_full[st] : &sh.k_full[st], (n >> 1) & 1, a.err, a.timeout_ns);
+    while (const Job* job = next_of_group(jobs, sh, a, V ? kBarV : kBarK, dead)) {
+        for (int j = 0; j < job->tiles; ++j, at.step()) {
+            uint8_t* stage = ring + at.st * (V ? F::kVBytes : F::kKBytes);
+            const bool ok = mbar_wait(V ? &sh.v_full[at.st] : &sh.k_full[at.st], at.ph, a.err, a.timeout_ns);
             uint4 raw[8];
             if (part < kUnits) {
                 const uint8_t* from = stage + kN / 8 * (kGroup / 2) + (r >> 3) * (kGroup / 2) + part * kAtom + (r & 7) * 128;
@@ -330,83 +367,86 @@ __device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, ui
             dead = !bar_and(V ? kBarV : kBarK, ok, 128);
             if (dead) break;
             if (part < kUnits) {
-                const int j0 = ctx.key0(j), key = j0 + r;
+                const int j0 = job->key0(j), key = j0 + r;
                 convert_row(raw, stage + (r >> 3) * kGroup + 2 * part * kAtom + (r & 7) * 128, r, factor, nan_bits,
-                            V && (key < ctx.it.lo || key >= ctx.it.hi), V && (j0 < ctx.wlo || j0 + kKT > ctx.whi));
+                            V && (key < job->it.lo || key >= job->it.hi), V && (j0 < job->wlo || j0 + kKT > job->whi));
             }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_first(V ? &sh.v_ready[st] : &sh.k_ready[st]);
+            if (lane == 0) arrive_first(V ? &sh.v_ready[at.st] : &sh.k_ready[at.st]);
         }
+        jobs.done(sh);
     }
 }
 
 // --------------------------------------------------------------- products ----
-// The MMA warp of the first CTA: Q K^T of a tile, then P V of the one before, so
-// that one tile's softmax runs beside another's products.
-// The MMA warp of the first CTA: Q K^T of a tile, then P V of the one before, so
-// that one tile's softmax runs beside another's products.
-template <int C>
+// The MMA warp of the first CTA: Q K^T of a tile, then P V of the one before, so that
+// one tile's softmax runs beside another's products.
+template <int C, bool FEW>
 __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, uint8_t* qs, uint8_t* ps, uint8_t* ks, uint8_t* vs) {
-    using F = Cfg<C>;
+    using F = Cfg<C, FEW>;
     constexpr uint32_t kIdQK = idesc(false, kKT), kIdPV = idesc(true, 256);
     const AttnArgs& a = la.a;
     const uint32_t colS = sh.tmem, colO = sh.tmem + kColO;
     const uint64_t qd = sdesc(smem_u32(qs), 16, 1024), pd = sdesc(smem_u32(ps), 16, 1024);
     const uint64_t kd = sdesc(smem_u32(ks), 16, F::kKGroup), rd = sdesc(smem_u32(ks) + F::kRope, 16, kAtom);
     const uint64_t vd = sdesc(smem_u32(vs), kAtom, F::kVGroup);
-    Ctx& ctx = sh.ctx[2];
-    ctx.start<32>(a, sh.plan, sh.first);
-    uint32_t qp = 0, g = 0;                                      // phase of q_ready; tiles begun
+    Jobs jobs;
+    Ring<F::kKStages> ka;                                        // K
+    Ring<2> sa, pa;                                              // S; P and V
+    uint32_t qp = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead) dead = !warp_wait(bar, parity, a.err, a.timeout_ns);
     };
-    while (!dead && ctx.next<32>(a)) {
-        const int T = ctx.tiles;
-        if (T == 0) continue;
-        wait(&sh.q_ready, qp);
-        qp ^= 1u;
-        for (int i = 0; i <= T && !dead; ++i) {
+    while (const Job* job = dead ? nullptr : jobs.next(sh, a)) {
+        const int T = job->tiles;
+        if (T > 0) {
+            wait(&sh.q_ready, qp);
+            qp ^= 1u;
+        }
+        for (int i = 0; i <= T && T > 0 && !dead; ++i) {
             if (i < T) {
-                const uint32_t st = g & 1u;
-                wait(&sh.k_ready[st], (g >> 1) & 1u);
+                wait(&sh.k_ready[ka.st], ka.ph);
                 if (dead) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t kk = kd + (st * F::kKBytes >> 4), rr = rd + (st * F::kKBytes >> 4);
+                    // (bases and constants: each operand worked out on its own would cost as much as its product)
+                    const uint64_t kk = kd + ka.st * (F::kKBytes >> 4), rr = rd + ka.st * (F::kKBytes >> 4);
 #pragma unroll
                     for (int x = 0; x <= C / 64; ++x)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            pair_mma(colS + 32 * st, qd + ((x * kRowPanel + k * 32) >> 4),
+                            pair_mma(colS + 32 * sa.st, qd + ((x * F::kQPanel + k * 32) >> 4),
                                      x < C / 64 ? kk + ((x * kAtom + k * 32) >> 4) : rr + (k * 32 >> 4), kIdQK, x > 0 || k > 0);
-                    pair_commit(&sh.s_full[st]);
-                    pair_commit(&sh.k_empty[st]);
+                    pair_commit(&sh.s_full[sa.st]);
+                    pair_commit(&sh.k_empty[ka.st]);
                 }
                 __syncwarp();
-                ++g;
+                ka.step();
+                sa.step();
             }
             if (i > 0) {
-                const uint32_t v = g - (i < T ? 2u : 1u), st = v & 1u, ph = (v >> 1) & 1u;
-                wait(&sh.v_ready[st], ph);
-                wait(&sh.p_ready[st], ph);
+                wait(&sh.v_ready[pa.st], pa.ph);
+                wait(&sh.p_ready[pa.st], pa.ph);
                 if (dead) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t pp = pd + (st * F::kPBytes >> 4), vv = vd + (st * F::kVBytes >> 4);
+                    const uint64_t pp = pd + pa.st * (F::kPBytes >> 4), vv = vd + pa.st * (F::kVBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int n = 0; n < F::kNV; ++n)
                             pair_mma(colO + 128 * n, pp + (k * 32 >> 4), vv + ((2 * n * kAtom + 2 * k * F::kVGroup) >> 4), kIdPV,
                                      i > 1 || k > 0);
-                    pair_commit(&sh.v_empty[st]);
-                    pair_commit(&sh.pv_done[st]);
+                    pair_commit(&sh.v_empty[pa.st]);
+                    pair_commit(&sh.pv_done[pa.st]);
                 }
                 __syncwarp();
+                pa.step();
             }
         }
+        jobs.done(sh);
     }
     // the products end before the accumulators are given back
     if (elect_one()) pair_commit(&sh.done);
@@ -418,13 +458,13 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
 // The CTA's rows of Q into shared memory, K-major with the 128-byte swizzle: a warp
 // copies whole rows, all of its 16 on their way at once; rows past the last are zeros.
 // (By registers, nine pieces a thread at a time, an item's start took 18,000 clocks.)
-template <int C>
+template <int C, bool FEW>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int row0, int count, bool negate, uint8_t* qs) {
     constexpr int kChunks = (C + kLatentRot) / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto place = [&](int r, int ch) { return qs + (ch >> 3) * kRowPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+    auto place = [&](int r, int ch) { return qs + (ch >> 3) * Cfg<C, FEW>::kQPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
 #pragma unroll 4
-    for (int r = warp; r < kRows; r += 4) {
+    for (int r = warp; r < Cfg<C, FEW>::kHeld; r += 4) {
         const int row = row0 + min(r, count - 1), qi = a.query_of(row), hd = row - qi * a.group;
         const uint16_t* src = a.q + int64_t(it.s.q0 + qi) * a.q_stride + hd * (C + kLatentRot);
         const uint32_t bytes = r < count ? 16u : 0u;
@@ -436,7 +476,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (negate) {
 #pragma unroll 1
-        for (int r = warp; r < kRows; r += 4)
+        for (int r = warp; r < Cfg<C, FEW>::kHeld; r += 4)
             for (int ch = lane; ch < kChunks; ch += 32) {
                 uint4* p = reinterpret_cast<uint4*>(place(r, ch));
                 const uint4 w = *p;
@@ -446,18 +486,16 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
     fence_async_smem();
 }
 
-template <int C>
+template <int C, bool FEW>
 __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uint8_t* qs, uint8_t* ps, int pair, uint32_t rank) {
-    using F = Cfg<C>;
+    using F = Cfg<C, FEW>;
     const AttnArgs& a = la.a;
     const int tid = threadIdx.x, lr = tid & 63, half = tid >> 6, lane = tid & 31;
     const uint32_t tm = sh.tmem + (static_cast<uint32_t>(tid & 96) << 16);
     const uint32_t colO = tm + kColO;
     uint8_t* p_row = ps + lr * 128;
     const bool draft = a.draft != nullptr;
-    Ctx& ctx = sh.ctx[0];
-    ctx.start<128>(a, sh.plan, sh.first);
-    const Item& it = ctx.it;
+    Jobs jobs;
     uint32_t g = 0;                                              // tiles so far
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -468,88 +506,91 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
     // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf), or NaN; the sign goes to the queries
     const float cs = a.scale * kLog2e;
     const float c = fmaxf(fabsf(cs), 1.2e-38f);
-    while (ctx.next<128>(a, kBarSoft)) {
-        const int row0 = static_cast<int>(rank) * ctx.half, count = rank ? ctx.rows - ctx.half : ctx.half;
-        const int T = ctx.tiles;
-        const bool valid = lr < count;
-        const int r = it.rt * kMT + row0 + (valid ? lr : 0), qi = a.query_of(r), hd = r - qi * a.group;
+    while (const Job* job = next_of_group(jobs, sh, a, kBarSoft, __any_sync(0xFFFFFFFFu, dead))) {
+        const Item& it = job->it;
+        const int row0 = static_cast<int>(rank) * job->half, count = rank ? job->rows - job->half : job->half;
+        const int T = job->tiles;
+        const bool valid = lr < count, warp_on = __any_sync(0xFFFFFFFFu, valid);   // (both warps of 32 rows alike)
+        const int r = it.rt * F::kItem + row0 + (valid ? lr : 0), qi = a.query_of(r), hd = r - qi * a.group;
         RowView view{0, 0, 0ull};
         if (valid) view = row_view(a, it.s, qi);
         if (T > 0) {
-            load_queries<C>(a, it, it.rt * kMT + row0, count, cs < 0.0f, qs);
+            load_queries<C, FEW>(a, it, it.rt * F::kItem + row0, count, cs < 0.0f, qs);
             __syncwarp();
             if (lane == 0) arrive_first(&sh.q_ready);
         }
         float ref = kNegInf, sum0 = 0.0f, sum1 = 0.0f;
         for (int j = 0; j < T; ++j, ++g) {
-            const int j0 = ctx.key0(j);
+            const int j0 = job->key0(j);
             wait(&sh.s_full[g & 1u], (g >> 1) & 1u);
-            float x[32];
-            tmem_ld32(tm + 32 * (g & 1u), x);
-            tmem_wait_ld();
-            if (j0 < ctx.wlo || j0 + kKT > ctx.whi) {
-                const uint32_t bits = row_bits(view, draft, it.s.first, j0 + half * kKeys);
+            if (warp_on) {
+                float x[32];
+                tmem_ld32(tm + 32 * (g & 1u), x);
+                tmem_wait_ld();
+                if (j0 < job->wlo || j0 + kKT > job->whi) {
+                    const uint32_t bits = row_bits(view, draft, it.s.first, j0 + half * kKeys);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!((bits >> e) & 1u)) x[e] = kNegInf;
-            }
-            float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[e + k]);
-            float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            sh.top[g & 1u][half][lr] = top;
-            // powers by the reference so far, while the row's other half says its maximum
-            uint32_t u[16];
-            float s0, s1;
-            auto powers = [&]() {
-                const float off = ref == kNegInf ? 0.0f : -ref;
-                s0 = sum0;
-                s1 = sum1;
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float p0, p1;
-                    fma2_to(p0, p1, x[e], x[e + 1], c, off);
-                    p0 = fast_exp2(p0);
-                    p1 = fast_exp2(p1);
-                    add2(s0, s1, p0, p1);
-                    u[e / 2] = pack_bf16(p0, p1);
+                    for (int e = 0; e < 32; ++e)
+                        if (!((bits >> e) & 1u)) x[e] = kNegInf;
                 }
-            };
-            if (j > 0) powers();
-            named_bar(kBarTop + ((tid >> 5) & 1), 64);
-            top = fmaxf(top, sh.top[g & 1u][half ^ 1][lr]) * c;
-            if (!(top > kNegInf)) top = kNegInf;                 // (NaN: the sums carry it)
-            const bool grow = top > ref + kLag || (ref == kNegInf && top > kNegInf);
-            if (__any_sync(0xFFFFFFFFu, grow) || j == 0) {
-                const float f = !grow ? 1.0f : (ref == kNegInf ? 0.0f : fast_exp2(ref - top));
-                sum0 *= f;
-                sum1 *= f;
-                if (grow) ref = top;
-                if (j > 0) {
-                    wait_pv(g - 1);
-#pragma unroll 1
-                    for (int q = 0; q < F::kNV * 8; ++q) {
-                        float o[16];
-                        tmem_ld16(colO + 16 * q, o);
-                        tmem_wait_ld();
-                        uint32_t w[16];
+                float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
-                        tmem_st16(colO + 16 * q, w);
+                for (int e = 0; e < 32; e += 4)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[e + k]);
+                float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                sh.top[g & 1u][half][lr] = top;
+                // powers by the reference so far, while the row's other half says its maximum
+                uint32_t u[16];
+                float s0, s1;
+                auto powers = [&]() {
+                    const float off = ref == kNegInf ? 0.0f : -ref;
+                    s0 = sum0;
+                    s1 = sum1;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float p0, p1;
+                        fma2_to(p0, p1, x[e], x[e + 1], c, off);
+                        p0 = fast_exp2(p0);
+                        p1 = fast_exp2(p1);
+                        add2(s0, s1, p0, p1);
+                        u[e / 2] = pack_bf16(p0, p1);
                     }
-                    tmem_wait_st();
-                }
-                powers();
-            }
-            sum0 = s0;
-            sum1 = s1;
-            // (P's room has been read: S of this tile came after P V of two before)
+                };
+                if (j > 0) powers();
+                named_bar(kBarTop + ((tid >> 5) & 1), 64);
+                top = fmaxf(top, sh.top[g & 1u][half ^ 1][lr]) * c;
+                if (!(top > kNegInf)) top = kNegInf;                 // (NaN: the sums carry it)
+                const bool grow = top > ref + kLag || (ref == kNegInf && top > kNegInf);
+                if (__any_sync(0xFFFFFFFFu, grow) || j == 0) {
+                    const float f = !grow ? 1.0f : (ref == kNegInf ? 0.0f : fast_exp2(ref - top));
+                    sum0 *= f;
+                    sum1 *= f;
+                    if (grow) ref = top;
+                    if (j > 0) {
+                        wait_pv(g - 1);
+#pragma unroll 1
+                        for (int q = 0; q < F::kNV * 8; ++q) {
+                            float o[16];
+                            tmem_ld16(colO + 16 * q, o);
+                            tmem_wait_ld();
+                            uint32_t w[16];
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                *reinterpret_cast<uint4*>(p_row + (g & 1u) * F::kPBytes + (((4 * half + ch) ^ (lr & 7)) << 4)) =
-                    make_uint4(u[4 * ch], u[4 * ch + 1], u[4 * ch + 2], u[4 * ch + 3]);
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+                            tmem_st16(colO + 16 * q, w);
+                        }
+                        tmem_wait_st();
+                    }
+                    powers();
+                }
+                sum0 = s0;
+                sum1 = s1;
+                // (P's room has been read: S of this tile came after P V of two before)
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    *reinterpret_cast<uint4*>(p_row + (g & 1u) * F::kPBytes + (((4 * half + ch) ^ (lr & 7)) << 4)) =
+                        make_uint4(u[4 * ch], u[4 * ch + 1], u[4 * ch + 2], u[4 * ch + 3]);
+            }
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
@@ -571,7 +612,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
                 a.lse[at] = ref == kNegInf ? kNegInf : (ref + log2f(sum)) * kLn2;
         }
         if (T > 0) wait_pv(g - 1);
-        if (__any_sync(0xFFFFFFFFu, valid)) {
+        if (warp_on) {
 #pragma unroll 1
             for (int q = 0; q < F::kNV * 4; ++q) {
                 float o[32];
@@ -598,27 +639,34 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
             }
         }
         tc_fence_before();
-        if (tid == 0 && rank == 0) note_split(a, it, ctx.rows, kMT, sh.plan, pair);
+        if (tid == 0 && rank == 0) note_split(a, it, job->rows, F::kItem, sh.plan, pair);
+        jobs.done(sh);
     }
 }
 
-template <int C, bool E4M3>
+template <int C, bool FEW, bool E4M3>
 __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const LatentAttnArgs la, const __grid_constant__ LatentMaps maps) {
-    using F = Cfg<C>;
+    using F = Cfg<C, FEW>;
     extern __shared__ __align__(1024) uint8_t dyn[];
     uint8_t* qs = dyn;
     uint8_t* ps = qs + F::kQBytes;
     uint8_t* ks = ps + 2 * F::kPBytes;
-    uint8_t* vs = ks + 2 * F::kKBytes;
+    uint8_t* vs = ks + F::kKStages * F::kKBytes;
     Shared& sh = *reinterpret_cast<Shared*>(dyn + F::kSmem);
     const AttnArgs& a = la.a;
     const int warp = threadIdx.x >> 5, pair = blockIdx.x >> 1;
     const uint32_t rank = cta_rank();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < F::kKStages; ++i) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.k_ready[i], E4M3 ? 8 : 2);             // both CTAs' passing warps
+        }
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(&sh.job_full[i], 1);
+            mbar_init(&sh.job_empty[i], 4 + 1 + (E4M3 ? 4 : 1) + 4 + (rank == 0 ? 1 : 0));   // softmax, values, passing on, MMA
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.v_full[i], 1);
             mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.v_ready[i], 8);
@@ -639,30 +687,28 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     cluster_sync();                                              // both CTAs' barriers are there
     pdl_wait();
     pdl_launch_dependents();
-    plan_work<kMT, kKT>(a, 1, sh.scan, &sh.plan, pair, gridDim.x >> 1, rank == 0);   // (its barriers publish sh.tmem)
-    if (threadIdx.x == 0 && sh.plan.u0 < sh.plan.u1) sh.first = load_seq(a.sq, a.kv.page, sh.plan.b, nullptr);
-    __syncthreads();
+    plan_work<F::kItem, kKT>(a, 1, sh.scan, &sh.plan, pair, gridDim.x >> 1, rank == 0);   // (its barriers publish sh.tmem)
     tc_fence_after();
     zero_pad_rows(a, sh.plan.seqs);
     if (warp < 4)
-        soften<C>(la, sh, qs, ps, pair, rank);
+        soften<C, FEW>(la, sh, qs, ps, pair, rank);
     else if (warp == 4)
-        produce<C, E4M3, false>(la, maps, sh, ks, rank);
+        produce<C, FEW, E4M3, false>(la, maps, sh, ks, rank);
     else if (warp == 5) {
-        if (rank == 0) multiply<C>(la, sh, qs, ps, ks, vs);
+        if (rank == 0) multiply<C, FEW>(la, sh, qs, ps, ks, vs);
     } else if (warp == 6)
-        produce<C, E4M3, true>(la, maps, sh, vs, rank);
+        produce<C, FEW, E4M3, true>(la, maps, sh, vs, rank);
     else if (warp >= 8) {
         if constexpr (E4M3) {
             if (warp < 12)
-                convert<C, true>(la, sh, vs);
+                convert<C, FEW, true>(la, sh, vs);
             else
-                convert<C, false>(la, sh, ks);
+                convert<C, FEW, false>(la, sh, ks);
         } else {
-            pass_v<C>(la, sh, vs);
+            pass_v<C, FEW>(la, sh, vs);
         }
     } else if (!E4M3) {
-        pass_k<C>(la, sh);
+        pass_k<C, FEW>(la, sh);
     }
     __syncwarp();
     tc_fence_before();
@@ -672,14 +718,14 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     if (warp == 6) pair_dealloc(sh.tmem);
 }
 
-template <int C, bool E4M3>
+template <int C, bool FEW, bool E4M3>
 cudaError_t launch(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cudaStream_t s) {
-    constexpr size_t smem = Cfg<C>::kSmem + sizeof(Shared);
+    constexpr size_t smem = Cfg<C, FEW>::kSmem + sizeof(Shared);
     static_assert(smem <= 232448, "227 KB a CTA");
-    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(latent_attn_kernel<C, E4M3>), static_cast<int>(smem));
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(latent_attn_kernel<C, FEW, E4M3>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int pairs = n_sms / 2 < kMaxPairs ? n_sms / 2 : kMaxPairs;
-    e = launch_pdl_cluster(latent_attn_kernel<C, E4M3>, dim3(2 * pairs), dim3(kThreads<E4M3>), 2, smem, s, a, m);
+    e = launch_pdl_cluster(latent_attn_kernel<C, FEW, E4M3>, dim3(2 * pairs), dim3(kThreads<E4M3>), 2, smem, s, a, m);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_pair_join<C, kLatentRows>(a.a, pairs, n_sms, s);
@@ -687,9 +733,13 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cuda
 
 }  // namespace
 
-cudaError_t launch_latent_attn(const LatentAttnArgs& a, const LatentMaps& m, int n_sms, cudaStream_t s) {
-    if (a.c.dim == 512) return a.c.e4m3 ? launch<512, true>(a, m, n_sms, s) : launch<512, false>(a, m, n_sms, s);
-    return a.c.e4m3 ? launch<256, true>(a, m, n_sms, s) : launch<256, false>(a, m, n_sms, s);
+cudaError_t launch_latent_attn(const LatentAttnArgs& a, const LatentMaps& m, bool few, int n_sms, cudaStream_t s) {
+    if (a.c.dim == 512) {
+        if (few) return a.c.e4m3 ? launch<512, true, true>(a, m, n_sms, s) : launch<512, true, false>(a, m, n_sms, s);
+        return a.c.e4m3 ? launch<512, false, true>(a, m, n_sms, s) : launch<512, false, false>(a, m, n_sms, s);
+    }
+    if (few) return a.c.e4m3 ? launch<256, true, true>(a, m, n_sms, s) : launch<256, true, false>(a, m, n_sms, s);
+    return a.c.e4m3 ? launch<256, false, true>(a, m, n_sms, s) : launch<256, false, false>(a, m, n_sms, s);
 }
 
 }  // namespace moe
