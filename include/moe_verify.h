@@ -757,7 +757,7 @@ moe_status_t moe_latent_attention(const moe_attn_t* attn, const moe_latent_cache
  *   out        bf16 [n_rows, latent_dim + 64], row stride out_stride (elements, a
  *              multiple of 8)
  *   ws         at least 256 bytes: the error word
- * cu_q and max_q of seqs are not read.  n_rows == 0 launches nothing.
+ * cu_q and max_q of seqs are not read.  n_rows is at most MOE_MAX_KV_LEN; 0 launches nothing.
  */
 moe_status_t moe_latent_gather(const moe_latent_cache_t* cache, const moe_seqs_t* seqs,
                                const int32_t* cu_k, int32_t n_rows, void* out, int64_t out_stride,

@@ -113,7 +113,7 @@ moe::AttnArgs attn_args(const moe_attn_t* at, const moe_seqs_t* s, const void* q
     return a;
 }
 
-// The cache's tensor maps (encoded anew by every call: 0.6 us of the host's time).
+// The cache's tensor maps, encoded anew by every call: nothing is kept by an address.
 bool make_maps(const moe_latent_cache_t* c, moe::LatentMaps* m) {
     auto fn = moe::encode_fn();
     if (!fn) return false;
@@ -248,6 +248,7 @@ moe_status_t moe_latent_gather(const moe_latent_cache_t* cache, const moe_seqs_t
     if (st != MOE_OK) return st;
     if ((st = check_seqs(seqs, false, true)) != MOE_OK) return st;
     if (n_rows < 0) return MOE_ERR_INVALID_ARG;
+    if (n_rows > MOE_MAX_KV_LEN) return MOE_ERR_UNSUPPORTED;
     if (n_rows == 0) return MOE_OK;
     if (seqs->n_seqs == 0) return MOE_ERR_INVALID_ARG;
     if (!cu_k || !aligned(cu_k, 4) || !rows_ok(out, out_stride, cache->latent_dim + moe::kLatentRot)) return MOE_ERR_INVALID_ARG;

@@ -126,7 +126,8 @@ def test_bad_attention_settings(lib, at, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(cu=None), INVALID), (dict(N=-1), INVALID), (dict(out=None), INVALID), (dict(os=568), INVALID), (dict(os=578), INVALID),
+    (dict(cu=None), INVALID), (dict(N=-1), INVALID), (dict(N=(1 << 31) - 1), UNSUPPORTED), (dict(out=None), INVALID),
+    (dict(os=568), INVALID), (dict(os=578), INVALID),
     (dict(ws=None), INVALID), (dict(n=255), WORKSPACE)])
 def test_gather_refusals(lib, kw, status):
     assert gather(lib, **kw) == status
