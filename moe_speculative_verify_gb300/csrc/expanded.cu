@@ -291,7 +291,8 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
 // items too; a burst is PV of a tile, then QK of the next (which writes S over that
 // P).  A warp's waits run beside the other's burst.  (Bursts in strict turns left the one
 // stream waiting for the other's last tiles under a causal mask, and both for each
-// other's items: 573 us where this takes 539; a lock about a burst 552.)
+// other's items: 573 us for 4 ragged chunks of 64 heads where this takes 522; a lock
+// about a burst 552.)
 template <int D>
 __device__ __forceinline__ void multiply(const ExpandedArgs& x, Shared& sh, uint8_t* qs, uint8_t* ks, uint8_t* vs, int s) {
     using F = Cfg<D>;
