@@ -490,16 +490,18 @@ __device__ __forceinline__ void note_split(const AttnArgs& a, const Item& it, in
 
 // Zeroes the output rows that belong to no sequence: those before and after
 // the rows of the sequences that fit, which follow one another.
-__device__ __forceinline__ void zero_pad_rows(const AttnArgs& a, int seqs) {
+// By the threads t of nt of worker c of `workers`.
+__device__ __forceinline__ void zero_pad_rows(const AttnArgs& a, int seqs, int c = blockIdx.x, int workers = gridDim.x,
+                                              int t0 = threadIdx.x, int nt = blockDim.x) {
     const int first = seqs > 0 ? a.sq.cu_q[0] : a.sq.tokens, last = seqs > 0 ? a.sq.cu_q[seqs] : a.sq.tokens;
     const int n = first + (a.sq.tokens - last);
-    for (int p = blockIdx.x; p < n; p += gridDim.x) {
+    for (int p = c; p < n; p += workers) {
         const int64_t t = p < first ? p : last + (p - first);
         uint4* o = reinterpret_cast<uint4*>(a.out + t * a.q_heads * a.kv.dim);
-        for (int i = threadIdx.x; i < a.q_heads * a.kv.dim / 8; i += blockDim.x)
+        for (int i = t0; i < a.q_heads * a.kv.dim / 8; i += nt)
             o[i] = make_uint4(0, 0, 0, 0);
         if (a.lse)
-            for (int i = threadIdx.x; i < a.q_heads; i += blockDim.x)
+            for (int i = t0; i < a.q_heads; i += nt)
                 a.lse[t * a.q_heads + i] = kNegInf;
     }
 }

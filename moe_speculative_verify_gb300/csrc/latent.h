@@ -74,9 +74,11 @@ inline int64_t expanded_workspace_bytes(int dim) {
 // Tensor maps of the cache: the latent as a 5-D tensor (64 elements or 128 codes of a
 // row, eight tokens, such part of the row, such eight tokens, page), keys in boxes of
 // whole rows of min(page, 32) tokens, values of half rows of min(page, 64); the rotary
-// key as a 3-D one (element, token, page) in boxes as the keys'.  128-byte swizzled.
+// key as a 3-D one (element, token, page) in boxes as the keys'; q, if its rows lie one
+// behind another, as a 3-D one (64 elements, row, such part of the row) in boxes of a
+// CTA's rows.  128-byte swizzled.
 struct LatentMaps {
-    CUtensorMap keys, values, rope;
+    CUtensorMap keys, values, rope, q;
 };
 
 // Absorbed attention: `a` with one kv head of the latent's width and its rows the
@@ -84,6 +86,7 @@ struct LatentMaps {
 struct LatentAttnArgs {
     AttnArgs a;
     LatentArgs c;
+    bool q_flat;             // q has no gaps between tokens
 };
 
 // Tensor maps of the expanded form: q and k as 4-D tensors (64 elements, token, such

@@ -139,6 +139,15 @@ bool make_maps(const moe_latent_cache_t* c, moe::LatentMaps* m) {
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_q_map(const moe::LatentAttnArgs& a, bool few, moe::LatentMaps* m) {
+    const cuuint64_t row = a.c.dim + moe::kLatentRot;
+    const cuuint64_t dims[3] = {64, cuuint64_t(a.a.sq.tokens) * a.a.q_heads, row / 64}, strides[2] = {row * 2, 128};
+    const cuuint32_t box[3] = {64, cuuint32_t(moe::kLatentRows / (few ? 4 : 2)), cuuint32_t(row / 64)}, one[3] = {1, 1, 1};
+    return moe::encode_fn()(&m->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.a.q), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_maps(const moe::ExpandedArgs& a, moe::ExpandedMaps* m) {
     auto fn = moe::encode_fn();
     if (!fn) return false;
@@ -235,9 +244,11 @@ moe_status_t moe_latent_attention(const moe_attn_t* attn, const moe_latent_cache
     a.a.kv.page = a.c.page;
     a.a.kv.page_log2 = a.c.page_log2;
     a.a.kv.n_pages = a.c.n_pages;
-    moe::LatentMaps maps;
-    if (!make_maps(cache, &maps)) return MOE_ERR_CUDA;
     const bool few = int64_t(seqs->max_q) * attn->n_q_heads <= moe::kLatentRows / 2;
+    a.q_flat = q_stride == int64_t(attn->n_q_heads) * (cache->latent_dim + moe::kLatentRot);
+    moe::LatentMaps maps{};
+    if (!make_maps(cache, &maps)) return MOE_ERR_CUDA;
+    if (a.q_flat && !make_q_map(a, few, &maps)) return MOE_ERR_CUDA;
     return cuda_status(moe::launch_latent_attn(a, maps, few, device_info().sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -102,7 +102,7 @@ struct Shared {
     float sum[2][kRows];
     int64_t scan[16];                       // plan_work's
     // of this CTA: what landed, and the room that the products gave back
-    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2], q_full, q_empty;
     // of the pair, in its first CTA: operands in place in both
     uint64_t k_ready[3], v_ready[2], p_ready[2], q_ready;
     // of this CTA: the pair's products are done
@@ -165,7 +165,7 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
 // box a page, each page by a lane of its own.  e4m3: the codes land in the second half
 // of their stage, see convert.
 template <int C, bool FEW, bool E4M3, bool V>
-__device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMaps& maps, Shared& sh, uint8_t* ring, uint32_t rank) {
+__device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMaps& maps, Shared& sh, uint8_t* qs, uint8_t* ring, uint32_t rank) {
     using F = Cfg<C, FEW>;
     constexpr int kN = V ? kKT : kKeys, kGroup = (V ? F::kVGroup : F::kKGroup) / (E4M3 ? 2 : 1);   // eight keys' bytes
     constexpr int kStages = V ? 2 : F::kKStages;
@@ -179,7 +179,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMa
     if (!V) walk.start(a, sh.plan);
     Jobs jobs;
     Ring<kStages> at;
-    int uses = 0;
+    int uses = 0, queries = 0;                                   // copies of tiles, of queries
     bool dead = false;
     while (!dead) {
         const Job* job;
@@ -225,9 +225,24 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMa
                 tma_load_5d(to, map, full, 0, 0, p0, slot / 8, page);
             }
             __syncwarp();
+            if (!V && j == 0 && la.q_flat) {
+                dead = !warp_wait(&sh.q_empty, (queries & 1) ^ 1, a.err, a.timeout_ns);
+                if (dead) {
+                    ++uses;                                      // (this tile's copy is under way)
+                    break;
+                }
+                if (lane == 0) {
+                    const int row = it.s.q0 * a.group + it.rt * F::kItem + static_cast<int>(rank) * job->half;
+                    mbar_arrive_expect_tx(&sh.q_full, F::kQBytes);
+                    tma_load_3d(qs, &maps.q, &sh.q_full, 0, row, 0);
+                }
+                __syncwarp();
+                ++queries;
+            }
         }
         if constexpr (V) jobs.done(sh);
     }
+    if (queries > 0) mbar_wait(&sh.q_full, (queries - 1) & 1, a.err, kDrainNs);
     // each stage's last copy
     for (int st = 0; st < kStages; ++st) {
         const int n = (uses + kStages - 1 - st) / kStages;
@@ -237,9 +252,18 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& la, const LatentMa
 
 // ------------------------------------------------------------ passing on ----
 // What landed in this CTA is told to the first one, whose MMA warp waits for both.
+// By a warp of each CTA, of an item's queries.
+__device__ __forceinline__ bool pass_q(const AttnArgs& a, Shared& sh, uint32_t& parity) {
+    const bool ok = warp_wait(&sh.q_full, parity, a.err, a.timeout_ns);
+    if (ok && (threadIdx.x & 31) == 0) arrive_first(&sh.q_ready);
+    parity ^= 1u;
+    return ok;
+}
+
 template <int C, bool FEW>
 __device__ __forceinline__ void pass_k(const LatentAttnArgs& la, Shared& sh) {
     const AttnArgs& a = la.a;
+    uint32_t qp = 0;
     Jobs jobs;
     Ring<Cfg<C, FEW>::kKStages> at;
     bool dead = false;
@@ -248,6 +272,8 @@ __device__ __forceinline__ void pass_k(const LatentAttnArgs& la, Shared& sh) {
             dead = !warp_wait(&sh.k_full[at.st], at.ph, a.err, a.timeout_ns);
             if (dead) break;
             if ((threadIdx.x & 31) == 0) arrive_first(&sh.k_ready[at.st]);
+            if (j == 0) dead = !pass_q(a, sh, qp);
+            if (dead) break;
         }
         jobs.done(sh);
     }
@@ -340,40 +366,54 @@ __device__ __forceinline__ void convert_row(const uint4 (&raw)[8], uint8_t* firs
 }
 
 // e4m3: four warps each for keys and values, a thread a key and 128 codes.  All codes
-// are read before any atom is written over them.
-template <int C, bool FEW, bool V>
-__device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, uint8_t* ring) {
+// are read before any atom is written over them.  Both run the same instructions, what
+// differs are numbers: with a copy of their own each, 184 us for 145 (16 verify blocks
+// over 4,099 to 16,411 rows), the softmax's, these and the products' no longer fitting the
+// instruction caches.
+template <int C, bool FEW>
+__device__ __forceinline__ void convert(const LatentAttnArgs& la, Shared& sh, uint8_t* ring, const bool values) {
     using F = Cfg<C, FEW>;
-    constexpr int kN = V ? kKT : kKeys, kGroup = V ? F::kVGroup : F::kKGroup, kUnits = V ? F::kVPanels / 2 : F::kParts;
-    static_assert(kN * kUnits <= 128, "a row's part a thread");
+    const int n = values ? kKT : kKeys, group = values ? F::kVGroup : F::kKGroup, units = values ? F::kVPanels / 2 : F::kParts;
+    const int bytes = values ? F::kVBytes : F::kKBytes, stages = values ? 2 : F::kKStages, id = values ? kBarV : kBarK;
+    static_assert(kKT * (F::kVPanels / 2) <= 128 && kKeys * F::kParts <= 128, "a row's part a thread");
+    uint64_t* full = values ? sh.v_full : sh.k_full;
+    uint64_t* ready = values ? sh.v_ready : sh.k_ready;
     const AttnArgs& a = la.a;
-    const int lane = threadIdx.x & 31, t = threadIdx.x & 127, r = t % kN, part = t / kN;
+    const int lane = threadIdx.x & 31, t = threadIdx.x & 127, r = t & (n - 1), part = t / n;
+    const uint32_t from = n / 8 * (group / 2) + (r >> 3) * (group / 2) + part * kAtom + (r & 7) * 128;
+    const uint32_t to = (r >> 3) * group + 2 * part * kAtom + (r & 7) * 128;
     // 2^120 times the cache's power of two (see e4m3x4_to_bf16), and 480 times it
     const uint32_t f = static_cast<uint32_t>(127 + 120 + la.c.scale_log2) << 7, factor = f | (f << 16);
     const uint32_t nan_bits = 0x43F0u + static_cast<uint32_t>(la.c.scale_log2 * 128);
     Jobs jobs;
-    Ring<V ? 2 : F::kKStages> at;
-    bool dead = false;
-    while (const Job* job = next_of_group(jobs, sh, a, V ? kBarV : kBarK, dead)) {
-        for (int j = 0; j < job->tiles; ++j, at.step()) {
-            uint8_t* stage = ring + at.st * (V ? F::kVBytes : F::kKBytes);
-            const bool ok = mbar_wait(V ? &sh.v_full[at.st] : &sh.k_full[at.st], at.ph, a.err, a.timeout_ns);
+    int st = 0;
+    uint32_t ph = 0, qp = 0;
+    bool dead = false, q_ok = true;                              // (q: the first warp's)
+    while (const Job* job = next_of_group(jobs, sh, a, id, dead || !q_ok)) {
+#pragma unroll 1
+        for (int j = 0; j < job->tiles; ++j) {
+            uint8_t* stage = ring + st * bytes;
+            const bool ok = mbar_wait(&full[st], ph, a.err, a.timeout_ns);
             uint4 raw[8];
-            if (part < kUnits) {
-                const uint8_t* from = stage + kN / 8 * (kGroup / 2) + (r >> 3) * (kGroup / 2) + part * kAtom + (r & 7) * 128;
+            if (part < units) {
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch) raw[ch] = *reinterpret_cast<const uint4*>(from + ((ch ^ (r & 7)) << 4));
+                for (int ch = 0; ch < 8; ++ch) raw[ch] = *reinterpret_cast<const uint4*>(stage + from + ((ch ^ (r & 7)) << 4));
             }
-            dead = !bar_and(V ? kBarV : kBarK, ok, 128);
+            dead = !bar_and(id, ok && q_ok, 128);
             if (dead) break;
-            if (part < kUnits) {
+            if (part < units) {
                 const int j0 = job->key0(j), key = j0 + r;
-                convert_row(raw, stage + (r >> 3) * kGroup + 2 * part * kAtom + (r & 7) * 128, r, factor, nan_bits,
-                            V && (key < job->it.lo || key >= job->it.hi), V && (j0 < job->wlo || j0 + kKT > job->whi));
+                convert_row(raw, stage + to, r, factor, nan_bits, values && (key < job->it.lo || key >= job->it.hi),
+                            values && (j0 < job->wlo || j0 + kKT > job->whi));
             }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_first(V ? &sh.v_ready[at.st] : &sh.k_ready[at.st]);
+            if (lane == 0) arrive_first(&ready[st]);
+            if (!values && j == 0 && t < 32) q_ok = pass_q(a, sh, qp);
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1u;
+            }
         }
         jobs.done(sh);
     }
@@ -421,6 +461,7 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
                                      x < C / 64 ? kk + ((x * kAtom + k * 32) >> 4) : rr + (k * 32 >> 4), kIdQK, x > 0 || k > 0);
                     pair_commit(&sh.s_full[sa.st]);
                     pair_commit(&sh.k_empty[ka.st]);
+                    if (i == T - 1) pair_commit(&sh.q_empty);
                 }
                 __syncwarp();
                 ka.step();
@@ -459,7 +500,7 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
 // copies whole rows, all of its 16 on their way at once; rows past the last are zeros.
 // (By registers, nine pieces a thread at a time, an item's start took 18,000 clocks.)
 template <int C, bool FEW>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int row0, int count, bool negate, uint8_t* qs) {
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int row0, int count, uint8_t* qs) {
     constexpr int kChunks = (C + kLatentRot) / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto place = [&](int r, int ch) { return qs + (ch >> 3) * Cfg<C, FEW>::kQPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
@@ -474,15 +515,6 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
                          : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (negate) {
-#pragma unroll 1
-        for (int r = warp; r < Cfg<C, FEW>::kHeld; r += 4)
-            for (int ch = lane; ch < kChunks; ch += 32) {
-                uint4* p = reinterpret_cast<uint4*>(place(r, ch));
-                const uint4 w = *p;
-                *p = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
-            }
-    }
     fence_async_smem();
 }
 
@@ -503,7 +535,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
         tc_fence_after();
     };
     auto wait_pv = [&](uint32_t tile) { wait(&sh.pv_done[tile & 1u], (tile >> 1) & 1u); };
-    // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf), or NaN; the sign goes to the queries
+    // log2 units a product: at least 1.2e-38 (an unseen key's -inf times it stays -inf), or NaN; the sign goes to the scores
     const float cs = a.scale * kLog2e;
     const float c = fmaxf(fabsf(cs), 1.2e-38f);
     while (const Job* job = next_of_group(jobs, sh, a, kBarSoft, __any_sync(0xFFFFFFFFu, dead))) {
@@ -514,10 +546,10 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
         const int r = it.rt * F::kItem + row0 + (valid ? lr : 0), qi = a.query_of(r), hd = r - qi * a.group;
         RowView view{0, 0, 0ull};
         if (valid) view = row_view(a, it.s, qi);
-        if (T > 0) {
-            load_queries<C, FEW>(a, it, it.rt * F::kItem + row0, count, cs < 0.0f, qs);
+        if (T > 0 && !la.q_flat) {
+            load_queries<C, FEW>(a, it, it.rt * F::kItem + row0, count, qs);
             __syncwarp();
-            if (lane == 0) arrive_first(&sh.q_ready);
+            if (lane == 0) mbar_arrive(&sh.q_full);
         }
         float ref = kNegInf, sum0 = 0.0f, sum1 = 0.0f;
         for (int j = 0; j < T; ++j, ++g) {
@@ -527,6 +559,10 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
                 float x[32];
                 tmem_ld32(tm + 32 * (g & 1u), x);
                 tmem_wait_ld();
+                if (cs < 0.0f) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = -x[e];
+                }
                 if (j0 < job->wlo || j0 + kKT > job->whi) {
                     const uint32_t bits = row_bits(view, draft, it.s.first, j0 + half * kKeys);
 #pragma unroll
@@ -674,7 +710,9 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
             mbar_init(&sh.p_ready[i], 8);
             mbar_init(&sh.pv_done[i], 1);
         }
-        mbar_init(&sh.q_ready, 8);
+        mbar_init(&sh.q_full, la.q_flat ? 1 : 4);                // the copy, or the softmax warps
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.q_ready, 2);
         mbar_init(&sh.done, 1);
         fence_barrier_init();
         prefetch_tensormap(&maps.keys);
@@ -689,21 +727,20 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     pdl_launch_dependents();
     plan_work<F::kItem, kKT>(a, 1, sh.scan, &sh.plan, pair, gridDim.x >> 1, rank == 0);   // (its barriers publish sh.tmem)
     tc_fence_after();
-    zero_pad_rows(a, sh.plan.seqs);
     if (warp < 4)
         soften<C, FEW>(la, sh, qs, ps, pair, rank);
     else if (warp == 4)
-        produce<C, FEW, E4M3, false>(la, maps, sh, ks, rank);
+        produce<C, FEW, E4M3, false>(la, maps, sh, qs, ks, rank);
     else if (warp == 5) {
-        if (rank == 0) multiply<C, FEW>(la, sh, qs, ps, ks, vs);
+        if (rank == 0)
+            multiply<C, FEW>(la, sh, qs, ps, ks, vs);
+        else                                                     // (it has nothing else to do)
+            zero_pad_rows(a, sh.plan.seqs, pair, gridDim.x >> 1, threadIdx.x & 31, 32);
     } else if (warp == 6)
-        produce<C, FEW, E4M3, true>(la, maps, sh, vs, rank);
+        produce<C, FEW, E4M3, true>(la, maps, sh, qs, vs, rank);
     else if (warp >= 8) {
         if constexpr (E4M3) {
-            if (warp < 12)
-                convert<C, FEW, true>(la, sh, vs);
-            else
-                convert<C, FEW, false>(la, sh, ks);
+            convert<C, FEW>(la, sh, warp < 12 ? vs : ks, warp < 12);
         } else {
             pass_v<C, FEW>(la, sh, vs);
         }

@@ -298,3 +298,37 @@ def test_nothing_is_written_without_tokens(fn):
     assert m.moe_get_device_error(ws) == 0
     for a, b in zip((p.latent, p.rope), before):
         assert torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news,heads", [([1, 1, 1], 64), ([9, 40, 2], 12)])
+@pytest.mark.parametrize("scale", [0.07, -0.07])
+def test_queries_with_and_without_gaps(news, heads, dtype, scale):
+    """Rows one behind another, and the same with room between the tokens: the same bits; pad rows beside them hold NaN."""
+    p = ref.Problem([700, 90, 64], news, heads, 512, 32, dtype, pads=(2, 3), seed=18)
+    p.scale = scale
+    p.q[:2] = float("nan")
+    p.q[-3:] = float("nan")
+    out, lse = attend(p)
+    ref.check(out, lse, *ref.latent_attention(p))
+    wide = torch.full((p.t, heads * (p.c + ROT) + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q = wide[:, :heads * (p.c + ROT)].view(p.t, heads, p.c + ROT)
+    q.copy_(p.q)
+    o2, l2 = attend(p, q=q)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_sequences_without_keys(dtype):
+    p = ref.Problem([0, 5, 0], [1, 7, 3], 24, 256, 16, dtype, seed=19)
+    out, lse = attend(p)
+    ref.check(out, lse, *ref.latent_attention(p))
+
+
+def test_expanded_length_past_the_rows():
+    """A length past the rows there are is cut to them, and recorded."""
+    p = Expanded([80], [30], 2, 64, seed=20)
+    want = p.want()
+    p.seqs = m.Seqs.from_tensors(i32(p.cu), i32([100]), torch.zeros(1, 0, dtype=torch.int32, device="cuda"), 30)
+    out, lse = p.run(error=1)
+    ref.check(out, lse, *want)
