@@ -496,8 +496,9 @@ __device__ __forceinline__ void multiply(const LatentAttnArgs& la, Shared& sh, u
 }
 
 // ---------------------------------------------------------------- softmax ----
-// The CTA's rows of Q into shared memory, K-major with the 128-byte swizzle: a warp
-// copies whole rows, all of its 16 on their way at once; rows past the last are zeros.
+// The CTA's rows of Q into shared memory where tokens have gaps between them (else one
+// tensor copy does it, see produce), K-major with the 128-byte swizzle: a warp copies
+// whole rows, all of its 16 on their way at once; rows past the last are zeros.
 // (By registers, nine pieces a thread at a time, an item's start took 18,000 clocks.)
 template <int C, bool FEW>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int row0, int count, uint8_t* qs) {
