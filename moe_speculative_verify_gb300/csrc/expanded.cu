@@ -618,7 +618,12 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
     __syncthreads();
     cluster_sync();                                              // nothing of the pair is in flight
     tc_fence_after();
-    if (warp == 8) pair_dealloc(sh.tmem);
+    if (warp == 8) {
+        // the last commits' arrivals, which the first CTA's MMA warps have seen in its own shared memory, in this CTA's too
+        for (int s = 0; s < 2; ++s) mbar_wait(&sh.done[s], 0, a.err, kDrainNs);
+        __syncwarp();
+        pair_dealloc(sh.tmem);
+    }
 }
 
 template <int D>

@@ -753,7 +753,12 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     __syncthreads();
     cluster_sync();                                              // nothing of the pair is in flight
     tc_fence_after();
-    if (warp == 6) pair_dealloc(sh.tmem);
+    if (warp == 6) {
+        // the last commit's arrival, which the first CTA's MMA warp has seen in its own shared memory, in this CTA's too
+        mbar_wait(&sh.done, 0, a.err, kDrainNs);
+        __syncwarp();
+        pair_dealloc(sh.tmem);
+    }
 }
 
 template <int C, bool FEW, bool E4M3>
