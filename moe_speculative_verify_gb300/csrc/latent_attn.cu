@@ -100,6 +100,7 @@ struct Job {
 struct Shared {
     float top[2][2][kRows];                 // a row's maximum by half of a tile's keys, two tiles in turn
     float sum[2][kRows];
+    uint8_t odd[2][kRows];                  // a key that the row sees scored -inf in a tile that some row sees in part
     int64_t scan[16];                       // plan_work's
     // of this CTA: what landed, and the room that the products gave back
     uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2], q_full, q_empty;
@@ -289,8 +290,10 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& w) {
 
 // Four warps.  Values of keys that no row of the item sees may be anything: they are
 // zeroed, as are, in tiles where some row does not see some key, those of a key with an
-// element that is not finite (its score is not finite for the rows that do see it,
-// which so become NaN all the same; a probability of 0 would make the others NaN).
+// element that is not finite (a probability of 0 would make the rows that do not see it
+// NaN).  The rows that do see it have a score of it that is not finite either: NaN or
+// +inf make all of the row NaN; after -inf, which is a weight of 0, soften puts the NaN of 0
+// times an infinite value back.
 template <int C, bool FEW>
 __device__ __forceinline__ void pass_v(const LatentAttnArgs& la, Shared& sh, uint8_t* vs) {
     using F = Cfg<C, FEW>;
@@ -519,7 +522,44 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
     fence_async_smem();
 }
 
-template <int C, bool FEW>
+// Which of 32 elements are infinite or NaN, a bit each.
+__device__ __forceinline__ uint32_t nonfinite32(const uint16_t* p) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p + 8 * i);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((x[k] & 0x7F80u) == 0x7F80u) bits |= 1u << (8 * i + 2 * k);
+            if ((x[k] & 0x7F800000u) == 0x7F800000u) bits |= 2u << (8 * i + 2 * k);
+        }
+    }
+    return bits;
+}
+
+// Of the elements d0 .. d0 + 31, those that are not finite in some key that a row sees in
+// the tiles where pass_v zeroed such keys.
+__device__ __noinline__ uint32_t lost_elements(const LatentAttnArgs& la, const Job& job, int lo, int hi, uint64_t draft, int d0) {
+    const AttnArgs& a = la.a;
+    const RowView view{lo, hi, draft};
+    const int32_t* table = a.sq.table + int64_t(job.it.b) * a.sq.max_pages;
+    uint32_t bits = 0;
+    for (int t = 0; t < job.tiles; ++t) {
+        const int j0 = job.key0(t);
+        if (j0 >= job.wlo && j0 + kKT <= job.whi) continue;
+        for (int j = max(j0, view.lo); j < min(j0 + kKT, view.hi); ++j) {
+            if (!row_sees(view, a.draft != nullptr, job.it.s.first, j)) continue;
+            const int page = table[j >> la.c.page_log2];
+            if (page < 0 || page >= la.c.n_pages) continue;
+            bits |= nonfinite32(reinterpret_cast<const uint16_t*>(la.c.latent) + page * la.c.lat_page +
+                                (j & (la.c.page - 1)) * la.c.lat_token + d0);
+        }
+    }
+    return bits;
+}
+
+template <int C, bool FEW, bool E4M3>
 __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uint8_t* qs, uint8_t* ps, int pair, uint32_t rank) {
     using F = Cfg<C, FEW>;
     const AttnArgs& a = la.a;
@@ -553,6 +593,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
             if (lane == 0) mbar_arrive(&sh.q_full);
         }
         float ref = kNegInf, sum0 = 0.0f, sum1 = 0.0f;
+        bool odd = false;                                        // (codes have no infinity)
         for (int j = 0; j < T; ++j, ++g) {
             const int j0 = job->key0(j);
             wait(&sh.s_full[g & 1u], (g >> 1) & 1u);
@@ -567,8 +608,10 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
                 if (j0 < job->wlo || j0 + kKT > job->whi) {
                     const uint32_t bits = row_bits(view, draft, it.s.first, j0 + half * kKeys);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 32; ++e) {
+                        if (!E4M3) odd = odd || (((bits >> e) & 1u) && x[e] == kNegInf);
                         if (!((bits >> e) & 1u)) x[e] = kNegInf;
+                    }
                 }
                 float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
@@ -635,8 +678,10 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
         }
         // --- the item's rows: normalised, or this pair's piece of them
         sh.sum[half][lr] = sum0 + sum1;
+        if (!E4M3) sh.odd[half][lr] = odd;
         named_bar(kBarSoft, 128);
         const float sum = sh.sum[0][lr] + sh.sum[1][lr];
+        if (!E4M3) odd = valid && (sh.odd[0][lr] | sh.odd[1][lr]) != 0;
         if (sum != sum) ref = fmaxf(ref, 0.0f);                  // a NaN is a result, not an empty row
         const bool piece = it.t0 > 0 || it.t1 < it.n;
         float* slot = a.partials + (int64_t(it.t0 == 0 ? 0 : kMaxPairs) + pair) * (kLatentRows * (C + 2));
@@ -658,6 +703,12 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = weight != 0.0f ? o[e] * weight : 0.0f;
                 const int d0 = half * (C / 2) + 32 * q;
+                if (!E4M3 && odd && weight != 0.0f) {
+                    const uint32_t lost = lost_elements(la, *job, view.lo, view.hi, view.draft, d0);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if ((lost >> e) & 1u) o[e] = __uint_as_float(0x7FFFFFFFu);
+                }
                 if (valid) {
                     if (piece) {
 #pragma unroll
@@ -729,7 +780,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const La
     plan_work<F::kItem, kKT>(a, 1, sh.scan, &sh.plan, pair, gridDim.x >> 1, rank == 0);   // (its barriers publish sh.tmem)
     tc_fence_after();
     if (warp < 4)
-        soften<C, FEW>(la, sh, qs, ps, pair, rank);
+        soften<C, FEW, E4M3>(la, sh, qs, ps, pair, rank);
     else if (warp == 4)
         produce<C, FEW, E4M3, false>(la, maps, sh, qs, ks, rank);
     else if (warp == 5) {

@@ -37,3 +37,59 @@ def test_kernels_that_follow_one_another(dtype):
     ref.check(outs[0], lse, *ref.latent_attention(p))
     ref.check(xouts[0], xl, *x.want())
     assert torch.equal(outs, outs[:1].expand_as(outs)) and torch.equal(xouts, xouts[:1].expand_as(xouts))
+
+
+def infinite_latent(p, value, place, part, causal=True, window=0, draft=None):
+    """Puts `value` into element 3 of a cached row of sequence 0 and calls: rows that do not see it are as without it; a row
+    that scores it +inf is NaN; where the score is -inf the row has no weight, but 0 times an infinite value is NaN in that one
+    element.  Returns what was called for, for a check of its own."""
+    n, first = p.news[0], p.lens[0] - p.news[0]
+    lat, rot = p.rows(0)
+    q, keys = p.q[p.cu[0]:p.cu[0] + n].double(), torch.cat([lat, rot], 1)
+    seen = ref.sees(p.lens[0], n, causal, window, None if draft is None else [int(x) for x in draft.cpu()[p.cu[0]:p.cu[0] + n]])
+    apart = seen.clone()
+    apart[:, place] = False
+    whole, less = ref.attend(q, keys, lat, seen, p.scale), ref.attend(q, keys, lat, apart, p.scale)
+    (p.latent if part == "latent" else p.rope)[int(p.table[0, place // p.page]), place % p.page, 3] = value
+    out, lse = (x[p.cu[0]:p.cu[0] + n] for x in attend(p, causal, window, draft))
+    sign = (p.q[p.cu[0]:p.cu[0] + n, :, 3 if part == "latent" else p.c + 3].double() * value * p.scale).sign()
+    sees_it = seen[:, place, None].expand(n, p.heads)
+    up, down = sees_it & (sign > 0), sees_it & (sign < 0)
+    assert bool((sees_it == (up | down)).all())
+    assert bool(torch.isnan(out[up]).all()) and not bool(torch.isfinite(lse[up]).any())
+    if bool((~sees_it).any()):
+        ref.check(out[~sees_it], lse[~sees_it], *(x[~sees_it] for x in whole))
+    if bool(down.any()):
+        got, want = out[down].clone(), [x[down] for x in less]
+        if part == "latent":
+            live = ~want[1].isneginf()                        # (a row with no other key: nothing has weight)
+            assert bool(torch.isnan(got[live][:, 3]).all())
+            got[live, 3] = want[0][live, 3].to(got.dtype)
+        ref.check(got, lse[down], *want)
+    return int(up.sum()), int(down.sum())
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("part", ["latent", "rope"])
+@pytest.mark.parametrize("heads,latent,news,page", [(8, 512, 8, 64), (16, 512, 8, 16), (5, 256, 40, 128)])   # items of 64 rows, of 128, several
+@pytest.mark.parametrize("place", ["old", "beside", "new", "last"])
+def test_infinite_latents_in_whole_and_cut_tiles(value, part, heads, latent, news, page, place):
+    """In a tile that all rows see, among the old keys of one that the causal mask cuts, and in new tokens' rows."""
+    p = ref.Problem([420 + news], [news], heads, latent, page, seed=43)
+    infinite_latent(p, value, {"old": 70, "beside": 418, "new": 420 + news // 2, "last": 419 + news}[place], part)
+
+
+@pytest.mark.parametrize("mask", ["window", "draft", "full", "negative", "long"])
+@pytest.mark.parametrize("heads", [8, 32])
+def test_infinite_latents_under_other_masks(mask, heads):
+    news = 8
+    p = ref.Problem([20000 if mask == "long" else 200], [news], heads, 512, 32, seed=44)
+    draft = None
+    if mask == "draft":
+        draft = torch.tensor([0b1, 0b11, 0b101, 0b1001, 0b10011, 0b100101, 0b1000001, 0b10000011], device="cuda")
+    if mask == "negative":
+        p.scale = -p.scale
+    n = p.lens[0]
+    up, down = infinite_latent(p, float("-inf"), {"window": n - 45, "draft": n - 7, "long": n - 10}.get(mask, n - 3), "latent", mask != "full",
+                               40 if mask == "window" else 0, draft)
+    assert up > 0 and down > 0
