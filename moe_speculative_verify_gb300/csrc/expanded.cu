@@ -394,7 +394,7 @@ __device__ __forceinline__ void follow(uint32_t colO, float top, bool started, R
             tmem_wait_ld();
             uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);   // (what is not finite stays so)
             tmem_st16(colO + 16 * q, u);
         }
     }
@@ -493,7 +493,8 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
         const bool piece = it.t0 > 0 || it.t1 < it.n;
         float* slot = a.partials + (int64_t(it.t0 == 0 ? 0 : kMaxPairs) + pair) * (kMT * (D + 2));
         const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + it.h;
-        const float weight = ref == kNegInf || n == 0 ? 0.0f : (piece ? 1.0f : 1.0f / sum);
+        // a piece whose keys all have weight 0 still says where 0 times infinity is
+        const float weight = n == 0 ? 0.0f : (piece ? 1.0f : (ref == kNegInf ? 0.0f : 1.0f / sum));
         if (valid) {
             if (piece)
                 *reinterpret_cast<float2*>(slot + kMT * D + 2 * (row0 + lr)) = make_float2(ref, sum);
@@ -514,7 +515,7 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
             for (int q = 0; q < D / 32; ++q) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[q][e] = weight != 0.0f ? o[q][e] * weight : 0.0f;
-                if (bad && valid) {
+                if (bad && valid && weight != 0.0f) {
                     // values that are not finite, of the masked tiles' keys that this row sees
                     const int64_t k0 = xa.cu_k[it.b];
                     for (int j = max(view.lo, job->key0(0)); j < min(view.hi, job->key0(job->tiles)); ++j) {

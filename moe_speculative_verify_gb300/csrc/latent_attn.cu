@@ -656,7 +656,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
                             tmem_wait_ld();
                             uint32_t w[16];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(f == 0.0f ? 0.0f : o[e] * f);
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);   // (what is not finite stays so)
                             tmem_st16(colO + 16 * q, w);
                         }
                         tmem_wait_st();
@@ -686,7 +686,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
         const bool piece = it.t0 > 0 || it.t1 < it.n;
         float* slot = a.partials + (int64_t(it.t0 == 0 ? 0 : kMaxPairs) + pair) * (kLatentRows * (C + 2));
         const int64_t at = int64_t(it.s.q0 + qi) * a.q_heads + hd;
-        const float weight = ref == kNegInf || T == 0 ? 0.0f : (piece ? 1.0f : 1.0f / sum);
+        // a piece whose keys all have weight 0 still says where 0 times infinity is
+        const float weight = T == 0 ? 0.0f : (piece ? 1.0f : (ref == kNegInf ? 0.0f : 1.0f / sum));
         if (valid && half == 0) {
             if (piece)
                 *reinterpret_cast<float2*>(slot + kLatentRows * C + 2 * (row0 + lr)) = make_float2(ref, sum);

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) pair_join_kernel(const AttnAr
         }
         const int r = n.row0 + row, q = a.query_of(r), hd = n.head * a.group + r - q * a.group;
         const int64_t at = int64_t(n.q0 + q) * a.q_heads + hd;
+        if (top == kNegInf) s = make_float4(0, 0, 0, 0);             // no key has weight, whatever its values
         const float inv = top == kNegInf ? 0.0f : 1.0f / sum;
         *reinterpret_cast<uint2*>(a.out + at * C + 4 * d4) = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
         if (d4 == 0 && a.lse) a.lse[at] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;

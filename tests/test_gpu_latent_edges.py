@@ -93,3 +93,47 @@ def test_infinite_latents_under_other_masks(mask, heads):
     up, down = infinite_latent(p, float("-inf"), {"window": n - 45, "draft": n - 7, "long": n - 10}.get(mask, n - 3), "latent", mask != "full",
                                40 if mask == "window" else 0, draft)
     assert up > 0 and down > 0
+
+
+@pytest.mark.parametrize("lens", [[400] * 100, [20000]])       # several tiles a pair of SMs; one sequence over all of them
+@pytest.mark.parametrize("bad", [1, 64, 300])
+@pytest.mark.parametrize("heads", [8, 96])
+def test_infinite_latents_before_a_heavy_key(lens, bad, heads):
+    """Rows of weight 0 whose element 3 is infinite, alone in their tiles or not, and then a key beside which all before it has
+    no weight in fp32: 0 times an infinite value is NaN, wherever the row lies."""
+    p = ref.Problem(lens, [1] * len(lens), heads, 512, 64, seed=45)
+    p.q[:] = p.q[:1, :1]
+    p.q[..., 3] = 1.0
+    flat = lambda j: (p.d_table[:, j // 64].long(), j % 64)
+    heavy = lens[0] - 80
+    p.latent[flat(heavy)] = (p.q[0, 0, :512].float() * (300.0 / p.scale / float(p.q[0, 0, :512].float().square().sum()))).bfloat16()
+    want = None
+    for b in range(len(lens)):
+        lat, rot = p.rows(b)
+        seen = ref.sees(lens[b], 1, True, 0, None)
+        seen[:, :bad] = False
+        w = ref.attend(p.q[b:b + 1].double(), torch.cat([lat, rot], 1), lat, seen, p.scale)
+        want = w if want is None else [torch.cat(x) for x in zip(want, w)]
+    for j in range(bad):
+        pg, sl = flat(j)
+        p.latent[pg, sl, 3] = float("-inf")
+    out, lse = attend(p)
+    assert bool(torch.isnan(out[..., 3]).all())
+    out[..., 3] = want[0][..., 3].to(out.dtype)
+    ref.check(out, lse, *want)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("heads,seqs", [(16, 8), (1, 1)])
+def test_expanded_infinite_values_before_a_heavy_key(heads, seqs, value):
+    """The same of the expanded form, whose values are apart from its keys: not finite, wherever the key lies."""
+    p = Expanded([900] * seqs, [200] * seqs, heads, 128, seed=46)
+    p.q[:] = p.q[:1, :1]
+    at = i32(p.ck[:-1]).long()
+    p.k[at + 650] = p.q[0, 0, :128] * (300.0 / p.scale / float(p.q[0, 0, :128].float().square().sum()))
+    want = p.want()
+    p.v[at + 5, :, 3] = value
+    out, lse = p.run()
+    assert not bool(torch.isfinite(out[..., 3]).any())
+    out[..., 3] = want[0][..., 3].to(out.dtype)
+    ref.check(out, lse, *want)
