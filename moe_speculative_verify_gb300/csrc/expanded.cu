@@ -96,7 +96,10 @@ struct Shared {
     Job job[kAhead];
     uint64_t job_full[kAhead], job_empty[kAhead];
     uint32_t tmem;
-    int bad;                                // some masked tile had values that are not finite
+    // by place in the queue: 1 + the last item that had values put right which are not finite.  Its
+    // number only grows, so that nothing has to clear it: an item that finds that of a later
+    // one in its place looks its own values over for nothing.
+    int bad[kAhead];
 };
 
 struct Slot {
@@ -217,7 +220,7 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 // all of them wlo .. whi - 1: where some row does not see some key, elements that are not
 // finite become zeros (a probability of 0 would make them NaN for that row).  The rows
 // that do see such a key get them when the item ends.
-__device__ __forceinline__ void mend_values(Shared& sh, uint8_t* tile, int j0, int see0, int see1, int wlo, int whi) {
+__device__ __forceinline__ void mend_values(Shared& sh, int item, uint8_t* tile, int j0, int see0, int see1, int wlo, int whi) {
     if (j0 >= max(see0, wlo) && j0 + kKT <= min(see1, whi)) return;
     // 16 bytes of eight keys at a time: in all but few tiles all is finite and nothing to be put right
     const int lane = threadIdx.x & 31;
@@ -245,8 +248,8 @@ __device__ __forceinline__ void mend_values(Shared& sh, uint8_t* tile, int j0, i
     if (any) {                                                   // in both CTAs: each has all columns of its rows
         for (uint32_t r = 0; r < 2; ++r)
             asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.u32 [p], %2;\n\t}" ::"r"(
-                             smem_u32(&sh.bad)),
-                         "r"(r), "r"(1)
+                             smem_u32(&sh.bad[item % kAhead])),
+                         "r"(r), "r"(item + 1)
                          : "memory");
         asm volatile("fence.acq_rel.cluster;" ::: "memory");
     }
@@ -271,7 +274,7 @@ __device__ __forceinline__ void pass_on(const ExpandedArgs& x, Shared& sh, uint8
             if (lane == 0) arrive_first(&sh.k_ready[at.st]);
             dead = !warp_wait(&sh.v_full[at.st], at.ph, a.err, a.timeout_ns);
             if (dead) break;
-            mend_values(sh, vs + at.st * F::kVBytes, job->key0(j), job->it.lo, job->it.hi, job->lo_all, job->hi_all);
+            mend_values(sh, jobs.n, vs + at.st * F::kVBytes, job->key0(j), job->it.lo, job->it.hi, job->lo_all, job->hi_all);
             if (lane == 0) arrive_first(&sh.v_ready[at.st]);
             for (int s = 0; s < 2 && j == 0; ++s) {
                 if (job->last(s) <= job->first(s)) continue;
@@ -425,6 +428,65 @@ __device__ __forceinline__ void hand_over(uint64_t* bar) {
     if ((threadIdx.x & 31) == 0) arrive_first(bar);
 }
 
+// Adds to a thread's row, as it was written, the values that are not finite, of the keys
+// lo .. hi - 1 in the tiles where mend_values takes such out: a piece's sums, or the output.  By
+// all of a warp, 32 keys at a time: a lane reads a key, and says of each element which
+// infinity it is (a NaN is both); a row takes what the keys say that it sees.  (One such
+// value in a call of 0.18 ms makes it 0.25, all of them 1.1.  Each thread its own keys, element by
+// element, took 1.2 ms an item of 512 rows.  On the sums in registers, before
+// they are written, the code beside the main loop cost 4 ragged chunks of 64 heads 25 of
+// 531 us.)
+template <int D>
+__device__ __noinline__ void add_nonfinite(const ExpandedArgs& x, const Job& job, int lo, int hi, float* sums, uint16_t* out) {
+    const int lane = threadIdx.x & 31;
+    const int64_t k0 = x.cu_k[job.it.b];
+    uint32_t up[D / 32] = {}, down[D / 32] = {};                 // the row's infinities, a bit an element
+#pragma unroll 1
+    for (int j0 = job.key0(0); j0 < job.key0(job.tiles); j0 += 32) {
+        const int tile = j0 - j0 % kKT, j = j0 + lane;
+        if (tile >= max(job.it.lo, job.lo_all) && tile + kKT <= min(job.it.hi, job.hi_all)) continue;
+        const bool there = j >= job.it.lo && j < job.it.hi && k0 + j >= 0 && k0 + j < x.n_keys;
+        const uint4* v = reinterpret_cast<const uint4*>(x.v + (there ? (k0 + j) * x.v_token : 0) + job.it.h * x.v_head);
+        const int l = min(max(lo - j0, 0), 32), h = min(max(hi - j0, 0), 32);
+        const uint32_t seen = l >= h ? 0u : (0xFFFFFFFFu << l) & (0xFFFFFFFFu >> (32 - h));
+        uint4 w[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = there ? v[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint32_t odd = carry2(w[i].x) | carry2(w[i].y) | carry2(w[i].z) | carry2(w[i].w);
+            if (!__any_sync(0xFFFFFFFFu, (odd & 0x80008000u) != 0)) continue;
+            const uint32_t p[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t n = (p[e / 2] >> (16 * (e & 1))) & 0xFFFFu, bit = 1u << ((8 * i + e) & 31);
+                const bool bad = (n & 0x7F80u) == 0x7F80u, nan = (n & 0x7Fu) != 0;
+                if (__ballot_sync(0xFFFFFFFFu, bad && (nan || n < 0x8000u)) & seen) up[i / 4] |= bit;
+                if (__ballot_sync(0xFFFFFFFFu, bad && (nan || n >= 0x8000u)) & seen) down[i / 4] |= bit;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < D; d += 4) {
+        const uint32_t u = up[d / 32] >> (d & 31), n = down[d / 32] >> (d & 31);
+        if (((u | n) & 15u) == 0) continue;
+        float add[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add[e] = ((u >> e) & 1u ? INFINITY : 0.0f) + ((n >> e) & 1u ? -INFINITY : 0.0f);
+        if (sums) {
+            float4* at = reinterpret_cast<float4*>(sums + d * kMT);
+            const float4 o = *at;
+            *at = make_float4(o.x + add[0], o.y + add[1], o.z + add[2], o.w + add[3]);
+        } else {
+            uint2* at = reinterpret_cast<uint2*>(out + d);
+            const uint2 o = *at;
+            *at = make_uint2(pack_bf16(bf16_bits_to_f32(o.x & 0xFFFFu) + add[0], __uint_as_float(o.x & 0xFFFF0000u) + add[1]),
+                             pack_bf16(bf16_bits_to_f32(o.y & 0xFFFFu) + add[2], __uint_as_float(o.y & 0xFFFF0000u) + add[3]));
+        }
+    }
+    __syncwarp();
+}
+
 template <int D>
 __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int pair, int rank) {
     const AttnArgs& a = xa.a;
@@ -505,7 +567,7 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
             wait(&sh.o_full[s], op);
             op ^= 1u;
         }
-        const bool bad = *const_cast<volatile int*>(&sh.bad) != 0;
+        const bool bad = __any_sync(0xFFFFFFFFu, *const_cast<volatile int*>(&sh.bad[jobs.n % kAhead]) > jobs.n);
         if (warp_on) {
             float o[D / 32][32];
 #pragma unroll
@@ -515,21 +577,6 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
             for (int q = 0; q < D / 32; ++q) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[q][e] = weight != 0.0f ? o[q][e] * weight : 0.0f;
-                if (bad && valid && weight != 0.0f) {
-                    // values that are not finite, of the masked tiles' keys that this row sees
-                    const int64_t k0 = xa.cu_k[it.b];
-                    for (int j = max(view.lo, job->key0(0)); j < min(view.hi, job->key0(job->tiles)); ++j) {
-                        const int tile = j - j % kKT;
-                        if (tile >= job->lo_all && tile + kKT <= min(it.hi, job->hi_all)) continue;
-                        if (k0 + j < 0 || k0 + j >= xa.n_keys) continue;
-                        const uint16_t* v = xa.v + (k0 + j) * xa.v_token + it.h * xa.v_head + 32 * q;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const uint32_t b = v[e];
-                            if ((b & 0x7F80u) == 0x7F80u) o[q][e] += bf16_bits_to_f32(b);
-                        }
-                    }
-                }
                 if (valid) {
                     if (piece) {
 #pragma unroll
@@ -545,6 +592,9 @@ __device__ __forceinline__ void soften(const ExpandedArgs& xa, Shared& sh, int p
                     }
                 }
             }
+            if (bad)
+                add_nonfinite<D>(xa, *job, view.lo, valid && weight != 0.0f ? view.hi : 0, piece ? slot + (row0 + lr) * 4 : nullptr,
+                                 a.out + at * D);
         }
         tc_fence_before();
         if (tid == 0 && rank == 0) note_split(a, it, job->rows, kMT, sh.plan, pair);
@@ -586,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const ExpandedArg
             mbar_init(&sh.job_full[i], 1);
             mbar_init(&sh.job_empty[i], 8 + 1 + (rank == 0 ? 2 : 0));   // softmax warps, passing on, MMA
         }
-        sh.bad = 0;
+        for (int i = 0; i < kAhead; ++i) sh.bad[i] = 0;
         fence_barrier_init();
         prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.k);

@@ -137,3 +137,82 @@ def test_expanded_infinite_values_before_a_heavy_key(heads, seqs, value):
     assert not bool(torch.isfinite(out[..., 3]).any())
     out[..., 3] = want[0][..., 3].to(out.dtype)
     ref.check(out, lse, *want)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("which", ["v", "k", "rope"])
+@pytest.mark.parametrize("shape", [([300, 700], [150, 130], 2, 128), ([600], [600], 3, 64), ([2000], [9], 1, 128)])
+def test_expanded_bad_rows_reach_those_that_see_them(shape, which, value):
+    """A value that is not finite comes out in its element of every row that sees its key, an infinite score as NaN or as no
+    weight; all else is as it was.  In the tiles that the causal mask cuts, with items of one pair of SMs and of several."""
+    p = Expanded(*shape, seed=47)
+    b, h, new = len(p.lens) - 1, p.heads - 1, p.news[-1] // 2
+    key = p.lens[b] - p.news[b] + new                         # of token `new`
+    row, tok = p.ck[b] + key, p.cu[b] + new
+    want, sign = p.want(), torch.zeros(p.t, p.heads, device="cuda", dtype=torch.float64)
+    hit = torch.zeros(p.t, p.heads, dtype=torch.bool, device="cuda")
+    if which == "v":
+        p.v[row, h, 3] = value
+        hit[tok:p.cu[b + 1], h] = True
+    else:
+        d = 3 if which == "k" else p.dim + 3
+        sign[tok:p.cu[b + 1]] = (p.q[tok:p.cu[b + 1], :, d].double() * value).sign()
+        hit[tok:p.cu[b + 1], h if which == "k" else slice(None)] = True
+        (p.k[row, h] if which == "k" else p.rope[row])[3] = value
+    out, lse = p.run()
+    ref.check(out[~hit], lse[~hit], *(x[~hit] for x in want))
+    if which == "v":
+        got = out[hit].clone()
+        assert bool((torch.isnan(got[:, 3]) if value != value else got[:, 3] == value).all())
+        got[:, 3] = want[0][hit][:, 3].to(got.dtype)
+        ref.check(got, lse[hit], *(x[hit] for x in want))
+        return
+    up, down = hit & ~(sign < 0), hit & (sign < 0)
+    assert bool(torch.isnan(out[up]).all()) and not bool(torch.isfinite(lse[up]).any())
+    if bool(down.any()):
+        # without that key: as if its own part were so small that it had no weight
+        heads = [h] if which == "k" else range(p.heads)
+        kr = slice(p.ck[b], p.ck[b] + p.lens[b])
+        (p.k[row, h] if which == "k" else p.rope[row])[3] = 0.0
+        keys = torch.cat([p.k[kr].double(), p.rope[kr].double()[:, None].expand(-1, p.heads, -1)], 2)
+        seen = ref.sees(p.lens[b], p.news[b], True, 0, None)
+        seen[:, key] = False
+        r = slice(p.cu[b], p.cu[b + 1])
+        less = ref.attend(p.q[r].double(), keys, p.v[kr].double(), seen, p.scale)
+        ref.check(out[r][down[r]], lse[r][down[r]], *(x[down[r]] for x in less))
+
+
+def test_a_bad_value_costs_its_own_item_only():
+    """One value that is not finite, in one head of many items: the others do not pay for it.  The wait limit is some ten times
+    what the call takes without it."""
+    p = Expanded([1500] * 8, [1024] * 8, 32, 128, seed=48)
+    attn = m.Attn(p.heads, p.scale, wait_timeout_us=200000)
+    ws = torch.zeros(m.moe_expanded_workspace_bytes(attn, 128), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros(p.t, p.heads, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    t = []
+    for k in range(2):
+        if k:
+            p.v[p.ck[0] + 600, 0, 3] = float("inf")
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            m.moe_expanded_attention(attn, p.seqs, p.d_ck, p.q, p.k, p.rope, p.v, outs[k], ws)
+            b.record()
+            torch.cuda.synchronize()
+        t.append(a.elapsed_time(b))
+    print("ms clean, one bad value:", t)
+    assert m.moe_get_device_error(ws) == 0
+    hit = torch.zeros(p.t, p.heads, 128, dtype=torch.bool, device="cuda")
+    hit[1024 - 900:1024, 0, 3] = True                         # tokens at places from 600 on
+    assert torch.equal(outs[0][~hit], outs[1][~hit]) and bool(torch.isposinf(outs[1][hit]).all())
+    assert t[1] < 4 * t[0]
+
+
+def test_expanded_values_that_are_all_nan():
+    """Nothing finite in any value: every row that sees a key is NaN, with its log-sum-exp as ever."""
+    p = Expanded([700, 90], [600, 90], 8, 128, seed=49)
+    p.v.fill_(float("nan"))
+    _, want, _, err = p.want()
+    out, lse = p.run()
+    assert bool(torch.isnan(out).all())
+    assert bool(((lse.double() - want).abs() <= err + 2.0 ** -20 * (1 + want.abs())).all())
