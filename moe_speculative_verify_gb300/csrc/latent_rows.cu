@@ -3,8 +3,9 @@
 // queries' rotary parts, rows stored; and cached rows gathered as bf16.
 //
 // A latent x of C elements becomes x * rsqrt(sum x^2 / C + eps) * gamma, the sum
-// in fp32 in a fixed order; e4m3 rows hold the code of that times 2^-e, which is
-// exact, so the code is the only rounding.  Pairs turn as in rope.cu, with angles
+// in fp32 in a fixed order (of x times a power of two where squares would leave
+// fp32's range); e4m3 rows hold the code of that times 2^-e, which is exact, so
+// the code is the only rounding.  Pairs turn as in rope.cu, with angles
 // right to fp32 at any |position| < 2^24.
 //
 // Both are copies bound by HBM at chunk sizes and by latency at verify sizes:
@@ -107,16 +108,32 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
         sincospif(2.0f * __fadd_rn(p - rintf(p), e), &sn, &cs);
         s_cs[tid] = make_float2(cs * a.magnitude, sn * a.magnitude);
     }
-    float x[8], sum = 0.0f;
+    float x[8];
     unpack8(lat, x);
-    if (row && a.gamma) {
+    const bool norm = row && a.gamma;
+    auto add_squares = [&](float f) {
+        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+        for (int i = 0; i < 8; ++i) sum = fmaf(x[i] * f, x[i] * f, sum);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
-    }
+    };
+    auto mean = [&](float eps) { return __fadd_rn((s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) / a.c.dim, eps); };
+    if (norm) add_squares(1.0f);
     __syncthreads();
+    float p2 = 1.0f, r = 1.0f;                   // x r p2 is the normalised row
+    if (norm) {
+        float m = mean(a.eps);
+        if (m == INFINITY || m < 0x1p-100f) {    // (all of the block: squares past fp32's end, or below where it keeps their bits)
+            p2 = m == INFINITY ? 0x1p-70f : 0x1p70f;
+            __syncthreads();
+            add_squares(p2);
+            __syncthreads();
+            m = mean(a.eps * p2 * p2);
+        }
+        r = 1.0f / sqrtf(m);
+    }
     // (from the first sequence on whose offsets do not fit, none has new tokens)
     const int b = s_seq < s_bad ? s_seq : -1;
     if (row) {
@@ -136,13 +153,11 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
         at &= a.c.page - 1;
         if (pg >= 0 && mine) {
             if (a.gamma) {
-                const float ss = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-                const float r = 1.0f / sqrtf(__fadd_rn(ss / a.c.dim, a.eps));
                 const float4 g0 = reinterpret_cast<const float4*>(a.gamma)[2 * tid];
                 const float4 g1 = reinterpret_cast<const float4*>(a.gamma)[2 * tid + 1];
                 const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), g[i]);
+                for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(__fmul_rn(x[i], r), p2), g[i]);
             }
             const int64_t o = pg * a.c.lat_page + at * a.c.lat_token + 8 * tid;
             if (a.c.e4m3) {

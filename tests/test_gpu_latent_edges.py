@@ -1,11 +1,11 @@
-"""Attention through a latent cache where it can go wrong: kernels that follow one
-another at once, numbers that are not finite in cached rows, every number of pieces."""
+"""The operators over a latent cache where they can go wrong: kernels that follow one another at once, numbers that are
+not finite in cached rows, magnitudes near the ends of bf16, every number of pieces."""
 import pytest
 import torch
 
 import latent_ref as ref
 import moe_speculative_verify_gb300 as m
-from latent_ref import i32
+from latent_ref import ROT, i32
 from test_gpu_latent import Expanded, attend
 
 pytestmark = pytest.mark.gpu
@@ -216,3 +216,34 @@ def test_expanded_values_that_are_all_nan():
     out, lse = p.run()
     assert bool(torch.isnan(out).all())
     assert bool(((lse.double() - want).abs() <= err + 2.0 ** -20 * (1 + want.abs())).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("latent", [256, 512])
+@pytest.mark.parametrize("eps", [1e-6, 0.0, 1e30])
+@pytest.mark.parametrize("size", ["lone", 3e38, 1e25, 2e19, 1e-15, 1e-25, 1e-38, 1e-40])
+def test_append_normalises_rows_of_any_size(dtype, latent, eps, size):
+    """Rows whose squares pass the end of fp32, or lose their bits below it.  Tolerances as test_gpu_latent_rows.py's, and half the
+    least bf16 (2^-134) for each of the result's two roundings where it is that small: a product's fp32 and the bf16."""
+    p = ref.Problem([64], [3], 1, latent, 64, dtype, seed=50)
+    freqs, mag = m.moe_rope_freqs(ROT)
+    g = torch.Generator().manual_seed(latent)
+    kv = torch.randn(3, latent + ROT, generator=g)
+    if size == "lone":
+        kv[1, 7] = 3e38
+    else:
+        kv[1, :latent] = kv[1, :latent].clamp(-1, 1) * size
+    kv = kv.bfloat16().cuda()
+    q = torch.zeros(3, 1, ROT, dtype=torch.bfloat16, device="cuda")
+    gamma = (1 + 0.3 * torch.randn(latent, generator=g)).cuda()
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    m.moe_latent_append(m.Rope.from_freqs(freqs.cuda(), False, mag), p.cache, p.seqs, kv, q, pos, torch.empty_like(q), gamma=gamma, eps=eps)
+    x = kv[:, :latent].double()
+    eps = float(torch.tensor(eps))                              # as fp32 has it
+    want = x / torch.sqrt((x * x).mean(1, keepdim=True) + eps) * gamma.double()
+    got = p.latent[int(p.table[0, 0]), 61:64].float().double() * 2.0 ** p.exp
+    tol, floor = (2.0 ** -8, 2.0 ** -133) if dtype == "bf16" else (2.0 ** -4, 2.0 ** (p.exp - 10))
+    if dtype == "e4m3":
+        want = want.clamp(-448 * 2.0 ** p.exp, 448 * 2.0 ** p.exp)
+    bad = ~((got - want).abs() <= (tol + 2.0 ** -18) * want.abs() + floor)
+    assert not bool(bad.any()), (got[bad][:4], want[bad][:4])
