@@ -247,3 +247,25 @@ def test_append_normalises_rows_of_any_size(dtype, latent, eps, size):
         want = want.clamp(-448 * 2.0 ** p.exp, 448 * 2.0 ** p.exp)
     bad = ~((got - want).abs() <= (tol + 2.0 ** -18) * want.abs() + floor)
     assert not bool(bad.any()), (got[bad][:4], want[bad][:4])
+
+
+def tiles_of(count, tile, rest):
+    """Keys that make so many tiles, `pairs` of them or so where it is a text; with the last of one key alone or whole."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    n = eval(count, {"pairs": pairs}) if isinstance(count, str) else count
+    return tile * (n - 1) + (rest or tile)
+
+
+@pytest.mark.parametrize("rest", [0, 1])
+@pytest.mark.parametrize("tiles", [1, 2, 3, 4, 5, 6, 7, 8, 9, 13, 31, 33, "pairs-1", "pairs", "pairs+1", "2*pairs+1"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+def test_every_number_of_tiles(form, tiles, rest):
+    """One item cut into as many pieces as it has tiles of keys (64 and 128), one a pair of SMs, and past that in runs."""
+    if form == "absorbed":
+        p = ref.Problem([tiles_of(tiles, 64, rest)], [1], 5, 512, 128, seed=51)
+        out, lse = attend(p)
+        ref.check(out, lse, *ref.latent_attention(p))
+    else:
+        x = Expanded([tiles_of(tiles, 128, rest)], [1], 1, 128, seed=52)
+        out, lse = x.run()
+        ref.check(out, lse, *x.want())
