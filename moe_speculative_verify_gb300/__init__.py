@@ -122,7 +122,14 @@ class KVCache(C.Structure):
         return c
 
 
+def _device(*tensors):
+    """The device that all of them (None and empty ones aside) are on: -1 the host, -2 several."""
+    devs = {t.get_device() for t in tensors if t is not None and t.numel()}
+    return devs.pop() if len(devs) == 1 else None if not devs else -2
+
+
 class LatentCache(C.Structure):
+    _dev = None                  # the tensors' device; None: made of bare pointers
     _fields_ = [("latent", C.c_void_p), ("rope", C.c_void_p), ("latent_page_stride", C.c_int64),
                 ("latent_token_stride", C.c_int64), ("rope_page_stride", C.c_int64),
                 ("rope_token_stride", C.c_int64), ("dtype", C.c_int32), ("scale_log2", C.c_int32),
@@ -145,11 +152,12 @@ class LatentCache(C.Structure):
             return t.stride(i) if t.shape[i] > 1 else t.shape[2]
         c = cls(latent.data_ptr(), rope.data_ptr(), st(latent, 0), st(latent, 1), st(rope, 0),
                 st(rope, 1), KV_E4M3 if latent.dtype in codes else KV_BF16, scale_log2, n, p, d)
-        c._tensors = (latent, rope)
+        c._tensors, c._dev = (latent, rope), _device(latent, rope)
         return c
 
 
 class Seqs(C.Structure):
+    _dev = None
     _fields_ = [("cu_q", C.c_void_p), ("kv_len", C.c_void_p), ("block_table", C.c_void_p),
                 ("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("max_q", C.c_int32)]
 
@@ -167,11 +175,12 @@ class Seqs(C.Structure):
             raise MoeError(1, "Seqs")
         s = cls(_ptr(cu_q), kv_len.data_ptr(), block_table.data_ptr(), n, block_table.shape[1],
                 max_q)
-        s._tensors = (cu_q, kv_len, block_table)
+        s._tensors, s._dev = (cu_q, kv_len, block_table), _device(cu_q, kv_len, block_table)
         return s
 
 
 class Rope(C.Structure):
+    _dev = None
     _fields_ = [("freqs", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
                 ("magnitude", C.c_float), ("err", C.c_void_p)]
 
@@ -185,7 +194,7 @@ class Rope(C.Structure):
                 or not freqs.is_contiguous()):
             raise MoeError(1, "Rope")
         r = cls(freqs.data_ptr(), 2 * freqs.shape[0], 1 if interleaved else 0, magnitude, _ptr(ws))
-        r._tensors = (freqs, ws)
+        r._tensors, r._dev = (freqs, ws), _device(freqs, ws)
         return r
 
 
@@ -573,11 +582,15 @@ def moe_cache_evict(cache: KVCache, seqs: Seqs, scores, budget: int, n_recent: i
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _here(*tensors) -> bool:
-    """All of them (None aside) on the current device, on whose stream a call runs."""
+def _here(held, *tensors) -> bool:
+    """All of them (None aside), and the tensors behind the structures `held`, on the
+    current device, on whose stream a call runs."""
     dev = tensors[0].get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         return False
+    for h in held:
+        if h._dev != dev and h._dev is not None:
+            return False
     for t in tensors:
         if t is not None and t.get_device() != dev:
             return False
@@ -599,7 +612,7 @@ def moe_latent_append(rope: Rope, cache: LatentCache, seqs: Seqs, kv, q_rope, po
             and kv.shape == (shape[0], L + 64) and kv.dtype is _BF16 and q_rope.dtype is _BF16
             and q_out.dtype is _BF16 and _flat(positions, _I32, shape[:1])
             and (gamma is None or _flat(gamma, _F32, (L,)))
-            and _here(kv, q_rope, q_out, positions, gamma), "moe_latent_append")
+            and _here((rope, cache, seqs), kv, q_rope, q_out, positions, gamma), "moe_latent_append")
     T, H, _ = shape
     kt, k1 = kv.stride()
     qt, qh, q1 = q_rope.stride()
@@ -631,7 +644,7 @@ def moe_latent_attention(attn: Attn, cache: LatentCache, seqs: Seqs, q, out, ws,
     _refuse(q.shape == (T, H, W) and q.dtype is _BF16 and _flat(out, _BF16, (T, H, L))
             and (lse is None or _flat(lse, _F32, (T, H)))
             and (draft_mask is None or _flat(draft_mask, torch.int64, (T,)))
-            and _here(q, out, lse, draft_mask, ws), "moe_latent_attention")
+            and _here((cache, seqs), q, out, lse, draft_mask, ws), "moe_latent_attention")
     qt, qh, q1 = q.stride()
     _refuse(q1 == 1 and (qh == W or H == 1), "moe_latent_attention")
     _check(load().moe_latent_attention(C.byref(attn), C.byref(cache), C.byref(seqs), q.data_ptr(),
@@ -645,7 +658,7 @@ def moe_latent_gather(cache: LatentCache, seqs: Seqs, cu_k, out, ws, stream=None
     stride), where each sequence's cached rows go; rows of none are zeroed."""
     N, W = out.shape[0], cache.latent_dim + 64
     _refuse(out.shape == (N, W) and out.dtype is _BF16 and _flat(cu_k, _I32, (seqs.n_seqs + 1,))
-            and _here(out, cu_k, ws), "moe_latent_gather")
+            and _here((cache, seqs), out, cu_k, ws), "moe_latent_gather")
     rows, r1 = out.stride()
     _refuse(r1 == 1, "moe_latent_gather")
     _check(load().moe_latent_gather(C.byref(cache), C.byref(seqs), cu_k.data_ptr(), N, out.data_ptr(),
@@ -672,7 +685,7 @@ def moe_expanded_attention(attn: Attn, seqs: Seqs, cu_k, q, k, k_rope, v, out, w
             and v.dtype is _BF16 and k_rope.dtype is _BF16 and _flat(out, _BF16, (T, H, D))
             and cu_k.dim() == 1 and cu_k.shape[0] >= seqs.n_seqs and _flat(cu_k, _I32, cu_k.shape)
             and (lse is None or _flat(lse, _F32, (T, H)))
-            and _here(q, k, k_rope, v, out, cu_k, lse, ws), "moe_expanded_attention")
+            and _here((seqs,), q, k, k_rope, v, out, cu_k, lse, ws), "moe_expanded_attention")
     qt, qh, q1 = q.stride()
     kt, kh, k1 = k.stride()
     vt, vh, v1 = v.stride()
