@@ -716,7 +716,8 @@ typedef struct {
  * width), below 2^32; pointers 16-byte aligned; q_out and the cache overlap no
  * other argument.
  * fp32 arithmetic, one rounding: bf16, or the saturating e4m3 code of
- * x / 2^scale_log2.  Tokens without a place and numbers that do not fit: as
+ * x / 2^scale_log2; finite rows of any size are normalised (the sum of squares is
+ * kept within fp32).  Tokens without a place and numbers that do not fit: as
  * moe_rope_append.  n_tokens == 0 launches nothing.
  */
 moe_status_t moe_latent_append(const moe_rope_t* rope, const moe_latent_cache_t* cache,
@@ -742,6 +743,9 @@ size_t moe_latent_workspace_bytes(const moe_attn_t* attn, const moe_latent_cache
  *   out        bf16 [n_tokens, n_q_heads, latent_dim] contiguous; pad rows +0
  *   lse        fp32 [n_tokens, n_q_heads] or NULL, as moe_paged_attention's
  * n_q_heads is free (1 .. MOE_MAX_HEADS).  The rest as moe_paged_attention.
+ * A cached row that is not finite reaches no row that does not see it.  One that does
+ * is NaN where its score is NaN or +inf; after a score of -inf (weight 0) only the elements
+ * are where the latent is infinite.
  */
 moe_status_t moe_latent_attention(const moe_attn_t* attn, const moe_latent_cache_t* cache,
                                   const moe_seqs_t* seqs, const void* q, int64_t q_stride,
@@ -781,7 +785,8 @@ size_t moe_expanded_workspace_bytes(const moe_attn_t* attn, int32_t v_dim);
  * Strides in elements, positive multiples of 8, below 2^32; pointers 16-byte
  * aligned.  block_table and max_pages of seqs are not read; no draft masks.  A
  * length past n_keys is cut to it, a row outside 0 .. n_keys - 1 reads as zeros;
- * both are recorded (MOE_ERR_INVALID_ARG).
+ * both are recorded (MOE_ERR_INVALID_ARG).  A value that is not finite makes its
+ * element of the rows that see its key not finite, and no other.
  */
 moe_status_t moe_expanded_attention(const moe_attn_t* attn, const moe_seqs_t* seqs,
                                     const int32_t* cu_k, int32_t n_keys, int32_t v_dim,

@@ -620,7 +620,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& la, Shared& sh, uin
                     for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[e + k]);
                 float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 sh.top[g & 1u][half][lr] = top;
-                // powers by the reference so far, while the row's other half says its maximum
+                // powers by the reference so far, while the row's other half says its maximum: summed in
+                // fp32, rounded to bf16 for the product with bf16 values (its range holds any power)
                 uint32_t u[16];
                 float s0, s1;
                 auto powers = [&]() {
